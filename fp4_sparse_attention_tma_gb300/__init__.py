@@ -11,7 +11,9 @@ The operation follows "[FlyDSL] Add FP4 LiteTopK prefill operator"
 (ROCm/aiter#5282): score every query row against its C4 window of the paged FP4
 K cache, score = sum_h w * ReLU(q_h . k), and return the exact TopK positions
 (physical slots and optional raw positions) without materialising the
-[rows, context] score matrix.
+[rows, context] score matrix.  The attention over the cache that the selection
+serves (paged, and over the selected slots) and the cache's eviction by
+accumulated weight are here as well.
 """
 from __future__ import annotations
 
@@ -29,14 +31,17 @@ __all__ = ["IdxError", "SUPPORTED_K", "idx_topk_fp4_prefill", "idx_topk_fp4_pref
            "idx_fp4_debug_scores", "idx_topk_select_scores", "idx_topk_supported_k",
            "idx_topk_status_string", "idx_topk_fp4_scratch_bytes", "idx_topk_scratch_high_water",
            "dense_score_bytes", "STATUS", "idx_topk_set_timing",
-           "idx_topk_last_timings", "idx_debug_bounded_wait"]
+           "idx_topk_last_timings", "idx_debug_bounded_wait",
+           "idx_attn_paged", "idx_attn_paged_async", "idx_attn_paged_scratch_bytes",
+           "idx_attn_selected", "idx_attn_selected_async", "idx_attn_selected_scratch_bytes",
+           "idx_cache_evict", "idx_cache_evict_async", "idx_cache_evict_scratch_bytes"]
 
 STATUS = {0: "OK", 1: "INVALID_ARGUMENT", 2: "UNSUPPORTED", 3: "INVALID_METADATA",
           4: "INVALID_PAGE", 5: "OVERFLOW", 6: "CUDA_ERROR", 7: "INTERNAL", 8: "TIMEOUT",
           9: "SCRATCH_LIMIT", 10: "INVALID_VALUE"}
 SUPPORTED_K = (512, 1024)
 
-_DT = {"uint8": 1, "int32": 2, "float32": 3}
+_DT = {"uint8": 1, "int32": 2, "float32": 3, "bfloat16": 4, "float16": 5}
 
 
 class IdxError(RuntimeError):
@@ -312,6 +317,119 @@ def idx_topk_last_timings() -> dict:
     buf = (ctypes.c_float * 4)()
     _lib.load().idx_topk_last_timings(buf)
     return {"plan_ms": buf[0], "score_ms": buf[1], "finish_ms": buf[2], "kernels_ms": buf[3]}
+
+
+def _space(workspace, status):
+    return (ctypes.c_void_p(workspace.data_ptr()),
+            ctypes.c_uint64(workspace.numel() * workspace.element_size()),
+            ctypes.c_void_p(status.data_ptr()))
+
+
+def idx_attn_paged(q, k_cache, v_cache, page_table, row_req, row_start, row_end, scale, out,
+                   out_lse=None, weight_in=None, weight_out=None, stream=None,
+                   raise_on_error=True) -> int:
+    """Attention of the rows' tokens over their windows of a paged 16-bit cache
+    [NP, 64, Hk, D]; optionally the log-sum-exp, and the softmax weights that every
+    position received added to a running total (weight_out may be weight_in)."""
+    lib = _lib.load()
+    keep, ds = _descs((q, k_cache, v_cache, page_table, row_req, row_start, row_end, out,
+                       out_lse, weight_in, weight_out))
+    code = lib.idx_attn_paged(*ds[:7], float(scale), *ds[7:], _stream(stream))
+    return _check(code, "idx_attn_paged", raise_on_error)
+
+
+def idx_attn_paged_async(q, k_cache, v_cache, page_table, row_req, row_start, row_end, scale, out,
+                         workspace, status, out_lse=None, weight_in=None, weight_out=None,
+                         stream=None, raise_on_error=True) -> int:
+    """idx_attn_paged without host synchronisation or allocation (graph-capturable):
+    `workspace` a uint8 device tensor of at least idx_attn_paged_scratch_bytes bytes,
+    `status` an int32 device tensor of one element."""
+    lib = _lib.load()
+    keep, ds = _descs((q, k_cache, v_cache, page_table, row_req, row_start, row_end, out,
+                       out_lse, weight_in, weight_out))
+    code = lib.idx_attn_paged_async(*ds[:7], float(scale), *ds[7:], *_space(workspace, status),
+                                    _stream(stream))
+    return _check(code, "idx_attn_paged_async", raise_on_error)
+
+
+def idx_attn_paged_scratch_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: int,
+                                 num_req: int, max_pages: int, with_weights: bool = False,
+                                 device: int = 0) -> int:
+    v = ctypes.c_uint64(0)
+    code = _lib.load().idx_attn_paged_scratch_bytes(
+        int(rows), int(q_heads), int(kv_heads), int(head_dim), int(num_req), int(max_pages),
+        1 if with_weights else 0, int(device), ctypes.byref(v))
+    _check(code, "idx_attn_paged_scratch_bytes", True)
+    return int(v.value)
+
+
+def idx_attn_selected(q, k_cache, v_cache, slots, scale, out, out_lse=None, stream=None,
+                      raise_on_error=True) -> int:
+    """Attention of each row over its list of physical slots [R, N] (-1: none), as
+    the TopK writes them to out_phys_slot."""
+    lib = _lib.load()
+    keep, ds = _descs((q, k_cache, v_cache, slots, out, out_lse))
+    code = lib.idx_attn_selected(*ds[:4], float(scale), ds[4], ds[5], _stream(stream))
+    return _check(code, "idx_attn_selected", raise_on_error)
+
+
+def idx_attn_selected_async(q, k_cache, v_cache, slots, scale, out, workspace, status,
+                            out_lse=None, stream=None, raise_on_error=True) -> int:
+    """idx_attn_selected without host synchronisation or allocation
+    (graph-capturable); `workspace` of idx_attn_selected_scratch_bytes bytes."""
+    lib = _lib.load()
+    keep, ds = _descs((q, k_cache, v_cache, slots, out, out_lse))
+    code = lib.idx_attn_selected_async(*ds[:4], float(scale), ds[4], ds[5],
+                                       *_space(workspace, status), _stream(stream))
+    return _check(code, "idx_attn_selected_async", raise_on_error)
+
+
+def idx_attn_selected_scratch_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: int,
+                                    selected: int, device: int = 0) -> int:
+    v = ctypes.c_uint64(0)
+    code = _lib.load().idx_attn_selected_scratch_bytes(
+        int(rows), int(q_heads), int(kv_heads), int(head_dim), int(selected), int(device),
+        ctypes.byref(v))
+    _check(code, "idx_attn_selected_scratch_bytes", True)
+    return int(v.value)
+
+
+def idx_cache_evict(k_cache, v_cache, page_table, seq_len, weight, budget, keep_first, keep_last,
+                    k_dst, v_dst, dst_page_table, out_keep_idx, out_len, out_page_table,
+                    out_weight, stream=None, raise_on_error=True) -> int:
+    """Cuts every request longer than `budget` to its first keep_first, its last
+    keep_last and its heaviest other positions, moved in order to the fresh pages of
+    dst_page_table; writes the kept positions, lengths, page table and weights."""
+    lib = _lib.load()
+    keep, ds = _descs((k_cache, v_cache, page_table, seq_len, weight, k_dst, v_dst,
+                       dst_page_table, out_keep_idx, out_len, out_page_table, out_weight))
+    code = lib.idx_cache_evict(*ds[:5], int(budget), int(keep_first), int(keep_last), *ds[5:],
+                               _stream(stream))
+    return _check(code, "idx_cache_evict", raise_on_error)
+
+
+def idx_cache_evict_async(k_cache, v_cache, page_table, seq_len, weight, budget, keep_first,
+                          keep_last, k_dst, v_dst, dst_page_table, out_keep_idx, out_len,
+                          out_page_table, out_weight, workspace, status, stream=None,
+                          raise_on_error=True) -> int:
+    """idx_cache_evict without host synchronisation or allocation
+    (graph-capturable); `workspace` of idx_cache_evict_scratch_bytes bytes."""
+    lib = _lib.load()
+    keep, ds = _descs((k_cache, v_cache, page_table, seq_len, weight, k_dst, v_dst,
+                       dst_page_table, out_keep_idx, out_len, out_page_table, out_weight))
+    code = lib.idx_cache_evict_async(*ds[:5], int(budget), int(keep_first), int(keep_last),
+                                     *ds[5:], *_space(workspace, status), _stream(stream))
+    return _check(code, "idx_cache_evict_async", raise_on_error)
+
+
+def idx_cache_evict_scratch_bytes(num_req: int, max_pages: int, dst_pages: int, budget: int,
+                                  device: int = 0) -> int:
+    v = ctypes.c_uint64(0)
+    code = _lib.load().idx_cache_evict_scratch_bytes(int(num_req), int(max_pages),
+                                                     int(dst_pages), int(budget), int(device),
+                                                     ctypes.byref(v))
+    _check(code, "idx_cache_evict_scratch_bytes", True)
+    return int(v.value)
 
 
 def dense_score_bytes(rows: int, context: int) -> int:

@@ -26,7 +26,8 @@ LIB_PATH = os.path.join(_HERE, "libidxtopk.so")
 # for a memory checker, run by the GPU tests on small cases)
 DEBUG_BUILD_DIR = os.path.join(_HERE, "_build_dbg")
 DEBUG_LIB_PATH = os.path.join(_HERE, "libidxtopk_dbg.so")
-SOURCES = ["host.cu", "plan.cu", "score.cu", "finish.cu"]
+SOURCES = ["host.cu", "plan.cu", "score.cu", "finish.cu", "attn_host.cu", "attn_paged.cu",
+           "attn_slots.cu", "attn_join.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "-I" + INCLUDE, "-I" + CSRC] + ARCH
@@ -132,6 +133,26 @@ EXPORTS = {
                                                   ctypes.POINTER(ctypes.c_uint64)]),
     "idx_topk_scratch_high_water": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)]),
     "idx_debug_bounded_wait": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
+    "idx_attn_paged": (ctypes.c_int, [_DESC_PTR] * 7 + [ctypes.c_float] + [_DESC_PTR] * 4 +
+                       [ctypes.c_void_p]),
+    "idx_attn_paged_async": (ctypes.c_int, [_DESC_PTR] * 7 + [ctypes.c_float] + [_DESC_PTR] * 4 +
+                             [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p]),
+    "idx_attn_paged_scratch_bytes": (ctypes.c_int, [ctypes.c_int32] * 8 +
+                                     [ctypes.POINTER(ctypes.c_uint64)]),
+    "idx_attn_selected": (ctypes.c_int, [_DESC_PTR] * 4 + [ctypes.c_float] + [_DESC_PTR] * 2 +
+                          [ctypes.c_void_p]),
+    "idx_attn_selected_async": (ctypes.c_int, [_DESC_PTR] * 4 + [ctypes.c_float] +
+                                [_DESC_PTR] * 2 + [ctypes.c_void_p, ctypes.c_uint64,
+                                                   ctypes.c_void_p, ctypes.c_void_p]),
+    "idx_attn_selected_scratch_bytes": (ctypes.c_int, [ctypes.c_int32] * 6 +
+                                        [ctypes.POINTER(ctypes.c_uint64)]),
+    "idx_cache_evict": (ctypes.c_int, [_DESC_PTR] * 5 + [ctypes.c_int32] * 3 + [_DESC_PTR] * 7 +
+                        [ctypes.c_void_p]),
+    "idx_cache_evict_async": (ctypes.c_int, [_DESC_PTR] * 5 + [ctypes.c_int32] * 3 +
+                              [_DESC_PTR] * 7 + [ctypes.c_void_p, ctypes.c_uint64,
+                                                 ctypes.c_void_p, ctypes.c_void_p]),
+    "idx_cache_evict_scratch_bytes": (ctypes.c_int, [ctypes.c_int32] * 5 +
+                                      [ctypes.POINTER(ctypes.c_uint64)]),
     "idx_topk_set_timing": (ctypes.c_int, [ctypes.c_int32]),
     "idx_topk_last_timings": (ctypes.c_int, [ctypes.POINTER(ctypes.c_float)]),
 }

@@ -1,0 +1,654 @@
+// The attention kernel: one pass over the cached positions of every row with the
+// running maximum and sum of the softmax,
+//
+//   s_hj = c * q_h . k_j,  m_h = max_j s_hj,  l_h = sum_j 2^(s_hj - m_h),
+//   out_h = (1 / l_h) sum_j 2^(s_hj - m_h) v_j,   c = scale * log2(e),
+//
+// products in 16 bits with fp32 accumulation, everything else in fp32; the weights
+// 2^(s - m) are rounded to the inputs' type for the second product (their sum is
+// not), which costs as much as the rounding of the output.
+//
+// What bounds it is the cache's traffic: a key and a value are read for 4 flops per
+// query head of their group and element, so up to about 70 query heads per key-value
+// head are below the tensor cores' ratio to HBM.  Hence warps that never wait for one
+// another: every warp owns a ring of asynchronous 16-byte copies (kSub positions of
+// keys and values a stage) and a range of subtiles (attn.h), and one warp-level matrix
+// instruction chain consumes a stage while the others are in flight.  The copies take
+// any page, slot and head stride and any list of slots, and fill with zero what no row
+// sees, so that what lies there cannot reach a sum.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "attn.h"
+#include "idx_launch.h"
+
+namespace idxk {
+namespace attn {
+
+constexpr float kNegInf = -INFINITY;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// 16-byte asynchronous copy; bytes = 0 writes zeros and reads nothing.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (BF16) {
+    __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *(uint32_t*)&t;
+  } else {
+    __half2 t = __floats2half2_rn(lo, hi);
+    return *(uint32_t*)&t;
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Divides the units' subtiles among the workers.
+struct Split {
+  int64_t total;    // subtiles of all units
+  int32_t active;   // workers with a range
+  __device__ int64_t first(int64_t w) const { return total * w / active; }
+  // the worker whose range holds subtile x
+  __device__ int32_t holder(int64_t x) const { return (int32_t)(((x + 1) * active - 1) / total); }
+};
+
+// A place in the list of units: subtile `s` of unit `u` of the group at row0.
+template <bool SLOTS>
+struct Cursor {
+  int32_t row0, nrows, req;   // the group
+  int32_t lo, hi;             // positions of its rows' windows, together
+  int32_t base, nsub;         // first subtile (absolute) and their number
+  int32_t u, s;
+
+  // The group that starts at `row`.  Called by the whole warp.
+  __device__ void load(const AttnParams& p, int32_t row) {
+    row0 = row;
+    if constexpr (SLOTS) {
+      nrows = 1;
+      req = 0;
+      lo = 0;
+      hi = p.n_slots;
+      base = 0;
+    } else {
+      const int lane = threadIdx.x & 31;
+      const int32_t r = row + lane;
+      const int32_t stop = min(p.rows, (row / p.group_rows + 1) * p.group_rows);
+      const bool in = r < stop;
+      const int32_t rr = in ? p.row_req[r] : -1;
+      req = __shfl_sync(~0u, rr, 0);
+      const uint32_t other = ~__ballot_sync(~0u, in && rr == req);
+      nrows = other ? __ffs(other) - 1 : 32;
+      int32_t a = INT32_MAX, b = 0;
+      if (lane < nrows) {
+        const int32_t a0 = p.row_start[r], b0 = p.row_end[r];
+        if (b0 > a0) a = a0, b = b0;
+      }
+      lo = __reduce_min_sync(~0u, a);
+      hi = __reduce_max_sync(~0u, b);
+      if (lo > hi) lo = hi;
+      base = lo / kSub;
+    }
+    nsub = hi > lo ? (hi + kSub - 1) / kSub - base : 0;
+  }
+  // The next subtile; the caller has not passed the end of the list.
+  __device__ void next(const AttnParams& p) {
+    if (++s < nsub) return;
+    s = 0;
+    if (++u < p.kv_heads * p.chunks) return;
+    u = 0;
+    do {
+      load(p, row0 + nrows);
+    } while (nsub == 0);
+  }
+};
+
+// Finds the range of every worker of the CTA: checks the rows' metadata (all of it, by
+// every CTA, so that all agree), counts the subtiles and leaves, for worker w =
+// warp * gridDim.x + blockIdx.x, the place where its range starts in `cur`.  False: an
+// error (recorded in *err) or nothing to do for this warp.
+template <bool SLOTS, int WARPS>
+__device__ bool find_range(const AttnParams& p, Split& sp, Cursor<SLOTS>& cur, int32_t worker, uint32_t* err) {
+  const int32_t units = p.kv_heads * p.chunks;
+  if constexpr (SLOTS) {
+    const int32_t n = (p.n_slots + kSub - 1) / kSub;
+    sp.total = (int64_t)p.rows * units * n;
+    const int64_t most = (sp.total + p.min_sub - 1) / p.min_sub;
+    sp.active = (int32_t)(most < p.workers ? most : p.workers);
+    if (worker >= sp.active) return false;
+    const int64_t t = sp.first(worker);
+    const int64_t per_row = (int64_t)units * n;
+    const int32_t row = (int32_t)(t / per_row);
+    const int64_t rest = t - row * per_row;
+    cur.load(p, row);
+    cur.u = (int32_t)(rest / n);
+    cur.s = (int32_t)(rest - (int64_t)cur.u * n);
+    return true;
+  } else {
+    constexpr int N = WARPS * 32;
+    __shared__ int64_t warp_sum[WARPS];
+    __shared__ int64_t pre[N];          // subtiles before each row of the pass, in the pass
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // subtiles of the group that starts at row r (0 where none does)
+    auto count = [&](int32_t r) -> int32_t {
+      if (r >= p.rows) return 0;
+      const int32_t req = p.row_req[r];
+      if (r % p.group_rows != 0 && p.row_req[r - 1] == req) return 0;
+      int32_t a = INT32_MAX, b = 0;
+      for (int32_t i = r; i < p.rows && (i == r || (i % p.group_rows != 0 && p.row_req[i] == req)); ++i) {
+        const int32_t a0 = p.row_start[i], b0 = p.row_end[i];
+        if (b0 > a0) a = min(a, a0), b = max(b, b0);
+      }
+      return b > a ? (b + kSub - 1) / kSub - a / kSub : 0;
+    };
+    int64_t sum = 0;
+    bool bad = false;
+    for (int32_t r = tid; r < p.rows; r += N) {
+      const int32_t q = p.row_req[r], a = p.row_start[r], b = p.row_end[r];
+      bad |= q < 0 || q >= p.num_req || a < 0 || b < a || (int64_t)b > (int64_t)p.max_pages * kPage;
+    }
+    if (__syncthreads_or(bad)) {
+      if (tid == 0) *err = kErrInvalidMetadata;
+      return false;
+    }
+    const bool one_pass = p.rows <= N;
+    int32_t mine = 0;
+    for (int32_t r = tid; r < p.rows; r += N) sum += mine = count(r);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) warp_sum[warp] = sum;
+    __syncthreads();
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) sum += warp_sum[i];
+    sp.total = sum * units;
+    const int64_t most = (sp.total + p.min_sub - 1) / p.min_sub;
+    sp.active = (int32_t)(most < p.workers ? most : p.workers);
+    const bool some = worker < sp.active;
+    const int64_t t = some ? sp.first(worker) : 0;
+    bool found = false;
+    int64_t before = 0;   // subtiles (of one unit each) before the pass
+    for (int32_t r0 = 0; r0 < p.rows; r0 += N) {
+      if (!one_pass) mine = count(r0 + tid);
+      int64_t inc = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += x;
+      }
+      __syncthreads();
+      if (lane == 31) warp_sum[warp] = inc;
+      __syncthreads();
+      int64_t base = 0, all = 0;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) {
+        if (i < warp) base += warp_sum[i];
+        all += warp_sum[i];
+      }
+      pre[tid] = base + inc - mine;
+      __syncthreads();
+      if (some && !found && t < (before + all) * units) {
+        // the last row of the pass whose subtiles start at or before t: the first row of the group that
+        // holds it (rows without a count of their own come before it, or start after t)
+        const int32_t n = min(N, p.rows - r0);
+        int32_t at = 0;
+        for (int32_t i = lane; i < n; i += 32)
+          if ((before + pre[i]) * units <= t) at = i;   // pre is non-decreasing
+        at = __reduce_max_sync(~0u, at);
+        const int64_t rest = t - (before + pre[at]) * units;
+        cur.load(p, r0 + at);
+        cur.u = (int32_t)(rest / cur.nsub);
+        cur.s = (int32_t)(rest - (int64_t)cur.u * cur.nsub);
+        found = true;
+      }
+      before += all;
+    }
+    return found;
+  }
+}
+
+template <bool BF16, int D, int TILE, int WARPS, int STAGES, bool SLOTS>
+__global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_constant__ AttnParams p) {
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr int MT = TILE / 16;          // matrix tiles of 16 query heads x rows
+  constexpr int KS = D / 16;             // steps of the first product
+  constexpr int NT = D / 8;              // tiles of 8 of the output's columns
+  constexpr int CH = D / 8;              // 16-byte pieces of a cached head
+  constexpr uint32_t kHalf = kSub * D * 2;  // bytes of a stage's keys (and of its values)
+
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ uint32_t err;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t worker = warp * gridDim.x + blockIdx.x;
+  if (threadIdx.x == 0) err = kOk;
+  __syncthreads();
+
+  Split sp;
+  Cursor<SLOTS> at;
+  const bool work = find_range<SLOTS, WARPS>(p, sp, at, worker, &err);
+  if (lane == 0) p.open_row[worker] = -1;
+  uint32_t warp_err = kOk;
+  if (work) {
+    const uint32_t my_ring = smem_addr(ring) + (uint32_t)warp * (STAGES * 2 * kHalf);
+    int64_t here = sp.first(worker);                 // flat index of the subtile computed next
+    const int64_t stop = sp.first(worker + 1);
+    int64_t to_fetch = stop - here;
+
+    // ---- fetching side ----
+    Cursor<SLOTS> f = at;
+    int32_t entry;   // page of the subtile to be fetched, or the slot of position lane % 16
+    auto look_up = [&]() {
+      if constexpr (SLOTS) {
+        const int32_t j = f.s * kSub + (lane & 15);
+        entry = j < p.n_slots ? p.slots[(int64_t)f.row0 * p.n_slots + j] : -1;
+      } else {
+        entry = p.page_table[(int64_t)f.req * p.max_pages + (f.base + f.s) * kSub / kPage];
+      }
+    };
+    if (to_fetch > 0) look_up();
+    auto fetch = [&](int stage) {
+      if (to_fetch > 0) {
+        const uint32_t dk = my_ring + (uint32_t)stage * (2 * kHalf), dv = dk + kHalf;
+        const int32_t head = f.u / p.chunks;
+        const T* k = (const T*)p.k + head * p.k_head;
+        const T* v = (const T*)p.v + head * p.v_head;
+        constexpr int ROWS = 32 / CH > 0 ? 32 / CH : 1;   // positions that one copy of the warp covers
+        const int chunk = lane % CH;
+        if constexpr (SLOTS) {
+          if (entry < -1 || entry >= p.num_pages * kPage) warp_err = kErrInvalidPage, entry = -1;
+        } else {
+          if (entry < 0 || entry >= p.num_pages) warp_err = kErrInvalidPage, entry = -1;
+          const int32_t off = (f.base + f.s) * kSub % kPage;
+          const int64_t page = entry < 0 ? 0 : entry;
+          k += page * p.k_page + off * p.k_slot;
+          v += page * p.v_page + off * p.v_slot;
+        }
+#pragma unroll
+        for (int i = 0; i < kSub / ROWS; ++i) {
+          const int r = i * ROWS + (ROWS > 1 ? lane / CH : 0);
+          const T *ks, *vs;
+          bool on;
+          if constexpr (SLOTS) {
+            const int32_t slot = __shfl_sync(~0u, entry, r);
+            on = slot >= 0;
+            const int64_t pg = on ? slot / kPage : 0;
+            const int32_t off = on ? slot % kPage : 0;
+            ks = k + pg * p.k_page + off * p.k_slot;
+            vs = v + pg * p.v_page + off * p.v_slot;
+          } else {
+            const int32_t pos = (f.base + f.s) * kSub + r;
+            on = entry >= 0 && pos >= f.lo && pos < f.hi;
+            ks = on ? k + r * p.k_slot : (const T*)p.k;
+            vs = on ? v + r * p.v_slot : (const T*)p.v;
+          }
+          const uint32_t d = (uint32_t)(r * (D * 2) + ((chunk ^ (r & 7)) << 4));
+          copy16(dk + d, ks + chunk * 8, on ? 16u : 0u);
+          copy16(dv + d, vs + chunk * 8, on ? 16u : 0u);
+        }
+        if (--to_fetch > 0) {
+          f.next(p);
+          look_up();
+        }
+      }
+      copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+
+    // ---- computing side ----
+    uint32_t qf[MT][KS][4];
+    float o[MT][NT][4];
+    float mx[MT][2], sum[MT][2];
+    int32_t w_lo[MT][2], w_hi[MT][2];   // windows of the thread's tile rows
+    uint32_t live = 0;                  // bit 2t + e: the thread's tile row is a row that sees something
+    bool seen = false;                  // (slots) some slot of the segment was one
+    int32_t full_lo, full_hi;           // positions that every row of the group sees
+    bool begin = true;                  // the next subtile is the first of a segment
+    bool cut_front = false;             // the segment starts inside its unit
+    int stage = 0;
+    const float c = p.scale_log2;
+    while (here < stop) {
+      const int32_t head = at.u / p.chunks, h0 = head * p.group + (at.u % p.chunks) * p.chunk_heads;
+      const int32_t heads = min(p.chunk_heads, p.group - (at.u % p.chunks) * p.chunk_heads);
+      // tile row m: row m / chunk_heads of the group, head h0 + m % chunk_heads
+      if (begin) {
+        begin = false;
+        cut_front = at.s > 0;
+        full_lo = 0, full_hi = INT32_MAX;
+        live = 0;
+        seen = false;
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int m = t * 16 + e * 8 + lane / 4;
+            const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
+            bool on = j < at.nrows && h < heads;
+            int32_t a = at.lo, b = at.hi;
+            if constexpr (!SLOTS) {
+              if (on) {
+                a = p.row_start[at.row0 + j], b = p.row_end[at.row0 + j];
+                if (b <= a) on = false, a = at.lo, b = at.hi;
+              }
+            }
+            if (on) live |= 1u << (2 * t + e);
+            w_lo[t][e] = a, w_hi[t][e] = b;
+            full_lo = max(full_lo, a), full_hi = min(full_hi, b);
+            mx[t][e] = kNegInf, sum[t][e] = 0.f;
+            const uint32_t* src =
+                (const uint32_t*)((const T*)p.q + (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              qf[t][k][e] = on ? src[k * 8 + (lane & 3)] : 0u;
+              qf[t][k][2 + e] = on ? src[k * 8 + 4 + (lane & 3)] : 0u;
+            }
+          }
+        if constexpr (SLOTS) full_hi = 0;  // the slots are looked at one by one
+        full_lo = __reduce_max_sync(~0u, full_lo);
+        full_hi = __reduce_min_sync(~0u, full_hi);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[t][n][x] = 0.f;
+      }
+
+      // the next stage goes where the last one computed was
+      copy_wait<STAGES - 2>();
+      __syncwarp();
+      fetch(stage == 0 ? STAGES - 1 : stage - 1);
+      const uint32_t sk = my_ring + (uint32_t)stage * (2 * kHalf), sv = sk + kHalf;
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+
+      // scores of the subtile: two tiles of 8 positions
+      float s[MT][2][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[t][n][x] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; k += 2)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          uint32_t b[4];
+          const int r = n * 8 + (lane & 7);
+          ldsm4(sk + (uint32_t)(r * (D * 2) + (((k * 2 + lane / 8) ^ (r & 7)) << 4)), b);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            mma16816<BF16>(s[t][n], qf[t][k], b[0], b[1]);
+            mma16816<BF16>(s[t][n], qf[t][k + 1], b[2], b[3]);
+          }
+        }
+
+      const int32_t pos0 = (at.base + at.s) * kSub;
+      bool edge;
+      if constexpr (SLOTS) {
+        // the slots again: only whether each is one
+        const int32_t j = pos0 + (lane & 15);
+        const int32_t slot = j < p.n_slots ? p.slots[(int64_t)at.row0 * p.n_slots + j] : -1;
+        const uint32_t on = __ballot_sync(~0u, slot >= 0 && slot < p.num_pages * kPage);
+        edge = (on & 0xFFFFu) != 0xFFFFu;
+        seen |= on != 0;
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (!(on >> (n * 8 + (lane & 3) * 2 + x) & 1)) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) s[t][n][x] = s[t][n][2 + x] = kNegInf;
+              }
+        }
+      } else {
+        edge = pos0 < full_lo || pos0 + kSub > full_hi;
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int32_t pos = pos0 + n * 8 + (lane & 3) * 2 + x;
+#pragma unroll
+              for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (pos < w_lo[t][e] || pos >= w_hi[t][e]) s[t][n][2 * e + x] = kNegInf;
+            }
+        }
+        if (p.logits) {
+          const int64_t width = (int64_t)p.max_pages * kPage;
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int m = t * 16 + e * 8 + lane / 4;
+              const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
+              if (live >> (2 * t + e) & 1) {
+                float* dst = p.logits + ((int64_t)(at.row0 + j) * p.q_heads + h0 + h) * width + pos0 + (lane & 3) * 2;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) *(float2*)(dst + n * 8) = make_float2(s[t][n][2 * e], s[t][n][2 * e + 1]);
+              }
+            }
+        }
+      }
+
+      // running maximum; the sums are scaled where it moved
+      float mc[MT][2];
+      bool moved = false;
+      float alpha[MT][2];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m = fmaxf(fmaxf(s[t][0][2 * e], s[t][0][2 * e + 1]), fmaxf(s[t][1][2 * e], s[t][1][2 * e + 1]));
+          m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+          m = fmaxf(m, mx[t][e]);
+          // a row without a finite score so far keeps 0 in its maximum's place
+          mc[t][e] = m == kNegInf ? 0.f : __fmul_rn(m, c);
+          alpha[t][e] = ex2(__fsub_rn(__fmul_rn(mx[t][e], c), mc[t][e]));
+          moved |= m != mx[t][e];
+          mx[t][e] = m;
+        }
+      if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) sum[t][e] *= alpha[t][e];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[t][n][0] *= alpha[t][0];
+            o[t][n][1] *= alpha[t][0];
+            o[t][n][2] *= alpha[t][1];
+            o[t][n][3] *= alpha[t][1];
+          }
+        }
+      }
+      uint32_t pf[MT][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a = ex2(fmaf(s[t][n][2 * e], c, -mc[t][e]));
+            const float b = ex2(fmaf(s[t][n][2 * e + 1], c, -mc[t][e]));
+            sum[t][e] += a + b;
+            pf[t][n * 2 + e] = pack2<BF16>(a, b);
+          }
+
+      const uint32_t va = sv + (uint32_t)((lane & 15) * (D * 2));
+      const uint32_t vx = (uint32_t)(lane & 7);
+      if (SLOTS || !edge || at.nrows == 1) {
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t b[4];
+          ldsm4t(va + (((uint32_t)(n + lane / 16) ^ vx) << 4), b);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            mma16816<BF16>(o[t][n], pf[t], b[0], b[1]);
+            mma16816<BF16>(o[t][n + 1], pf[t], b[2], b[3]);
+          }
+        }
+      } else {
+        // some rows of the group see a position and others do not: row by row, with the values that the
+        // row does not see set to zero (0 x infinity or NaN would not be)
+        for (int j = 0; j < at.nrows; ++j) {
+          const int32_t a0 = p.row_start[at.row0 + j], b0 = p.row_end[at.row0 + j];
+          if (b0 <= a0) continue;
+          uint32_t keep[2];   // of the thread's pairs of positions
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int32_t pos = pos0 + x * 8 + (lane & 3) * 2;
+            keep[x] = (pos >= a0 && pos < b0 ? 0xFFFFu : 0u) | (pos + 1 >= a0 && pos + 1 < b0 ? 0xFFFF0000u : 0u);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; n += 2) {
+            uint32_t b[4];
+            ldsm4t(va + (((uint32_t)(n + lane / 16) ^ vx) << 4), b);
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816<BF16>(d, pf[t], b[2 * y] & keep[0], b[2 * y + 1] & keep[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if ((t * 16 + e * 8 + lane / 4) / p.chunk_heads == j) {
+                    o[t][n + y][2 * e] += d[2 * e];
+                    o[t][n + y][2 * e + 1] += d[2 * e + 1];
+                  }
+              }
+          }
+        }
+      }
+
+      ++here;
+      const bool unit_end = at.s + 1 == at.nsub;
+      if (unit_end || here == stop) {
+        // the segment ends: finish the unit, or leave its part
+        begin = true;
+        const bool whole = unit_end && !cut_front;
+        const int which = cut_front ? 0 : 1;
+        if (!unit_end && !cut_front && lane == 0) {
+          p.open_row[worker] = at.row0;
+          p.open_info[worker] = make_int4(at.nrows, at.u, sp.holder(here + (at.nsub - at.s) - 2), 0);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float l = sum[t][e];
+            l += __shfl_xor_sync(~0u, l, 1);
+            l += __shfl_xor_sync(~0u, l, 2);
+            const int m = t * 16 + e * 8 + lane / 4;
+            const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
+            const bool on = live >> (2 * t + e) & 1;
+            const float mcs = __fmul_rn(mx[t][e], c);
+            if (!whole) {
+              const int64_t at_part = ((int64_t)worker * 2 + which) * TILE + m;
+              if (on) {
+                // a sum of -1: the part saw no position at all
+                if ((lane & 3) == 0) p.part_ml[at_part] = make_float2(mcs, SLOTS && !seen ? -1.f : l);
+                float2* dst = (float2*)(p.part_o + at_part * D) + (lane & 3);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) dst[n * 4] = make_float2(o[t][n][2 * e], o[t][n][2 * e + 1]);
+              }
+            } else if (on) {
+              const int64_t row = at.row0 + j;
+              const int32_t qh = h0 + h;
+              const float inv = SLOTS && !seen ? 0.f : 1.f / l;
+              T* dst = (T*)p.out + row * p.out_row + (int64_t)qh * p.out_head + (lane & 3) * 2;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                *(uint32_t*)(dst + n * 8) = pack2<BF16>(o[t][n][2 * e] * inv, o[t][n][2 * e + 1] * inv);
+              if ((lane & 3) == 0) {
+                if (p.lse) p.lse[row * p.q_heads + qh] = (mcs + log2f(l)) * 0.6931471805599453f;
+                if (p.row_stat) p.row_stat[row * p.q_heads + qh] = make_float2(mcs == kNegInf ? 0.f : mcs, inv);
+              }
+            }
+          }
+      }
+      if (here < stop) at.next(p);
+    }
+    copy_wait<0>();
+  }
+  // rows that see nothing
+  if constexpr (!SLOTS) {
+    for (int64_t i = (int64_t)blockIdx.x * (WARPS * 32) + threadIdx.x; i < p.rows * (int64_t)p.q_heads;
+         i += (int64_t)gridDim.x * (WARPS * 32)) {
+      const int32_t r = (int32_t)(i / p.q_heads), h = (int32_t)(i - (int64_t)r * p.q_heads);
+      if (p.row_end[r] > p.row_start[r]) continue;
+      uint4* o = (uint4*)((T*)p.out + r * p.out_row + h * p.out_head);
+      for (int j = 0; j < CH; ++j) o[j] = make_uint4(0, 0, 0, 0);
+      if (p.lse) p.lse[i] = kNegInf;
+      if (p.row_stat) p.row_stat[i] = make_float2(0.f, 0.f);
+    }
+  }
+  warp_err = __reduce_max_sync(~0u, warp_err);
+  if (lane == 0 && warp_err != kOk) atomicMax(&err, warp_err);
+  __syncthreads();
+  if (threadIdx.x == 0) p.cta_status[blockIdx.x] = err;
+}
+
+template <bool BF16, int D, int TILE, int WARPS, int STAGES, bool SLOTS>
+cudaError_t launch_one(const AttnParams& p, int sm_count, cudaStream_t stream) {
+  auto* kernel = attn_kernel<BF16, D, TILE, WARPS, STAGES, SLOTS>;
+  constexpr int smem = WARPS * STAGES * 2 * kSub * D * 2;
+  static std::atomic<bool> done[64];
+  cudaError_t e = set_smem_once(kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  kernel<<<sm_count, WARPS * 32, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace attn
+}  // namespace idxk

@@ -1,0 +1,125 @@
+// Shared definitions of the attention operators (attention of new tokens over a
+// paged key-value cache, and over lists of physical slots): parameters, the
+// division of the work, the workspace layout and the launchers.
+//
+// The work of a call is a list of units.  A unit is one key-value head (or, where
+// more query heads share it than one matrix tile holds, one chunk of them) of one
+// row group: consecutive rows of one request, as many as share a tile, so that
+// their cached positions are read once.  A unit is cut into subtiles of kSub
+// positions; the units' subtiles, one after another, are dealt to the workers (one
+// warp each) in equal contiguous ranges.  A unit that lies inside one worker's range
+// is finished there; one that is cut leaves partial sums (the maximum, the sum of
+// the exponentials and the weighted values, all fp32), which attn_join_kernel
+// combines.  A worker's range cuts at most two units, so the workspace is bounded by
+// the machine, not by rows or context.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "idx_internal.h"
+
+namespace idxk {
+
+constexpr int kSub = 16;           // cached positions per subtile
+constexpr int kMaxTile = 32;       // most query heads x rows of a unit
+constexpr int kMaxGroupRows = 32;  // most rows of a group (one lane each)
+
+struct AttnParams {
+  const void *q, *k, *v;
+  void* out;
+  float* lse;                       // [rows, q_heads] or null
+  int64_t q_row, q_head;            // strides in elements
+  int64_t k_page, k_slot, k_head;
+  int64_t v_page, v_slot, v_head;
+  int64_t out_row, out_head;
+  const int32_t *page_table, *row_req, *row_start, *row_end;
+  const int32_t* slots;             // [rows, n_slots]: attention over slot lists, else null
+  int32_t n_slots;
+  int32_t rows, num_req, max_pages, num_pages;
+  int32_t q_heads, kv_heads;
+  int32_t group;                    // query heads per key-value head
+  int32_t chunks, chunk_heads;      // a key-value head's query heads in chunks of at most a tile
+  int32_t group_rows;               // rows per group, at most (1 where there are several chunks)
+  int32_t workers;                  // warps of the grid
+  int32_t min_sub;                  // a worker's range holds at least this many subtiles
+  float scale_log2;                 // softmax scale x log2(e)
+  // workspace
+  uint32_t* cta_status;             // [CTAs] first error that the CTA saw
+  int32_t n_cta;
+  int32_t* open_row;                // [workers] first row of the unit cut at the range's end, or -1
+  int4* open_info;                  // [workers] {rows of its group, unit index in the group, last worker, 0}
+  float2* part_ml;                  // [workers][2][tile] maximum (in units of log2, scaled) and sum
+  float* part_o;                    // [workers][2][tile][dim]
+  int32_t tile;                     // 16 or 32
+  int32_t dim;
+  // accumulated weights
+  float* logits;                    // [rows * q_heads][max_pages * 64] or null
+  float2* row_stat;                 // [rows * q_heads] maximum (scaled) and 1 / sum, or null
+  const float* weight_in;           // [num_req][max_pages * 64] or null
+  float* weight_out;
+  uint32_t* status_out;
+};
+
+// Byte offsets of a call's workspace.
+struct AttnLayout {
+  size_t cta_status, open_row, open_info, part_ml, part_o, row_stat, logits, total;
+};
+
+inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int64_t dim, int64_t stat_rows,
+                              int64_t logit_width) {
+  AttnLayout L{};
+  size_t off = 0;
+  L.cta_status = off; off = align_up(off + (size_t)n_cta * 4, 256);
+  L.open_row = off;   off = align_up(off + (size_t)workers * 4, 256);
+  L.open_info = off;  off = align_up(off + (size_t)workers * 16, 256);
+  L.part_ml = off;    off = align_up(off + (size_t)workers * 2 * tile * 8, 256);
+  L.part_o = off;     off = align_up(off + (size_t)workers * 2 * tile * dim * 4, 256);
+  L.row_stat = off;   off = align_up(off + (size_t)stat_rows * 8, 256);
+  L.logits = off;     off = align_up(off + (size_t)stat_rows * (size_t)logit_width * 4, 256);
+  L.total = off;
+  return L;
+}
+
+// How a call's kernel is laid out: warps and ring stages of a CTA by the head
+// dimension (a stage holds kSub keys and values; all stages of a CTA fit the
+// shared memory of an SM).
+struct AttnShape {
+  int tile, warps, stages;
+};
+AttnShape attn_shape(int32_t dim, int32_t tile);
+
+// The attention kernel; bf16: the inputs' type (else fp16).
+cudaError_t launch_attn(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
+// Combines the units that were cut, publishes the status, fails closed.
+cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
+// weight_out = weight_in + the weights that every position received.
+cudaError_t launch_attn_weights(const AttnParams& p, cudaStream_t stream);
+
+// ------------------------------------------------------------- eviction ----
+
+struct EvictParams {
+  const void *k, *v;
+  void *k_dst, *v_dst;
+  // strides in bytes
+  int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
+  int64_t kd_page, kd_slot, kd_head, vd_page, vd_slot, vd_head;
+  const int32_t *page_table, *seq_len, *dst_table;
+  const float* weight;
+  int32_t *keep, *new_len, *new_table;
+  float* new_weight;
+  int32_t num_req, max_pages, num_pages, dst_pages, dst_width;
+  int32_t budget, keep_first, keep_last;
+  int32_t kv_heads, head_bytes;
+  int32_t same_pool;                // the destination pages are pages of the source tensors
+  int32_t slice_cap;                // keys of a CTA's slice that fit its shared memory
+  uint32_t* hdr_status;             // workspace: first error
+  uint32_t* dst_mark;               // workspace: one bit per destination page
+  uint32_t* status_out;
+};
+
+cudaError_t launch_evict(EvictParams p, cudaStream_t stream);
+
+}  // namespace idxk

@@ -1,0 +1,281 @@
+// What follows the attention kernel: the join of the units that were cut, and the
+// accumulated weights.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "attn.h"
+
+namespace idxk {
+
+cudaError_t launch_attn_pages(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
+cudaError_t launch_attn_slots(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
+
+AttnShape attn_shape(int32_t dim, int32_t tile) {
+  return {tile, dim == 256 ? 4 : 8, dim == 64 ? 6 : 3};
+}
+
+cudaError_t launch_attn(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream) {
+  return p.slots ? launch_attn_slots(p, bf16, sm_count, stream) : launch_attn_pages(p, bf16, sm_count, stream);
+}
+
+namespace {
+
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// First error of the CTAs of the attention kernel, seen by every thread.
+__device__ uint32_t call_status(const AttnParams& p) {
+  uint32_t e = kOk;
+  for (int i = threadIdx.x; i < p.n_cta; i += blockDim.x) e = max(e, p.cta_status[i]);
+  for (int o = 16; o; o >>= 1) e = max(e, __shfl_xor_sync(~0u, e, o));
+  __shared__ uint32_t all;
+  if (threadIdx.x == 0) all = kOk;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0 && e != kOk) atomicMax(&all, e);
+  __syncthreads();
+  return all;
+}
+
+constexpr int kJoinWarps = 8;
+
+// One tile row (query head x row) of one cut unit at a time: its parts lie with the
+// worker that opened the unit (part 1) and the workers after it (part 0), and
+//   M = max m_i, l = sum l_i 2^(m_i - M), out = sum o_i 2^(m_i - M) / l.
+// The warps take the parts in turn, in a fixed order, and one sums what they found.
+// Bound by the parts' bytes in L2 (tile x dim x 4 a worker).
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p) {
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr int V = D / 32;   // columns of a lane
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ int32_t open[];   // [workers] the cut units' first workers
+  __shared__ int32_t n_open, base_open;
+  __shared__ int32_t warp_n[kJoinWarps];
+  __shared__ float wm[kJoinWarps], wl[kJoinWarps];
+  __shared__ float wo[kJoinWarps][D];
+  const uint32_t status = call_status(p);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.status_out) *p.status_out = status;
+  if (status != kOk) {
+    const float nan = __uint_as_float(0x7FC00000u);
+    const int64_t n = (int64_t)p.rows * p.q_heads;
+    for (int64_t i = (int64_t)blockIdx.x * kJoinWarps + warp; i < n; i += (int64_t)gridDim.x * kJoinWarps) {
+      const int64_t r = i / p.q_heads, h = i - r * p.q_heads;
+      T* o = (T*)p.out + r * p.out_row + h * p.out_head;
+      for (int j = lane; j < D; j += 32) o[j] = (T)nan;
+      if (p.lse && lane == 0) p.lse[i] = nan;
+    }
+    return;
+  }
+  // the cut units, in order
+  if (threadIdx.x == 0) base_open = 0;
+  __syncthreads();
+  for (int w0 = 0; w0 < p.workers; w0 += kJoinWarps * 32) {
+    const int w = w0 + (int)threadIdx.x;
+    const bool on = w < p.workers && p.open_row[w] >= 0;
+    const uint32_t b = __ballot_sync(~0u, on);
+    if (lane == 0) warp_n[warp] = __popc(b);
+    __syncthreads();
+    int before = base_open;
+    for (int i = 0; i < warp; ++i) before += warp_n[i];
+    if (on) open[before + __popc(b & ((1u << lane) - 1))] = w;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int n = 0;
+      for (int i = 0; i < kJoinWarps; ++i) n += warp_n[i];
+      base_open += n;
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) n_open = base_open;
+  __syncthreads();
+
+  for (int job = blockIdx.x; job < n_open * p.tile; job += gridDim.x) {
+    const int w0 = open[job / p.tile], m = job % p.tile;
+    const int4 info = p.open_info[w0];
+    const int row0 = p.open_row[w0];
+    const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
+    const int chunk = info.y % p.chunks;
+    const int in_group = chunk * p.chunk_heads + h;
+    const int64_t row = row0 + j;
+    // block-uniform: rows of the tile that are none, and rows that see nothing
+    if (j >= info.x || in_group >= p.group) continue;
+    if (!p.slots && p.row_end[row] <= p.row_start[row]) continue;
+    const int qh = (info.y / p.chunks) * p.group + in_group;
+    const int n = info.z - w0 + 1;
+    float M = -INFINITY, l = 0.f, acc[V];
+    bool seen = false;
+#pragma unroll
+    for (int x = 0; x < V; ++x) acc[x] = 0.f;
+    constexpr int U = 4;   // parts in flight
+    for (int i0 = warp; i0 < n; i0 += kJoinWarps * U) {
+      float2 ml[U];
+      float o[U][V];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kJoinWarps;
+        ml[u] = make_float2(-INFINITY, -1.f);
+#pragma unroll
+        for (int x = 0; x < V; ++x) o[u][x] = 0.f;
+        if (i < n) {
+          const int64_t part = ((int64_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * p.tile + m;
+          ml[u] = p.part_ml[part];
+          const float* src = p.part_o + part * D + lane * V;
+#pragma unroll
+          for (int x = 0; x < V; x += 2) {
+            const float2 t = *(const float2*)(src + x);
+            o[u][x] = t.x, o[u][x + 1] = t.y;
+          }
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+      const float base = top == -INFINITY ? 0.f : top;
+      const float a = pow2(M - base);
+      l *= a;
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[x] *= a;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (ml[u].y == -1.f) continue;
+        seen = true;
+        const float e = pow2(ml[u].x - base);
+        l += ml[u].y * e;
+#pragma unroll
+        for (int x = 0; x < V; ++x) acc[x] += o[u][x] * e;
+      }
+      M = top;
+    }
+    if (lane == 0) wm[warp] = M, wl[warp] = seen ? l : -1.f;
+#pragma unroll
+    for (int x = 0; x < V; ++x) wo[warp][lane * V + x] = acc[x];
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, wm[i]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i)
+      if (wl[i] != -1.f) any = true, total += wl[i] * pow2(wm[i] - base);
+    const float inv = any ? 1.f / total : 0.f;
+    T* dst = (T*)p.out + row * p.out_row + (int64_t)qh * p.out_head;
+    for (int x = threadIdx.x; x < D; x += kJoinWarps * 32) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kJoinWarps; ++i)
+        if (wl[i] != -1.f) sum += wo[i][x] * pow2(wm[i] - base);
+      dst[x] = (T)(sum * inv);
+    }
+    if (threadIdx.x == 0) {
+      const int64_t at = row * p.q_heads + qh;
+      if (p.lse) p.lse[at] = (top + log2f(total)) * 0.6931471805599453f;
+      if (p.row_stat) p.row_stat[at] = make_float2(base, inv);
+    }
+    __syncthreads();
+  }
+}
+
+// weight_out[i, s] = weight_in[i, s] + the sum over request i's rows (in order) and
+// query heads of 2^(logit - M) / l.  Reads every logit once; a thread owns 4
+// positions, so the sum's order is fixed.  Bound by the logits' traffic.
+constexpr int kWeightThreads = 128;
+constexpr int kRowList = 256;
+
+__global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __grid_constant__ AttnParams p) {
+  const int64_t width = (int64_t)p.max_pages * kPage;
+  const int64_t pos = ((int64_t)blockIdx.x * kWeightThreads + threadIdx.x) * 4;
+  const bool in = pos < width;
+  const bool failed = call_status(p) != kOk;
+  __shared__ int32_t list[kRowList];
+  __shared__ int32_t warp_n[kWeightThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float c = p.scale_log2;
+  for (int32_t req = blockIdx.y; req < p.num_req; req += gridDim.y) {
+    const int64_t at = (int64_t)req * width + pos;
+    if (failed) {
+      // totals kept in place stay as they were
+      const float nan = __uint_as_float(0x7FC00000u);
+      if (in && p.weight_in != p.weight_out) *(float4*)(p.weight_out + at) = make_float4(nan, nan, nan, nan);
+      continue;
+    }
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in && p.weight_in) w = *(const float4*)(p.weight_in + at);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int64_t b0 = (int64_t)blockIdx.x * kWeightThreads * 4, b1 = b0 + kWeightThreads * 4;
+    int n = 0;
+    auto flush = [&]() {
+      for (int i = 0; i < n; ++i) {
+        const int32_t r = list[i];
+        const int32_t a = p.row_start[r], b = p.row_end[r];
+        if (!in || pos + 4 <= a || pos >= b) continue;
+        const float* lg = p.logits + (int64_t)r * p.q_heads * width + pos;
+        const float2* st = p.row_stat + (int64_t)r * p.q_heads;
+        const bool m0 = pos >= a, m1 = pos + 1 >= a && pos + 1 < b, m2 = pos + 2 >= a && pos + 2 < b, m3 = pos + 3 < b;
+#pragma unroll 8
+        for (int h = 0; h < p.q_heads; ++h) {
+          const float4 x = __ldcs((const float4*)(lg + h * width));
+          const float2 s = st[h];
+          if (m0) sum.x += pow2(fmaf(x.x, c, -s.x)) * s.y;
+          if (m1) sum.y += pow2(fmaf(x.y, c, -s.x)) * s.y;
+          if (m2) sum.z += pow2(fmaf(x.z, c, -s.x)) * s.y;
+          if (m3) sum.w += pow2(fmaf(x.w, c, -s.x)) * s.y;
+        }
+      }
+    };
+    for (int32_t r0 = 0; r0 < p.rows; r0 += kWeightThreads) {
+      const int32_t r = r0 + (int32_t)threadIdx.x;
+      const bool on = r < p.rows && p.row_req[r] == req && p.row_end[r] > b0 && p.row_start[r] < b1;
+      const uint32_t b = __ballot_sync(~0u, on);
+      if (lane == 0) warp_n[warp] = __popc(b);
+      __syncthreads();
+      int before = n, all = 0;
+#pragma unroll
+      for (int i = 0; i < kWeightThreads / 32; ++i) {
+        if (i < warp) before += warp_n[i];
+        all += warp_n[i];
+      }
+      if (on) list[before + __popc(b & ((1u << lane) - 1))] = r;
+      n += all;
+      __syncthreads();
+      if (n + kWeightThreads > kRowList) {
+        flush();
+        n = 0;
+        __syncthreads();
+      }
+    }
+    flush();
+    if (in) *(float4*)(p.weight_out + at) = make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+template <bool BF16>
+static cudaError_t pick_join(const AttnParams& p, int grid, cudaStream_t stream) {
+  const size_t smem = (size_t)p.workers * 4;
+  if (p.dim == 64) attn_join_kernel<BF16, 64><<<grid, kJoinWarps * 32, smem, stream>>>(p);
+  else if (p.dim == 128) attn_join_kernel<BF16, 128><<<grid, kJoinWarps * 32, smem, stream>>>(p);
+  else attn_join_kernel<BF16, 256><<<grid, kJoinWarps * 32, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream) {
+  return bf16 ? pick_join<true>(p, sm_count * 2, stream) : pick_join<false>(p, sm_count * 2, stream);
+}
+
+cudaError_t launch_attn_weights(const AttnParams& p, cudaStream_t stream) {
+  const int64_t per = kWeightThreads * 4;
+  const int64_t x = ((int64_t)p.max_pages * kPage + per - 1) / per;
+  const dim3 grid((unsigned)x, (unsigned)(p.num_req < 65535 ? p.num_req : 65535));
+  attn_weights_kernel<<<grid, kWeightThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace idxk

@@ -14,6 +14,7 @@
 #include <mutex>
 #include <vector>
 
+#include "idx_host.h"
 #include "idx_internal.h"
 #include "idx_launch.h"
 #include "idxtopk.h"
@@ -21,15 +22,6 @@
 using namespace idxk;
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-
-struct DeviceState {
-  bool init = false;
-  int sm_count = 0;
-  int cc_major = 0, cc_minor = 0;
-  cudaMemPool_t pool = nullptr;
-};
 
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
@@ -73,7 +65,9 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
-int device_state(int dev, DeviceState** out) {
+}  // namespace
+
+int idxk::device_state(int dev, DeviceState** out) {
   if (dev < 0 || dev >= kMaxDevices) return IDX_ERR_INVALID_ARGUMENT;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState& d = g_dev[dev];
@@ -113,75 +107,7 @@ int device_state(int dev, DeviceState** out) {
   return IDX_OK;
 }
 
-// ---------------------------------------------------------- validation ----
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  if (a < 0 || b < 0) return false;
-  if (a != 0 && b > INT64_MAX / a) return false;
-  *out = a * b;
-  return true;
-}
-
-// Validates one descriptor: dtype, rank, non-negative shape, C-contiguous
-// strides, 16-byte aligned base (unless empty or need_align is false: host
-// tensors that are only copied).  Returns IDX_OK or an error.
-int check_tensor(const idx_tensor_t* t, int dtype, int ndim, bool need_align = true) {
-  if (!t) return IDX_ERR_INVALID_ARGUMENT;
-  if (t->dtype != dtype || t->ndim != ndim) return IDX_ERR_INVALID_ARGUMENT;
-  int64_t numel = 1;
-  for (int i = 0; i < ndim; ++i) {
-    if (t->shape[i] < 0) return IDX_ERR_INVALID_ARGUMENT;
-    if (!mul_ok(numel, t->shape[i], &numel)) return IDX_ERR_OVERFLOW;
-  }
-  int64_t expect = 1;
-  for (int i = ndim - 1; i >= 0; --i) {
-    if (t->shape[i] > 1 && t->stride[i] != expect) return IDX_ERR_INVALID_ARGUMENT;
-    if (!mul_ok(expect, t->shape[i] > 0 ? t->shape[i] : 1, &expect)) return IDX_ERR_OVERFLOW;
-  }
-  int64_t bytes;
-  if (!mul_ok(numel, dtype == IDX_U8 ? 1 : 4, &bytes)) return IDX_ERR_OVERFLOW;
-  if (numel > 0) {
-    if (!t->data) return IDX_ERR_INVALID_ARGUMENT;
-    if (need_align && ((uintptr_t)t->data & 15u) != 0) return IDX_ERR_INVALID_ARGUMENT;
-  }
-  return IDX_OK;
-}
-
-int64_t numel_of(const idx_tensor_t* t) {
-  int64_t n = 1;
-  for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
-  return n;
-}
-
-// Device that owns `ptr` (device or managed memory), or -1.
-int device_of(const void* ptr) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
-    cudaGetLastError();
-    return -1;
-  }
-  if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return -1;
-  return a.device;
-}
-
-class DeviceGuard {
- public:
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev_) != cudaSuccess) {
-      cudaGetLastError();
-      prev_ = -1;
-    }
-    if (prev_ != dev) ok_ = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    if (prev_ >= 0) cudaSetDevice(prev_);
-  }
-  bool ok() const { return ok_; }
-
- private:
-  int prev_ = -1;
-  bool ok_ = true;
-};
+namespace {
 
 struct Outputs {
   const idx_tensor_t* t[2] = {nullptr, nullptr};
@@ -267,43 +193,6 @@ int check_output(const idx_tensor_t* out, int64_t rows, int32_t topk, bool need_
 }
 
 bool topk_supported(int32_t k) { return k == 512 || k == 1024; }
-
-// Every non-empty tensor must be device memory of one device; returns it.
-int common_device(const idx_tensor_t* const* ts, int n, int* dev) {
-  int d = -1;
-  for (int i = 0; i < n; ++i) {
-    const idx_tensor_t* t = ts[i];
-    if (!t || numel_of(t) == 0) continue;
-    const int td = device_of(t->data);
-    if (td < 0) return IDX_ERR_INVALID_ARGUMENT;
-    if (d >= 0 && td != d) return IDX_ERR_INVALID_ARGUMENT;
-    d = td;
-  }
-  if (d < 0 && cudaGetDevice(&d) != cudaSuccess) {
-    cudaGetLastError();
-    return IDX_ERR_CUDA;
-  }
-  *dev = d;
-  return IDX_OK;
-}
-
-int check_stream(cudaStream_t stream, int dev) {
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
-    cudaGetLastError();
-    return IDX_ERR_CUDA;
-  }
-  if (cs != cudaStreamCaptureStatusNone) return IDX_ERR_UNSUPPORTED;
-  if (stream != nullptr) {
-    int sd = -1;
-    if (cudaStreamGetDevice(stream, &sd) != cudaSuccess) {
-      cudaGetLastError();
-      return IDX_ERR_INVALID_ARGUMENT;
-    }
-    if (sd != dev) return IDX_ERR_INVALID_ARGUMENT;
-  }
-  return IDX_OK;
-}
 
 int encode_2d_u8(CUtensorMap* map, void* base, uint64_t rows, uint32_t box_rows) {
   cuuint64_t dims[2] = {(cuuint64_t)kDimBytes, (cuuint64_t)rows};
@@ -587,9 +476,9 @@ int fixed_scratch(int dev, void** out) {
   return IDX_OK;
 }
 
-// SM count and compute capability of `dev`, and the tensor-map encoder; unlike
-// device_state this creates no memory pool.
-int device_info_no_pool(int dev, int* sm, int* major, int* minor) {
+}  // namespace
+
+int idxk::device_info_no_pool(int dev, int* sm, int* major, int* minor) {
   if (dev < 0 || dev >= kMaxDevices) return IDX_ERR_INVALID_ARGUMENT;
   if (cudaDeviceGetAttribute(sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
@@ -611,6 +500,8 @@ int device_info_no_pool(int dev, int* sm, int* major, int* minor) {
   }
   return IDX_OK;
 }
+
+namespace {
 
 // The fused path of run() with its scratch taken from the fixed buffer: the
 // same checks, kernels, status read-back and fail-closed behaviour, and no

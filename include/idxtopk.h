@@ -35,7 +35,9 @@
  *    allocated stream-ordered on that stream from a library-owned pool and is
  *    bounded by rows, topk and the SM count -- never by the context length
  *    (aiter#5282 Changes, last paragraph).
- *  - Every tensor must be C-contiguous with a 16-byte-aligned base address.
+ *  - Every tensor must be C-contiguous with a 16-byte-aligned base address
+ *    (the 16-bit tensors of the attention and eviction operators may have
+ *    strides, see there).
  *  - Offsets are computed in 64 bits (aiter#5309 Implementation).
  *  - Fail closed (aiter#5309 Implementation): any error returns a nonzero
  *    code, and, when the output descriptors themselves are valid, the outputs
@@ -99,7 +101,7 @@ typedef enum {
 #define IDX_MAX_SCALE_BYTE 167
 #define IDX_MAX_ABS_WEIGHT 16777216.0f
 
-typedef enum { IDX_U8 = 1, IDX_I32 = 2, IDX_F32 = 3 } idx_dtype_t;
+typedef enum { IDX_U8 = 1, IDX_I32 = 2, IDX_F32 = 3, IDX_BF16 = 4, IDX_F16 = 5 } idx_dtype_t;
 
 /* Descriptor of one device tensor.  shape/stride are in elements; only the
  * first ndim entries are read. */
@@ -460,6 +462,159 @@ int idx_dense_topk_fp4_prefill(const idx_tensor_t* q_fp4, const idx_tensor_t* q_
                                const idx_tensor_t* out_phys_slot,
                                const idx_tensor_t* out_raw_idx,
                                const idx_tensor_t* score_workspace, idx_stream_t stream);
+
+/*
+ * Attention over the cache, and its eviction.
+ *
+ * The operators below serve the layers that the indexer works for: attention of
+ * new tokens over all cached positions of their request (idx_attn_paged), over
+ * the slots that the indexer chose (idx_attn_selected), and the eviction of what
+ * received little attention (idx_cache_evict).  They have no counterpart on the
+ * pages.
+ *
+ * Common to all of them:
+ *   q        [R, Hq, D]        queries of R rows
+ *   k_cache  [NP, 64, Hk, D]   keys, physical page by page (page size 64)
+ *   v_cache  [NP, 64, Hk, D]   values
+ * of one type, IDX_BF16 or IDX_F16; D 64, 128 or 256; Hq a multiple of Hk (query
+ * head h reads key-value head h / (Hq / Hk)).  These tensors and `out` may have
+ * any strides whose last dimension is contiguous and whose others are
+ * non-negative multiples of 8 elements (a cache laid out head by head, keys and
+ * values in one allocation, a slice of a fused projection); base addresses are
+ * 16-byte aligned.  All other tensors are contiguous.  Outputs must lie apart
+ * from the inputs and from each other (their address ranges), except where a
+ * function says otherwise.
+ *
+ * Each has a synchronous form, with the conventions at the top of this file, and
+ * a stream-ordered one (_async) that allocates and synchronises nothing and may be
+ * captured into a CUDA graph: `workspace` is device memory, 256-byte aligned, of
+ * at least the bytes that the _scratch_bytes function gives for the sizes, not
+ * used by another call at the same time; `status` is a device uint32 that holds
+ * the call's status once its work is done.  Errors that the host finds return
+ * their code with nothing enqueued and the outputs untouched.  After an error that
+ * the device finds (IDX_ERR_INVALID_METADATA, IDX_ERR_INVALID_PAGE) floating
+ * outputs are NaN and integer outputs -1.  Sums, maxima and weights are held in
+ * fp32; outputs are rounded once, and the softmax weights are rounded to the
+ * inputs' type for their product with the values.  Results do not depend on the
+ * stream, on timing, or on other calls.
+ */
+
+/*
+ * Attention of new tokens over a paged cache (no counterpart on the pages).  Row r
+ * attends over the logical positions [row_start, row_end) of request row_req:
+ *   s_hj = scale * q[r, h] . k[j],  out[r, h] = sum_j softmax_j(s_hj) v[j],
+ *   out_lse[r, h] = log sum_j exp(s_hj).
+ * A row whose window is empty gets out 0 and out_lse -infinity.  Positions
+ * outside a row's window never reach its outputs, whatever their keys and values
+ * hold; within it infinities and NaN propagate as in the formula.  Rows of one
+ * request that follow one another read the cache together.
+ *   page_table i32 [NR, MP], row_req / row_start / row_end i32 [R] as above
+ *   scale      finite, above 0
+ *   out        [R, Hq, D], q's type
+ *   out_lse    f32 [R, Hq] or NULL
+ *   weight_in, weight_out  f32 [NR, MP * 64] or NULL: weight_out[i, s] =
+ *              weight_in[i, s] (0 where it is NULL) + the softmax weights that
+ *              logical position s of request i received, summed over the
+ *              request's rows and query heads in a fixed order.  weight_out may be
+ *              weight_in itself; after a device error it then keeps its values.
+ *              The workspace then holds R * Hq * MP * 64 fp32 logits.
+ * Errors: metadata out of range IDX_ERR_INVALID_METADATA, a page entry under a
+ * window outside [0, NP) IDX_ERR_INVALID_PAGE.
+ */
+int idx_attn_paged(const idx_tensor_t* q, const idx_tensor_t* k_cache, const idx_tensor_t* v_cache,
+                   const idx_tensor_t* page_table, const idx_tensor_t* row_req,
+                   const idx_tensor_t* row_start, const idx_tensor_t* row_end, float scale,
+                   const idx_tensor_t* out, const idx_tensor_t* out_lse,
+                   const idx_tensor_t* weight_in, const idx_tensor_t* weight_out,
+                   idx_stream_t stream);
+
+/* Stream-ordered idx_attn_paged (no counterpart on the pages). */
+int idx_attn_paged_async(const idx_tensor_t* q, const idx_tensor_t* k_cache,
+                         const idx_tensor_t* v_cache, const idx_tensor_t* page_table,
+                         const idx_tensor_t* row_req, const idx_tensor_t* row_start,
+                         const idx_tensor_t* row_end, float scale, const idx_tensor_t* out,
+                         const idx_tensor_t* out_lse, const idx_tensor_t* weight_in,
+                         const idx_tensor_t* weight_out, void* workspace, uint64_t workspace_bytes,
+                         uint32_t* status, idx_stream_t stream);
+
+/* Workspace of idx_attn_paged_async for these sizes on `device` (no counterpart on
+ * the pages); without weights it does not depend on the context. */
+int idx_attn_paged_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, int32_t num_req, int32_t max_pages,
+                                 int32_t with_weights, int32_t device, uint64_t* bytes);
+
+/*
+ * Attention of each row over its own list of physical slots, as the TopK writes
+ * them to out_phys_slot (no counterpart on the pages: what the indexer's selection
+ * is for).
+ *   slots  i32 [R, N], N >= 1: physical slot (page * 64 + offset), or -1 for no
+ *          position; in any order, empty entries anywhere; a slot listed twice
+ *          counts twice.  Row r attends over its slots as idx_attn_paged over a
+ *          window; a row without slots gets out 0 and out_lse -infinity.
+ * A slot below -1 or at or above NP * 64 is IDX_ERR_INVALID_PAGE.
+ */
+int idx_attn_selected(const idx_tensor_t* q, const idx_tensor_t* k_cache,
+                      const idx_tensor_t* v_cache, const idx_tensor_t* slots, float scale,
+                      const idx_tensor_t* out, const idx_tensor_t* out_lse, idx_stream_t stream);
+
+/* Stream-ordered idx_attn_selected (no counterpart on the pages). */
+int idx_attn_selected_async(const idx_tensor_t* q, const idx_tensor_t* k_cache,
+                            const idx_tensor_t* v_cache, const idx_tensor_t* slots, float scale,
+                            const idx_tensor_t* out, const idx_tensor_t* out_lse, void* workspace,
+                            uint64_t workspace_bytes, uint32_t* status, idx_stream_t stream);
+
+/* Workspace of idx_attn_selected_async for these sizes on `device` (no counterpart
+ * on the pages). */
+int idx_attn_selected_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads,
+                                    int32_t head_dim, int32_t selected, int32_t device,
+                                    uint64_t* bytes);
+
+/*
+ * Eviction of a paged cache by accumulated weight (no counterpart on the pages).  A
+ * request of seq_len > budget keeps exactly `budget` positions: its first
+ * keep_first, its last keep_last and, of those between, the heaviest (weight
+ * descending, +0 above -0, NaN below every number, lower position first: the
+ * TopK's order).  Their keys and values are copied, in order of position, to
+ * positions 0 .. budget - 1 of the pages that dst_page_table names; the pages that
+ * they came from are left as they are, for the caller to free.  A request within
+ * the budget keeps its pages, and nothing of it moves.
+ *   page_table     i32 [NR, MP], seq_len i32 [NR], weight f32 [NR, MP * 64]
+ *   budget >= 1, keep_first >= 0, keep_last >= 0, keep_first + keep_last <= budget
+ *   k_dst, v_dst   [DN, 64, Hk, D]: the caches themselves (same address and strides),
+ *                  or tensors that lie apart from them
+ *   dst_page_table i32 [NR, DP]: fresh pages, DP <= MP, DP * 64 >= min(budget, MP * 64)
+ *   out_keep_idx   i32 [NR, budget]  kept positions, ascending, then -1
+ *   out_len        i32 [NR]          min(seq_len, budget)
+ *   out_page_table i32 [NR, MP]      a cut request's row of dst_page_table, then -1;
+ *                                    another's row of page_table
+ *   out_weight     f32 [NR, MP * 64] the kept positions' weights at their new
+ *                                    positions, then 0
+ * Errors: a length outside [0, MP * 64] IDX_ERR_INVALID_METADATA; a page entry under
+ * a request's positions outside [0, NP), a fresh page of a cut request outside
+ * [0, DN), named twice, or (the caches themselves) under any request's positions
+ * IDX_ERR_INVALID_PAGE.  On an error no key or value has moved.
+ */
+int idx_cache_evict(const idx_tensor_t* k_cache, const idx_tensor_t* v_cache,
+                    const idx_tensor_t* page_table, const idx_tensor_t* seq_len,
+                    const idx_tensor_t* weight, int32_t budget, int32_t keep_first,
+                    int32_t keep_last, const idx_tensor_t* k_dst, const idx_tensor_t* v_dst,
+                    const idx_tensor_t* dst_page_table, const idx_tensor_t* out_keep_idx,
+                    const idx_tensor_t* out_len, const idx_tensor_t* out_page_table,
+                    const idx_tensor_t* out_weight, idx_stream_t stream);
+
+/* Stream-ordered idx_cache_evict (no counterpart on the pages). */
+int idx_cache_evict_async(const idx_tensor_t* k_cache, const idx_tensor_t* v_cache,
+                          const idx_tensor_t* page_table, const idx_tensor_t* seq_len,
+                          const idx_tensor_t* weight, int32_t budget, int32_t keep_first,
+                          int32_t keep_last, const idx_tensor_t* k_dst, const idx_tensor_t* v_dst,
+                          const idx_tensor_t* dst_page_table, const idx_tensor_t* out_keep_idx,
+                          const idx_tensor_t* out_len, const idx_tensor_t* out_page_table,
+                          const idx_tensor_t* out_weight, void* workspace,
+                          uint64_t workspace_bytes, uint32_t* status, idx_stream_t stream);
+
+/* Workspace of idx_cache_evict_async for these sizes (no counterpart on the pages). */
+int idx_cache_evict_scratch_bytes(int32_t num_req, int32_t max_pages, int32_t dst_pages,
+                                  int32_t budget, int32_t device, uint64_t* bytes);
 
 #ifdef __cplusplus
 }
