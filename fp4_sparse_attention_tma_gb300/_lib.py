@@ -27,7 +27,7 @@ LIB_PATH = os.path.join(_HERE, "libidxtopk.so")
 DEBUG_BUILD_DIR = os.path.join(_HERE, "_build_dbg")
 DEBUG_LIB_PATH = os.path.join(_HERE, "libidxtopk_dbg.so")
 SOURCES = ["host.cu", "plan.cu", "score.cu", "finish.cu", "attn_host.cu", "attn_paged.cu",
-           "attn_slots.cu", "attn_join.cu", "evict.cu"]
+           "attn_slots.cu", "attn_tc.cu", "attn_join.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "-I" + INCLUDE, "-I" + CSRC] + ARCH

@@ -18,240 +18,10 @@
 // sees, so that what lies there cannot reach a sum.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-#include <stdint.h>
-
-#include <atomic>
-#include <type_traits>
-
-#include "attn.h"
-#include "idx_launch.h"
+#include "attn_common.cuh"
 
 namespace idxk {
 namespace attn {
-
-constexpr float kNegInf = -INFINITY;
-
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-// 16-byte asynchronous copy; bytes = 0 writes zeros and reads nothing.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
-
-template <bool BF16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (BF16) {
-    __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-    return *(uint32_t*)&t;
-  } else {
-    __half2 t = __floats2half2_rn(lo, hi);
-    return *(uint32_t*)&t;
-  }
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Divides the units' subtiles among the workers.
-struct Split {
-  int64_t total;    // subtiles of all units
-  int32_t active;   // workers with a range
-  __device__ int64_t first(int64_t w) const { return total * w / active; }
-  // the worker whose range holds subtile x
-  __device__ int32_t holder(int64_t x) const { return (int32_t)(((x + 1) * active - 1) / total); }
-};
-
-// A place in the list of units: subtile `s` of unit `u` of the group at row0.
-template <bool SLOTS>
-struct Cursor {
-  int32_t row0, nrows, req;   // the group
-  int32_t lo, hi;             // positions of its rows' windows, together
-  int32_t base, nsub;         // first subtile (absolute) and their number
-  int32_t u, s;
-
-  // The group that starts at `row`.  Called by the whole warp.
-  __device__ void load(const AttnParams& p, int32_t row) {
-    row0 = row;
-    if constexpr (SLOTS) {
-      nrows = 1;
-      req = 0;
-      lo = 0;
-      hi = p.n_slots;
-      base = 0;
-    } else {
-      const int lane = threadIdx.x & 31;
-      const int32_t r = row + lane;
-      const int32_t stop = min(p.rows, (row / p.group_rows + 1) * p.group_rows);
-      const bool in = r < stop;
-      const int32_t rr = in ? p.row_req[r] : -1;
-      req = __shfl_sync(~0u, rr, 0);
-      const uint32_t other = ~__ballot_sync(~0u, in && rr == req);
-      nrows = other ? __ffs(other) - 1 : 32;
-      int32_t a = INT32_MAX, b = 0;
-      if (lane < nrows) {
-        const int32_t a0 = p.row_start[r], b0 = p.row_end[r];
-        if (b0 > a0) a = a0, b = b0;
-      }
-      lo = __reduce_min_sync(~0u, a);
-      hi = __reduce_max_sync(~0u, b);
-      if (lo > hi) lo = hi;
-      base = lo / kSub;
-    }
-    nsub = hi > lo ? (hi + kSub - 1) / kSub - base : 0;
-  }
-  // The next subtile; the caller has not passed the end of the list.
-  __device__ void next(const AttnParams& p) {
-    if (++s < nsub) return;
-    s = 0;
-    if (++u < p.kv_heads * p.chunks) return;
-    u = 0;
-    do {
-      load(p, row0 + nrows);
-    } while (nsub == 0);
-  }
-};
-
-// Finds the range of every worker of the CTA: checks the rows' metadata (all of it, by
-// every CTA, so that all agree), counts the subtiles and leaves, for worker w =
-// warp * gridDim.x + blockIdx.x, the place where its range starts in `cur`.  False: an
-// error (recorded in *err) or nothing to do for this warp.
-template <bool SLOTS, int WARPS>
-__device__ bool find_range(const AttnParams& p, Split& sp, Cursor<SLOTS>& cur, int32_t worker, uint32_t* err) {
-  const int32_t units = p.kv_heads * p.chunks;
-  if constexpr (SLOTS) {
-    const int32_t n = (p.n_slots + kSub - 1) / kSub;
-    sp.total = (int64_t)p.rows * units * n;
-    const int64_t most = (sp.total + p.min_sub - 1) / p.min_sub;
-    sp.active = (int32_t)(most < p.workers ? most : p.workers);
-    if (worker >= sp.active) return false;
-    const int64_t t = sp.first(worker);
-    const int64_t per_row = (int64_t)units * n;
-    const int32_t row = (int32_t)(t / per_row);
-    const int64_t rest = t - row * per_row;
-    cur.load(p, row);
-    cur.u = (int32_t)(rest / n);
-    cur.s = (int32_t)(rest - (int64_t)cur.u * n);
-    return true;
-  } else {
-    constexpr int N = WARPS * 32;
-    __shared__ int64_t warp_sum[WARPS];
-    __shared__ int64_t pre[N];          // subtiles before each row of the pass, in the pass
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // subtiles of the group that starts at row r (0 where none does)
-    auto count = [&](int32_t r) -> int32_t {
-      if (r >= p.rows) return 0;
-      const int32_t req = p.row_req[r];
-      if (r % p.group_rows != 0 && p.row_req[r - 1] == req) return 0;
-      int32_t a = INT32_MAX, b = 0;
-      for (int32_t i = r; i < p.rows && (i == r || (i % p.group_rows != 0 && p.row_req[i] == req)); ++i) {
-        const int32_t a0 = p.row_start[i], b0 = p.row_end[i];
-        if (b0 > a0) a = min(a, a0), b = max(b, b0);
-      }
-      return b > a ? (b + kSub - 1) / kSub - a / kSub : 0;
-    };
-    int64_t sum = 0;
-    bool bad = false;
-    for (int32_t r = tid; r < p.rows; r += N) {
-      const int32_t q = p.row_req[r], a = p.row_start[r], b = p.row_end[r];
-      bad |= q < 0 || q >= p.num_req || a < 0 || b < a || (int64_t)b > (int64_t)p.max_pages * kPage;
-    }
-    if (__syncthreads_or(bad)) {
-      if (tid == 0) *err = kErrInvalidMetadata;
-      return false;
-    }
-    const bool one_pass = p.rows <= N;
-    int32_t mine = 0;
-    for (int32_t r = tid; r < p.rows; r += N) sum += mine = count(r);
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if (lane == 0) warp_sum[warp] = sum;
-    __syncthreads();
-    sum = 0;
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) sum += warp_sum[i];
-    sp.total = sum * units;
-    const int64_t most = (sp.total + p.min_sub - 1) / p.min_sub;
-    sp.active = (int32_t)(most < p.workers ? most : p.workers);
-    const bool some = worker < sp.active;
-    const int64_t t = some ? sp.first(worker) : 0;
-    bool found = false;
-    int64_t before = 0;   // subtiles (of one unit each) before the pass
-    for (int32_t r0 = 0; r0 < p.rows; r0 += N) {
-      if (!one_pass) mine = count(r0 + tid);
-      int64_t inc = mine;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(~0u, inc, o);
-        if (lane >= o) inc += x;
-      }
-      __syncthreads();
-      if (lane == 31) warp_sum[warp] = inc;
-      __syncthreads();
-      int64_t base = 0, all = 0;
-#pragma unroll
-      for (int i = 0; i < WARPS; ++i) {
-        if (i < warp) base += warp_sum[i];
-        all += warp_sum[i];
-      }
-      pre[tid] = base + inc - mine;
-      __syncthreads();
-      if (some && !found && t < (before + all) * units) {
-        // the last row of the pass whose subtiles start at or before t: the first row of the group that
-        // holds it (rows without a count of their own come before it, or start after t)
-        const int32_t n = min(N, p.rows - r0);
-        int32_t at = 0;
-        for (int32_t i = lane; i < n; i += 32)
-          if ((before + pre[i]) * units <= t) at = i;   // pre is non-decreasing
-        at = __reduce_max_sync(~0u, at);
-        const int64_t rest = t - (before + pre[at]) * units;
-        cur.load(p, r0 + at);
-        cur.u = (int32_t)(rest / cur.nsub);
-        cur.s = (int32_t)(rest - (int64_t)cur.u * cur.nsub);
-        found = true;
-      }
-      before += all;
-    }
-    return found;
-  }
-}
 
 template <bool BF16, int D, int TILE, int WARPS, int STAGES, bool SLOTS>
 __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_constant__ AttnParams p) {
@@ -271,7 +41,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
 
   Split sp;
   Cursor<SLOTS> at;
-  const bool work = find_range<SLOTS, WARPS>(p, sp, at, worker, &err);
+  const bool work = find_range<Cursor<SLOTS>, SLOTS, WARPS>(p, sp, at, worker, &err);
   if (lane == 0) p.open_row[worker] = -1;
   uint32_t warp_err = kOk;
   if (work) {

@@ -7,7 +7,8 @@
 // row group: consecutive rows of one request, as many as share a tile, so that
 // their cached positions are read once.  A unit is cut into subtiles of kSub
 // positions; the units' subtiles, one after another, are dealt to the workers (one
-// warp each) in equal contiguous ranges.  A unit that lies inside one worker's range
+// warp each; in attn_tc.cuh one CTA each, with tiles of 128 positions) in equal
+// contiguous ranges.  A unit that lies inside one worker's range
 // is finished there; one that is cut leaves partial sums (the maximum, the sum of
 // the exponentials and the weighted values, all fp32), which attn_join_kernel
 // combines.  A worker's range cuts at most two units, so the workspace is bounded by
@@ -24,8 +25,6 @@
 namespace idxk {
 
 constexpr int kSub = 16;           // cached positions per subtile
-constexpr int kMaxTile = 32;       // most query heads x rows of a unit
-constexpr int kMaxGroupRows = 32;  // most rows of a group (one lane each)
 
 struct AttnParams {
   const void *q, *k, *v;
@@ -43,6 +42,8 @@ struct AttnParams {
   int32_t group;                    // query heads per key-value head
   int32_t chunks, chunk_heads;      // a key-value head's query heads in chunks of at most a tile
   int32_t group_rows;               // rows per group, at most (1 where there are several chunks)
+  int32_t row_cols;                 // tile rows between the rows of a group (chunk_heads of them in use)
+  int32_t tensor_core;              // 1: the kernel of attn_tc.cuh
   int32_t workers;                  // warps of the grid
   int32_t min_sub;                  // a worker's range holds at least this many subtiles
   float scale_log2;                 // softmax scale x log2(e)
@@ -53,7 +54,7 @@ struct AttnParams {
   int4* open_info;                  // [workers] {rows of its group, unit index in the group, last worker, 0}
   float2* part_ml;                  // [workers][2][tile] maximum (in units of log2, scaled) and sum
   float* part_o;                    // [workers][2][tile][dim]
-  int32_t tile;                     // 16 or 32
+  int32_t tile;                     // tile rows of a unit: 16 or 32; tensor_core: 64 or 128
   int32_t dim;
   // accumulated weights
   float* logits;                    // [rows * q_heads][max_pages * 64] or null
@@ -83,13 +84,9 @@ inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int6
   return L;
 }
 
-// How a call's kernel is laid out: warps and ring stages of a CTA by the head
-// dimension (a stage holds kSub keys and values; all stages of a CTA fit the
-// shared memory of an SM).
-struct AttnShape {
-  int tile, warps, stages;
-};
-AttnShape attn_shape(int32_t dim, int32_t tile);
+// Warps of a CTA of the kernel of attn.cuh (with its ring stages, what fits the shared
+// memory of an SM).
+inline int attn_warps(int32_t dim) { return dim == 256 ? 4 : 8; }
 
 // The attention kernel; bf16: the inputs' type (else fp16).
 cudaError_t launch_attn(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);

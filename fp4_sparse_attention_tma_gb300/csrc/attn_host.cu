@@ -194,22 +194,36 @@ int check_space(const Space& s) {
 // --------------------------------------------------------------- attention ----
 
 struct AttnPlan {
-  int32_t group, chunks, chunk_heads, group_rows, tile, workers;
+  int32_t group, chunks, chunk_heads, group_rows, row_cols, tile, workers;
+  bool tensor_core;
 };
 
-// How the query heads of a key-value head are laid on matrix tiles.  A tile holds 16
-// (query head, row) pairs; where a group, or its rows that share the cache, need more, 32
-// (two tiles that share every key and value read), up to head dimension 128 (beyond it two
-// tiles' sums do not fit a thread's registers).
+// Which kernel, and how the query heads of a key-value head are laid on its tiles.
+//
+// More than 16 query heads per key-value head at head dimension 128: attn_tc.cuh, 64
+// columns a row, two rows of a request together where requests have several.  Otherwise
+// attn.cuh: a tile holds 16 (query head, row) pairs; where a group, or its rows that share
+// the cache, need more, 32 (two tiles that share every key and value read), up to head
+// dimension 128 (beyond it two tiles' sums do not fit a thread's registers).
 AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_heads, int64_t dim, int sm) {
   AttnPlan a{};
   a.group = (int32_t)(q_heads / kv_heads);
   const int64_t per_req = num_req > 0 ? (rows + num_req - 1) / num_req : 1;
-  a.tile = dim <= 128 && (int64_t)a.group * per_req > 16 ? 32 : 16;
-  a.chunks = (a.group + a.tile - 1) / a.tile;
+  a.tensor_core = dim == 128 && a.group > 16;
+  const int32_t most = a.tensor_core ? 64 : dim <= 128 && (int64_t)a.group * per_req > 16 ? 32 : 16;
+  a.chunks = (a.group + most - 1) / most;
   a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
-  a.group_rows = a.chunks > 1 ? 1 : a.tile / a.group;
-  a.workers = sm * attn_shape((int32_t)dim, a.tile).warps;
+  if (a.tensor_core) {
+    a.group_rows = a.chunks == 1 && per_req > 1 ? 2 : 1;
+    a.row_cols = most;
+    a.tile = a.group_rows * most;
+    a.workers = sm;
+  } else {
+    a.group_rows = a.chunks > 1 ? 1 : most / a.group;
+    a.row_cols = a.chunk_heads;
+    a.tile = most;
+    a.workers = sm * attn_warps((int32_t)dim);
+  }
   return a;
 }
 
@@ -311,6 +325,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   p.rows = (int32_t)R, p.num_req = (int32_t)NR, p.max_pages = (int32_t)MP, p.num_pages = (int32_t)NP;
   p.q_heads = (int32_t)Hq, p.kv_heads = (int32_t)Hk;
   p.group = a.group, p.chunks = a.chunks, p.chunk_heads = a.chunk_heads, p.group_rows = a.group_rows;
+  p.row_cols = a.row_cols, p.tensor_core = a.tensor_core;
   p.workers = R > 0 ? a.workers : 0;
   p.n_cta = R > 0 ? m.sm : 0;
   p.min_sub = 1;

@@ -10,12 +10,10 @@ namespace idxk {
 
 cudaError_t launch_attn_pages(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
 cudaError_t launch_attn_slots(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
-
-AttnShape attn_shape(int32_t dim, int32_t tile) {
-  return {tile, dim == 256 ? 4 : 8, dim == 64 ? 6 : 3};
-}
+cudaError_t launch_attn_tc(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
 
 cudaError_t launch_attn(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream) {
+  if (p.tensor_core) return launch_attn_tc(p, bf16, sm_count, stream);
   return p.slots ? launch_attn_slots(p, bf16, sm_count, stream) : launch_attn_pages(p, bf16, sm_count, stream);
 }
 
@@ -41,20 +39,78 @@ __device__ uint32_t call_status(const AttnParams& p) {
 }
 
 constexpr int kJoinWarps = 8;
+constexpr int kFewParts = 8;   // units of at most so many parts are joined by one warp a tile row
 
-// One tile row (query head x row) of one cut unit at a time: its parts lie with the
-// worker that opened the unit (part 1) and the workers after it (part 0), and
+struct OpenUnit {
+  int32_t w0, n;             // first worker and parts
+  int32_t row0, nrows, u;    // its group's rows and its index in the group
+};
+
+// Parts i0, i0 + step, ... of a tile row added up by one warp; a lane has D / 32 columns.
+template <int D>
+__device__ __forceinline__ void join_parts(const AttnParams& p, const OpenUnit& un, int m, int i0, int step, float& M,
+                                           float& l, float (&acc)[D / 32], bool& seen) {
+  constexpr int V = D / 32, U = 4;   // U parts in flight
+  const int lane = threadIdx.x & 31;
+  M = -INFINITY, l = 0.f, seen = false;
+#pragma unroll
+  for (int x = 0; x < V; ++x) acc[x] = 0.f;
+  for (; i0 < un.n; i0 += step * U) {
+    float2 ml[U];
+    float o[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * step;
+      ml[u] = make_float2(-INFINITY, -1.f);
+#pragma unroll
+      for (int x = 0; x < V; ++x) o[u][x] = 0.f;
+      if (i < un.n) {
+        const int64_t part = ((int64_t)(un.w0 + i) * 2 + (i == 0 ? 1 : 0)) * p.tile + m;
+        ml[u] = p.part_ml[part];
+        const float* src = p.part_o + part * D + lane * V;
+#pragma unroll
+        for (int x = 0; x < V; x += 2) {
+          const float2 t = *(const float2*)(src + x);
+          o[u][x] = t.x, o[u][x + 1] = t.y;
+        }
+      }
+    }
+    // a sum of -1: the part saw no position (its values mean nothing)
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (ml[u].y != -1.f) top = fmaxf(top, ml[u].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    const float a = pow2(M - base);
+    l *= a;
+#pragma unroll
+    for (int x = 0; x < V; ++x) acc[x] *= a;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ml[u].y == -1.f) continue;
+      seen = true;
+      const float e = pow2(ml[u].x - base);
+      l += ml[u].y * e;
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[x] += o[u][x] * e;
+    }
+    M = top;
+  }
+}
+
+// One tile row (query head x row) of one cut unit at a time: its parts lie with the worker
+// that opened the unit (part 1) and the workers after it (part 0), and
 //   M = max m_i, l = sum l_i 2^(m_i - M), out = sum o_i 2^(m_i - M) / l.
-// The warps take the parts in turn, in a fixed order, and one sums what they found.
-// Bound by the parts' bytes in L2 (tile x dim x 4 a worker).
+// Where a unit has few parts, each warp joins a row by itself; where it has many (few rows
+// over a long context), the warps of a CTA take the row's parts in turn, in a fixed order,
+// and their sums are joined in the same way.  Bound by the parts' bytes in L2.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr int V = D / 32;   // columns of a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  extern __shared__ int32_t open[];   // [workers] the cut units' first workers
-  __shared__ int32_t n_open, base_open;
-  __shared__ int32_t warp_n[kJoinWarps];
+  extern __shared__ OpenUnit open[];   // [workers]: units of few parts from the front, others from the back
+  __shared__ int32_t warp_n[kJoinWarps][2];
   __shared__ float wm[kJoinWarps], wl[kJoinWarps];
   __shared__ float wo[kJoinWarps][D];
   const uint32_t status = call_status(p);
@@ -70,86 +126,70 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     }
     return;
   }
-  // the cut units, in order
-  if (threadIdx.x == 0) base_open = 0;
-  __syncthreads();
+  // the cut units
+  int few = 0, many = 0;
   for (int w0 = 0; w0 < p.workers; w0 += kJoinWarps * 32) {
     const int w = w0 + (int)threadIdx.x;
-    const bool on = w < p.workers && p.open_row[w] >= 0;
-    const uint32_t b = __ballot_sync(~0u, on);
-    if (lane == 0) warp_n[warp] = __popc(b);
-    __syncthreads();
-    int before = base_open;
-    for (int i = 0; i < warp; ++i) before += warp_n[i];
-    if (on) open[before + __popc(b & ((1u << lane) - 1))] = w;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int n = 0;
-      for (int i = 0; i < kJoinWarps; ++i) n += warp_n[i];
-      base_open += n;
+    OpenUnit un{};
+    un.row0 = w < p.workers ? p.open_row[w] : -1;
+    const bool on = un.row0 >= 0;
+    if (on) {
+      const int4 info = p.open_info[w];
+      un.w0 = w, un.nrows = info.x, un.u = info.y, un.n = info.z - w + 1;
     }
+    const bool is_few = on && un.n <= kFewParts, is_many = on && !is_few;
+    const uint32_t bf = __ballot_sync(~0u, is_few), bm = __ballot_sync(~0u, is_many);
+    if (lane == 0) warp_n[warp][0] = __popc(bf), warp_n[warp][1] = __popc(bm);
+    __syncthreads();
+    int at_few = few, at_many = many;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) {
+      if (i < warp) at_few += warp_n[i][0], at_many += warp_n[i][1];
+      few += warp_n[i][0], many += warp_n[i][1];
+    }
+    const uint32_t below = (1u << lane) - 1;
+    if (is_few) open[at_few + __popc(bf & below)] = un;
+    if (is_many) open[p.workers - 1 - at_many - __popc(bm & below)] = un;
     __syncthreads();
   }
-  if (threadIdx.x == 0) n_open = base_open;
-  __syncthreads();
 
-  for (int job = blockIdx.x; job < n_open * p.tile; job += gridDim.x) {
-    const int w0 = open[job / p.tile], m = job % p.tile;
-    const int4 info = p.open_info[w0];
-    const int row0 = p.open_row[w0];
-    const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
-    const int chunk = info.y % p.chunks;
-    const int in_group = chunk * p.chunk_heads + h;
-    const int64_t row = row0 + j;
-    // block-uniform: rows of the tile that are none, and rows that see nothing
-    if (j >= info.x || in_group >= p.group) continue;
-    if (!p.slots && p.row_end[row] <= p.row_start[row]) continue;
-    const int qh = (info.y / p.chunks) * p.group + in_group;
-    const int n = info.z - w0 + 1;
-    float M = -INFINITY, l = 0.f, acc[V];
-    bool seen = false;
+  // the output row of tile row m: false where it is none, or sees nothing
+  auto row_of = [&](const OpenUnit& un, int m, int64_t& row, int& qh) {
+    const int j = m / p.row_cols, h = m - j * p.row_cols;
+    const int in_group = un.u % p.chunks * p.chunk_heads + h;
+    row = un.row0 + j;
+    qh = un.u / p.chunks * p.group + in_group;
+    return j < un.nrows && h < p.chunk_heads && in_group < p.group &&
+           (p.slots || p.row_end[row] > p.row_start[row]);
+  };
+  const int per = p.tile / kJoinWarps;
+  for (int job = blockIdx.x; job < few * per; job += gridDim.x) {
+    const OpenUnit un = open[job / per];
+    const int m = job % per * kJoinWarps + warp;
+    int64_t row;
+    int qh;
+    if (!row_of(un, m, row, qh)) continue;
+    float M, l, acc[V];
+    bool seen;
+    join_parts<D>(p, un, m, 0, 1, M, l, acc, seen);
+    const float inv = seen ? 1.f / l : 0.f;
+    T* dst = (T*)p.out + row * p.out_row + (int64_t)qh * p.out_head + lane * V;
 #pragma unroll
-    for (int x = 0; x < V; ++x) acc[x] = 0.f;
-    constexpr int U = 4;   // parts in flight
-    for (int i0 = warp; i0 < n; i0 += kJoinWarps * U) {
-      float2 ml[U];
-      float o[U][V];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kJoinWarps;
-        ml[u] = make_float2(-INFINITY, -1.f);
-#pragma unroll
-        for (int x = 0; x < V; ++x) o[u][x] = 0.f;
-        if (i < n) {
-          const int64_t part = ((int64_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * p.tile + m;
-          ml[u] = p.part_ml[part];
-          const float* src = p.part_o + part * D + lane * V;
-#pragma unroll
-          for (int x = 0; x < V; x += 2) {
-            const float2 t = *(const float2*)(src + x);
-            o[u][x] = t.x, o[u][x + 1] = t.y;
-          }
-        }
-      }
-      float top = M;
-#pragma unroll
-      for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
-      const float base = top == -INFINITY ? 0.f : top;
-      const float a = pow2(M - base);
-      l *= a;
-#pragma unroll
-      for (int x = 0; x < V; ++x) acc[x] *= a;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (ml[u].y == -1.f) continue;
-        seen = true;
-        const float e = pow2(ml[u].x - base);
-        l += ml[u].y * e;
-#pragma unroll
-        for (int x = 0; x < V; ++x) acc[x] += o[u][x] * e;
-      }
-      M = top;
+    for (int x = 0; x < V; ++x) dst[x] = (T)(acc[x] * inv);
+    if (lane == 0) {
+      const int64_t at = row * p.q_heads + qh;
+      if (p.lse) p.lse[at] = (M + log2f(l)) * 0.6931471805599453f;
+      if (p.row_stat) p.row_stat[at] = make_float2(M == -INFINITY ? 0.f : M, inv);
     }
+  }
+  for (int job = blockIdx.x; job < many * p.tile; job += gridDim.x) {
+    const OpenUnit un = open[p.workers - 1 - job / p.tile];
+    int64_t row;
+    int qh;
+    if (!row_of(un, job % p.tile, row, qh)) continue;   // the same for the whole CTA
+    float M, l, acc[V];
+    bool seen;
+    join_parts<D>(p, un, job % p.tile, warp, kJoinWarps, M, l, acc, seen);
     if (lane == 0) wm[warp] = M, wl[warp] = seen ? l : -1.f;
 #pragma unroll
     for (int x = 0; x < V; ++x) wo[warp][lane * V + x] = acc[x];
@@ -259,7 +299,7 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __gr
 
 template <bool BF16>
 static cudaError_t pick_join(const AttnParams& p, int grid, cudaStream_t stream) {
-  const size_t smem = (size_t)p.workers * 4;
+  const size_t smem = (size_t)p.workers * sizeof(OpenUnit);
   if (p.dim == 64) attn_join_kernel<BF16, 64><<<grid, kJoinWarps * 32, smem, stream>>>(p);
   else if (p.dim == 128) attn_join_kernel<BF16, 128><<<grid, kJoinWarps * 32, smem, stream>>>(p);
   else attn_join_kernel<BF16, 256><<<grid, kJoinWarps * 32, smem, stream>>>(p);
