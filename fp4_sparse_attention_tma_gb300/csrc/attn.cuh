@@ -65,9 +65,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
     auto fetch = [&](int stage) {
       if (to_fetch > 0) {
         const uint32_t dk = my_ring + (uint32_t)stage * (2 * kHalf), dv = dk + kHalf;
-        const int32_t head = f.u / p.chunks;
-        const T* k = (const T*)p.k + head * p.k_head;
-        const T* v = (const T*)p.v + head * p.v_head;
+        const T* k = (const T*)p.k + f.kv * p.k_head;
+        const T* v = (const T*)p.v + f.kv * p.v_head;
         constexpr int ROWS = 32 / CH > 0 ? 32 / CH : 1;   // positions that one copy of the warp covers
         const int chunk = lane % CH;
         if constexpr (SLOTS) {
@@ -124,8 +123,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
     int stage = 0;
     const float c = p.scale_log2;
     while (here < stop) {
-      const int32_t head = at.u / p.chunks, h0 = head * p.group + (at.u % p.chunks) * p.chunk_heads;
-      const int32_t heads = min(p.chunk_heads, p.group - (at.u % p.chunks) * p.chunk_heads);
+      const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
+      const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
       // tile row m: row m / chunk_heads of the group, head h0 + m % chunk_heads
       if (begin) {
         begin = false;
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
         const int which = cut_front ? 0 : 1;
         if (!unit_end && !cut_front && lane == 0) {
           p.open_row[worker] = at.row0;
-          p.open_info[worker] = make_int4(at.nrows, at.u, sp.holder(here + (at.nsub - at.s) - 2), 0);
+          p.open_info[worker] = make_int4(at.nrows, at.kv * p.chunks + at.chunk, sp.holder(here + (at.nsub - at.s) - 2), 0);
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)

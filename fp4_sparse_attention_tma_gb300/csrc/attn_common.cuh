@@ -90,13 +90,13 @@ __device__ __forceinline__ bool starts_group(const AttnParams& p, int32_t r) {
   return r < p.rows && (r % p.group_rows == 0 || p.row_req[r - 1] != p.row_req[r]);
 }
 
-// A place in the list of units: subtile `s` of unit `u` of the group at row0.
+// A place in the list of units: subtile `s` of one unit of the group at row0.
 template <bool SLOTS>
 struct Cursor {
   int32_t row0, nrows, req;   // the group
   int32_t lo, hi;             // positions of its rows' windows, together
   int32_t base, nsub;         // first subtile (absolute) and their number
-  int32_t u, s;
+  int32_t kv, chunk, s;       // the unit: key-value head and chunk of its query heads
 
   // The group that starts at `row`.  Called by the whole warp.
   __device__ void load(const AttnParams& p, int32_t row) {
@@ -145,8 +145,10 @@ struct Cursor {
   __device__ void next(const AttnParams& p) {
     if (++s < nsub) return;
     s = 0;
-    if (++u < p.kv_heads * p.chunks) return;
-    u = 0;
+    if (++chunk < p.chunks) return;
+    chunk = 0;
+    if (++kv < p.kv_heads) return;
+    kv = 0;
     do {
       load(p, row0 + nrows);
     } while (nsub == 0);
@@ -171,8 +173,10 @@ __device__ bool find_range(const AttnParams& p, Split& sp, Cur& cur, int32_t wor
     const int32_t row = (int32_t)(t / per_row);
     const int64_t rest = t - row * per_row;
     cur.load(p, row);
-    cur.u = (int32_t)(rest / n);
-    cur.s = (int32_t)(rest - (int64_t)cur.u * n);
+    const int32_t u = (int32_t)(rest / n);
+    cur.s = (int32_t)(rest - (int64_t)u * n);
+    cur.kv = u / p.chunks;
+    cur.chunk = u % p.chunks;
     return true;
   } else {
     constexpr int N = WARPS * 32;
@@ -233,8 +237,10 @@ __device__ bool find_range(const AttnParams& p, Split& sp, Cur& cur, int32_t wor
         at = __reduce_max_sync(~0u, at);
         const int64_t rest = t - (before + pre[at]) * units;
         cur.load(p, r0 + at);
-        cur.u = (int32_t)(rest / cur.nsub);
-        cur.s = (int32_t)(rest - (int64_t)cur.u * cur.nsub);
+        const int32_t u = (int32_t)(rest / cur.nsub);
+        cur.s = (int32_t)(rest - (int64_t)u * cur.nsub);
+        cur.kv = u / p.chunks;
+        cur.chunk = u % p.chunks;
         found = true;
       }
       before += all;

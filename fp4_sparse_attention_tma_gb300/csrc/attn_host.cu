@@ -59,13 +59,19 @@ int elem_bytes(const idx_tensor_t* t) {
   return t->dtype == IDX_U8 ? 1 : t->dtype == IDX_BF16 || t->dtype == IDX_F16 ? 2 : 4;
 }
 
-// The addresses that `t` spans.
-void range_of(const idx_tensor_t* t, uintptr_t* a, uintptr_t* b) {
+// The bytes that `t` spans.
+int64_t span_of(const idx_tensor_t* t) {
   int64_t reach = 1;
   for (int i = 0; i < t->ndim; ++i)
     if (t->shape[i] > 1) reach += (t->shape[i] - 1) * t->stride[i];
+  return reach * elem_bytes(t);
+}
+constexpr int64_t kFar = ((int64_t)1 << 32) * 16 - 16;
+
+// The addresses that `t` spans.
+void range_of(const idx_tensor_t* t, uintptr_t* a, uintptr_t* b) {
   *a = (uintptr_t)t->data;
-  *b = *a + (uintptr_t)reach * elem_bytes(t);
+  *b = *a + (uintptr_t)span_of(t);
 }
 
 bool apart(const idx_tensor_t* x, const idx_tensor_t* y) {
@@ -204,12 +210,13 @@ struct AttnPlan {
 // columns a row, two rows of a request together where requests have several.  Otherwise
 // attn.cuh: a tile holds 16 (query head, row) pairs; where a group, or its rows that share
 // the cache, need more, 32 (two tiles that share every key and value read), up to head
-// dimension 128 (beyond it two tiles' sums do not fit a thread's registers).
-AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_heads, int64_t dim, int sm) {
+// dimension 128 (beyond it two tiles' sums do not fit a thread's registers).  `far`: a cache
+// spans 64 GB or more, where attn_tc.cuh's offsets (32 bits, in units of 16 bytes) end.
+AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_heads, int64_t dim, bool far, int sm) {
   AttnPlan a{};
   a.group = (int32_t)(q_heads / kv_heads);
   const int64_t per_req = num_req > 0 ? (rows + num_req - 1) / num_req : 1;
-  a.tensor_core = dim == 128 && a.group > 16;
+  a.tensor_core = dim == 128 && a.group > 16 && !far;
   const int32_t most = a.tensor_core ? 64 : dim <= 128 && (int64_t)a.group * per_req > 16 ? 32 : 16;
   a.chunks = (a.group + most - 1) / most;
   a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
@@ -300,7 +307,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   if (!guard.ok()) return IDX_ERR_CUDA;
   if ((st = check_arch(&m))) return st;
   const bool weights = c.weight_out != nullptr && numel_of(c.weight_out) > 0;
-  const AttnPlan a = plan_of(R, c.slots ? R : NR, Hq, Hk, D, m.sm);
+  const AttnPlan a = plan_of(R, c.slots ? R : NR, Hq, Hk, D, span_of(c.k) >= kFar || span_of(c.v) >= kFar, m.sm);
   int64_t logit_rows, logit_bytes;
   if (weights && (!mul_ok(R * Hq, MP * kPage, &logit_rows) || !mul_ok(logit_rows, 4, &logit_bytes) ||
                   logit_bytes > (INT64_MAX >> 2)))
@@ -362,8 +369,13 @@ int attn_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim, int
   if (st) return st;
   int64_t n;
   if (weights && (!mul_ok(rows * q_heads, max_pages * kPage, &n) || n > (INT64_MAX >> 4))) return IDX_ERR_OVERFLOW;
-  *bytes = layout_of(plan_of(rows, num_req, q_heads, kv_heads, dim, sm), sm, rows, q_heads, dim, max_pages, weights)
-               .total;
+  // whichever kernel the cache's extent allows
+  *bytes = 0;
+  for (bool far : {false, true}) {
+    const AttnPlan a = plan_of(rows, num_req, q_heads, kv_heads, dim, far, sm);
+    const uint64_t n = layout_of(a, sm, rows, q_heads, dim, max_pages, weights).total;
+    if (n > *bytes) *bytes = n;
+  }
   return IDX_OK;
 }
 

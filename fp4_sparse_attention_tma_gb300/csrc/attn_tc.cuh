@@ -12,9 +12,9 @@
 // A tensor memory lane is a position in the first product and an output column in the second.
 // A thread owns one position: its sums of 2^(s - m) stay in registers and are added up over
 // the lanes once, at the segment's end.  The reference m of a column is not its running
-// maximum but one that a tile raises when it exceeds it by more than 2^8 (the first tile sets
-// it): the sums stay exact in fp32, P stays below 2^8, and the accumulator in tensor memory is
-// scaled only then.  Columns are 64 a row; with two rows of one request both use the tiles
+// maximum: the segment's first tile sets it (to the tile's maximum; in bf16, whose range allows
+// it, to the score of the first position), and a tile raises it when a weight would exceed
+// 2^kRaise.  Only then are the sums and the accumulator in tensor memory scaled.  Columns are 64 a row; with two rows of one request both use the tiles
 // that both see in full, and the tiles at the windows' edges are visited row by row, so that
 // what one row does not see is zero for it.
 //
@@ -42,7 +42,10 @@ constexpr uint32_t kPBytes = kPos * 128;        // a row's weights
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kLoaders = 64;              // threads that copy keys (and as many values)
-constexpr float kRaise = 8.f;             // a column's reference is raised when exceeded by 2^8
+// A column's reference is raised when a weight exceeds 2^kRaise: fp16 weights have to stay
+// below 2^16, bf16 ones far enough below the largest value for their product with any value.
+template <bool BF16>
+constexpr float kRaise = BF16 ? 16.f : 8.f;
 
 template <int NB>
 struct Smem {
@@ -107,7 +110,7 @@ struct Walk {
   int32_t a[NB], b[NB];          // windows of the group's rows (0, 0: none)
   int32_t c0, c1;                // tiles that both rows see in full
   int32_t nsub;                  // visits of a unit
-  int32_t u, s;
+  int32_t kv, chunk, s;
 
   __device__ static int32_t lo(int32_t a) { return a / kPos; }
   __device__ static int32_t hi(int32_t b) { return (b + kPos - 1) / kPos; }
@@ -164,8 +167,10 @@ struct Walk {
   __device__ void next(const AttnParams& p) {
     if (++s < nsub) return;
     s = 0;
-    if (++u < p.kv_heads * p.chunks) return;
-    u = 0;
+    if (++chunk < p.chunks) return;
+    chunk = 0;
+    if (++kv < p.kv_heads) return;
+    kv = 0;
     do {
       load(p, row0 + nrows);
     } while (nsub == 0);
@@ -219,14 +224,55 @@ __device__ __forceinline__ float over_lanes(float (&x)[32]) {
   return x[0];
 }
 
+// Two fp32 operations in one instruction, and a maximum of three.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float bx, float by) {
+  asm("{\n\t.reg .b64 v, m, s;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmov.b64 s, {%3, %4};\n\t"
+      "fma.rn.f32x2 v, v, m, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(bx), "f"(by));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, s;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// One lane of the warp, the same each time: what it commits is what it issued.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
+}
+
+// Arrives on `bar` (one of its expected arrivals) when this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_when_copied(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // A bounded wait: false when it gave up (after kWaitLimitNs, or because another role did).
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  const uint64_t t0 = global_timer_ns();
+  uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 63u) {
       if (*abort) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitLimitNs) {
         *abort = 1;
         atomicMax(err, (uint32_t)kErrTimeout);
         return false;
@@ -252,8 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   __shared__ uint32_t err, tmem_base;
   __shared__ int abort_flag;
   __shared__ __align__(8) uint64_t bars[2 * L::kRingK + 2 * L::kRingV + L::kQ + NB * 6 + 1];
-  __shared__ __align__(16) float ref[2][kMine];    // columns' references, in units of log2
-  __shared__ float red[2][4][32];
+  __shared__ __align__(16) float ref[2][kMine];    // columns' references, negated, in units of log2
+  __shared__ __align__(16) float raise[2][32];     // what they were raised by
+  __shared__ __align__(16) float red[2][4][32];
+  __shared__ uint32_t valid[2][4];                 // lanes whose position is one
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_addr(bars);
@@ -316,7 +364,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       float mine_ref[kMine / 32];    // lane i: the reference of column 32 h + i, -inf if unset
       bool unset[kMine / 32];
       uint32_t n = 0;                // visits of this row so far
-      bool ok = true, begin = true, cut_front = false, visited = false, seen = false;
+      bool ok = true, dead = false, begin = true, cut_front = false, visited = false, seen = false;
+      // (slots) the slot of this thread's position of the next visit, asked for a visit ahead
+      Walk<NB, SLOTS> ahead = at;
+      int32_t slot = -1;
+      auto look_ahead = [&]() {
+        if constexpr (SLOTS) {
+          const int32_t pos = ahead.s * kPos + x;
+          slot = pos < p.n_slots ? p.slots[(int64_t)ahead.row0 * p.n_slots + pos] : -1;
+        }
+      };
+      look_ahead();
       while (here < stop) {
         if (begin) {
           begin = false;
@@ -330,21 +388,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         int32_t tile;
         uint32_t rows;
         at.visit(tile, rows);
-        const int32_t chunk = at.u % p.chunks;
-        const int32_t h0 = (at.u / p.chunks) * p.group + chunk * p.chunk_heads;   // first query head
-        const int32_t heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
+        const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;   // first query head
+        const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
         if (rows >> j & 1) {
           const int32_t pos = tile * kPos + x;
           bool on;
           if constexpr (SLOTS) {
-            const int32_t slot = pos < p.n_slots ? p.slots[(int64_t)at.row0 * p.n_slots + pos] : -1;
             on = slot >= 0 && slot < p.num_pages * kPage;
+            if (here + 1 < stop) {
+              ahead.next(p);
+              look_ahead();
+            }
           } else {
             on = pos >= at.a[j] && pos < at.b[j];
           }
           const bool had = visited;   // the segment's output of this row has been begun
           visited = true;
           seen |= on;
+          const uint32_t lanes_on = __ballot_sync(~0u, on);
           ok &= wait(full_s(j, n & 1), n >> 1 & 1, abort, &err);
           tc_fence_after();
 #pragma unroll
@@ -358,7 +419,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
             float d[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) d[i] = on ? __uint_as_float(rs[i]) : kNegInf;
+            for (int i = 0; i < 32; ++i) d[i] = __uint_as_float(rs[i]);
+            if (lanes_on != ~0u) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) d[i] = on ? d[i] : kNegInf;
+            }
             if constexpr (!SLOTS) {
               if (p.logits && on) {
                 const int64_t width = (int64_t)p.max_pages * kPage;
@@ -368,61 +433,87 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                   if ((int)col0 + h * 32 + i < heads) dst[i * width] = d[i];
               }
             }
-            float top = kNegInf;
+            float top = kNegInf, top2 = kNegInf;
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (!unset[h]) r = *(const float4*)&ref[wg][h * 32 + i];
-              d[i] = fmaf(d[i], c, -r.x);
-              d[i + 1] = fmaf(d[i + 1], c, -r.y);
-              d[i + 2] = fmaf(d[i + 2], c, -r.z);
-              d[i + 3] = fmaf(d[i + 3], c, -r.w);
-              top = fmaxf(top, fmaxf(fmaxf(d[i], d[i + 1]), fmaxf(d[i + 2], d[i + 3])));
+              if (!unset[h]) r = *(const float4*)&ref[wg][h * 32 + i];   // the negated references
+              fma2(d[i], d[i + 1], c, r.x, r.y);
+              fma2(d[i + 2], d[i + 3], c, r.z, r.w);
+              top = max3(top, d[i], d[i + 1]);
+              top2 = max3(top2, d[i + 2], d[i + 3]);
             }
-            if (bar_red_or(bar_id, 128, unset[h] || top > kRaise || !ok)) {
-              // a reference is to be set or raised (or a wait gave up)
-              if (n > 0) ok &= wait(done_pv(j), (n - 1) & 1, abort, &err);
-              tc_fence_after();
-              float t[32];
+            top = fmaxf(top, top2);
+            for (int attempt = 0; attempt < 2; ++attempt) {
+              if (!bar_red_or(bar_id, 128, unset[h] || top > kRaise<BF16> || !ok)) break;
+              // a reference is to be set or raised (or a wait gave up): in bf16 first to the first
+              // position's score, and where that leaves too large a weight, as always in fp16, to the maximum
+              if (had) {
+                ok &= wait(done_pv(j), (n - 1) & 1, abort, &err);
+                tc_fence_after();
+              }
+              // lane i of every warp: what column i is compared with
+              const bool first = BF16 && attempt == 0 && unset[h];
+              if (lane == 0) valid[wg][warp & 3] = lanes_on;
+              if (first) {
+                if (lane == __ffs(lanes_on) - 1) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) t[i] = d[i];
-              red[wg][warp & 3][lane] = over_lanes<true>(t);
-              if (bar_red_or(bar_id, 128, !ok)) break;
-              const float m = fmaxf(fmaxf(red[wg][0][lane], red[wg][1][lane]), fmaxf(red[wg][2][lane], red[wg][3][lane]));
+                  for (int i = 0; i < 32; i += 4)
+                    *(float4*)&red[wg][warp & 3][i] = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+                }
+              } else {
+                float t[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) t[i] = d[i];
+                red[wg][warp & 3][lane] = over_lanes<true>(t);
+              }
+              if (bar_red_or(bar_id, 128, !ok)) {
+                dead = true;
+                break;
+              }
+              float m = kNegInf;
+#pragma unroll
+              for (int i = 3; i >= 0; --i) {
+                const float y = red[wg][i][lane];
+                if (valid[wg][i]) m = first ? y : fmaxf(m, y);
+              }
               const bool was = mine_ref[h] != kNegInf;
               const float base = was ? mine_ref[h] : 0.f;
               // never lowered; set at the first finite score
               const bool set = m != kNegInf && (m > 0.f || !was);
               const float raised = set ? base + m : base;
-              const float adj = __fsub_rn(raised, base);
               if (set) mine_ref[h] = raised;
-              const float f = ex2(-adj);
-              const bool moved = __any_sync(~0u, set);
-              if (moved) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  d[i] -= __shfl_sync(~0u, adj, i);
-                  sum[h * 32 + i] *= __shfl_sync(~0u, f, i);
-                }
-                if (had) {
-                  const uint32_t o = tmem + lanes + kO + j * kCols + col0 + h * 32;
-#pragma unroll
-                  for (int y = 0; y < 2; ++y) {
-                    uint32_t r[16];
-                    tmem_ld16(o + y * 16, r);
-                    tmem_wait_ld16(r);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                      r[i] = __float_as_uint(__uint_as_float(r[i]) * __shfl_sync(~0u, f, y * 16 + i));
-                    tmem_st16(o + y * 16, r);
-                  }
-                  tmem_wait_st();
-                }
+              if ((warp & 3) == 0) {
+                ref[wg][h * 32 + lane] = mine_ref[h] == kNegInf ? 0.f : -mine_ref[h];
+                raise[wg][lane] = __fsub_rn(raised, base);
               }
-              if ((warp & 3) == 0) ref[wg][h * 32 + lane] = mine_ref[h] == kNegInf ? 0.f : mine_ref[h];
               unset[h] = __any_sync(~0u, mine_ref[h] == kNegInf);
               bar_sync(bar_id, 128);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                uint32_t r[16];
+                const uint32_t o = tmem + lanes + kO + j * kCols + col0 + h * 32 + y * 16;
+                if (had) {
+                  tmem_ld16(o, r);
+                  tmem_wait_ld16(r);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float by = raise[wg][y * 16 + i];
+                  d[y * 16 + i] -= by;
+                  top = y + i == 0 ? d[0] : fmaxf(top, d[y * 16 + i]);
+                  if (had) {
+                    const float f = ex2(-by);
+                    sum[h * 32 + y * 16 + i] *= f;
+                    r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                  }
+                }
+                if (had) tmem_st16(o, r);
+              }
+              if (had) tmem_wait_st();
+              if (!first) break;
             }
+            if (dead) break;
             if (h == 0 && n > 0) ok &= wait(done_pv(j), (n - 1) & 1, abort, &err);
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
@@ -430,8 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 const float e0 = ex2(d[i + 2 * y]), e1 = ex2(d[i + 2 * y + 1]);
-                sum[h * 32 + i + 2 * y] += e0;
-                sum[h * 32 + i + 2 * y + 1] += e1;
+                add2(sum[h * 32 + i + 2 * y], sum[h * 32 + i + 2 * y + 1], e0, e1);
                 w[y] = pack2<BF16>(e0, e1);
               }
               const uint32_t piece = (col0 + h * 32 + i) / 8;
@@ -453,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           const int which = cut_front ? 0 : 1;
           if (!unit_end && !cut_front && threadIdx.x == 0) {
             p.open_row[blockIdx.x] = at.row0;
-            p.open_info[blockIdx.x] = make_int4(at.nrows, at.u, sp.holder(here + (at.nsub - at.s) - 2), 0);
+            p.open_info[blockIdx.x] = make_int4(at.nrows, at.kv * p.chunks + at.chunk, sp.holder(here + (at.nsub - at.s) - 2), 0);
           }
           if (visited) ok &= wait(done_pv(j), (n - 1) & 1, abort, &err);
           tc_fence_after();
@@ -466,11 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 32; ++i) t[i] = sum[h * 32 + i];
             red[wg][warp & 3][lane] = over_lanes<false>(t);
-            if (bar_red_or(bar_id, 128, !ok)) break;
+            if (bar_red_or(bar_id, 128, !ok)) {
+              dead = true;
+              break;
+            }
             const float l = (red[wg][0][lane] + red[wg][1][lane]) + (red[wg][2][lane] + red[wg][3][lane]);
             const int32_t first = col0 + h * 32;
             const int32_t cols = min(32, heads - first);
             const float inv = SLOTS && !seen ? 0.f : 1.f / l;
+            if ((warp & 3) == 0) raise[wg][lane] = whole ? inv : 1.f;
+            bar_sync(bar_id, 128);
             const int64_t part = ((int64_t)blockIdx.x * 2 + which) * (NB * kCols) + j * kCols + first;
             if ((warp & 3) == 0 && lane < cols && live) {
               const float m = mine_ref[h];
@@ -484,31 +579,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
             if (live && (whole || visited)) {
               const uint32_t o = tmem + lanes + kO + j * kCols + first;
-              T* out = (T*)p.out + row * p.out_row + (int64_t)(h0 + first) * p.out_head + x;
-              float* po = p.part_o + part * kHead + x;
+              uint32_t r[32];
+              tmem_ld32(o, r);
+              tmem_wait_ld32(r);
+              if (whole) {
+                T* out = (T*)p.out + row * p.out_row + (int64_t)(h0 + first) * p.out_head + x;
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                uint32_t r[16];
-                tmem_ld16(o + y * 16, r);
-                tmem_wait_ld16(r);
+                for (int i = 0; i < 32; ++i, out += p.out_head)
+                  if (i < cols) *out = (T)(__uint_as_float(r[i]) * raise[wg][i]);
+              } else {
+                float* po = p.part_o + part * kHead + x;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float scale = __shfl_sync(~0u, inv, y * 16 + i);
-                  if (y * 16 + i < cols) {
-                    if (whole)
-                      out[(int64_t)(y * 16 + i) * p.out_head] = (T)(__uint_as_float(r[i]) * scale);
-                    else
-                      po[(y * 16 + i) * kHead] = __uint_as_float(r[i]);
-                  }
-                }
+                for (int i = 0; i < 32; ++i)
+                  if (i < cols) po[i * kHead] = __uint_as_float(r[i]);
               }
             }
             bar_sync(bar_id, 128);   // red is free again
           }
           tc_fence_before();
         }
-        // a wait that gave up ends the role, for the whole warpgroup at once
-        if (bar_red_or(bar_id, 128, !ok)) break;
+        if (dead) break;   // a wait gave up: the whole warpgroup has voted
         if (here < stop) at.next(p);
       }
     } else if (warp < 12) {
@@ -521,58 +611,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const T* cache = (const T*)(values ? p.v : p.k);
       const int64_t s_page = values ? p.v_page : p.k_page, s_slot = values ? p.v_slot : p.k_slot,
                     s_head = values ? p.v_head : p.k_head;
-      uint32_t n = 0, handed = 0, seg = 0;   // tiles asked for, tiles handed over, segments
+      uint32_t n = 0, seg = 0;   // tiles, segments
       bool begin = true, ok = true;
       uint32_t bad = kOk;
-      auto hand_over = [&]() {               // the oldest, which has arrived
-        fence_proxy_async_smem();
-        mbar_arrive(values ? full_v(handed % depth) : full_k(handed % depth));
-        ++handed;
+      // the slots, or the pages, of this thread's two positions of the next visit, asked for a visit
+      // ahead (and a row's slots brought to L2 a row ahead)
+      Walk<NB, SLOTS> ahead = at;
+      int32_t entry[2];
+      auto look_ahead = [&]() {
+        if constexpr (SLOTS) {
+          if (warp == 10 && ahead.s == 0 && ahead.row0 + 1 < p.rows)
+            for (int32_t i = lane * 32; i < p.n_slots; i += 32 * 32)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(p.slots + (int64_t)(ahead.row0 + 1) * p.n_slots + i));
+        }
+        int32_t tile;
+        uint32_t rows;
+        ahead.visit(tile, rows);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int32_t pos = tile * kPos + half * 64 + e * 32 + lane;
+          if constexpr (SLOTS)
+            entry[e] = pos < p.n_slots ? p.slots[(int64_t)ahead.row0 * p.n_slots + pos] : -1;
+          else
+            entry[e] = pos / kPage < p.max_pages ? p.page_table[(int64_t)ahead.req * p.max_pages + pos / kPage] : -1;
+        }
       };
+      look_ahead();
       while (here < stop) {
-        const int32_t chunk = at.u % p.chunks, kv = at.u / p.chunks;
+        const int32_t chunk = at.chunk, kv = at.kv;
         int32_t tile;
         uint32_t rows;
         at.visit(tile, rows);
-        // positions 64 half + lane and + 32 of the tile: where they lie, and whether they are read
-        const T* from[2];
-        bool on[2];
-        {
-          int32_t lo = 0, hi = INT32_MAX;   // seen by every row of the visit
-          if constexpr (!SLOTS) {
+        // positions 64 half + lane and + 32 of the tile: where they lie, in units of 16 bytes, or ~0
+        uint32_t from[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int32_t pos = tile * kPos + half * 64 + e * 32 + lane;
+          bool on;
+          int32_t page, off;
+          if constexpr (SLOTS) {
+            on = entry[e] >= 0 && entry[e] < p.num_pages * kPage;
+            if (!on && entry[e] != -1) bad = kErrInvalidPage;
+            page = entry[e] / kPage, off = entry[e] % kPage;
+          } else {
+            on = true;   // seen by every row of the visit
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-              if (rows >> j & 1) lo = max(lo, at.a[j]), hi = min(hi, at.b[j]);
+              if (rows >> j & 1) on &= pos >= at.a[j] && pos < at.b[j];
+            page = entry[e], off = pos % kPage;
+            if (on && (page < 0 || page >= p.num_pages)) bad = kErrInvalidPage, on = false;
           }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int32_t pos = tile * kPos + half * 64 + e * 32 + lane;
-            int64_t page = 0;
-            int32_t off = 0;
-            if constexpr (SLOTS) {
-              const int32_t slot = pos < p.n_slots ? p.slots[(int64_t)at.row0 * p.n_slots + pos] : -1;
-              on[e] = slot >= 0 && slot < p.num_pages * kPage;
-              if (!on[e] && slot != -1) bad = kErrInvalidPage;
-              if (on[e]) page = slot / kPage, off = slot % kPage;
-            } else {
-              on[e] = pos >= lo && pos < hi;
-              if (on[e]) {
-                page = p.page_table[(int64_t)at.req * p.max_pages + pos / kPage];
-                off = pos % kPage;
-                if (page < 0 || page >= p.num_pages) bad = kErrInvalidPage, on[e] = false, page = 0;
-              }
-            }
-            from[e] = cache + page * s_page + off * s_slot + kv * s_head;
-          }
+          from[e] = on ? (uint32_t)((page * s_page + off * s_slot) / 8) : ~0u;
+        }
+        if (here + 1 < stop) {
+          ahead.next(p);
+          look_ahead();
         }
         if (begin && !values) {
           // the queries, with the segment's first tile of keys
           const uint32_t b = seg % L::kQ;
-          if (L::kQ == 1 && handed < n) {
-            // the products that free the queries' place wait for the last tile
-            copy_wait<0>();
-            hand_over();
-          }
           ok = __all_sync(~0u, wait(empty_q(b), (seg / L::kQ & 1) ^ 1, abort, &err));
           if (!ok) break;
           const int32_t h0 = kv * p.group + chunk * p.chunk_heads;
@@ -596,26 +693,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         ok = __all_sync(~0u, wait(values ? empty_v(slot) : empty_k(slot), (n / depth & 1) ^ 1, abort, &err));
         if (!ok) break;
         {
-          const int x = lane & 15;
+          const int x = lane & 15, r0 = lane / 16;   // rows r0 + 2 i of this warp's 64
           const uint32_t dst = ring + slot * kTileBytes + (x / 8) * kHalfTile + (uint32_t)half * (64 * 128);
+          uint32_t to[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) to[i] = dst + (2 * i + r0) * 128 + (((x & 7) ^ (2 * i + r0)) << 4);
+          const char* base = (const char*)(cache + kv * s_head + x * 8);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int r = i * 2 + lane / 16;   // of this warp's 64 positions
-            const unsigned long long base = __shfl_sync(~0u, (unsigned long long)from[i / 16], r & 31);
-            const bool in = __shfl_sync(~0u, (int)on[i / 16], r & 31);
-            copy16(dst + r * 128 + (((x & 7) ^ (r & 7)) << 4), (const T*)base + x * 8, in ? 16u : 0u);
+            const uint32_t o = __shfl_sync(~0u, from[i / 16], (2 * i + r0) & 31);
+            const bool in = o != ~0u;
+            copy16(to[i & 3] + (i >> 2) * 1024, base + (uint64_t)(in ? o : 0u) * 16, in ? 16u : 0u);
           }
         }
-        copy_commit();
+        arrive_when_copied(values ? full_v(slot) : full_k(slot));
         ++n;
-        if (handed + 1 < n) {
-          copy_wait<1>();   // the tile before this one
-          hand_over();
-        }
         if (++here < stop) at.next(p);
       }
-      copy_wait<0>();
-      if (ok && handed < n) hand_over();
+      copy_wait_all();
       bad = __reduce_max_sync(~0u, bad);
       if (lane == 0 && bad != kOk) atomicMax(&err, bad);
     } else {
@@ -633,24 +728,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       auto outputs = [&](uint32_t visit) {
         const uint32_t slot = visit % L::kRingV;
         ok = ok && __all_sync(~0u, wait(full_v(slot), visit / L::kRingV & 1, abort, &err));
+        fence_proxy_async_smem();   // the copies' writes before the products' reads
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           if (!(last_rows >> j & 1)) continue;
           ok = ok && __all_sync(~0u, wait(full_p(j), np[j] & 1, abort, &err));
           tc_fence_after();
-          if (ok && lane == 0) {
-            const uint32_t a = smem + L::v + slot * kTileBytes, b = smem + L::p + j * kPBytes;
+          if (ok && elect_one()) {
+            const uint64_t a = desc128(smem + L::v + slot * kTileBytes, kHalfTile, 1024),
+                           b = desc128(smem + L::p + j * kPBytes, 1024, 1024);
 #pragma unroll
-            for (int k = 0; k < kPos / 16; ++k)
-              mma_f16(tmem + kO + j * kCols, desc128(a + k * 2048, kHalfTile, 1024), desc128(b + k * 2048, 1024, 1024), kPV,
-                      !fresh[j] || k > 0);
+            for (int k = 0; k < kPos / 16; ++k)   // 16 positions: 2048 bytes of either
+              mma_f16(tmem + kO + j * kCols, a + k * (2048 >> 4), b + k * (2048 >> 4), kPV, !fresh[j] || k > 0);
             tc_commit(done_pv(j));
           }
           __syncwarp();
           fresh[j] = false;
           ++np[j];
         }
-        if (ok && lane == 0) tc_commit(empty_v(slot));
+        if (ok && elect_one()) tc_commit(empty_v(slot));
         __syncwarp();
         if (last_end) {
 #pragma unroll
@@ -664,19 +760,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (begin && n > 0) ++seg;
         const uint32_t slot = n % L::kRingK;
         ok = __all_sync(~0u, wait(full_k(slot), n / L::kRingK & 1, abort, &err));
+        fence_proxy_async_smem();   // the copies' writes before the products' reads
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           if (!(rows >> j & 1)) continue;
           const uint32_t b = ns[j] & 1;
           ok = ok && __all_sync(~0u, wait(empty_s(j, b), (ns[j] >> 1 & 1) ^ 1, abort, &err));
           tc_fence_after();
-          if (ok && lane == 0) {
-            const uint32_t a = smem + L::k + slot * kTileBytes,
-                           q = smem + L::q + (seg % L::kQ) * (NB * kQBytes) + j * kQBytes;
+          if (ok && elect_one()) {
+            const uint64_t a = desc128(smem + L::k + slot * kTileBytes, 16, 1024),
+                           q = desc128(smem + L::q + (seg % L::kQ) * (NB * kQBytes) + j * kQBytes, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < kHead / 16; ++k)
-              mma_f16(tmem + (j * 2 + b) * kCols, desc128(a + (k / 4) * kHalfTile + (k % 4) * 32, 16, 1024),
-                      desc128(q + (k / 4) * kQHalf + (k % 4) * 32, 16, 1024), kQK, k > 0);
+            for (int k = 0; k < kHead / 16; ++k)   // 16 elements: 32 bytes of a row
+              mma_f16(tmem + (j * 2 + b) * kCols, a + (k / 4) * (kHalfTile >> 4) + (k % 4) * 2,
+                      q + (k / 4) * (kQHalf >> 4) + (k % 4) * 2, kQK, k > 0);
             tc_commit(full_s(j, b));
           }
           __syncwarp();
@@ -684,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         ++here;
         const bool end = at.s + 1 == at.nsub || here == stop;
-        if (ok && lane == 0) {
+        if (ok && elect_one()) {
           tc_commit(empty_k(slot));
           if (end) tc_commit(empty_q(seg % L::kQ));
         }
@@ -715,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   // the products in flight end before the tensor memory is given back
   if (warp == 12) {
     __syncwarp();
-    if (lane == 0) tc_commit(drain);
+    if (elect_one()) tc_commit(drain);
     __syncwarp();
     for (uint32_t i = 0; i < 1u << 20; ++i)
       if (mbar_try_wait(drain, 0)) break;

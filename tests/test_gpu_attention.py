@@ -514,3 +514,42 @@ def test_refused_arguments():
     assert m.idx_attn_selected(c.q, c.k, c.v, slots, 0.1, c.out, raise_on_error=False) == INVALID_ARGUMENT
     with pytest.raises(m.IdxError):
         m.idx_attn_selected(c.q, c.k, c.v, slots, 0.1, c.out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows", [1, 2])
+def test_paged_references_of_a_column(dtype, rows):
+    """Scores that rise far above, or fall far below, those of the first positions, by tile and
+    within one; a first key of -infinity; a first tile of nothing but -infinity."""
+    import torch
+    n = 900
+    for kind in range(5):
+        c = Case([n], [(0, 0, n)] * rows, 64, 1, 128, dtype)
+        t = c.table.cpu()[0]
+        pos = torch.arange(n)
+        page, off = t[pos // PAGE].long().cuda(), (pos % PAGE).cuda()
+        c.q.abs_()
+        k = c.k[page, off].float() * 0.05
+        ramp = torch.arange(n, device="cuda").float()[:, None, None]
+        if kind == 0:
+            k += ramp * 0.01                      # ever higher
+        elif kind == 1:
+            k += 9.0 - ramp * 0.01                # ever lower
+        elif kind == 2:
+            k[0] -= 20.0                          # the first far below the rest of its tile
+        elif kind == 3:
+            k[0] = -float("inf")
+            k[500] += 12.0
+        else:
+            k[:130] = -float("inf")
+        c.k[page, off] = k.to(_dt(dtype))
+        assert run_paged(c) == 0
+        if kind < 3:
+            c.check()
+        else:
+            kk, vv = c.rows()[0]
+            on = torch.isfinite(kk[:, 0, 0])
+            for r in range(rows):
+                want, wl, _, bo, bl, _ = A.attend(c.q[r], kk[on], vv[on], c.scale)
+                assert bool(((c.out[r].double() - want).abs() <= bo).all()), (kind, r)
+                assert bool(((c.lse[r].double() - wl).abs() <= bl).all()), (kind, r)
