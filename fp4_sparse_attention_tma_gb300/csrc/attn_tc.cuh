@@ -20,8 +20,8 @@
 //
 // Roles: two warpgroups of softmax (for one row 32 columns each, for two a row each), two
 // warps that copy keys (and the queries), two that copy values (16-byte asynchronous copies
-// into the 128-byte swizzle, any stride, page or slot), one that issues the products.  Every
-// wait is bounded.
+// into the 128-byte swizzle, any stride, page or slot), one warp that issues the scores'
+// products and one the outputs'.  Every wait is bounded.
 #pragma once
 
 #include "attn_common.cuh"
@@ -164,8 +164,8 @@ struct Walk {
     }
     nsub = visits(a, b, c0, c1);
   }
-  __device__ void next(const AttnParams& p) {
-    if (++s < nsub) return;
+  // The next unit, at its first visit; the caller has not passed the end of the list.
+  __device__ void next_unit(const AttnParams& p) {
     s = 0;
     if (++chunk < p.chunks) return;
     chunk = 0;
@@ -175,13 +175,13 @@ struct Walk {
       load(p, row0 + nrows);
     } while (nsub == 0);
   }
-  // The visit: its tile and its rows (bit j).
-  __device__ void visit(int32_t& tile, uint32_t& rows) const {
+  // Visit v of the unit: its tile and its rows (bit j).
+  __device__ void visit(int32_t v, int32_t& tile, uint32_t& rows) const {
     if constexpr (NB == 1) {
-      tile = lo(a[0]) + s;
+      tile = lo(a[0]) + v;
       rows = 1;
     } else {
-      int32_t x = s;
+      int32_t x = v;
       const bool both = c1 > c0;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       mbar_init(full_p(j), kSoft);
       mbar_init(done_pv(j), 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -346,9 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   Walk<NB, SLOTS> at;
   const bool work = find_range<Walk<NB, SLOTS>, SLOTS, kWarps>(p, sp, at, blockIdx.x, &err);
   if (work) {
-    int64_t here = sp.first(blockIdx.x);
+    // A role walks over its segments (the part of a unit in the CTA's range) and a segment's visits.
+    int64_t here = sp.first(blockIdx.x);                  // flat index of the segment's first visit
     const int64_t stop = sp.first(blockIdx.x + 1);
-
     // registers: 512 threads are launched with 128 each; two warpgroups of 152 and two of 104 are as many
     if (warp < 8) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
@@ -364,43 +364,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       float mine_ref[kMine / 32];    // lane i: the reference of column 32 h + i, -inf if unset
       bool unset[kMine / 32];
       uint32_t n = 0;                // visits of this row so far
-      bool ok = true, dead = false, begin = true, cut_front = false, visited = false, seen = false;
+      bool ok = true, dead = false;
       // (slots) the slot of this thread's position of the next visit, asked for a visit ahead
-      Walk<NB, SLOTS> ahead = at;
       int32_t slot = -1;
-      auto look_ahead = [&]() {
-        if constexpr (SLOTS) {
-          const int32_t pos = ahead.s * kPos + x;
-          slot = pos < p.n_slots ? p.slots[(int64_t)ahead.row0 * p.n_slots + pos] : -1;
-        }
-      };
-      look_ahead();
-      while (here < stop) {
-        if (begin) {
-          begin = false;
-          cut_front = at.s > 0;
-          visited = seen = false;
-#pragma unroll
-          for (int i = 0; i < kMine; ++i) sum[i] = 0.f;
-#pragma unroll
-          for (int h = 0; h < kMine / 32; ++h) mine_ref[h] = kNegInf, unset[h] = true;
-        }
-        int32_t tile;
-        uint32_t rows;
-        at.visit(tile, rows);
+      if constexpr (SLOTS) {
+        const int32_t pos = at.s * kPos + x;
+        if (pos < p.n_slots) slot = p.slots[(int64_t)at.row0 * p.n_slots + pos];
+      }
+      while (here < stop && !dead) {
+        const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
+        const bool cut_front = v0 > 0;
         const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;   // first query head
         const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
-        if (rows >> j & 1) {
+        int32_t win_a = at.a[0], win_b = at.b[0];                        // this row's window
+        if (NB == 2 && j == 1) win_a = at.a[NB - 1], win_b = at.b[NB - 1];
+        const bool live = win_b > win_a;
+        bool visited = false, seen = false;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) sum[i] = 0.f;
+#pragma unroll
+        for (int h = 0; h < kMine / 32; ++h) mine_ref[h] = kNegInf, unset[h] = true;
+        const int32_t* list = nullptr;
+        if constexpr (SLOTS) list = p.slots + (int64_t)at.row0 * p.n_slots;
+        for (int32_t v = v0; v < v1; ++v) {
+          int32_t tile;
+          uint32_t rows;
+          at.visit(v, tile, rows);
+          if (NB == 2 && !(rows >> j & 1)) continue;
           const int32_t pos = tile * kPos + x;
           bool on;
           if constexpr (SLOTS) {
             on = slot >= 0 && slot < p.num_pages * kPage;
-            if (here + 1 < stop) {
-              ahead.next(p);
-              look_ahead();
+            slot = -1;
+            if (v + 1 < v1) {
+              if (pos + kPos < p.n_slots) slot = list[pos + kPos];
+            } else if (here + (v1 - v0) < stop) {
+              // the next unit's first: of this row, or of the next
+              if (at.chunk + 1 == p.chunks && at.kv + 1 == p.kv_heads) list += p.n_slots;
+              if (x < p.n_slots) slot = list[x];
             }
           } else {
-            on = pos >= at.a[j] && pos < at.b[j];
+            on = pos >= win_a && pos < win_b;
           }
           const bool had = visited;   // the segment's output of this row has been begun
           visited = true;
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               if (had) tmem_wait_st();
               if (!first) break;
             }
-            if (dead) break;
+            if (dead) break;   // a wait gave up: the whole warpgroup has voted
             if (h == 0 && n > 0) ok &= wait(done_pv(j), (n - 1) & 1, abort, &err);
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
@@ -530,25 +534,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                            : "memory");
             }
           }
+          if (dead) break;
           fence_proxy_async_smem();
           tc_fence_before();
           mbar_arrive(full_p(j));
           ++n;
         }
-        ++here;
-        const bool unit_end = at.s + 1 == at.nsub;
-        if (unit_end || here == stop) {
-          begin = true;
+        here += v1 - v0;
+        if (!dead) {
+          const bool unit_end = v1 == at.nsub;
           const bool whole = unit_end && !cut_front;
           const int which = cut_front ? 0 : 1;
           if (!unit_end && !cut_front && threadIdx.x == 0) {
             p.open_row[blockIdx.x] = at.row0;
-            p.open_info[blockIdx.x] = make_int4(at.nrows, at.kv * p.chunks + at.chunk, sp.holder(here + (at.nsub - at.s) - 2), 0);
+            p.open_info[blockIdx.x] =
+                make_int4(at.nrows, at.kv * p.chunks + at.chunk, sp.holder(here + (at.nsub - v1) - 1), 0);
           }
           if (visited) ok &= wait(done_pv(j), (n - 1) & 1, abort, &err);
           tc_fence_after();
           if constexpr (SLOTS) seen = bar_red_or(bar_id, 128, seen);
-          const bool live = at.b[j] > at.a[j];
           const int64_t row = at.row0 + j;
 #pragma unroll
           for (int h = 0; h < kMine / 32; ++h) {
@@ -598,8 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
           tc_fence_before();
         }
-        if (dead) break;   // a wait gave up: the whole warpgroup has voted
-        if (here < stop) at.next(p);
+        if (here < stop && !dead) at.next_unit(p);
       }
     } else if (warp < 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -611,104 +614,138 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const T* cache = (const T*)(values ? p.v : p.k);
       const int64_t s_page = values ? p.v_page : p.k_page, s_slot = values ? p.v_slot : p.k_slot,
                     s_head = values ? p.v_head : p.k_head;
-      uint32_t n = 0, seg = 0;   // tiles, segments
-      bool begin = true, ok = true;
+      // Offsets are in units of 16 bytes (the caches span less than 64 GB).
+      const uint32_t page16 = (uint32_t)(s_page / 8), slot16 = (uint32_t)(s_slot / 8);
+      const int x = lane & 15, r0 = lane / 16;   // this lane's piece of a head, and its rows r0 + 2 i of the warp's 64
+      uint32_t n = 0, seg = 0;                   // tiles, segments
+      bool ok = true;
       uint32_t bad = kOk;
-      // the slots, or the pages, of this thread's two positions of the next visit, asked for a visit
-      // ahead (and a row's slots brought to L2 a row ahead)
-      Walk<NB, SLOTS> ahead = at;
+      // the slots of this thread's two positions, or the page of the warp's 64, of the next visit: asked
+      // for a visit ahead (and a row's slots brought to L2 a row ahead)
       int32_t entry[2];
-      auto look_ahead = [&]() {
+      auto ask = [&](const int32_t* list, int32_t tile) {
         if constexpr (SLOTS) {
-          if (warp == 10 && ahead.s == 0 && ahead.row0 + 1 < p.rows)
-            for (int32_t i = lane * 32; i < p.n_slots; i += 32 * 32)
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(p.slots + (int64_t)(ahead.row0 + 1) * p.n_slots + i));
-        }
-        int32_t tile;
-        uint32_t rows;
-        ahead.visit(tile, rows);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int32_t pos = tile * kPos + half * 64 + e * 32 + lane;
-          if constexpr (SLOTS)
-            entry[e] = pos < p.n_slots ? p.slots[(int64_t)ahead.row0 * p.n_slots + pos] : -1;
-          else
-            entry[e] = pos / kPage < p.max_pages ? p.page_table[(int64_t)ahead.req * p.max_pages + pos / kPage] : -1;
+          for (int e = 0; e < 2; ++e) {
+            const int32_t pos = tile * kPos + half * 64 + e * 32 + lane;
+            entry[e] = pos < p.n_slots ? list[pos] : -1;
+          }
+        } else {
+          const int32_t i = tile * 2 + half;
+          entry[0] = i < p.max_pages ? list[i] : -1;
         }
       };
-      look_ahead();
-      while (here < stop) {
-        const int32_t chunk = at.chunk, kv = at.kv;
+      const int32_t* list = nullptr;
+      if constexpr (SLOTS) ask(p.slots + (int64_t)at.row0 * p.n_slots, at.s);
+      while (here < stop && ok) {
+        const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
+        here += v1 - v0;
         int32_t tile;
         uint32_t rows;
-        at.visit(tile, rows);
-        // positions 64 half + lane and + 32 of the tile: where they lie, in units of 16 bytes, or ~0
-        uint32_t from[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int32_t pos = tile * kPos + half * 64 + e * 32 + lane;
-          bool on;
-          int32_t page, off;
-          if constexpr (SLOTS) {
-            on = entry[e] >= 0 && entry[e] < p.num_pages * kPage;
-            if (!on && entry[e] != -1) bad = kErrInvalidPage;
-            page = entry[e] / kPage, off = entry[e] % kPage;
-          } else {
-            on = true;   // seen by every row of the visit
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-              if (rows >> j & 1) on &= pos >= at.a[j] && pos < at.b[j];
-            page = entry[e], off = pos % kPage;
-            if (on && (page < 0 || page >= p.num_pages)) bad = kErrInvalidPage, on = false;
-          }
-          from[e] = on ? (uint32_t)((page * s_page + off * s_slot) / 8) : ~0u;
+        if constexpr (SLOTS) {
+          list = p.slots + (int64_t)at.row0 * p.n_slots;
+          if (warp == 10 && at.row0 + 1 < p.rows)
+            for (int32_t i = lane * 32; i < p.n_slots; i += 32 * 32)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(list + p.n_slots + i));
+        } else {
+          list = p.page_table + (int64_t)at.req * p.max_pages;
+          at.visit(v0, tile, rows);
+          ask(list, tile);
         }
-        if (here + 1 < stop) {
-          ahead.next(p);
-          look_ahead();
-        }
-        if (begin && !values) {
+        if (!values) {
           // the queries, with the segment's first tile of keys
           const uint32_t b = seg % L::kQ;
           ok = __all_sync(~0u, wait(empty_q(b), (seg / L::kQ & 1) ^ 1, abort, &err));
           if (!ok) break;
-          const int32_t h0 = kv * p.group + chunk * p.chunk_heads;
-          const int32_t heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
+          const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
+          const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
           const uint32_t dst = smem + L::q + b * (NB * kQBytes);
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
             const bool live = at.b[j] > at.a[j];
             const T* q = (const T*)p.q + (int64_t)(at.row0 + (live ? j : 0)) * p.q_row + (int64_t)h0 * p.q_head;
+#pragma unroll 4
             for (int i = t; i < kCols * 16; i += kLoaders) {
-              const int r = i / 16, x = i % 16;
+              const int r = i / 16, y = i % 16;
               const bool in = live && r < heads;
-              copy16(dst + j * kQBytes + (x / 8) * kQHalf + r * 128 + (((x & 7) ^ (r & 7)) << 4),
-                     q + (in ? (int64_t)r * p.q_head : 0) + x * 8, in ? 16u : 0u);
+              copy16(dst + j * kQBytes + (y / 8) * kQHalf + r * 128 + (((y & 7) ^ (r & 7)) << 4),
+                     q + (in ? (int64_t)r * p.q_head : 0) + y * 8, in ? 16u : 0u);
             }
           }
           ++seg;
         }
-        begin = at.s + 1 == at.nsub;
-        const uint32_t slot = n % depth;
-        ok = __all_sync(~0u, wait(values ? empty_v(slot) : empty_k(slot), (n / depth & 1) ^ 1, abort, &err));
-        if (!ok) break;
-        {
-          const int x = lane & 15, r0 = lane / 16;   // rows r0 + 2 i of this warp's 64
+        const char* base = (const char*)(cache + at.kv * s_head + x * 8);
+        for (int32_t v = v0; v < v1; ++v) {
+          at.visit(v, tile, rows);
+          // where the warp's 64 positions lie; `all`: every one of them is read
+          uint32_t from[2];
+          bool all = true;
+          if constexpr (SLOTS) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool on = entry[e] >= 0 && entry[e] < p.num_pages * kPage;
+              if (!on && entry[e] != -1) bad = kErrInvalidPage;
+              from[e] = on ? (uint32_t)(entry[e] / kPage) * page16 + (uint32_t)(entry[e] % kPage) * slot16 : ~0u;
+              all &= on;
+            }
+            if (v + 1 < v1) {
+              ask(list, v + 1);
+            } else if (here < stop) {
+              // the next unit's first: of this row, or of the next
+              ask(list + (at.chunk + 1 == p.chunks && at.kv + 1 == p.kv_heads ? p.n_slots : 0), 0);
+            }
+          } else {
+            int32_t lo = 0, hi = INT32_MAX;   // seen by every row of the visit
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+              if (rows >> j & 1) lo = max(lo, at.a[j]), hi = min(hi, at.b[j]);
+            const int32_t first = tile * kPos + half * 64;
+            const bool any = first < hi && first + 64 > lo, there = entry[0] >= 0 && entry[0] < p.num_pages;
+            if (any && !there) bad = kErrInvalidPage;
+            const uint32_t page = there ? (uint32_t)entry[0] * page16 : 0u;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int32_t pos = first + e * 32 + lane;
+              const bool on = there && pos >= lo && pos < hi;
+              from[e] = on ? page + (uint32_t)(e * 32 + lane) * slot16 : ~0u;
+              all &= on;
+            }
+            if (v + 1 < v1) {
+              int32_t next_tile;
+              uint32_t next_rows;
+              at.visit(v + 1, next_tile, next_rows);
+              ask(list, next_tile);
+            }
+          }
+          all = __all_sync(~0u, all);
+          const uint32_t slot = n % depth;
+          ok = __all_sync(~0u, wait(values ? empty_v(slot) : empty_k(slot), (n / depth & 1) ^ 1, abort, &err));
+          if (!ok) break;
           const uint32_t dst = ring + slot * kTileBytes + (x / 8) * kHalfTile + (uint32_t)half * (64 * 128);
           uint32_t to[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) to[i] = dst + (2 * i + r0) * 128 + (((x & 7) ^ (2 * i + r0)) << 4);
-          const char* base = (const char*)(cache + kv * s_head + x * 8);
+          if (!SLOTS && all) {
+            const char* src = base + (uint64_t)__shfl_sync(~0u, from[0], 0) * 16 + (int64_t)r0 * s_slot * 2;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint32_t o = __shfl_sync(~0u, from[i / 16], (2 * i + r0) & 31);
-            const bool in = o != ~0u;
-            copy16(to[i & 3] + (i >> 2) * 1024, base + (uint64_t)(in ? o : 0u) * 16, in ? 16u : 0u);
+            for (int i = 0; i < 32; ++i, src += 4 * s_slot) copy16(to[i & 3] + (i >> 2) * 1024, src, 16u);
+          } else if (all) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              copy16(to[i & 3] + (i >> 2) * 1024,
+                     base + (uint64_t)__shfl_sync(~0u, from[i / 16], (2 * i + r0) & 31) * 16, 16u);
+          } else {
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i) {
+              const uint32_t o = __shfl_sync(~0u, i < 16 ? from[0] : from[1], (2 * i + r0) & 31);
+              const bool in = o != ~0u;
+              copy16(to[i & 3] + (i >> 2) * 1024, base + (uint64_t)(in ? o : 0u) * 16, in ? 16u : 0u);
+            }
           }
+          arrive_when_copied(values ? full_v(slot) : full_k(slot));
+          ++n;
         }
-        arrive_when_copied(values ? full_v(slot) : full_k(slot));
-        ++n;
-        if (++here < stop) at.next(p);
+        if (here < stop && ok) at.next_unit(p);
       }
       copy_wait_all();
       bad = __reduce_max_sync(~0u, bad);
@@ -716,84 +753,97 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
       // ----------------------------------------------------------- products ----
-      constexpr uint32_t kQK = idesc_f16<BF16>(128, kCols, false), kPV = idesc_f16<BF16>(128, kCols, true);
-      uint32_t n = 0, seg = 0;          // visits, segments
-      uint32_t ns[NB], np[NB];          // visits of each row: scores issued, outputs issued
-      bool fresh[NB];                   // the row's output is to be begun anew
+      // One warp issues the scores' products and one the outputs', each its own waits in order; the
+      // other two warps have no work.
+      bool ok = true;
+      uint32_t n = 0;                   // visits
+      if (warp == 12) {
+        constexpr uint32_t kQK = idesc_f16<BF16>(128, kCols, false);
+        uint32_t seg = 0, ns[NB];       // segments; visits of each row
 #pragma unroll
-      for (int j = 0; j < NB; ++j) ns[j] = np[j] = 0, fresh[j] = true;
-      uint32_t last_rows = 0;           // rows of the visit before, whose outputs are still to be issued
-      bool last_end = false;            // it was its segment's last
-      bool ok = true, begin = true;
-      auto outputs = [&](uint32_t visit) {
-        const uint32_t slot = visit % L::kRingV;
-        ok = ok && __all_sync(~0u, wait(full_v(slot), visit / L::kRingV & 1, abort, &err));
-        fence_proxy_async_smem();   // the copies' writes before the products' reads
+        for (int j = 0; j < NB; ++j) ns[j] = 0;
+        while (here < stop && ok) {
+          const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
+          here += v1 - v0;
+          const uint32_t qb = seg % L::kQ;
+          const uint64_t q = desc128(smem + L::q + qb * (NB * kQBytes), 16, 1024);
+          for (int32_t v = v0; v < v1; ++v) {
+            int32_t tile;
+            uint32_t rows;
+            at.visit(v, tile, rows);
+            const uint32_t slot = n % L::kRingK;
+            ok = __all_sync(~0u, wait(full_k(slot), n / L::kRingK & 1, abort, &err));
+            fence_proxy_async_smem();   // the copies' writes before the products' reads
+            const uint64_t a = desc128(smem + L::k + slot * kTileBytes, 16, 1024);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          if (!(last_rows >> j & 1)) continue;
-          ok = ok && __all_sync(~0u, wait(full_p(j), np[j] & 1, abort, &err));
-          tc_fence_after();
-          if (ok && elect_one()) {
-            const uint64_t a = desc128(smem + L::v + slot * kTileBytes, kHalfTile, 1024),
-                           b = desc128(smem + L::p + j * kPBytes, 1024, 1024);
+            for (int j = 0; j < NB; ++j) {
+              if (!(rows >> j & 1)) continue;
+              const uint32_t b = ns[j] & 1;
+              ok = ok && __all_sync(~0u, wait(empty_s(j, b), (ns[j] >> 1 & 1) ^ 1, abort, &err));
+              tc_fence_after();
+              if (ok && elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kPos / 16; ++k)   // 16 positions: 2048 bytes of either
-              mma_f16(tmem + kO + j * kCols, a + k * (2048 >> 4), b + k * (2048 >> 4), kPV, !fresh[j] || k > 0);
-            tc_commit(done_pv(j));
+                for (int k = 0; k < kHead / 16; ++k)   // 16 elements: 32 bytes of a row
+                  mma_f16(tmem + (j * 2 + b) * kCols, a + (k / 4) * (kHalfTile >> 4) + (k % 4) * 2,
+                          q + j * (kQBytes >> 4) + (k / 4) * (kQHalf >> 4) + (k % 4) * 2, kQK, k > 0);
+                tc_commit(full_s(j, b));
+              }
+              __syncwarp();
+              ++ns[j];
+            }
+            if (!ok) break;
+            if (elect_one()) tc_commit(empty_k(slot));
+            __syncwarp();
+            ++n;
           }
+          if (ok && elect_one()) tc_commit(empty_q(qb));
           __syncwarp();
-          fresh[j] = false;
-          ++np[j];
+          ++seg;
+          if (here < stop && ok) at.next_unit(p);
         }
-        if (ok && elect_one()) tc_commit(empty_v(slot));
-        __syncwarp();
-        if (last_end) {
+      } else if (warp == 13) {
+        constexpr uint32_t kPV = idesc_f16<BF16>(128, kCols, true);
+        uint32_t np[NB];                // visits of each row
+        bool fresh[NB];                 // the row's output is to be begun anew
+#pragma unroll
+        for (int j = 0; j < NB; ++j) np[j] = 0, fresh[j] = true;
+        while (here < stop && ok) {
+          const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
+          here += v1 - v0;
 #pragma unroll
           for (int j = 0; j < NB; ++j) fresh[j] = true;
-        }
-      };
-      while (warp == 12 && here < stop && ok) {   // the warps beside it have no work
-        int32_t tile;
-        uint32_t rows;
-        at.visit(tile, rows);
-        if (begin && n > 0) ++seg;
-        const uint32_t slot = n % L::kRingK;
-        ok = __all_sync(~0u, wait(full_k(slot), n / L::kRingK & 1, abort, &err));
-        fence_proxy_async_smem();   // the copies' writes before the products' reads
+          for (int32_t v = v0; v < v1; ++v) {
+            int32_t tile;
+            uint32_t rows;
+            at.visit(v, tile, rows);
+            const uint32_t slot = n % L::kRingV;
+            ok = __all_sync(~0u, wait(full_v(slot), n / L::kRingV & 1, abort, &err));
+            fence_proxy_async_smem();   // the copies' writes before the products' reads
+            const uint64_t a = desc128(smem + L::v + slot * kTileBytes, kHalfTile, 1024);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          if (!(rows >> j & 1)) continue;
-          const uint32_t b = ns[j] & 1;
-          ok = ok && __all_sync(~0u, wait(empty_s(j, b), (ns[j] >> 1 & 1) ^ 1, abort, &err));
-          tc_fence_after();
-          if (ok && elect_one()) {
-            const uint64_t a = desc128(smem + L::k + slot * kTileBytes, 16, 1024),
-                           q = desc128(smem + L::q + (seg % L::kQ) * (NB * kQBytes) + j * kQBytes, 16, 1024);
+            for (int j = 0; j < NB; ++j) {
+              if (!(rows >> j & 1)) continue;
+              ok = ok && __all_sync(~0u, wait(full_p(j), np[j] & 1, abort, &err));
+              tc_fence_after();
+              if (ok && elect_one()) {
+                const uint64_t b = desc128(smem + L::p + j * kPBytes, 1024, 1024);
 #pragma unroll
-            for (int k = 0; k < kHead / 16; ++k)   // 16 elements: 32 bytes of a row
-              mma_f16(tmem + (j * 2 + b) * kCols, a + (k / 4) * (kHalfTile >> 4) + (k % 4) * 2,
-                      q + (k / 4) * (kQHalf >> 4) + (k % 4) * 2, kQK, k > 0);
-            tc_commit(full_s(j, b));
+                for (int k = 0; k < kPos / 16; ++k)   // 16 positions: 2048 bytes of either
+                  mma_f16(tmem + kO + j * kCols, a + k * (2048 >> 4), b + k * (2048 >> 4), kPV, !fresh[j] || k > 0);
+                tc_commit(done_pv(j));
+              }
+              __syncwarp();
+              fresh[j] = false;
+              ++np[j];
+            }
+            if (!ok) break;
+            if (elect_one()) tc_commit(empty_v(slot));
+            __syncwarp();
+            ++n;
           }
-          __syncwarp();
-          ++ns[j];
+          if (here < stop && ok) at.next_unit(p);
         }
-        ++here;
-        const bool end = at.s + 1 == at.nsub || here == stop;
-        if (ok && elect_one()) {
-          tc_commit(empty_k(slot));
-          if (end) tc_commit(empty_q(seg % L::kQ));
-        }
-        __syncwarp();
-        begin = end;
-        if (n > 0 && ok) outputs(n - 1);
-        last_rows = rows;
-        last_end = end;
-        ++n;
-        if (here < stop) at.next(p);
       }
-      if (n > 0 && ok) outputs(n - 1);
     }
   }
 
@@ -810,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
   }
   // the products in flight end before the tensor memory is given back
-  if (warp == 12) {
+  if (warp == 12 || warp == 13) {
     __syncwarp();
     if (elect_one()) tc_commit(drain);
     __syncwarp();
