@@ -66,8 +66,11 @@ def _desc(t):
 
 # idx_tensor_t as packed bytes: data pointer, dtype, ndim, shape[4], stride[4]
 _DESC = struct.Struct("=Qii4q4q")
-_ZERO4 = (0, 0, 0, 0)
+_pack = _DESC.pack
 _DT_CODE = {}  # torch.dtype -> code, filled on first use
+_ABSENT = bytes(_DESC.size)
+# zeros behind the shape and the strides of a tensor of each rank
+_FILL = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
 
 
 def _dtype_code(dt) -> int:
@@ -81,29 +84,49 @@ def _descs(ts):
     """Descriptors of the tensors `ts` (None: absent) packed into one buffer.
     Returns the buffer, which must stay alive for the call, and each
     descriptor's address (None for an absent tensor)."""
-    buf = ctypes.create_string_buffer(_DESC.size * len(ts))
-    base = ctypes.addressof(buf)
-    addrs = [None] * len(ts)
-    for i, t in enumerate(ts):
+    parts = []
+    for t in ts:
         if t is None:
+            parts.append(_ABSENT)
             continue
         sh = t.shape
         st = t.stride()
-        n = len(sh)
-        if n < 4:
-            sh = (*sh, *_ZERO4[n:])
-            st = (*st, *_ZERO4[n:])
-        _DESC.pack_into(buf, _DESC.size * i, t.data_ptr() if t.numel() else 0,
-                        _dtype_code(t.dtype), n, *sh[:4], *st[:4])
-        addrs[i] = base + _DESC.size * i
-    return buf, addrs
+        nd = len(st)
+        dt = t.dtype
+        # (an empty tensor's data_ptr() is 0)
+        code = _DT_CODE[dt] if dt in _DT_CODE else _dtype_code(dt)
+        if nd <= 4:
+            fill = _FILL[nd]
+            parts.append(_pack(t.data_ptr(), code, nd, *sh, *fill, *st, *fill))
+        else:
+            parts.append(_pack(t.data_ptr(), code, nd, *sh[:4], *st[:4]))
+    buf = ctypes.create_string_buffer(b"".join(parts), 80 * len(parts))
+    at = ctypes.addressof(buf)
+    return buf, [None if t is None else at + 80 * i for i, t in enumerate(ts)]
+
+
+def _raw_stream():
+    """Function that gives the handle of the current device's current stream."""
+    import torch
+    try:
+        handle, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    except AttributeError:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: handle(device())
+
+
+_current = None
 
 
 def _stream(stream):
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    global _current
+    if stream is not None:
+        return stream.cuda_stream
+    if _current is None:
+        import torch
+        torch.cuda.current_stream()   # initialises CUDA
+        _current = _raw_stream()
+    return _current()
 
 
 def _check(code: int, fn: str, raise_on_error: bool):
@@ -320,9 +343,7 @@ def idx_topk_last_timings() -> dict:
 
 
 def _space(workspace, status):
-    return (ctypes.c_void_p(workspace.data_ptr()),
-            ctypes.c_uint64(workspace.numel() * workspace.element_size()),
-            ctypes.c_void_p(status.data_ptr()))
+    return workspace.data_ptr(), workspace.nbytes, status.data_ptr()
 
 
 def idx_attn_paged(q, k_cache, v_cache, page_table, row_req, row_start, row_end, scale, out,

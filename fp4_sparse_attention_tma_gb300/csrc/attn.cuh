@@ -36,13 +36,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
   __shared__ uint32_t err;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t worker = warp * gridDim.x + blockIdx.x;
+  allow_launch_after();
   if (threadIdx.x == 0) err = kOk;
   __syncthreads();
 
   Split sp;
   Cursor<SLOTS> at;
   const bool work = find_range<Cursor<SLOTS>, SLOTS, WARPS>(p, sp, at, worker, &err);
-  if (lane == 0) p.open_row[worker] = -1;
+  if (work && lane == 0) p.open_row[worker] = -1;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.active = sp.active;
   uint32_t warp_err = kOk;
   if (work) {
     const uint32_t my_ring = smem_addr(ring) + (uint32_t)warp * (STAGES * 2 * kHalf);

@@ -50,7 +50,8 @@ struct AttnParams {
   // workspace
   uint32_t* cta_status;             // [CTAs] first error that the CTA saw
   int32_t n_cta;
-  int32_t* open_row;                // [workers] first row of the unit cut at the range's end, or -1
+  int32_t* active;                  // workers that have a range (the first so many)
+  int32_t* open_row;                // [active] first row of the unit cut at the range's end, or -1
   int4* open_info;                  // [workers] {rows of its group, unit index in the group, last worker, 0}
   float2* part_ml;                  // [workers][2][tile] maximum (in units of log2, scaled) and sum
   float* part_o;                    // [workers][2][tile][dim]
@@ -66,7 +67,7 @@ struct AttnParams {
 
 // Byte offsets of a call's workspace.
 struct AttnLayout {
-  size_t cta_status, open_row, open_info, part_ml, part_o, row_stat, logits, total;
+  size_t cta_status, active, open_row, open_info, part_ml, part_o, row_stat, logits, total;
 };
 
 inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int64_t dim, int64_t stat_rows,
@@ -74,6 +75,7 @@ inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int6
   AttnLayout L{};
   size_t off = 0;
   L.cta_status = off; off = align_up(off + (size_t)n_cta * 4, 256);
+  L.active = off;     off = align_up(off + 4, 256);
   L.open_row = off;   off = align_up(off + (size_t)workers * 4, 256);
   L.open_info = off;  off = align_up(off + (size_t)workers * 16, 256);
   L.part_ml = off;    off = align_up(off + (size_t)workers * 2 * tile * 8, 256);

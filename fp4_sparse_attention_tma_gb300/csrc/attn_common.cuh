@@ -78,8 +78,8 @@ __device__ __forceinline__ float ex2(float x) {
 
 // Divides the units' subtiles among the workers.
 struct Split {
-  int64_t total;    // subtiles of all units
-  int32_t active;   // workers with a range
+  int64_t total = 0;    // subtiles of all units
+  int32_t active = 0;   // workers with a range
   __device__ int64_t first(int64_t w) const { return total * w / active; }
   // the worker whose range holds subtile x
   __device__ int32_t holder(int64_t x) const { return (int32_t)(((x + 1) * active - 1) / total); }

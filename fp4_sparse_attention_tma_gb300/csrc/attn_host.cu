@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "attn.h"
@@ -142,11 +143,21 @@ int find_machine(const idx_tensor_t* const* ts, int n, const void* status, const
   return IDX_OK;
 }
 
+// SM count, and whether the device is one that the kernels are built for: asked once a
+// device (neither changes).
 int check_arch(Machine* m) {
-  int major = 0, minor = 0;
-  int st = device_info_no_pool(m->dev, &m->sm, &major, &minor);
-  if (st) return st;
-  return major == 10 && minor == 3 ? IDX_OK : IDX_ERR_UNSUPPORTED;
+  static std::atomic<int> known[kMaxDevices];   // SM count + 1, or -1 for another architecture
+  if (m->dev < 0 || m->dev >= kMaxDevices) return IDX_ERR_INVALID_ARGUMENT;
+  int k = known[m->dev].load(std::memory_order_acquire);
+  if (k == 0) {
+    int sm = 0, major = 0, minor = 0;
+    const int st = device_info_no_pool(m->dev, &sm, &major, &minor);
+    if (st) return st;
+    k = major == 10 && minor == 3 ? sm + 1 : -1;
+    known[m->dev].store(k, std::memory_order_release);
+  }
+  m->sm = k - 1;
+  return k > 0 ? IDX_OK : IDX_ERR_UNSUPPORTED;
 }
 
 // Where a call's workspace and status word come from.
@@ -341,6 +352,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   const bool bf16 = c.q->dtype == IDX_BF16;
   return with_space(space, L.total, m, stream, [&](char* base, uint32_t* status) -> cudaError_t {
     p.cta_status = (uint32_t*)(base + L.cta_status);
+    p.active = (int32_t*)(base + L.active);
     p.open_row = (int32_t*)(base + L.open_row);
     p.open_info = (int4*)(base + L.open_info);
     p.part_ml = (float2*)(base + L.part_ml);

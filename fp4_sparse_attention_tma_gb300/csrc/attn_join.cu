@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "idx_launch.h"
 
 namespace idxk {
 
@@ -109,10 +110,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr int V = D / 32;   // columns of a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  extern __shared__ OpenUnit open[];   // [workers]: units of few parts from the front, others from the back
+  // [workers]: units of few parts from the front, others from the back; first worker | parts << 16
+  extern __shared__ uint32_t open[];
   __shared__ int32_t warp_n[kJoinWarps][2];
   __shared__ float wm[kJoinWarps], wl[kJoinWarps];
   __shared__ float wo[kJoinWarps][D];
+  allow_launch_after();
+  wait_for_launch_before();
   const uint32_t status = call_status(p);
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.status_out) *p.status_out = status;
   if (status != kOk) {
@@ -128,16 +132,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   }
   // the cut units
   int few = 0, many = 0;
-  for (int w0 = 0; w0 < p.workers; w0 += kJoinWarps * 32) {
+  const int active = p.n_cta > 0 ? *p.active : 0;
+  for (int w0 = 0; w0 < active; w0 += kJoinWarps * 32) {
     const int w = w0 + (int)threadIdx.x;
-    OpenUnit un{};
-    un.row0 = w < p.workers ? p.open_row[w] : -1;
-    const bool on = un.row0 >= 0;
-    if (on) {
-      const int4 info = p.open_info[w];
-      un.w0 = w, un.nrows = info.x, un.u = info.y, un.n = info.z - w + 1;
-    }
-    const bool is_few = on && un.n <= kFewParts, is_many = on && !is_few;
+    const bool on = w < active && p.open_row[w] >= 0;
+    const int n = on ? p.open_info[w].z - w + 1 : 0;
+    const bool is_few = on && n <= kFewParts, is_many = on && !is_few;
     const uint32_t bf = __ballot_sync(~0u, is_few), bm = __ballot_sync(~0u, is_many);
     if (lane == 0) warp_n[warp][0] = __popc(bf), warp_n[warp][1] = __popc(bm);
     __syncthreads();
@@ -147,11 +147,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
       if (i < warp) at_few += warp_n[i][0], at_many += warp_n[i][1];
       few += warp_n[i][0], many += warp_n[i][1];
     }
-    const uint32_t below = (1u << lane) - 1;
-    if (is_few) open[at_few + __popc(bf & below)] = un;
-    if (is_many) open[p.workers - 1 - at_many - __popc(bm & below)] = un;
+    const uint32_t below = (1u << lane) - 1, entry = (uint32_t)w | (uint32_t)n << 16;
+    if (is_few) open[at_few + __popc(bf & below)] = entry;
+    if (is_many) open[p.workers - 1 - at_many - __popc(bm & below)] = entry;
     __syncthreads();
   }
+  auto unit_of = [&](uint32_t entry) {
+    OpenUnit un;
+    un.w0 = entry & 0xFFFFu;
+    un.n = entry >> 16;
+    un.row0 = p.open_row[un.w0];
+    const int4 info = p.open_info[un.w0];
+    un.nrows = info.x, un.u = info.y;
+    return un;
+  };
 
   // the output row of tile row m: false where it is none, or sees nothing
   auto row_of = [&](const OpenUnit& un, int m, int64_t& row, int& qh) {
@@ -164,7 +173,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   };
   const int per = p.tile / kJoinWarps;
   for (int job = blockIdx.x; job < few * per; job += gridDim.x) {
-    const OpenUnit un = open[job / per];
+    const OpenUnit un = unit_of(open[job / per]);
     const int m = job % per * kJoinWarps + warp;
     int64_t row;
     int qh;
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     }
   }
   for (int job = blockIdx.x; job < many * p.tile; job += gridDim.x) {
-    const OpenUnit un = open[p.workers - 1 - job / p.tile];
+    const OpenUnit un = unit_of(open[p.workers - 1 - job / p.tile]);
     int64_t row;
     int qh;
     if (!row_of(un, job % p.tile, row, qh)) continue;   // the same for the whole CTA
@@ -231,6 +240,7 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __gr
   const int64_t width = (int64_t)p.max_pages * kPage;
   const int64_t pos = ((int64_t)blockIdx.x * kWeightThreads + threadIdx.x) * 4;
   const bool in = pos < width;
+  wait_for_launch_before();
   const bool failed = call_status(p) != kOk;
   __shared__ int32_t list[kRowList];
   __shared__ int32_t warp_n[kWeightThreads / 32];
@@ -299,11 +309,10 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __gr
 
 template <bool BF16>
 static cudaError_t pick_join(const AttnParams& p, int grid, cudaStream_t stream) {
-  const size_t smem = (size_t)p.workers * sizeof(OpenUnit);
-  if (p.dim == 64) attn_join_kernel<BF16, 64><<<grid, kJoinWarps * 32, smem, stream>>>(p);
-  else if (p.dim == 128) attn_join_kernel<BF16, 128><<<grid, kJoinWarps * 32, smem, stream>>>(p);
-  else attn_join_kernel<BF16, 256><<<grid, kJoinWarps * 32, smem, stream>>>(p);
-  return cudaGetLastError();
+  const size_t smem = (size_t)p.workers * 4;
+  if (p.dim == 64) return launch_overlapped(attn_join_kernel<BF16, 64>, dim3(grid), dim3(kJoinWarps * 32), smem, stream, p);
+  if (p.dim == 128) return launch_overlapped(attn_join_kernel<BF16, 128>, dim3(grid), dim3(kJoinWarps * 32), smem, stream, p);
+  return launch_overlapped(attn_join_kernel<BF16, 256>, dim3(grid), dim3(kJoinWarps * 32), smem, stream, p);
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream) {
@@ -314,8 +323,7 @@ cudaError_t launch_attn_weights(const AttnParams& p, cudaStream_t stream) {
   const int64_t per = kWeightThreads * 4;
   const int64_t x = ((int64_t)p.max_pages * kPage + per - 1) / per;
   const dim3 grid((unsigned)x, (unsigned)(p.num_req < 65535 ? p.num_req : 65535));
-  attn_weights_kernel<<<grid, kWeightThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(attn_weights_kernel, grid, dim3(kWeightThreads), 0, stream, p);
 }
 
 }  // namespace idxk

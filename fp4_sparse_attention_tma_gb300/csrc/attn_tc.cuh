@@ -317,10 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   auto done_pv = [&](uint32_t j) { return bar0 + 8 * (kRow + j * 6 + 5); };
   const uint32_t drain = bar0 + 8 * (kRow + NB * 6);
 
+  allow_launch_after();
   if (threadIdx.x == 0) {
     err = kOk;
     abort_flag = 0;
-    p.open_row[blockIdx.x] = -1;
     for (int i = 0; i < L::kRingK; ++i) mbar_init(full_k(i), kLoaders), mbar_init(empty_k(i), 1);
     for (int i = 0; i < L::kRingV; ++i) mbar_init(full_v(i), kLoaders), mbar_init(empty_v(i), 1);
     for (int i = 0; i < L::kQ; ++i) mbar_init(empty_q(i), 1);
@@ -345,6 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   Split sp;
   Walk<NB, SLOTS> at;
   const bool work = find_range<Walk<NB, SLOTS>, SLOTS, kWarps>(p, sp, at, blockIdx.x, &err);
+  if (threadIdx.x == 0) {
+    if (work) p.open_row[blockIdx.x] = -1;
+    if (blockIdx.x == 0) *p.active = sp.active;
+  }
   if (work) {
     // A role walks over its segments (the part of a unit in the CTA's range) and a segment's visits.
     int64_t here = sp.first(blockIdx.x);                  // flat index of the segment's first visit

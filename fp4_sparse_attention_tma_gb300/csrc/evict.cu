@@ -31,6 +31,7 @@ __device__ __forceinline__ bool bad_length(const EvictParams& p, int32_t n) {
 
 // Lengths, and the destination pages: each inside the pool and named once.  One CTA.
 __global__ void __launch_bounds__(kPrepThreads) evict_check_kernel(const __grid_constant__ EvictParams p) {
+  allow_launch_after();
   __shared__ uint32_t err;
   if (threadIdx.x == 0) err = kOk;
   const int32_t words = (p.dst_pages + 31) / 32;
@@ -60,6 +61,8 @@ __global__ void __launch_bounds__(kPrepThreads) evict_check_kernel(const __grid_
 // the counts do not depend on the order of the additions.  Bound by latency (the barriers
 // of the passes), not by the weights' bytes.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  allow_launch_after();
+  wait_for_launch_before();
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int32_t req = blockIdx.x / C;
@@ -221,6 +224,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
 // and, after an error, fills the outputs.  Bound by HBM: every kept byte read and written
 // once.
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_constant__ EvictParams p) {
+  wait_for_launch_before();
   const uint32_t status = *p.hdr_status;
   const int32_t used = (p.budget + kPage - 1) / kPage;
   const int64_t job = blockIdx.x;
@@ -286,18 +290,19 @@ cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   if ((e = cudaLaunchKernelEx(&cfg, evict_select_kernel, (const EvictParams)p)) != cudaSuccess) return e;
   const int64_t used = (p.budget + kPage - 1) / kPage;
   // a budget above every length moves nothing
   const int64_t jobs = p.budget >= width ? 1 : p.num_req * used * 2;
-  evict_copy_kernel<<<(unsigned)jobs, kCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(evict_copy_kernel, dim3((unsigned)jobs), dim3(kCopyThreads), 0, stream, p);
 }
 
 }  // namespace idxk

@@ -27,6 +27,32 @@ inline cudaError_t set_smem_once(Kernel kernel, int bytes, std::atomic<bool> (&d
   return err;
 }
 
+// Launches `kernel` so that it may start while the kernel before it on the stream still
+// runs; it has to wait for that kernel's end (wait_for_launch_before) before it touches
+// anything that the other reads or writes.
+template <typename... A, typename... B>
+inline cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                     B&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+#ifdef __CUDACC__
+// The device side: lets the kernel launched after this one start, and waits until the
+// kernel before this one has ended and its writes are visible.
+__device__ __forceinline__ void allow_launch_after() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 // One CTA waiting through the bounded mbarrier wait on a phase that its own
 // thread completes (never = false) or that nothing completes (never = true:
 // kErrTimeout is recorded in hdr after the wait limit).
