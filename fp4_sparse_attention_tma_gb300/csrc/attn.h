@@ -114,11 +114,16 @@ struct EvictParams {
   int32_t kv_heads, head_bytes;
   int32_t same_pool;                // the destination pages are pages of the source tensors
   int32_t slice_cap;                // keys of a CTA's slice that fit its shared memory
-  uint32_t* hdr_status;             // workspace: first error
-  uint32_t* dst_mark;               // workspace: one bit per destination page
+  int32_t mark_shared;              // the bitmap of the fresh pages fits shared memory
+  int32_t copy_rows;                // rows of a page that a CTA of the copy moves
+  uint32_t* part_status;            // workspace: [num_req + 1] first error of each cluster
+  uint32_t* dst_mark;               // workspace: [CTAs of a cluster] bitmaps, where shared memory is too small
   uint32_t* status_out;
 };
 
+// CTAs of a cluster, and whether the fresh pages' bitmap lies in shared memory.
+int evict_cluster(int64_t max_pages);
+bool evict_mark_shared(int64_t dst_pages);
 cudaError_t launch_evict(EvictParams p, cudaStream_t stream);
 
 }  // namespace idxk

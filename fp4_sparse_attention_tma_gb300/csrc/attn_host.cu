@@ -399,9 +399,11 @@ struct EvictCall {
   const idx_tensor_t *k_dst, *v_dst, *dst_table, *keep, *new_len, *new_table, *new_weight;
 };
 
-size_t evict_space(int64_t dst_pages, size_t* mark) {
-  *mark = 256;
-  return align_up(*mark + (size_t)(dst_pages + 31) / 32 * 4, 256);
+// Workspace: a status word per cluster, then the bitmaps (if they are not in shared memory).
+size_t evict_space(int64_t num_req, int64_t max_pages, int64_t dst_pages, size_t* mark) {
+  *mark = align_up((size_t)(num_req + 1) * 4, 256);
+  const size_t bitmap = evict_mark_shared(dst_pages) ? 0 : (size_t)((dst_pages + 31) / 32) * 4;
+  return *mark + align_up(bitmap * evict_cluster(max_pages), 256);
 }
 
 int run_evict(const EvictCall& c, const Space& space, cudaStream_t stream) {
@@ -423,7 +425,7 @@ int run_evict(const EvictCall& c, const Space& space, cudaStream_t stream) {
   }
   if (Hk < 1) return IDX_ERR_INVALID_ARGUMENT;
   if ((D != 64 && D != 128 && D != 256) || c.k->shape[1] != kPage) return IDX_ERR_UNSUPPORTED;
-  if (NP * kPage > INT32_MAX || DN * kPage > INT32_MAX || MP * kPage > INT32_MAX || Hk > 65536 || NR > INT32_MAX / 8)
+  if (NP * kPage > INT32_MAX || DN * kPage > INT32_MAX || MP * kPage > INT32_MAX || Hk > 65536 || NR >= INT32_MAX / 8)
     return IDX_ERR_OVERFLOW;
   if (c.budget < 1 || c.first < 0 || c.last < 0 || (int64_t)c.first + c.last > c.budget)
     return IDX_ERR_INVALID_ARGUMENT;
@@ -435,7 +437,7 @@ int run_evict(const EvictCall& c, const Space& space, cudaStream_t stream) {
     return IDX_ERR_INVALID_ARGUMENT;
   if (NR > 0 && (MP < 1 || NP < 1 || DN < 1)) return IDX_ERR_INVALID_ARGUMENT;
   const int64_t used = (c.budget + kPage - 1) / kPage;
-  if (NR * used > INT32_MAX / 2) return IDX_ERR_OVERFLOW;
+  if (NR * used > INT32_MAX / 32) return IDX_ERR_OVERFLOW;   // CTAs of the copy
   // the fresh pages are pages of the same tensors, or of others that lie apart from them
   const bool same = NR > 0 && same_layout(c.k, c.k_dst) && same_layout(c.v, c.v_dst);
   if (!no_overlap(c.k_dst) || !no_overlap(c.v_dst)) return IDX_ERR_INVALID_ARGUMENT;
@@ -477,10 +479,10 @@ int run_evict(const EvictCall& c, const Space& space, cudaStream_t stream) {
   p.kv_heads = (int32_t)Hk, p.head_bytes = (int32_t)D * 2;
   p.same_pool = same ? 1 : 0;
   size_t mark;
-  const size_t bytes = evict_space(DN, &mark);
+  const size_t bytes = evict_space(NR, MP, DN, &mark);
   return with_space(space, bytes, m, stream, [&](char* base, uint32_t* status) -> cudaError_t {
     if (NR == 0) return cudaMemsetAsync(status, 0, sizeof(uint32_t), stream);
-    p.hdr_status = (uint32_t*)base;
+    p.part_status = (uint32_t*)base;
     p.dst_mark = (uint32_t*)(base + mark);
     p.status_out = status;
     return launch_evict(p, stream);
@@ -569,7 +571,7 @@ int idx_cache_evict_scratch_bytes(int32_t num_req, int32_t max_pages, int32_t ds
   if (!bytes || num_req < 0 || max_pages < 0 || dst_pages < 0 || budget < 1 || device < 0)
     return IDX_ERR_INVALID_ARGUMENT;
   size_t mark;
-  *bytes = evict_space(dst_pages, &mark);
+  *bytes = evict_space(num_req, max_pages, dst_pages, &mark);
   return IDX_OK;
 }
 

@@ -4,9 +4,8 @@
 // -0, NaN below every number, lower position first).  What is kept moves, in order of
 // position, into fresh pages.
 //
-// Three kernels: the check of the destination pages, the selection (one cluster per
-// request), and the copy, which waits for all checks, so that a call that fails has moved
-// nothing.
+// Two kernels: the selection (one cluster per request, and one that checks the fresh pages
+// meanwhile), and the copy, which sees what all of them found before it moves anything.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -17,88 +16,102 @@
 namespace idxk {
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kPrepThreads = 1024;
 constexpr int kSelThreads = 1024;
 constexpr int kCopyThreads = 256;
+constexpr int kBins = 2048;          // digits of 11, 11 and 10 bits of the key
+constexpr int64_t kSliceKeys = 48 * 1024;          // keys of a CTA's slice that fit its shared memory
+constexpr int64_t kMarkBytes = kSliceKeys * 4;     // and the bitmap of the destination pages
 
-__device__ __forceinline__ void raise(uint32_t* status, uint32_t code) { atomicCAS(status, (uint32_t)kOk, code); }
+// First error of a cluster: the CTAs' own words are gathered at its end.
+__device__ __forceinline__ void note(uint32_t* err, uint32_t code) { atomicMax(err, code); }
 
 __device__ __forceinline__ bool bad_length(const EvictParams& p, int32_t n) {
   return n < 0 || (int64_t)n > (int64_t)p.max_pages * kPage;
 }
 
-// Lengths, and the destination pages: each inside the pool and named once.  One CTA.
-__global__ void __launch_bounds__(kPrepThreads) evict_check_kernel(const __grid_constant__ EvictParams p) {
-  allow_launch_after();
-  __shared__ uint32_t err;
-  if (threadIdx.x == 0) err = kOk;
+// The check of the fresh pages, by the cluster after the requests': each inside the pool and
+// named once and, where the pool is the cache itself, under no request's positions.  Every CTA
+// marks all fresh pages (in shared memory, or in its own part of the workspace where they do
+// not fit) and looks at its share of the pages in use.
+__device__ void check_fresh(const EvictParams& p, int C, int rank, uint32_t* shared, uint32_t* err) {
+  const int tid = threadIdx.x;
   const int32_t words = (p.dst_pages + 31) / 32;
-  for (int32_t i = threadIdx.x; i < words; i += kPrepThreads) p.dst_mark[i] = 0;
+  uint32_t* mark = p.mark_shared ? shared : p.dst_mark + (int64_t)rank * words;
+  for (int32_t i = tid; i < words; i += kSelThreads) mark[i] = 0;
   __syncthreads();
   const int32_t used = (p.budget + kPage - 1) / kPage;   // pages of a request that was cut
-  for (int32_t r = threadIdx.x; r < p.num_req; r += kPrepThreads)
-    if (bad_length(p, p.seq_len[r])) atomicMax(&err, (uint32_t)kErrInvalidMetadata);
-  for (int64_t i = threadIdx.x; i < (int64_t)p.num_req * used; i += kPrepThreads) {
+#pragma unroll 4
+  for (int64_t i = tid; i < (int64_t)p.num_req * used; i += kSelThreads) {
     const int32_t r = (int32_t)(i / used), j = (int32_t)(i - (int64_t)r * used);
     const int32_t n = p.seq_len[r];
     if (n <= p.budget || bad_length(p, n)) continue;
     const int32_t page = p.dst_table[(int64_t)r * p.dst_width + j];
-    if (page < 0 || page >= p.dst_pages ||
-        (atomicOr(&p.dst_mark[page / 32], 1u << (page % 32)) >> (page % 32) & 1u))
-      atomicMax(&err, (uint32_t)kErrInvalidPage);
+    if (page < 0 || page >= p.dst_pages || (atomicOr(&mark[page / 32], 1u << (page % 32)) >> (page % 32) & 1u))
+      note(err, kErrInvalidPage);
   }
   __syncthreads();
-  if (threadIdx.x == 0) *p.hdr_status = err;
+  if (!p.same_pool) return;
+#pragma unroll 4
+  for (int64_t i = (int64_t)rank * kSelThreads + tid; i < (int64_t)p.num_req * p.max_pages; i += (int64_t)C * kSelThreads) {
+    const int32_t r = (int32_t)(i / p.max_pages), j = (int32_t)(i - (int64_t)r * p.max_pages);
+    const int32_t n = p.seq_len[r], page = p.page_table[i];
+    if (bad_length(p, n) || j >= (n + kPage - 1) / kPage || page < 0 || page >= p.num_pages) continue;
+    if (mark[page / 32] >> (page % 32) & 1u) note(err, kErrInvalidPage);
+  }
 }
 
 // The selection.  Every CTA of a request's cluster holds a slice of its positions (their
-// keys in shared memory where they fit); four passes over 8 bits of the key each count the
-// slice's keys by digit, add the counts up over the cluster and keep the digit that holds
-// the last key to be kept.  Then every warp counts what it keeps of its part of the slice,
-// the counts are added up in order, and the positions go to their ranks.  Deterministic:
-// the counts do not depend on the order of the additions.  Bound by latency (the barriers
-// of the passes), not by the weights' bytes.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  allow_launch_after();
-  wait_for_launch_before();
-  cg::cluster_group cluster = cg::this_cluster();
+// keys in shared memory where they fit); three passes over 11, 11 and 10 bits of the key each
+// count the slice's keys by digit, add the counts up over the cluster and keep the digit that
+// holds the last key to be kept.  (Of the first 11 bits 9 are sign and exponent: fewer bits
+// would send most keys to a handful of counters.)  Then every warp counts what it keeps of its
+// part of the slice, the counts are added up in order, and the positions go to their ranks.
+// Deterministic: the counts do not depend on the order of the additions.  Bound by latency
+// (the barriers of the passes), not by the weights' bytes.
+__device__ void select(const EvictParams& p, cooperative_groups::cluster_group& cluster, int32_t req, uint32_t* keys,
+                       uint32_t* err) {
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int32_t req = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kSelThreads / 32;
-  extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[2][256];   // counts of a pass, read by the cluster
-  __shared__ uint32_t total[256];
-  __shared__ uint32_t picked[2];      // digit, keys above it
+  __shared__ __align__(16) uint32_t hist[2][kBins];   // counts of a pass, read by the cluster two at a time
+  __shared__ uint32_t picked[2];        // digit, keys above it
   __shared__ uint32_t warp_gt[kWarps], warp_eq[kWarps];
-  __shared__ uint32_t cta_cnt[2];     // this CTA's kept above the threshold, and at it
+  __shared__ uint32_t cta_cnt[2];       // this CTA's kept above the threshold, and at it
 
   const int64_t width = (int64_t)p.max_pages * kPage;
   int32_t n = p.seq_len[req];
-  if (bad_length(p, n)) n = 0;        // an error: nothing is written that stays
+  if (bad_length(p, n)) {
+    if (tid == 0) note(err, kErrInvalidMetadata);
+    n = 0;
+  }
   const bool cut = n > p.budget;
   const int32_t new_len = cut ? p.budget : n;
   const int64_t gtid = (int64_t)rank * kSelThreads + tid, gthreads = (int64_t)C * kSelThreads;
+  const float* weight = p.weight + (int64_t)req * width;
+  float* new_weight = p.new_weight + (int64_t)req * width;
+  int32_t* keep = p.keep + (int64_t)req * p.budget;
+
+  // positions [lo, hi) compete for `want` places
+  const int32_t lo = p.keep_first, hi = n - p.keep_last;
+  uint32_t want = (uint32_t)(p.budget - p.keep_first - p.keep_last);
+  const int32_t slice = ((n + C - 1) / C + 31) / 32 * 32;
+  const int32_t s0 = min((int64_t)n, (int64_t)rank * slice), s1 = min((int64_t)n, (int64_t)s0 + slice);
+  const bool held = slice <= p.slice_cap;
+  if (cut && held) {
+#pragma unroll 8
+    for (int32_t i = s0 + tid; i < s1; i += kSelThreads) keys[i - s0] = score_key(weight[i]);
+  }
+  auto key_at = [&](int32_t i) { return held ? keys[i - s0] : score_key(weight[i]); };
 
   // the pages of the request, and its new table
   const int32_t pages = (n + kPage - 1) / kPage;
   for (int64_t i = gtid; i < p.max_pages; i += gthreads) {
     const int32_t page = p.page_table[(int64_t)req * p.max_pages + i];
-    if (i < pages) {
-      if (page < 0 || page >= p.num_pages)
-        raise(p.hdr_status, kErrInvalidPage);
-      else if (p.same_pool && (p.dst_mark[page / 32] >> (page % 32) & 1u))
-        raise(p.hdr_status, kErrInvalidPage);
-    }
+    if (i < pages && (page < 0 || page >= p.num_pages)) note(err, kErrInvalidPage);
     p.new_table[(int64_t)req * p.max_pages + i] =
         !cut ? page : i < p.dst_width ? p.dst_table[(int64_t)req * p.dst_width + i] : -1;
   }
   if (rank == 0 && tid == 0) p.new_len[req] = new_len;
-  const float* weight = p.weight + (int64_t)req * width;
-  float* new_weight = p.new_weight + (int64_t)req * width;
-  int32_t* keep = p.keep + (int64_t)req * p.budget;
   for (int64_t i = new_len + gtid; i < width; i += gthreads) new_weight[i] = 0.f;
   for (int64_t i = new_len + gtid; i < p.budget; i += gthreads) keep[i] = -1;
   if (!cut) {
@@ -109,53 +122,43 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     return;   // the whole cluster
   }
 
-  // positions [lo, hi) compete for `want` places
-  const int32_t lo = p.keep_first, hi = n - p.keep_last;
-  uint32_t want = (uint32_t)(p.budget - p.keep_first - p.keep_last);
-  const int32_t slice = ((n + C - 1) / C + 31) / 32 * 32;
-  const int32_t s0 = min((int64_t)n, (int64_t)rank * slice), s1 = min((int64_t)n, (int64_t)s0 + slice);
-  const bool held = slice <= p.slice_cap;
-  if (held)
-    for (int32_t i = s0 + tid; i < s1; i += kSelThreads) keys[i - s0] = score_key(weight[i]);
-  auto key_at = [&](int32_t i) { return held ? keys[i - s0] : score_key(weight[i]); };
-
   // the threshold: of the competing keys, `want` are kept, all above `thr` and `want` (as it
   // is then) of those equal to it.  Nothing competes for no place: then thr stays the top.
   uint32_t thr = 0xFFFFFFFFu;
   if (want > 0) {
     uint32_t prefix = 0;
-    for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass, buf = pass & 1;
-      if (tid < 256) hist[buf][tid] = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, buf = pass & 1;
+      const uint32_t digits = pass == 2 ? 1024u : (uint32_t)kBins;
+      const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFFFFFFFu << 21 : 0xFFFFFFFFu << 10;
+      for (int i = tid; i < kBins; i += kSelThreads) hist[buf][i] = 0;
       __syncthreads();
-      const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
+#pragma unroll 4
       for (int32_t i = max(s0, lo) + tid; i < min(s1, hi); i += kSelThreads) {
         const uint32_t k = key_at(i);
-        if ((k & mask) == prefix) atomicAdd(&hist[buf][k >> shift & 255u], 1u);
+        if ((k & mask) == prefix) atomicAdd(&hist[buf][k >> shift & (digits - 1)], 1u);
       }
       cluster.sync();
-      if (tid < 256) {
-        uint32_t t = 0;
-        for (int i = 0; i < C; ++i) t += cluster.map_shared_rank(&hist[buf][0], i)[tid];
-        total[tid] = t;
+      // thread t: the digits 2047 - 2t and 2046 - 2t of the whole cluster (from the top); the counts
+      // above them by a scan over the CTA
+      uint32_t hi_n = 0, lo_n = 0;
+      for (int i = 0; i < C; ++i) {
+        const uint2 two = ((const uint2*)cluster.map_shared_rank(&hist[buf][0], i))[kBins / 2 - 1 - tid];
+        lo_n += two.x, hi_n += two.y;
       }
+      uint32_t inc = hi_n + lo_n;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) warp_gt[warp] = inc;
       __syncthreads();
-      if (warp == 0) {
-        // lane l: digits 255 - 8l .. 248 - 8l, from the top
-        uint32_t sum = 0;
-        for (int i = 0; i < 8; ++i) sum += total[255 - 8 * lane - i];
-        uint32_t inc = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t x = __shfl_up_sync(~0u, inc, o);
-          if (lane >= o) inc += x;
-        }
-        uint32_t above = inc - sum;
-        if (above < want && inc >= want) {
-          int d = 255 - 8 * lane;
-          while (above + total[d] < want) above += total[d--];
-          picked[0] = (uint32_t)d;
-          picked[1] = above;
-        }
+      uint32_t above = inc - hi_n - lo_n;
+      for (int i = 0; i < warp; ++i) above += warp_gt[i];
+      if (above < want && above + hi_n + lo_n >= want) {
+        const bool low = above + hi_n < want;
+        picked[0] = kBins - 1 - 2 * tid - (low ? 1 : 0);
+        picked[1] = above + (low ? hi_n : 0);
       }
       __syncthreads();
       prefix |= picked[0] << shift;
@@ -182,18 +185,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     }
   };
   uint32_t n_gt = 0, n_eq = 0;
+#pragma unroll 4
   for (int32_t i0 = w0; i0 < w1; i0 += 32) {
     bool gt, eq;
     classify(i0 + lane, gt, eq);
     n_gt += __popc(__ballot_sync(~0u, gt));
     n_eq += __popc(__ballot_sync(~0u, eq));
   }
+  __syncthreads();   // warp_gt is free
   if (lane == 0) warp_gt[warp] = n_gt, warp_eq[warp] = n_eq;
   __syncthreads();
-  if (tid == 0) {
-    uint32_t a = 0, b = 0;
-    for (int i = 0; i < kWarps; ++i) a += warp_gt[i], b += warp_eq[i];
-    cta_cnt[0] = a, cta_cnt[1] = b;
+  if (warp == 0) {
+    const uint32_t a = __reduce_add_sync(~0u, warp_gt[lane]), b = __reduce_add_sync(~0u, warp_eq[lane]);
+    if (lane == 0) cta_cnt[0] = a, cta_cnt[1] = b;
   }
   cluster.sync();
   uint32_t gt0 = 0, eq0 = 0;   // before this warp's part
@@ -201,7 +205,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     const uint32_t* c = cluster.map_shared_rank(&cta_cnt[0], i);
     gt0 += c[0], eq0 += c[1];
   }
-  for (int i = 0; i < warp; ++i) gt0 += warp_gt[i], eq0 += warp_eq[i];
+  gt0 += __reduce_add_sync(~0u, lane < warp ? warp_gt[lane] : 0u);
+  eq0 += __reduce_add_sync(~0u, lane < warp ? warp_eq[lane] : 0u);
+#pragma unroll 4
   for (int32_t i0 = w0; i0 < w1; i0 += 32) {
     bool gt, eq;
     classify(i0 + lane, gt, eq);
@@ -216,16 +222,46 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     gt0 += __popc(bg);
     eq0 += __popc(be);
   }
-  cluster.sync();   // no CTA leaves while another reads its counts
 }
 
-// Moves the kept keys and values, 16 bytes a thread at a time, one destination page of
-// keys or of values per CTA; the last kernel of the call, so it also publishes the status
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  allow_launch_after();
+  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int32_t req = blockIdx.x / C;
+  extern __shared__ __align__(16) uint32_t room[];
+  __shared__ uint32_t err;
+  if (threadIdx.x == 0) err = kOk;
+  __syncthreads();
+  if (req < p.num_req)
+    select(p, cluster, req, room, &err);
+  else
+    check_fresh(p, C, rank, room, &err);
+  cluster.sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    uint32_t all = kOk;
+    for (int i = 0; i < C; ++i) all = max(all, *cluster.map_shared_rank(&err, i));
+    p.part_status[req] = all;
+  }
+  cluster.sync();   // no CTA leaves while another reads its words
+}
+
+// Moves the kept keys and values, 16 bytes a thread at a time, some rows of a destination page
+// of keys or of values per CTA; the last kernel of the call, so it also publishes the status
 // and, after an error, fills the outputs.  Bound by HBM: every kept byte read and written
 // once.
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_constant__ EvictParams p) {
   wait_for_launch_before();
-  const uint32_t status = *p.hdr_status;
+  uint32_t status = kOk;
+  {
+    __shared__ uint32_t all;
+    if (threadIdx.x == 0) all = kOk;
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i <= p.num_req; i += kCopyThreads) status = max(status, p.part_status[i]);
+    if (status != kOk) atomicMax(&all, status);
+    __syncthreads();
+    status = all;
+  }
   const int32_t used = (p.budget + kPage - 1) / kPage;
   const int64_t job = blockIdx.x;
   if (job == 0 && threadIdx.x == 0) *p.status_out = status;
@@ -240,30 +276,36 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_c
     return;
   }
   const bool values = job & 1;
-  const int64_t at = job >> 1;
+  const int32_t per_page = kPage / p.copy_rows;
+  const int64_t at = (job >> 1) / per_page;
+  const int32_t part = (int32_t)((job >> 1) - at * per_page);
   const int32_t req = (int32_t)(at / used), j = (int32_t)(at - (int64_t)req * used);
   if (req >= p.num_req || p.seq_len[req] <= p.budget) return;
   __shared__ int64_t from[kPage];
-  const int32_t rows = min(kPage, p.budget - j * kPage);
+  const int32_t first = j * kPage + part * p.copy_rows;   // rank of the CTA's first row
+  const int32_t rows = min(p.copy_rows, p.budget - first);
+  if (rows <= 0) return;
   if ((int)threadIdx.x < rows) {
-    const int32_t pos = p.keep[(int64_t)req * p.budget + j * kPage + threadIdx.x];
+    const int32_t pos = p.keep[(int64_t)req * p.budget + first + threadIdx.x];
     const int64_t page = p.page_table[(int64_t)req * p.max_pages + pos / kPage];
     from[threadIdx.x] = page * (values ? p.v_page : p.k_page) + pos % kPage * (values ? p.v_slot : p.k_slot);
   }
   __syncthreads();
   const char* src = (const char*)(values ? p.v : p.k);
   const int64_t page = p.dst_table[(int64_t)req * p.dst_width + j];
-  char* dst = (char*)(values ? p.v_dst : p.k_dst) + page * (values ? p.vd_page : p.kd_page);
   const int64_t sh = values ? p.v_head : p.k_head, dh = values ? p.vd_head : p.kd_head;
   const int64_t ds = values ? p.vd_slot : p.kd_slot;
-  const int32_t pieces = p.head_bytes / 16;   // a power of two
-  const int32_t n = rows * p.kv_heads * pieces;
+  char* dst = (char*)(values ? p.v_dst : p.k_dst) + page * (values ? p.vd_page : p.kd_page) + part * p.copy_rows * ds;
+  const uint32_t pieces = (uint32_t)p.head_bytes / 16;   // a power of two
+  const uint32_t shift = 31 - __clz(pieces);
+  const uint32_t n = (uint32_t)rows * p.kv_heads * pieces;
   // the faster index over pieces and then over what lies closer together in the source
   const bool slots_inner = sh > (values ? p.v_slot : p.k_slot);
-#pragma unroll 4
-  for (int32_t i = threadIdx.x; i < n; i += kCopyThreads) {
-    const int32_t x = i % pieces, y = i / pieces;
-    const int32_t h = slots_inner ? y / rows : y % p.kv_heads, r = slots_inner ? y % rows : y / p.kv_heads;
+  const uint32_t inner = slots_inner ? rows : p.kv_heads;
+#pragma unroll 8
+  for (uint32_t i = threadIdx.x; i < n; i += kCopyThreads) {
+    const uint32_t x = i & (pieces - 1), y = i >> shift, a = y / inner, b = y - a * inner;
+    const uint32_t h = slots_inner ? a : b, r = slots_inner ? b : a;
     const uint4 t = __ldcs((const uint4*)(src + from[r] + h * sh + x * 16));
     __stcs((uint4*)(dst + r * ds + h * dh + x * 16), t);
   }
@@ -271,37 +313,45 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_c
 
 }  // namespace
 
-cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
-  // one CTA of a cluster for 8192 positions of the widest request, at most 8
+int evict_cluster(int64_t max_pages) {
+  // one CTA for 8192 positions of the widest request, at most 8
   int C = 1;
+  while (C < 8 && (int64_t)C * 8192 < max_pages * kPage) C *= 2;
+  return C;
+}
+
+bool evict_mark_shared(int64_t dst_pages) { return (dst_pages + 31) / 32 * 4 <= kMarkBytes; }
+
+cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
+  const int C = evict_cluster(p.max_pages);
   const int64_t width = (int64_t)p.max_pages * kPage;
-  while (C < 8 && (int64_t)C * 8192 < width) C *= 2;
   const int64_t slice = ((width + C - 1) / C + 31) / 32 * 32;
-  constexpr int64_t kMost = 48 * 1024;   // keys of a slice in shared memory
-  p.slice_cap = (int32_t)(slice < kMost ? slice : kMost);
-  const int smem = p.slice_cap * 4;
+  p.slice_cap = (int32_t)(slice < kSliceKeys ? slice : kSliceKeys);
+  p.mark_shared = evict_mark_shared(p.dst_pages);
+  int smem = p.slice_cap * 4;
+  const int mark = (int)((p.dst_pages + 31) / 32 * 4);
+  if (p.mark_shared && mark > smem) smem = mark;
   static std::atomic<bool> done[64];
-  cudaError_t e = set_smem_once(evict_select_kernel, (int)kMost * 4, done);
+  cudaError_t e = set_smem_once(evict_select_kernel, (int)kMarkBytes, done);
   if (e != cudaSuccess) return e;
-  evict_check_kernel<<<1, kPrepThreads, 0, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.num_req * C));
+  cfg.gridDim = dim3((unsigned)((p.num_req + 1) * C));
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, evict_select_kernel, (const EvictParams)p)) != cudaSuccess) return e;
+  // a CTA of the copy moves up to 32 KB: short rows a page at a time, long ones some of a page's
+  p.copy_rows = kPage;
+  while (p.copy_rows > 4 && (int64_t)p.copy_rows * p.kv_heads * p.head_bytes > 32 * 1024) p.copy_rows /= 2;
   const int64_t used = (p.budget + kPage - 1) / kPage;
   // a budget above every length moves nothing
-  const int64_t jobs = p.budget >= width ? 1 : p.num_req * used * 2;
+  const int64_t jobs = p.budget >= width ? 1 : p.num_req * used * 2 * (kPage / p.copy_rows);
   return launch_overlapped(evict_copy_kernel, dim3((unsigned)jobs), dim3(kCopyThreads), 0, stream, p);
 }
 

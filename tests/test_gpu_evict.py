@@ -233,3 +233,36 @@ def test_evict_refused_arguments():
     refused(out_weight=c.weight)
     refused(v_cache=c.v.half())
     refused(k_dst=c.k_to[:, :1].expand(-1, PAGE, -1, -1))
+
+
+def test_evict_many_requests():
+    """More requests than a wave of clusters, short and long."""
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.integers(0, 400, 700)]
+    c = Case(lens, 100, 2, 10, hk=1, pool="same")
+    assert c.run() == 0
+    c.check()
+
+
+def test_evict_large_pool():
+    """A pool whose bitmap of fresh pages does not fit shared memory."""
+    import torch
+    import fp4_sparse_attention_tma_gb300 as m
+    c = Case([500, 100, 300], 130, hk=1)
+    pages = 1_700_000
+    kd = torch.zeros(pages, PAGE, 1, 64, dtype=torch.bfloat16, device="cuda")
+    vd = torch.zeros_like(kd)
+    far = torch.arange(c.fresh.numel(), device="cuda", dtype=torch.int32).view_as(c.fresh) * 7 + (pages - 7 * c.fresh.numel())
+    args = list(c.args())
+    args[8], args[9], args[10] = kd, vd, far
+    assert m.idx_cache_evict(*args) == 0
+    torch.cuda.synchronize()
+    for i in (0, 2):
+        kept = torch.tensor(A.keep_positions(c.h_weight[i], c.lens[i], 130, 0, 0))
+        sp = torch.from_numpy(c.h_table[i])[kept // PAGE].long().cuda()
+        to = torch.arange(130, device="cuda")
+        got = kd[far[i][to // PAGE].long(), to % PAGE]
+        assert torch.equal(got.view(torch.int16), c.k[sp, (kept % PAGE).cuda()].view(torch.int16))
+    args[10] = far.clone()
+    args[10][0, 1] = far[2, 0]           # named by two requests
+    assert m.idx_cache_evict(*args, raise_on_error=False) == INVALID_PAGE
