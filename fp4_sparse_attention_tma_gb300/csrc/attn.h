@@ -122,8 +122,8 @@ struct EvictParams {
 };
 
 // CTAs of a cluster, and whether the fresh pages' bitmap lies in shared memory.
-int evict_cluster(int64_t max_pages);
+int evict_cluster(int64_t num_req, int64_t max_pages, int sm_count);
 bool evict_mark_shared(int64_t dst_pages);
-cudaError_t launch_evict(EvictParams p, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams p, int sm_count, cudaStream_t stream);
 
 }  // namespace idxk

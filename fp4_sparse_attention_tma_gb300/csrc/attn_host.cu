@@ -17,6 +17,10 @@ using namespace idxk;
 
 namespace {
 
+// Positions of a request, at most: the kernels step past a range's end by less than the rest
+// of an int32.
+constexpr int64_t kMostPositions = INT32_MAX - 65536;
+
 // Validates a 16-bit tensor with free strides: type, rank, 16-byte aligned base, last
 // dimension contiguous, other strides non-negative multiples of 8 elements whose offsets
 // stay within 63 bits.
@@ -286,7 +290,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   if (c.slots) {
     if ((st = check_tensor(c.slots, IDX_I32, 2))) return st;
     if (c.slots->shape[0] != R || c.slots->shape[1] < 1) return IDX_ERR_INVALID_ARGUMENT;
-    if (c.slots->shape[1] > INT32_MAX - kPage) return IDX_ERR_OVERFLOW;
+    if (c.slots->shape[1] > kMostPositions) return IDX_ERR_OVERFLOW;
   } else {
     if ((st = check_tensor(c.page_table, IDX_I32, 2)) || (st = check_tensor(c.row_req, IDX_I32, 1)) ||
         (st = check_tensor(c.row_start, IDX_I32, 1)) || (st = check_tensor(c.row_end, IDX_I32, 1)))
@@ -294,7 +298,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
     NR = c.page_table->shape[0], MP = c.page_table->shape[1];
     if (c.row_req->shape[0] != R || c.row_start->shape[0] != R || c.row_end->shape[0] != R)
       return IDX_ERR_INVALID_ARGUMENT;
-    if (MP * (int64_t)kPage > INT32_MAX || NR > INT32_MAX) return IDX_ERR_OVERFLOW;
+    if (MP * (int64_t)kPage > kMostPositions || NR > INT32_MAX) return IDX_ERR_OVERFLOW;
     if (R > 0 && (NR < 1 || MP < 1)) return IDX_ERR_INVALID_ARGUMENT;
   }
   if (c.weight_in && !c.weight_out) return IDX_ERR_INVALID_ARGUMENT;
@@ -400,10 +404,10 @@ struct EvictCall {
 };
 
 // Workspace: a status word per cluster, then the bitmaps (if they are not in shared memory).
-size_t evict_space(int64_t num_req, int64_t max_pages, int64_t dst_pages, size_t* mark) {
+size_t evict_space(int64_t num_req, int64_t dst_pages, size_t* mark) {
   *mark = align_up((size_t)(num_req + 1) * 4, 256);
   const size_t bitmap = evict_mark_shared(dst_pages) ? 0 : (size_t)((dst_pages + 31) / 32) * 4;
-  return *mark + align_up(bitmap * evict_cluster(max_pages), 256);
+  return *mark + align_up(bitmap * 8, 256);   // a cluster has at most 8 CTAs
 }
 
 int run_evict(const EvictCall& c, const Space& space, cudaStream_t stream) {
@@ -425,7 +429,7 @@ int run_evict(const EvictCall& c, const Space& space, cudaStream_t stream) {
   }
   if (Hk < 1) return IDX_ERR_INVALID_ARGUMENT;
   if ((D != 64 && D != 128 && D != 256) || c.k->shape[1] != kPage) return IDX_ERR_UNSUPPORTED;
-  if (NP * kPage > INT32_MAX || DN * kPage > INT32_MAX || MP * kPage > INT32_MAX || Hk > 65536 || NR >= INT32_MAX / 8)
+  if (NP * kPage > INT32_MAX || DN * kPage > INT32_MAX || MP * kPage > kMostPositions || Hk > 65536 || NR >= INT32_MAX / 8)
     return IDX_ERR_OVERFLOW;
   if (c.budget < 1 || c.first < 0 || c.last < 0 || (int64_t)c.first + c.last > c.budget)
     return IDX_ERR_INVALID_ARGUMENT;
@@ -479,13 +483,13 @@ int run_evict(const EvictCall& c, const Space& space, cudaStream_t stream) {
   p.kv_heads = (int32_t)Hk, p.head_bytes = (int32_t)D * 2;
   p.same_pool = same ? 1 : 0;
   size_t mark;
-  const size_t bytes = evict_space(NR, MP, DN, &mark);
+  const size_t bytes = evict_space(NR, DN, &mark);
   return with_space(space, bytes, m, stream, [&](char* base, uint32_t* status) -> cudaError_t {
     if (NR == 0) return cudaMemsetAsync(status, 0, sizeof(uint32_t), stream);
     p.part_status = (uint32_t*)base;
     p.dst_mark = (uint32_t*)(base + mark);
     p.status_out = status;
-    return launch_evict(p, stream);
+    return launch_evict(p, m.sm, stream);
   });
 }
 
@@ -571,7 +575,7 @@ int idx_cache_evict_scratch_bytes(int32_t num_req, int32_t max_pages, int32_t ds
   if (!bytes || num_req < 0 || max_pages < 0 || dst_pages < 0 || budget < 1 || device < 0)
     return IDX_ERR_INVALID_ARGUMENT;
   size_t mark;
-  *bytes = evict_space(num_req, max_pages, dst_pages, &mark);
+  *bytes = evict_space(num_req, dst_pages, &mark);
   return IDX_OK;
 }
 

@@ -60,33 +60,49 @@ __device__ void check_fresh(const EvictParams& p, int C, int rank, uint32_t* sha
   }
 }
 
+// Barrier of the cluster (of the CTA, where that is all of it).
+__device__ __forceinline__ void sync_all(cooperative_groups::cluster_group& cluster, int C) {
+  if (C == 1)
+    __syncthreads();
+  else
+    cluster.sync();
+}
+
 // The selection.  Every CTA of a request's cluster holds a slice of its positions (their
-// keys in shared memory where they fit); three passes over 11, 11 and 10 bits of the key each
-// count the slice's keys by digit, add the counts up over the cluster and keep the digit that
-// holds the last key to be kept.  (Of the first 11 bits 9 are sign and exponent: fewer bits
-// would send most keys to a handful of counters.)  Then every warp counts what it keeps of its
-// part of the slice, the counts are added up in order, and the positions go to their ranks.
+// weights in shared memory where they fit); three passes over 11, 11 and 10 bits of the key
+// each count the slice's keys by digit, find in the whole cluster's counts (first by groups of
+// 64 digits, then in one group) the digit that holds the last key to be kept, and go on with
+// the keys of that digit.  (Of the first 11 bits 9 are sign and exponent: fewer bits would send
+// most keys to a handful of counters.)  Then every warp counts what it keeps of its part of the
+// slice, the counts are added up in order, and the positions go to their ranks.
 // Deterministic: the counts do not depend on the order of the additions.  Bound by latency
-// (the barriers of the passes), not by the weights' bytes.
-__device__ void select(const EvictParams& p, cooperative_groups::cluster_group& cluster, int32_t req, uint32_t* keys,
+// (about 2 us a pass, most of it barriers and reads of the other CTAs' counts), not by the
+// weights' bytes.
+__device__ void select(const EvictParams& p, cooperative_groups::cluster_group& cluster, int32_t req, uint32_t* bits,
                        uint32_t* err) {
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kSelThreads / 32;
+  static_assert(kWarps == 32 && kBins == 64 * 32, "one group of 64 digits per warp");
   __shared__ __align__(16) uint32_t hist[2][kBins];   // counts of a pass, read by the cluster two at a time
+  __shared__ uint32_t group[2][32];     // counts of 64 digits each
   __shared__ uint32_t picked[2];        // digit, keys above it
   __shared__ uint32_t warp_gt[kWarps], warp_eq[kWarps];
   __shared__ uint32_t cta_cnt[2];       // this CTA's kept above the threshold, and at it
 
   const int64_t width = (int64_t)p.max_pages * kPage;
   int32_t n = p.seq_len[req];
+  // this thread's entry of the two page tables (most requests have no more than the cluster has threads)
+  const int32_t g = rank * kSelThreads + tid, all_threads = C * kSelThreads;
+  const int32_t* table = p.page_table + (int64_t)req * p.max_pages;
+  const int32_t* fresh = p.dst_table + (int64_t)req * p.dst_width;
+  int32_t page = g < p.max_pages ? table[g] : -1, fresh_page = g < p.dst_width ? fresh[g] : -1;
   if (bad_length(p, n)) {
     if (tid == 0) note(err, kErrInvalidMetadata);
     n = 0;
   }
   const bool cut = n > p.budget;
   const int32_t new_len = cut ? p.budget : n;
-  const int64_t gtid = (int64_t)rank * kSelThreads + tid, gthreads = (int64_t)C * kSelThreads;
   const float* weight = p.weight + (int64_t)req * width;
   float* new_weight = p.new_weight + (int64_t)req * width;
   int32_t* keep = p.keep + (int64_t)req * p.budget;
@@ -99,28 +115,29 @@ __device__ void select(const EvictParams& p, cooperative_groups::cluster_group& 
   const bool held = slice <= p.slice_cap;
   if (cut && held) {
 #pragma unroll 8
-    for (int32_t i = s0 + tid; i < s1; i += kSelThreads) keys[i - s0] = score_key(weight[i]);
+    for (int32_t i = s0 + tid; i < s1; i += kSelThreads) bits[i - s0] = __float_as_uint(weight[i]);
   }
-  auto key_at = [&](int32_t i) { return held ? keys[i - s0] : score_key(weight[i]); };
+  auto weight_at = [&](int32_t i) { return held ? __uint_as_float(bits[i - s0]) : weight[i]; };
+  for (int i = tid; i < 2 * kBins; i += kSelThreads) hist[0][i] = 0;
 
-  // the pages of the request, and its new table
+  // the pages of the request, its new table, and what lies behind the kept positions
   const int32_t pages = (n + kPage - 1) / kPage;
-  for (int64_t i = gtid; i < p.max_pages; i += gthreads) {
-    const int32_t page = p.page_table[(int64_t)req * p.max_pages + i];
+  for (int32_t i = g; i < p.max_pages; i += all_threads) {
+    if (i != g) page = table[i], fresh_page = i < p.dst_width ? fresh[i] : -1;
     if (i < pages && (page < 0 || page >= p.num_pages)) note(err, kErrInvalidPage);
-    p.new_table[(int64_t)req * p.max_pages + i] =
-        !cut ? page : i < p.dst_width ? p.dst_table[(int64_t)req * p.dst_width + i] : -1;
+    p.new_table[(int64_t)req * p.max_pages + i] = cut ? fresh_page : page;
   }
-  if (rank == 0 && tid == 0) p.new_len[req] = new_len;
-  for (int64_t i = new_len + gtid; i < width; i += gthreads) new_weight[i] = 0.f;
-  for (int64_t i = new_len + gtid; i < p.budget; i += gthreads) keep[i] = -1;
+  if (g == 0) p.new_len[req] = new_len;
+  for (int64_t i = (int64_t)new_len + g; i < width; i += all_threads) new_weight[i] = 0.f;
+  for (int64_t i = (int64_t)new_len + g; i < p.budget; i += all_threads) keep[i] = -1;
   if (!cut) {
-    for (int64_t i = gtid; i < n; i += gthreads) {
+    for (int64_t i = g; i < n; i += all_threads) {
       new_weight[i] = weight[i];
       keep[i] = (int32_t)i;
     }
     return;   // the whole cluster
   }
+  __syncthreads();
 
   // the threshold: of the competing keys, `want` are kept, all above `thr` and `want` (as it
   // is then) of those equal to it.  Nothing competes for no place: then thr stays the top.
@@ -131,55 +148,68 @@ __device__ void select(const EvictParams& p, cooperative_groups::cluster_group& 
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, buf = pass & 1;
       const uint32_t digits = pass == 2 ? 1024u : (uint32_t)kBins;
       const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFFFFFFFu << 21 : 0xFFFFFFFFu << 10;
-      for (int i = tid; i < kBins; i += kSelThreads) hist[buf][i] = 0;
-      __syncthreads();
 #pragma unroll 4
       for (int32_t i = max(s0, lo) + tid; i < min(s1, hi); i += kSelThreads) {
-        const uint32_t k = key_at(i);
+        const uint32_t k = score_key(weight_at(i));
         if ((k & mask) == prefix) atomicAdd(&hist[buf][k >> shift & (digits - 1)], 1u);
       }
-      cluster.sync();
-      // thread t: the digits 2047 - 2t and 2046 - 2t of the whole cluster (from the top); the counts
-      // above them by a scan over the CTA
-      uint32_t hi_n = 0, lo_n = 0;
-      for (int i = 0; i < C; ++i) {
-        const uint2 two = ((const uint2*)cluster.map_shared_rank(&hist[buf][0], i))[kBins / 2 - 1 - tid];
-        lo_n += two.x, hi_n += two.y;
-      }
-      uint32_t inc = hi_n + lo_n;
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(~0u, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) warp_gt[warp] = inc;
       __syncthreads();
-      uint32_t above = inc - hi_n - lo_n;
-      for (int i = 0; i < warp; ++i) above += warp_gt[i];
-      if (above < want && above + hi_n + lo_n >= want) {
-        const bool low = above + hi_n < want;
-        picked[0] = kBins - 1 - 2 * tid - (low ? 1 : 0);
-        picked[1] = above + (low ? hi_n : 0);
+      const uint2 mine = ((const uint2*)&hist[buf][warp * 64])[lane];
+      const uint32_t sum = __reduce_add_sync(~0u, mine.x + mine.y);
+      if (lane == 0) group[buf][warp] = sum;
+      sync_all(cluster, C);
+      if (warp == 0) {
+        // lane l: group 31 - l, so that a scan counts from the top
+        uint32_t cnt = 0;
+        for (int i = 0; i < C; ++i) cnt += cluster.map_shared_rank(&group[buf][0], i)[31 - lane];
+        uint32_t inc = cnt;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(~0u, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const uint32_t at = __ballot_sync(~0u, inc >= want);
+        const int l = __ffs(at) - 1;   // the competing keys are at least `want`
+        uint32_t above = __shfl_sync(~0u, inc - cnt, l);
+        // its digits 63 - 2 lane and 62 - 2 lane
+        uint32_t hi_n = 0, lo_n = 0;
+        for (int i = 0; i < C; ++i) {
+          const uint2 two = ((const uint2*)(cluster.map_shared_rank(&hist[buf][0], i) + (31 - l) * 64))[31 - lane];
+          lo_n += two.x, hi_n += two.y;
+        }
+        inc = hi_n + lo_n;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(~0u, inc, o);
+          if (lane >= o) inc += y;
+        }
+        above += inc - hi_n - lo_n;
+        if (above < want && above + hi_n + lo_n >= want) {
+          const bool low = above + hi_n < want;
+          picked[0] = (31 - l) * 64 + 63 - 2 * lane - (low ? 1 : 0);
+          picked[1] = above + (low ? hi_n : 0);
+        }
+      } else if (pass == 1) {
+        // the counters of the third pass: those of the first, which every CTA has read by now
+        for (int i = tid - 32; i < kBins; i += kSelThreads - 32) hist[0][i] = 0;
       }
       __syncthreads();
       prefix |= picked[0] << shift;
       want -= picked[1];
     }
     thr = prefix;
-  } else {
-    __syncthreads();   // the keys
   }
 
   // what every warp keeps of its part of the slice
   const int32_t part = (slice / 32 + kWarps - 1) / kWarps * 32;
   const int32_t w0 = min(s1, s0 + warp * part), w1 = min(s1, w0 + part);
   const uint32_t take = want;   // of the keys equal to thr
-  auto classify = [&](int32_t i, bool& gt, bool& eq) {
+  auto classify = [&](int32_t i, float& w, bool& gt, bool& eq) {
     gt = eq = false;
     if (i >= w1) return;
+    w = weight_at(i);
     if (i < lo || i >= hi) {
       gt = true;
     } else if (p.budget > p.keep_first + p.keep_last) {
-      const uint32_t k = key_at(i);
+      const uint32_t k = score_key(w);
       gt = k > thr;
       eq = k == thr;
     }
@@ -188,36 +218,38 @@ __device__ void select(const EvictParams& p, cooperative_groups::cluster_group& 
 #pragma unroll 4
   for (int32_t i0 = w0; i0 < w1; i0 += 32) {
     bool gt, eq;
-    classify(i0 + lane, gt, eq);
+    float w;
+    classify(i0 + lane, w, gt, eq);
     n_gt += __popc(__ballot_sync(~0u, gt));
     n_eq += __popc(__ballot_sync(~0u, eq));
   }
-  __syncthreads();   // warp_gt is free
   if (lane == 0) warp_gt[warp] = n_gt, warp_eq[warp] = n_eq;
   __syncthreads();
   if (warp == 0) {
     const uint32_t a = __reduce_add_sync(~0u, warp_gt[lane]), b = __reduce_add_sync(~0u, warp_eq[lane]);
     if (lane == 0) cta_cnt[0] = a, cta_cnt[1] = b;
   }
-  cluster.sync();
-  uint32_t gt0 = 0, eq0 = 0;   // before this warp's part
-  for (int i = 0; i < rank; ++i) {
-    const uint32_t* c = cluster.map_shared_rank(&cta_cnt[0], i);
+  sync_all(cluster, C);
+  // before this warp's part
+  uint32_t gt0 = lane < warp ? warp_gt[lane] : 0u, eq0 = lane < warp ? warp_eq[lane] : 0u;
+  if (lane < rank) {
+    const uint32_t* c = cluster.map_shared_rank(&cta_cnt[0], lane);
     gt0 += c[0], eq0 += c[1];
   }
-  gt0 += __reduce_add_sync(~0u, lane < warp ? warp_gt[lane] : 0u);
-  eq0 += __reduce_add_sync(~0u, lane < warp ? warp_eq[lane] : 0u);
+  gt0 = __reduce_add_sync(~0u, gt0);
+  eq0 = __reduce_add_sync(~0u, eq0);
 #pragma unroll 4
   for (int32_t i0 = w0; i0 < w1; i0 += 32) {
     bool gt, eq;
-    classify(i0 + lane, gt, eq);
+    float w;
+    classify(i0 + lane, w, gt, eq);
     const uint32_t bg = __ballot_sync(~0u, gt), be = __ballot_sync(~0u, eq);
     const uint32_t below = (1u << lane) - 1;
     const uint32_t e = eq0 + __popc(be & below);
     if (gt || (eq && e < take)) {
       const uint32_t at = gt0 + __popc(bg & below) + min(e, take);
       keep[at] = i0 + lane;
-      new_weight[at] = weight[i0 + lane];
+      new_weight[at] = w;
     }
     gt0 += __popc(bg);
     eq0 += __popc(be);
@@ -237,13 +269,13 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     select(p, cluster, req, room, &err);
   else
     check_fresh(p, C, rank, room, &err);
-  cluster.sync();
+  sync_all(cluster, C);
   if (rank == 0 && threadIdx.x == 0) {
     uint32_t all = kOk;
     for (int i = 0; i < C; ++i) all = max(all, *cluster.map_shared_rank(&err, i));
     p.part_status[req] = all;
   }
-  cluster.sync();   // no CTA leaves while another reads its words
+  sync_all(cluster, C);   // no CTA leaves while another reads its words
 }
 
 // Moves the kept keys and values, 16 bytes a thread at a time, some rows of a destination page
@@ -313,17 +345,19 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_c
 
 }  // namespace
 
-int evict_cluster(int64_t max_pages) {
-  // one CTA for 8192 positions of the widest request, at most 8
+int evict_cluster(int64_t num_req, int64_t max_pages, int sm_count) {
+  // one CTA for 8192 positions of the widest request, at most 8, and no more than a wave of
+  // them (a CTA fills an SM): 32 requests of up to 65,536 positions take 24 us with clusters of
+  // 8 in two waves
   int C = 1;
-  while (C < 8 && (int64_t)C * 8192 < max_pages * kPage) C *= 2;
+  while (C < 8 && (int64_t)C * 8192 < max_pages * kPage && (num_req + 1) * 2 * C <= sm_count) C *= 2;
   return C;
 }
 
 bool evict_mark_shared(int64_t dst_pages) { return (dst_pages + 31) / 32 * 4 <= kMarkBytes; }
 
-cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
-  const int C = evict_cluster(p.max_pages);
+cudaError_t launch_evict(EvictParams p, int sm_count, cudaStream_t stream) {
+  const int C = evict_cluster(p.num_req, p.max_pages, sm_count);
   const int64_t width = (int64_t)p.max_pages * kPage;
   const int64_t slice = ((width + C - 1) / C + 31) / 32 * 32;
   p.slice_cap = (int32_t)(slice < kSliceKeys ? slice : kSliceKeys);

@@ -496,7 +496,8 @@ int idx_dense_topk_fp4_prefill(const idx_tensor_t* q_fp4, const idx_tensor_t* q_
  * outputs are NaN and integer outputs -1.  Sums, maxima and weights are held in
  * fp32; outputs are rounded once, and the softmax weights are rounded to the
  * inputs' type for their product with the values.  Results do not depend on the
- * stream, on timing, or on other calls.
+ * stream, on timing, or on other calls.  More than INT32_MAX - 65536 positions or
+ * slots of a request or row, or NP * 64 above INT32_MAX, are IDX_ERR_OVERFLOW.
  */
 
 /*
