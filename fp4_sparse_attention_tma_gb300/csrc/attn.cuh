@@ -48,133 +48,171 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
   uint32_t warp_err = kOk;
   if (work) {
     const uint32_t my_ring = smem_addr(ring) + (uint32_t)warp * (STAGES * 2 * kHalf);
-    int64_t here = sp.first(worker);                 // flat index of the subtile computed next
+    int64_t here = sp.first(worker);                 // flat index of the segment's first subtile
     const int64_t stop = sp.first(worker + 1);
-    int64_t to_fetch = stop - here;
 
-    // ---- fetching side ----
+    // ---- fetching side: runs STAGES - 1 subtiles ahead, over the ends of segments ----
+    constexpr int ROWS = 32 / CH > 0 ? 32 / CH : 1;   // positions that one copy of the warp covers
+    constexpr int COPIES = kSub / ROWS;
+    const int piece = lane % CH, row_in = ROWS > 1 ? lane / CH : 0;
+    uint32_t to[8 / ROWS > 0 ? 8 / ROWS : 1];         // where the lane's pieces go: the swizzle repeats every 8 rows
+    constexpr int TO = sizeof(to) / sizeof(to[0]);
+#pragma unroll
+    for (int i = 0; i < TO; ++i) {
+      const int r = i * ROWS + row_in;
+      to[i] = (uint32_t)(r * (D * 2) + ((piece ^ (r & 7)) << 4));
+    }
     Cursor<SLOTS> f = at;
-    int32_t entry;   // page of the subtile to be fetched, or the slot of position lane % 16
+    int64_t f_left = stop - here;                     // subtiles still to be fetched
+    const T *f_k, *f_v;                               // the head's keys and values, at this lane's piece
+    const int32_t* f_list;                            // the request's pages, or the row's slots
+    int32_t entry;                                    // page of the next subtile, or slot of its position lane % 16
+    uint64_t shown = 0;                               // (slots) which positions of the fetched subtiles are one, 16 bits each
     auto look_up = [&]() {
       if constexpr (SLOTS) {
         const int32_t j = f.s * kSub + (lane & 15);
-        entry = j < p.n_slots ? p.slots[(int64_t)f.row0 * p.n_slots + j] : -1;
+        entry = j < p.n_slots ? f_list[j] : -1;
       } else {
-        entry = p.page_table[(int64_t)f.req * p.max_pages + (f.base + f.s) * kSub / kPage];
+        entry = f_list[(f.base + f.s) / (kPage / kSub)];
       }
     };
-    if (to_fetch > 0) look_up();
+    auto begin_fetch = [&]() {
+      f_k = (const T*)p.k + f.kv * p.k_head + piece * 8;
+      f_v = (const T*)p.v + f.kv * p.v_head + piece * 8;
+      f_list = SLOTS ? p.slots + (int64_t)f.row0 * p.n_slots : p.page_table + (int64_t)f.req * p.max_pages;
+      look_up();
+    };
+    begin_fetch();
     auto fetch = [&](int stage) {
-      if (to_fetch > 0) {
+      if (f_left > 0) {
         const uint32_t dk = my_ring + (uint32_t)stage * (2 * kHalf), dv = dk + kHalf;
-        const T* k = (const T*)p.k + f.kv * p.k_head;
-        const T* v = (const T*)p.v + f.kv * p.v_head;
-        constexpr int ROWS = 32 / CH > 0 ? 32 / CH : 1;   // positions that one copy of the warp covers
-        const int chunk = lane % CH;
+        auto place = [&](int i) { return to[i % TO] + (uint32_t)(i / TO) * (8 * D * 2); };
         if constexpr (SLOTS) {
-          if (entry < -1 || entry >= p.num_pages * kPage) warp_err = kErrInvalidPage, entry = -1;
-        } else {
-          if (entry < 0 || entry >= p.num_pages) warp_err = kErrInvalidPage, entry = -1;
-          const int32_t off = (f.base + f.s) * kSub % kPage;
-          const int64_t page = entry < 0 ? 0 : entry;
-          k += page * p.k_page + off * p.k_slot;
-          v += page * p.v_page + off * p.v_slot;
-        }
+          const bool on = entry >= 0 && entry < p.num_pages * kPage;
+          if (!on && entry != -1) warp_err = kErrInvalidPage;
+          const uint32_t mask = __ballot_sync(~0u, on) & 0xFFFFu;
+          shown |= (uint64_t)mask << ((STAGES - 1) * 16);
+          const int32_t page = on ? entry / kPage : 0, off = on ? entry % kPage : 0;
+          if (!p.far) {
+            // offsets in units of 16 bytes
+            const uint32_t ok = on ? (uint32_t)page * (uint32_t)(p.k_page / 8) + (uint32_t)off * (uint32_t)(p.k_slot / 8) : 0u;
+            const uint32_t ov = on ? (uint32_t)page * (uint32_t)(p.v_page / 8) + (uint32_t)off * (uint32_t)(p.v_slot / 8) : 0u;
 #pragma unroll
-        for (int i = 0; i < kSub / ROWS; ++i) {
-          const int r = i * ROWS + (ROWS > 1 ? lane / CH : 0);
-          const T *ks, *vs;
-          bool on;
-          if constexpr (SLOTS) {
-            const int32_t slot = __shfl_sync(~0u, entry, r);
-            on = slot >= 0;
-            const int64_t pg = on ? slot / kPage : 0;
-            const int32_t off = on ? slot % kPage : 0;
-            ks = k + pg * p.k_page + off * p.k_slot;
-            vs = v + pg * p.v_page + off * p.v_slot;
+            for (int i = 0; i < COPIES; ++i) {
+              const int r = i * ROWS + row_in;
+              const uint32_t bytes = mask >> r & 1u ? 16u : 0u;
+              copy16(dk + place(i), f_k + (uint64_t)__shfl_sync(~0u, ok, r) * 8, bytes);
+              copy16(dv + place(i), f_v + (uint64_t)__shfl_sync(~0u, ov, r) * 8, bytes);
+            }
           } else {
-            const int32_t pos = (f.base + f.s) * kSub + r;
-            on = entry >= 0 && pos >= f.lo && pos < f.hi;
-            ks = on ? k + r * p.k_slot : (const T*)p.k;
-            vs = on ? v + r * p.v_slot : (const T*)p.v;
+            const unsigned long long ok = page * p.k_page + off * p.k_slot, ov = page * p.v_page + off * p.v_slot;
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) {
+              const int r = i * ROWS + row_in;
+              const uint32_t bytes = mask >> r & 1u ? 16u : 0u;
+              copy16(dk + place(i), f_k + __shfl_sync(~0u, ok, r), bytes);
+              copy16(dv + place(i), f_v + __shfl_sync(~0u, ov, r), bytes);
+            }
           }
-          const uint32_t d = (uint32_t)(r * (D * 2) + ((chunk ^ (r & 7)) << 4));
-          copy16(dk + d, ks + chunk * 8, on ? 16u : 0u);
-          copy16(dv + d, vs + chunk * 8, on ? 16u : 0u);
+        } else {
+          const bool there = entry >= 0 && entry < p.num_pages;
+          if (!there) warp_err = kErrInvalidPage;
+          const int32_t pos0 = (f.base + f.s) * kSub, off = pos0 % kPage + row_in;
+          const int64_t page = there ? entry : 0;
+          const T* k = f_k + page * p.k_page + off * p.k_slot;
+          const T* v = f_v + page * p.v_page + off * p.v_slot;
+          const int64_t ks = ROWS * p.k_slot, vs = ROWS * p.v_slot;
+          if (there && pos0 >= f.lo && pos0 + kSub <= f.hi) {
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i, k += ks, v += vs) {
+              copy16(dk + place(i), k, 16u);
+              copy16(dv + place(i), v, 16u);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i, k += ks, v += vs) {
+              const int32_t pos = pos0 + i * ROWS + row_in;
+              const bool on = there && pos >= f.lo && pos < f.hi;
+              copy16(dk + place(i), on ? k : (const T*)p.k, on ? 16u : 0u);
+              copy16(dv + place(i), on ? v : (const T*)p.v, on ? 16u : 0u);
+            }
+          }
         }
-        if (--to_fetch > 0) {
-          f.next(p);
-          look_up();
+        if (--f_left > 0) {
+          if (++f.s < f.nsub) {
+            look_up();
+          } else {
+            f.next_unit(p);
+            begin_fetch();
+          }
         }
       }
       copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+    for (int i = 0; i < STAGES - 1; ++i) {
+      fetch(i);
+      shown >>= 16;
+    }
 
     // ---- computing side ----
-    uint32_t qf[MT][KS][4];
-    float o[MT][NT][4];
-    float mx[MT][2], sum[MT][2];
-    int32_t w_lo[MT][2], w_hi[MT][2];   // windows of the thread's tile rows
-    uint32_t live = 0;                  // bit 2t + e: the thread's tile row is a row that sees something
-    bool seen = false;                  // (slots) some slot of the segment was one
-    int32_t full_lo, full_hi;           // positions that every row of the group sees
-    bool begin = true;                  // the next subtile is the first of a segment
-    bool cut_front = false;             // the segment starts inside its unit
     int stage = 0;
     const float c = p.scale_log2;
     while (here < stop) {
+      const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
+      const bool cut_front = v0 > 0;      // the segment starts inside its unit
       const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
       const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
+      uint32_t qf[MT][KS][4];
+      float o[MT][NT][4];
+      float mx[MT][2], sum[MT][2];
+      int32_t w_lo[MT][2], w_hi[MT][2];   // windows of the thread's tile rows
+      uint32_t live = 0;                  // bit 2t + e: the thread's tile row is a row that sees something
+      bool seen = false;                  // (slots) some slot of the segment was one
+      int32_t full_lo = 0, full_hi = INT32_MAX;   // positions that every row of the group sees
       // tile row m: row m / chunk_heads of the group, head h0 + m % chunk_heads
-      if (begin) {
-        begin = false;
-        cut_front = at.s > 0;
-        full_lo = 0, full_hi = INT32_MAX;
-        live = 0;
-        seen = false;
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int m = t * 16 + e * 8 + lane / 4;
-            const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
-            bool on = j < at.nrows && h < heads;
-            int32_t a = at.lo, b = at.hi;
-            if constexpr (!SLOTS) {
-              if (on) {
-                a = p.row_start[at.row0 + j], b = p.row_end[at.row0 + j];
-                if (b <= a) on = false, a = at.lo, b = at.hi;
-              }
-            }
-            if (on) live |= 1u << (2 * t + e);
-            w_lo[t][e] = a, w_hi[t][e] = b;
-            full_lo = max(full_lo, a), full_hi = min(full_hi, b);
-            mx[t][e] = kNegInf, sum[t][e] = 0.f;
-            const uint32_t* src =
-                (const uint32_t*)((const T*)p.q + (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              qf[t][k][e] = on ? src[k * 8 + (lane & 3)] : 0u;
-              qf[t][k][2 + e] = on ? src[k * 8 + 4 + (lane & 3)] : 0u;
+        for (int e = 0; e < 2; ++e) {
+          const int m = t * 16 + e * 8 + lane / 4;
+          const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
+          bool on = j < at.nrows && h < heads;
+          int32_t a = at.lo, b = at.hi;
+          if constexpr (!SLOTS) {
+            if (on) {
+              a = p.row_start[at.row0 + j], b = p.row_end[at.row0 + j];
+              if (b <= a) on = false, a = at.lo, b = at.hi;
             }
           }
-        if constexpr (SLOTS) full_hi = 0;  // the slots are looked at one by one
-        full_lo = __reduce_max_sync(~0u, full_lo);
-        full_hi = __reduce_min_sync(~0u, full_hi);
+          if (on) live |= 1u << (2 * t + e);
+          w_lo[t][e] = a, w_hi[t][e] = b;
+          full_lo = max(full_lo, a), full_hi = min(full_hi, b);
+          mx[t][e] = kNegInf, sum[t][e] = 0.f;
+          const uint32_t* src =
+              (const uint32_t*)((const T*)p.q + (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+          for (int k = 0; k < KS; ++k) {
+            qf[t][k][e] = on ? src[k * 8 + (lane & 3)] : 0u;
+            qf[t][k][2 + e] = on ? src[k * 8 + 4 + (lane & 3)] : 0u;
+          }
+        }
+      full_lo = __reduce_max_sync(~0u, full_lo);
+      full_hi = __reduce_min_sync(~0u, full_hi);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) o[t][n][x] = 0.f;
-      }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[t][n][x] = 0.f;
 
+      for (int32_t sub = v0; sub < v1; ++sub) {
       // the next stage goes where the last one computed was
       copy_wait<STAGES - 2>();
       __syncwarp();
+      const uint32_t on = (uint32_t)shown & 0xFFFFu;
       fetch(stage == 0 ? STAGES - 1 : stage - 1);
+      shown >>= 16;
       const uint32_t sk = my_ring + (uint32_t)stage * (2 * kHalf), sv = sk + kHalf;
       stage = stage == STAGES - 1 ? 0 : stage + 1;
 
@@ -200,14 +238,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
           }
         }
 
-      const int32_t pos0 = (at.base + at.s) * kSub;
+      const int32_t pos0 = (at.base + sub) * kSub;
       bool edge;
       if constexpr (SLOTS) {
-        // the slots again: only whether each is one
-        const int32_t j = pos0 + (lane & 15);
-        const int32_t slot = j < p.n_slots ? p.slots[(int64_t)at.row0 * p.n_slots + j] : -1;
-        const uint32_t on = __ballot_sync(~0u, slot >= 0 && slot < p.num_pages * kPage);
-        edge = (on & 0xFFFFu) != 0xFFFFu;
+        edge = on != 0xFFFFu;
         seen |= on != 0;
         if (edge) {
 #pragma unroll
@@ -342,16 +376,17 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
         }
       }
 
-      ++here;
-      const bool unit_end = at.s + 1 == at.nsub;
-      if (unit_end || here == stop) {
-        // the segment ends: finish the unit, or leave its part
-        begin = true;
-        const bool whole = unit_end && !cut_front;
+      }
+
+      // the segment ends: finish the unit, or leave its part
+      here += v1 - v0;
+      {
+        const bool unit_end = v1 == at.nsub, whole = unit_end && !cut_front;
         const int which = cut_front ? 0 : 1;
         if (!unit_end && !cut_front && lane == 0) {
           p.open_row[worker] = at.row0;
-          p.open_info[worker] = make_int4(at.nrows, at.kv * p.chunks + at.chunk, sp.holder(here + (at.nsub - at.s) - 2), 0);
+          p.open_info[worker] =
+              make_int4(at.nrows, at.kv * p.chunks + at.chunk, sp.holder(here + (at.nsub - v1) - 1), 0);
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -388,7 +423,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
             }
           }
       }
-      if (here < stop) at.next(p);
+      if (here < stop) at.next_unit(p);
     }
     copy_wait<0>();
   }

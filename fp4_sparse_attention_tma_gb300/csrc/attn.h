@@ -44,6 +44,7 @@ struct AttnParams {
   int32_t group_rows;               // rows per group, at most (1 where there are several chunks)
   int32_t row_cols;                 // tile rows between the rows of a group (chunk_heads of them in use)
   int32_t tensor_core;              // 1: the kernel of attn_tc.cuh
+  int32_t far;                      // 1: a cache spans 64 GB or more
   int32_t workers;                  // warps of the grid
   int32_t min_sub;                  // a worker's range holds at least this many subtiles
   float scale_log2;                 // softmax scale x log2(e)
@@ -88,7 +89,7 @@ inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int6
 
 // Warps of a CTA of the kernel of attn.cuh (with its ring stages, what fits the shared
 // memory of an SM).
-inline int attn_warps(int32_t dim) { return dim == 256 ? 4 : 8; }
+inline int attn_warps(int32_t dim, int32_t tile) { return dim == 256 ? 4 : dim == 128 ? 8 : tile == 32 ? 12 : 16; }
 
 // The attention kernel; bf16: the inputs' type (else fp16).
 cudaError_t launch_attn(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);

@@ -141,9 +141,8 @@ struct Cursor {
   }
   // Subtiles of every row of a call over slots.
   __device__ static int32_t row_count(const AttnParams& p) { return (p.n_slots + kSub - 1) / kSub; }
-  // The next subtile; the caller has not passed the end of the list.
-  __device__ void next(const AttnParams& p) {
-    if (++s < nsub) return;
+  // The next unit, at its first subtile; the caller has not passed the end of the list.
+  __device__ void next_unit(const AttnParams& p) {
     s = 0;
     if (++chunk < p.chunks) return;
     chunk = 0;

@@ -244,7 +244,7 @@ AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_head
     a.group_rows = a.chunks > 1 ? 1 : most / a.group;
     a.row_cols = a.chunk_heads;
     a.tile = most;
-    a.workers = sm * attn_warps((int32_t)dim);
+    a.workers = sm * attn_warps((int32_t)dim, most);
   }
   return a;
 }
@@ -322,7 +322,8 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   if (!guard.ok()) return IDX_ERR_CUDA;
   if ((st = check_arch(&m))) return st;
   const bool weights = c.weight_out != nullptr && numel_of(c.weight_out) > 0;
-  const AttnPlan a = plan_of(R, c.slots ? R : NR, Hq, Hk, D, span_of(c.k) >= kFar || span_of(c.v) >= kFar, m.sm);
+  const bool far = span_of(c.k) >= kFar || span_of(c.v) >= kFar;
+  const AttnPlan a = plan_of(R, c.slots ? R : NR, Hq, Hk, D, far, m.sm);
   int64_t logit_rows, logit_bytes;
   if (weights && (!mul_ok(R * Hq, MP * kPage, &logit_rows) || !mul_ok(logit_rows, 4, &logit_bytes) ||
                   logit_bytes > (INT64_MAX >> 2)))
@@ -348,6 +349,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   p.q_heads = (int32_t)Hq, p.kv_heads = (int32_t)Hk;
   p.group = a.group, p.chunks = a.chunks, p.chunk_heads = a.chunk_heads, p.group_rows = a.group_rows;
   p.row_cols = a.row_cols, p.tensor_core = a.tensor_core;
+  p.far = far;
   p.workers = R > 0 ? a.workers : 0;
   p.n_cta = R > 0 ? m.sm : 0;
   p.min_sub = 1;
