@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
 
   Split sp;
   Cursor<SLOTS> at;
-  const bool work = find_range<Cursor<SLOTS>, SLOTS, WARPS>(p, sp, at, worker, &err);
+  Rows rows{};
+  const bool work = find_range<Cursor<SLOTS>, SLOTS, WARPS>(p, rows, sp, at, worker, &err);
   if (work && lane == 0) p.open_row[worker] = -1;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.active = sp.active;
   uint32_t warp_err = kOk;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
           if (++f.s < f.nsub) {
             look_up();
           } else {
-            f.next_unit(p);
+            f.next_unit(p, rows);
             begin_fetch();
           }
         }
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
           int32_t a = at.lo, b = at.hi;
           if constexpr (!SLOTS) {
             if (on) {
-              a = p.row_start[at.row0 + j], b = p.row_end[at.row0 + j];
+              a = rows.start[at.row0 + j], b = rows.end[at.row0 + j];
               if (b <= a) on = false, a = at.lo, b = at.hi;
             }
           }
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
         // some rows of the group see a position and others do not: row by row, with the values that the
         // row does not see set to zero (0 x infinity or NaN would not be)
         for (int j = 0; j < at.nrows; ++j) {
-          const int32_t a0 = p.row_start[at.row0 + j], b0 = p.row_end[at.row0 + j];
+          const int32_t a0 = rows.start[at.row0 + j], b0 = rows.end[at.row0 + j];
           if (b0 <= a0) continue;
           uint32_t keep[2];   // of the thread's pairs of positions
 #pragma unroll
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
             }
           }
       }
-      if (here < stop) at.next_unit(p);
+      if (here < stop) at.next_unit(p, rows);
     }
     copy_wait<0>();
   }

@@ -85,9 +85,15 @@ struct Split {
   __device__ int32_t holder(int64_t x) const { return (int32_t)(((x + 1) * active - 1) / total); }
 };
 
+// The rows' metadata: the caller's arrays, or a copy in shared memory (where they fit; every
+// role and warp walks over them, and its waits for them would add up).
+struct Rows {
+  const int32_t *req, *start, *end;
+};
+
 // Row groups: a row starts one where the request changes, and every group_rows rows.
-__device__ __forceinline__ bool starts_group(const AttnParams& p, int32_t r) {
-  return r < p.rows && (r % p.group_rows == 0 || p.row_req[r - 1] != p.row_req[r]);
+__device__ __forceinline__ bool starts_group(const AttnParams& p, const Rows& rows, int32_t r) {
+  return r < p.rows && (r % p.group_rows == 0 || rows.req[r - 1] != rows.req[r]);
 }
 
 // A place in the list of units: subtile `s` of one unit of the group at row0.
@@ -99,7 +105,7 @@ struct Cursor {
   int32_t kv, chunk, s;       // the unit: key-value head and chunk of its query heads
 
   // The group that starts at `row`.  Called by the whole warp.
-  __device__ void load(const AttnParams& p, int32_t row) {
+  __device__ void load(const AttnParams& p, const Rows& rows, int32_t row) {
     row0 = row;
     if constexpr (SLOTS) {
       nrows = 1;
@@ -112,13 +118,13 @@ struct Cursor {
       const int32_t r = row + lane;
       const int32_t stop = min(p.rows, (row / p.group_rows + 1) * p.group_rows);
       const bool in = r < stop;
-      const int32_t rr = in ? p.row_req[r] : -1;
+      const int32_t rr = in ? rows.req[r] : -1;
       req = __shfl_sync(~0u, rr, 0);
       const uint32_t other = ~__ballot_sync(~0u, in && rr == req);
       nrows = other ? __ffs(other) - 1 : 32;
       int32_t a = INT32_MAX, b = 0;
       if (lane < nrows) {
-        const int32_t a0 = p.row_start[r], b0 = p.row_end[r];
+        const int32_t a0 = rows.start[r], b0 = rows.end[r];
         if (b0 > a0) a = a0, b = b0;
       }
       lo = __reduce_min_sync(~0u, a);
@@ -129,12 +135,12 @@ struct Cursor {
     nsub = hi > lo ? (hi + kSub - 1) / kSub - base : 0;
   }
   // Subtiles of the group that starts at row r; 0 where none does.
-  __device__ static int32_t count(const AttnParams& p, int32_t r) {
-    if (!starts_group(p, r)) return 0;
-    const int32_t req = p.row_req[r];
+  __device__ static int32_t count(const AttnParams& p, const Rows& rows, int32_t r) {
+    if (!starts_group(p, rows, r)) return 0;
+    const int32_t req = rows.req[r];
     int32_t a = INT32_MAX, b = 0;
-    for (int32_t i = r; i < p.rows && (i == r || (i % p.group_rows != 0 && p.row_req[i] == req)); ++i) {
-      const int32_t a0 = p.row_start[i], b0 = p.row_end[i];
+    for (int32_t i = r; i < p.rows && (i == r || (i % p.group_rows != 0 && rows.req[i] == req)); ++i) {
+      const int32_t a0 = rows.start[i], b0 = rows.end[i];
       if (b0 > a0) a = min(a, a0), b = max(b, b0);
     }
     return b > a ? (b + kSub - 1) / kSub - a / kSub : 0;
@@ -142,14 +148,14 @@ struct Cursor {
   // Subtiles of every row of a call over slots.
   __device__ static int32_t row_count(const AttnParams& p) { return (p.n_slots + kSub - 1) / kSub; }
   // The next unit, at its first subtile; the caller has not passed the end of the list.
-  __device__ void next_unit(const AttnParams& p) {
+  __device__ void next_unit(const AttnParams& p, const Rows& rows) {
     s = 0;
     if (++chunk < p.chunks) return;
     chunk = 0;
     if (++kv < p.kv_heads) return;
     kv = 0;
     do {
-      load(p, row0 + nrows);
+      load(p, rows, row0 + nrows);
     } while (nsub == 0);
   }
 };
@@ -159,7 +165,7 @@ struct Cursor {
 // differ from warp to warp).  Called by the whole CTA.  False: an error (recorded in *err)
 // or nothing to do for this warp.
 template <class Cur, bool SLOTS, int WARPS>
-__device__ bool find_range(const AttnParams& p, Split& sp, Cur& cur, int32_t worker, uint32_t* err) {
+__device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur, int32_t worker, uint32_t* err) {
   const int32_t units = p.kv_heads * p.chunks;
   if constexpr (SLOTS) {
     const int32_t n = Cur::row_count(p);
@@ -171,7 +177,7 @@ __device__ bool find_range(const AttnParams& p, Split& sp, Cur& cur, int32_t wor
     const int64_t per_row = (int64_t)units * n;
     const int32_t row = (int32_t)(t / per_row);
     const int64_t rest = t - row * per_row;
-    cur.load(p, row);
+    cur.load(p, rows, row);
     const int32_t u = (int32_t)(rest / n);
     cur.s = (int32_t)(rest - (int64_t)u * n);
     cur.kv = u / p.chunks;
@@ -182,19 +188,22 @@ __device__ bool find_range(const AttnParams& p, Split& sp, Cur& cur, int32_t wor
     __shared__ int64_t warp_sum[WARPS];
     __shared__ int64_t pre[N];          // subtiles before each row of the pass, in the pass
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int32_t copy[3][N];
     int64_t sum = 0;
     bool bad = false;
+    const bool one_pass = p.rows <= N;
     for (int32_t r = tid; r < p.rows; r += N) {
       const int32_t q = p.row_req[r], a = p.row_start[r], b = p.row_end[r];
       bad |= q < 0 || q >= p.num_req || a < 0 || b < a || (int64_t)b > (int64_t)p.max_pages * kPage;
+      if (one_pass) copy[0][r] = q, copy[1][r] = a, copy[2][r] = b;
     }
+    rows = one_pass ? Rows{copy[0], copy[1], copy[2]} : Rows{p.row_req, p.row_start, p.row_end};
     if (__syncthreads_or(bad)) {
       if (tid == 0) *err = kErrInvalidMetadata;
       return false;
     }
-    const bool one_pass = p.rows <= N;
     int32_t mine = 0;
-    for (int32_t r = tid; r < p.rows; r += N) sum += mine = Cur::count(p, r);
+    for (int32_t r = tid; r < p.rows; r += N) sum += mine = Cur::count(p, rows, r);
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     if (lane == 0) warp_sum[warp] = sum;
     __syncthreads();
@@ -209,7 +218,7 @@ __device__ bool find_range(const AttnParams& p, Split& sp, Cur& cur, int32_t wor
     bool found = false;
     int64_t before = 0;   // subtiles (of one unit each) before the pass
     for (int32_t r0 = 0; r0 < p.rows; r0 += N) {
-      if (!one_pass) mine = Cur::count(p, r0 + tid);
+      if (!one_pass) mine = Cur::count(p, rows, r0 + tid);
       int64_t inc = mine;
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(~0u, inc, o);
@@ -235,7 +244,7 @@ __device__ bool find_range(const AttnParams& p, Split& sp, Cur& cur, int32_t wor
           if ((before + pre[i]) * units <= t) at = i;   // pre is non-decreasing
         at = __reduce_max_sync(~0u, at);
         const int64_t rest = t - (before + pre[at]) * units;
-        cur.load(p, r0 + at);
+        cur.load(p, rows, r0 + at);
         const int32_t u = (int32_t)(rest / cur.nsub);
         cur.s = (int32_t)(rest - (int64_t)u * cur.nsub);
         cur.kv = u / p.chunks;

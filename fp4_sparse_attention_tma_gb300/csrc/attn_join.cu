@@ -43,8 +43,9 @@ constexpr int kJoinWarps = 8;
 constexpr int kFewParts = 8;   // units of at most so many parts are joined by one warp a tile row
 
 struct OpenUnit {
-  int32_t w0, n;             // first worker and parts
-  int32_t row0, nrows, u;    // its group's rows and its index in the group
+  uint16_t w0, n;            // first worker and parts
+  int32_t row0;              // its group's first row
+  uint32_t nrows : 8, u : 24;   // its group's rows and its index in the group
 };
 
 // Parts i0, i0 + step, ... of a tile row added up by one warp; a lane has D / 32 columns.
@@ -110,8 +111,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr int V = D / 32;   // columns of a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // [workers]: units of few parts from the front, others from the back; first worker | parts << 16
-  extern __shared__ uint32_t open[];
+  extern __shared__ OpenUnit open[];   // [workers]: units of few parts from the front, others from the back
   __shared__ int32_t warp_n[kJoinWarps][2];
   __shared__ float wm[kJoinWarps], wl[kJoinWarps];
   __shared__ float wo[kJoinWarps][D];
@@ -135,8 +135,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   const int active = p.n_cta > 0 ? *p.active : 0;
   for (int w0 = 0; w0 < active; w0 += kJoinWarps * 32) {
     const int w = w0 + (int)threadIdx.x;
-    const bool on = w < active && p.open_row[w] >= 0;
-    const int n = on ? p.open_info[w].z - w + 1 : 0;
+    OpenUnit un{};
+    un.row0 = w < active ? p.open_row[w] : -1;
+    const int4 info = w < active ? p.open_info[w] : make_int4(0, 0, 0, 0);   // (means nothing where no unit is open)
+    un.w0 = (uint16_t)w, un.nrows = info.x, un.u = info.y, un.n = (uint16_t)(info.z - w + 1);
+    const bool on = un.row0 >= 0;
+    const int n = un.n;
     const bool is_few = on && n <= kFewParts, is_many = on && !is_few;
     const uint32_t bf = __ballot_sync(~0u, is_few), bm = __ballot_sync(~0u, is_many);
     if (lane == 0) warp_n[warp][0] = __popc(bf), warp_n[warp][1] = __popc(bm);
@@ -147,40 +151,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
       if (i < warp) at_few += warp_n[i][0], at_many += warp_n[i][1];
       few += warp_n[i][0], many += warp_n[i][1];
     }
-    const uint32_t below = (1u << lane) - 1, entry = (uint32_t)w | (uint32_t)n << 16;
-    if (is_few) open[at_few + __popc(bf & below)] = entry;
-    if (is_many) open[p.workers - 1 - at_many - __popc(bm & below)] = entry;
+    const uint32_t below = (1u << lane) - 1;
+    if (is_few) open[at_few + __popc(bf & below)] = un;
+    if (is_many) open[p.workers - 1 - at_many - __popc(bm & below)] = un;
     __syncthreads();
   }
-  auto unit_of = [&](uint32_t entry) {
-    OpenUnit un;
-    un.w0 = entry & 0xFFFFu;
-    un.n = entry >> 16;
-    un.row0 = p.open_row[un.w0];
-    const int4 info = p.open_info[un.w0];
-    un.nrows = info.x, un.u = info.y;
-    return un;
-  };
-
   // the output row of tile row m: false where it is none, or sees nothing
   auto row_of = [&](const OpenUnit& un, int m, int64_t& row, int& qh) {
     const int j = m / p.row_cols, h = m - j * p.row_cols;
     const int in_group = un.u % p.chunks * p.chunk_heads + h;
     row = un.row0 + j;
     qh = un.u / p.chunks * p.group + in_group;
-    return j < un.nrows && h < p.chunk_heads && in_group < p.group &&
-           (p.slots || p.row_end[row] > p.row_start[row]);
+    return j < un.nrows && h < p.chunk_heads && in_group < p.group;
   };
   const int per = p.tile / kJoinWarps;
   for (int job = blockIdx.x; job < few * per; job += gridDim.x) {
-    const OpenUnit un = unit_of(open[job / per]);
+    const OpenUnit un = open[job / per];
     const int m = job % per * kJoinWarps + warp;
     int64_t row;
     int qh;
     if (!row_of(un, m, row, qh)) continue;
+    const int32_t a = p.slots ? 0 : p.row_start[row], b = p.slots ? 1 : p.row_end[row];
     float M, l, acc[V];
     bool seen;
     join_parts<D>(p, un, m, 0, 1, M, l, acc, seen);
+    if (b <= a) continue;   // the row sees nothing, and its parts mean nothing
     const float inv = seen ? 1.f / l : 0.f;
     T* dst = (T*)p.out + row * p.out_row + (int64_t)qh * p.out_head + lane * V;
 #pragma unroll
@@ -192,10 +187,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     }
   }
   for (int job = blockIdx.x; job < many * p.tile; job += gridDim.x) {
-    const OpenUnit un = unit_of(open[p.workers - 1 - job / p.tile]);
+    const OpenUnit un = open[p.workers - 1 - job / p.tile];
     int64_t row;
     int qh;
-    if (!row_of(un, job % p.tile, row, qh)) continue;   // the same for the whole CTA
+    // the same for the whole CTA
+    if (!row_of(un, job % p.tile, row, qh) || (!p.slots && p.row_end[row] <= p.row_start[row])) continue;
     float M, l, acc[V];
     bool seen;
     join_parts<D>(p, un, job % p.tile, warp, kJoinWarps, M, l, acc, seen);
@@ -309,14 +305,14 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __gr
 
 template <bool BF16>
 static cudaError_t pick_join(const AttnParams& p, int grid, cudaStream_t stream) {
-  const size_t smem = (size_t)p.workers * 4;
+  const size_t smem = (size_t)p.workers * sizeof(OpenUnit);
   if (p.dim == 64) return launch_overlapped(attn_join_kernel<BF16, 64>, dim3(grid), dim3(kJoinWarps * 32), smem, stream, p);
   if (p.dim == 128) return launch_overlapped(attn_join_kernel<BF16, 128>, dim3(grid), dim3(kJoinWarps * 32), smem, stream, p);
   return launch_overlapped(attn_join_kernel<BF16, 256>, dim3(grid), dim3(kJoinWarps * 32), smem, stream, p);
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream) {
-  return bf16 ? pick_join<true>(p, sm_count * 2, stream) : pick_join<false>(p, sm_count * 2, stream);
+  return bf16 ? pick_join<true>(p, sm_count * 4, stream) : pick_join<false>(p, sm_count * 4, stream);
 }
 
 cudaError_t launch_attn_weights(const AttnParams& p, cudaStream_t stream) {

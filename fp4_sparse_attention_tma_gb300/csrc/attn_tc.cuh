@@ -130,21 +130,21 @@ struct Walk {
     }
     return n;
   }
-  __device__ static int32_t count(const AttnParams& p, int32_t r) {
-    if (!starts_group(p, r)) return 0;
+  __device__ static int32_t count(const AttnParams& p, const Rows& rows, int32_t r) {
+    if (!starts_group(p, rows, r)) return 0;
     int32_t a[NB], b[NB], c0, c1;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int32_t i = r + j;
-      const bool in = i < p.rows && (j == 0 || (i % p.group_rows != 0 && p.row_req[i] == p.row_req[r]));
-      a[j] = in ? p.row_start[i] : 0;
-      b[j] = in ? p.row_end[i] : 0;
+      const bool in = i < p.rows && (j == 0 || (i % p.group_rows != 0 && rows.req[i] == rows.req[r]));
+      a[j] = in ? rows.start[i] : 0;
+      b[j] = in ? rows.end[i] : 0;
     }
     return visits(a, b, c0, c1);
   }
   __device__ static int32_t row_count(const AttnParams& p) { return hi(p.n_slots); }
 
-  __device__ void load(const AttnParams& p, int32_t row) {
+  __device__ void load(const AttnParams& p, const Rows& rows, int32_t row) {
     row0 = row;
     req = 0;
     nrows = 1;
@@ -152,27 +152,27 @@ struct Walk {
       a[0] = 0;
       b[0] = p.n_slots;
     } else {
-      req = p.row_req[row];
+      req = rows.req[row];
       if constexpr (NB == 2)
-        if (row + 1 < p.rows && (row + 1) % p.group_rows != 0 && p.row_req[row + 1] == req) nrows = 2;
+        if (row + 1 < p.rows && (row + 1) % p.group_rows != 0 && rows.req[row + 1] == req) nrows = 2;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        a[j] = j < nrows ? p.row_start[row + j] : 0;
-        b[j] = j < nrows ? p.row_end[row + j] : 0;
+        a[j] = j < nrows ? rows.start[row + j] : 0;
+        b[j] = j < nrows ? rows.end[row + j] : 0;
         if (b[j] <= a[j]) a[j] = b[j] = 0;
       }
     }
     nsub = visits(a, b, c0, c1);
   }
   // The next unit, at its first visit; the caller has not passed the end of the list.
-  __device__ void next_unit(const AttnParams& p) {
+  __device__ void next_unit(const AttnParams& p, const Rows& rows) {
     s = 0;
     if (++chunk < p.chunks) return;
     chunk = 0;
     if (++kv < p.kv_heads) return;
     kv = 0;
     do {
-      load(p, row0 + nrows);
+      load(p, rows, row0 + nrows);
     } while (nsub == 0);
   }
   // Visit v of the unit: its tile and its rows (bit j).
@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 
   Split sp;
   Walk<NB, SLOTS> at;
-  const bool work = find_range<Walk<NB, SLOTS>, SLOTS, kWarps>(p, sp, at, blockIdx.x, &err);
+  Rows meta{};
+  const bool work = find_range<Walk<NB, SLOTS>, SLOTS, kWarps>(p, meta, sp, at, blockIdx.x, &err);
   if (threadIdx.x == 0) {
     if (work) p.open_row[blockIdx.x] = -1;
     if (blockIdx.x == 0) *p.active = sp.active;
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
           tc_fence_before();
         }
-        if (here < stop && !dead) at.next_unit(p);
+        if (here < stop && !dead) at.next_unit(p, meta);
       }
     } else if (warp < 12) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           arrive_when_copied(values ? full_v(slot) : full_k(slot));
           ++n;
         }
-        if (here < stop && ok) at.next_unit(p);
+        if (here < stop && ok) at.next_unit(p, meta);
       }
       copy_wait_all();
       bad = __reduce_max_sync(~0u, bad);
@@ -803,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           if (ok && elect_one()) tc_commit(empty_q(qb));
           __syncwarp();
           ++seg;
-          if (here < stop && ok) at.next_unit(p);
+          if (here < stop && ok) at.next_unit(p, meta);
         }
       } else if (warp == 13) {
         constexpr uint32_t kPV = idesc_f16<BF16>(128, kCols, true);
@@ -845,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             __syncwarp();
             ++n;
           }
-          if (here < stop && ok) at.next_unit(p);
+          if (here < stop && ok) at.next_unit(p, meta);
         }
       }
     }
