@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
   Split sp;
   Cursor<SLOTS> at;
   Rows rows{};
-  const bool work = find_range<Cursor<SLOTS>, SLOTS, WARPS>(p, rows, sp, at, worker, &err);
+  const bool work = find_range<Cursor<SLOTS>, SLOTS, WARPS>(p, rows, sp, at, worker, ring, &err);
   if (work && lane == 0) p.open_row[worker] = -1;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.active = sp.active;
   uint32_t warp_err = kOk;

@@ -85,8 +85,9 @@ struct Split {
   __device__ int32_t holder(int64_t x) const { return (int32_t)(((x + 1) * active - 1) / total); }
 };
 
-// The rows' metadata: the caller's arrays, or a copy in shared memory (where they fit; every
-// role and warp walks over them, and its waits for them would add up).
+// The rows' metadata: the caller's arrays, or a copy in shared memory (of up to so many rows;
+// every role and warp walks over them, and its waits for them would add up).
+constexpr int kRowCopies = 512;
 struct Rows {
   const int32_t *req, *start, *end;
 };
@@ -163,9 +164,9 @@ struct Cursor {
 // Checks the rows' metadata (all of it, by every CTA, so that all agree), counts the
 // subtiles, and leaves the place where the worker's range starts in `cur` (`worker` may
 // differ from warp to warp).  Called by the whole CTA.  False: an error (recorded in *err)
-// or nothing to do for this warp.
+// or nothing to do for this warp.  `room`: 8 bytes of shared memory a thread.
 template <class Cur, bool SLOTS, int WARPS>
-__device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur, int32_t worker, uint32_t* err) {
+__device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur, int32_t worker, void* room, uint32_t* err) {
   const int32_t units = p.kv_heads * p.chunks;
   if constexpr (SLOTS) {
     const int32_t n = Cur::row_count(p);
@@ -186,18 +187,19 @@ __device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur,
   } else {
     constexpr int N = WARPS * 32;
     __shared__ int64_t warp_sum[WARPS];
-    __shared__ int64_t pre[N];          // subtiles before each row of the pass, in the pass
+    int64_t* pre = (int64_t*)room;      // [N] subtiles before each row of the pass, in the pass
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ int32_t copy[3][N];
+    __shared__ int32_t copy[3][kRowCopies];
+    const bool copied = p.rows <= kRowCopies;
     int64_t sum = 0;
     bool bad = false;
     const bool one_pass = p.rows <= N;
     for (int32_t r = tid; r < p.rows; r += N) {
       const int32_t q = p.row_req[r], a = p.row_start[r], b = p.row_end[r];
       bad |= q < 0 || q >= p.num_req || a < 0 || b < a || (int64_t)b > (int64_t)p.max_pages * kPage;
-      if (one_pass) copy[0][r] = q, copy[1][r] = a, copy[2][r] = b;
+      if (copied) copy[0][r] = q, copy[1][r] = a, copy[2][r] = b;
     }
-    rows = one_pass ? Rows{copy[0], copy[1], copy[2]} : Rows{p.row_req, p.row_start, p.row_end};
+    rows = copied ? Rows{copy[0], copy[1], copy[2]} : Rows{p.row_req, p.row_start, p.row_end};
     if (__syncthreads_or(bad)) {
       if (tid == 0) *err = kErrInvalidMetadata;
       return false;
@@ -253,6 +255,7 @@ __device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur,
       }
       before += all;
     }
+    __syncthreads();   // `room` is free again
     return found;
   }
 }

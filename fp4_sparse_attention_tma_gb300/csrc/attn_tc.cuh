@@ -1,27 +1,31 @@
-// The attention kernel for many query heads on one key-value head (17 to 64 a chunk,
-// head dimension 128), on the fifth-generation tensor cores.
+// The attention kernel for many query heads on one key-value head (17 to 64 a chunk, head
+// dimension 128), on the fifth-generation tensor cores.
 //
-// With that many heads the products, not the copies, bound warps that load every key and
-// value once per 16 heads.  Here one CTA takes a tile of 128 positions for all 64 columns
-// (query heads) of a row, in the transposed form, in which nothing is padded:
+// With that many heads the products, not the copies, bound warps that load every key and value
+// once per 16 heads.  Here a CTA takes tiles of 128 positions for a matrix of 128 rows:
 //
-//   S^T [128 positions x 64] = K Q^T          (keys K-major, queries K-major)
-//   O^T [128 (the head dimension) x 64] += V^T P^T   (both operands MN-major: the values as
-//                                              they lie in the cache, P^T as a thread writes it)
+//   S [128 x 128 positions] = Q K^T      (queries and keys in shared memory, K-major)
+//   O [128 x 128] += P V                 (weights in tensor memory, values as they lie in the cache)
 //
-// A tensor memory lane is a position in the first product and an output column in the second.
-// A thread owns one position: its sums of 2^(s - m) stay in registers and are added up over
-// the lanes once, at the segment's end.  The reference m of a column is not its running
-// maximum: the segment's first tile sets it (to the tile's maximum; in bf16, whose range allows
-// it, to the score of the first position), and a tile raises it when a weight would exceed
-// 2^kRaise.  Only then are the sums and the accumulator in tensor memory scaled.  Columns are 64 a row; with two rows of one request both use the tiles
-// that both see in full, and the tiles at the windows' edges are visited row by row, so that
-// what one row does not see is zero for it.
+// A matrix row is a tensor memory lane and a thread of the softmax warpgroup: its maximum, its sum
+// and its weights need no other thread, the weights are written over the scores they come from, and
+// nothing of a visit but the barriers passes through shared memory, whose bandwidth (keys and values
+// in once, operands out to the products) is what bounds the kernel after HBM.  O is scaled only when
+// a row's maximum exceeds the reference of its weights by 2^kRaise.
 //
-// Roles: two warpgroups of softmax (for one row 32 columns each, for two a row each), two
-// warps that copy keys (and the queries), two that copy values (16-byte asynchronous copies
-// into the 128-byte swizzle, any stride, page or slot), one warp that issues the scores'
-// products and one the outputs'.  Every wait is bounded.
+// Two rows of one request: matrix rows 0..63 and 64..127 are theirs; both use the tiles that both
+// see in full.  What only one row sees is visited for it alone, in an order and with a second
+// accumulator such that it never meets the other's sums (0 x infinity is not 0): first the first
+// row's own tiles, then (the second row's lanes set back to 0) the common ones, then the second
+// row's own into the second accumulator.
+//
+// One row: its heads stand in both halves of the matrix.  The lower half weighs and sums the first 64
+// positions of every tile, the upper half the others, each with its own reference and accumulator;
+// they are joined at the segment's end.
+//
+// Roles: one warpgroup of softmax, one that copies keys (and the queries), one that copies values
+// (16-byte asynchronous copies into the 128-byte swizzle, any stride, page or slot), one warp that
+// issues the scores' products and one the outputs'.  Every wait is bounded.
 #pragma once
 
 #include "attn_common.cuh"
@@ -32,35 +36,24 @@ namespace attn {
 namespace tc {
 
 constexpr int kPos = 128;                 // positions of a tile
-constexpr int kCols = 64;                 // columns of a row
+constexpr int kCols = 64;                 // matrix rows of one row of the call (query heads of a chunk)
 constexpr int kHead = 128;                // head dimension
-constexpr uint32_t kHalfTile = kPos * 128;      // 64 of the dimension's elements of 128 positions
-constexpr uint32_t kTileBytes = 2 * kHalfTile;  // a tile of keys or of values
-constexpr uint32_t kQHalf = kCols * 128;
-constexpr uint32_t kQBytes = 2 * kQHalf;        // a row's queries
-constexpr uint32_t kPBytes = kPos * 128;        // a row's weights
+constexpr uint32_t kHalfTile = kPos * 128;      // 64 of the dimension's elements of 128 rows
+constexpr uint32_t kTileBytes = 2 * kHalfTile;  // a tile of keys, of values or of queries
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kLoaders = 64;              // threads that copy keys (and as many values)
-// A column's reference is raised when a weight exceeds 2^kRaise: fp16 weights have to stay
-// below 2^16, bf16 ones far enough below the largest value for their product with any value.
-template <bool BF16>
-constexpr float kRaise = BF16 ? 16.f : 8.f;
+constexpr int kLoaders = 128;             // threads that copy keys (and as many values)
+constexpr float kRaise = 8.f;             // weights are at most 2^kRaise
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOut = 256;            // first column of the accumulators, after two tiles of scores
+constexpr int kRingK = 2, kRingV = 3;     // tiles of keys and of values in shared memory
+constexpr uint32_t kKeys = 0, kValues = kKeys + kRingK * kTileBytes, kQueries = kValues + kRingV * kTileBytes,
+                   kStage = kQueries + kTileBytes;   // offsets; then room to pass sums between the halves
+constexpr int kStageRow = 33;             // floats
+constexpr int kSmemBytes = (int)kStage + 2 * kCols * kStageRow * 4 + 1024;   // the base is aligned to 1024 by hand
 
-template <int NB>
-struct Smem {
-  static constexpr int kRingK = NB == 1 ? 3 : 2;
-  static constexpr int kRingV = 2;
-  static constexpr int kQ = NB == 1 ? 2 : 1;
-  static constexpr uint32_t k = 0;
-  static constexpr uint32_t v = k + kRingK * kTileBytes;
-  static constexpr uint32_t q = v + kRingV * kTileBytes;
-  static constexpr uint32_t p = q + kQ * NB * kQBytes;
-  static constexpr uint32_t total = p + NB * kPBytes;
-  static constexpr int bytes = (int)total + 1024;   // the base is aligned to 1024 by hand
-};
-
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// D += A B^T with both operands in shared memory, or A in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
@@ -68,7 +61,34 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 
+// 8 columns of tensor memory, this warp's 32 lanes, loaded (and waited for) or stored.
+__device__ __forceinline__ void tmem_load8(uint32_t a, float (&r)[8]) {
+  uint32_t u[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+      : "r"(a)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void tmem_store8(uint32_t a, const float (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a),
+               "r"(__float_as_uint(r[0])), "r"(__float_as_uint(r[1])), "r"(__float_as_uint(r[2])),
+               "r"(__float_as_uint(r[3])), "r"(__float_as_uint(r[4])), "r"(__float_as_uint(r[5])),
+               "r"(__float_as_uint(r[6])), "r"(__float_as_uint(r[7]))
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -96,11 +116,11 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead, uint32
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// Instruction descriptor, kind::f16 with fp32 accumulation; `mn` : both operands MN-major.
+// Instruction descriptor, kind::f16 with fp32 accumulation, A K-major; `mn`: B MN-major.
 template <bool BF16>
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N, bool mn) {
-  return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((mn ? 1u : 0u) << 15) |
-         ((mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+  return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((mn ? 1u : 0u) << 16) | ((N >> 3) << 17) |
+         ((M >> 4) << 24);
 }
 
 // The walk over the units; a unit's steps are visits of (tile, rows).
@@ -181,48 +201,31 @@ struct Walk {
       tile = lo(a[0]) + v;
       rows = 1;
     } else {
-      int32_t x = v;
+      // what only the first row sees in full, what both see, what only the second does
       const bool both = c1 > c0;
+      rows = 1;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int32_t n = (both ? c0 : hi(b[j])) - lo(a[j]);
-        if (x < n) {
-          tile = lo(a[j]) + x;
+        const int32_t front = both ? c0 - lo(a[j]) : hi(b[j]) - lo(a[j]), back = both ? hi(b[j]) - c1 : 0;
+        if (v < front + back) {
+          tile = v < front ? lo(a[j]) + v : c1 + v - front;
           rows = 1u << j;
           return;
         }
-        x -= n;
+        v -= front + back;
+        if (j == 0) {
+          if (v < c1 - c0) {
+            tile = c0 + v;
+            rows = 3;
+            return;
+          }
+          v -= c1 - c0;
+        }
       }
-      if (x < c1 - c0) {
-        tile = c0 + x;
-        rows = 3;
-        return;
-      }
-      x -= c1 - c0;
-      const int32_t n = hi(b[0]) - c1;
-      rows = x < n ? 1u : 2u;
-      tile = c1 + (x < n ? x : x - n);
+      tile = 0;   // (not reached)
     }
   }
 };
-
-// Lane i of the result: the sum (or maximum) over the lanes of x[i].  x is used up.
-template <bool MAX>
-__device__ __forceinline__ float over_lanes(float (&x)[32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int n = 16; n; n >>= 1) {
-    const bool up = lane & n;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float give = up ? x[i] : x[i + n];
-      const float keep = up ? x[i + n] : x[i];
-      const float got = __shfl_xor_sync(~0u, give, n);
-      x[i] = MAX ? fmaxf(keep, got) : keep + got;
-    }
-  }
-  return x[0];
-}
 
 // Two fp32 operations in one instruction, and a maximum of three.
 __device__ __forceinline__ void fma2(float& x, float& y, float a, float bx, float by) {
@@ -288,47 +291,36 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 template <bool BF16, int NB, bool SLOTS>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  using L = Smem<NB>;
-  constexpr int kSoft = NB == 1 ? 256 : 128;      // softmax threads of a row
-  constexpr int kMine = NB == 1 ? 32 : 64;        // columns of a softmax thread
-  constexpr uint32_t kTmemCols = NB == 1 ? 256 : 512;
-  constexpr uint32_t kO = NB * 128;               // first column of the outputs
+  constexpr bool SPLIT = NB == 1;           // one row: either half of the matrix takes half of a tile's positions
+  constexpr int kSoft = 128;                // softmax threads
 
-  extern __shared__ unsigned char raw[];
+  extern __shared__ __align__(16) unsigned char raw[];
   __shared__ uint32_t err, tmem_base;
   __shared__ int abort_flag;
-  __shared__ __align__(8) uint64_t bars[2 * L::kRingK + 2 * L::kRingV + L::kQ + NB * 6 + 1];
-  __shared__ __align__(16) float ref[2][kMine];    // columns' references, negated, in units of log2
-  __shared__ __align__(16) float raise[2][32];     // what they were raised by
-  __shared__ __align__(16) float red[2][4][32];
-  __shared__ uint32_t valid[2][4];                 // lanes whose position is one
+  __shared__ __align__(8) uint64_t bars[2 * kRingK + 2 * kRingV + 1 + 3 * 2 + 1];
+  __shared__ float2 half_ml[2][kCols];      // (one row) reference and sum of either half, -1 where nothing was seen
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_addr(bars);
   auto full_k = [&](uint32_t i) { return bar0 + 8 * i; };
-  auto empty_k = [&](uint32_t i) { return bar0 + 8 * (L::kRingK + i); };
-  auto full_v = [&](uint32_t i) { return bar0 + 8 * (2 * L::kRingK + i); };
-  auto empty_v = [&](uint32_t i) { return bar0 + 8 * (2 * L::kRingK + L::kRingV + i); };
-  auto empty_q = [&](uint32_t i) { return bar0 + 8 * (2 * L::kRingK + 2 * L::kRingV + i); };
-  constexpr uint32_t kRow = 2 * L::kRingK + 2 * L::kRingV + L::kQ;
-  auto full_s = [&](uint32_t j, uint32_t i) { return bar0 + 8 * (kRow + j * 6 + i); };
-  auto empty_s = [&](uint32_t j, uint32_t i) { return bar0 + 8 * (kRow + j * 6 + 2 + i); };
-  auto full_p = [&](uint32_t j) { return bar0 + 8 * (kRow + j * 6 + 4); };
-  auto done_pv = [&](uint32_t j) { return bar0 + 8 * (kRow + j * 6 + 5); };
-  const uint32_t drain = bar0 + 8 * (kRow + NB * 6);
+  auto empty_k = [&](uint32_t i) { return bar0 + 8 * (kRingK + i); };
+  auto full_v = [&](uint32_t i) { return bar0 + 8 * (2 * kRingK + i); };
+  auto empty_v = [&](uint32_t i) { return bar0 + 8 * (2 * kRingK + kRingV + i); };
+  constexpr uint32_t kRest = 2 * kRingK + 2 * kRingV;
+  const uint32_t empty_q = bar0 + 8 * kRest, drain = bar0 + 8 * (kRest + 7);
+  // by tile of scores (visits take them in turn):
+  auto full_s = [&](uint32_t b) { return bar0 + 8 * (kRest + 1 + b); };    // scores are there
+  auto full_p = [&](uint32_t b) { return bar0 + 8 * (kRest + 3 + b); };    // weights are there
+  auto done_pv = [&](uint32_t b) { return bar0 + 8 * (kRest + 5 + b); };   // and summed: the tile is free
 
   allow_launch_after();
   if (threadIdx.x == 0) {
     err = kOk;
     abort_flag = 0;
-    for (int i = 0; i < L::kRingK; ++i) mbar_init(full_k(i), kLoaders), mbar_init(empty_k(i), 1);
-    for (int i = 0; i < L::kRingV; ++i) mbar_init(full_v(i), kLoaders), mbar_init(empty_v(i), 1);
-    for (int i = 0; i < L::kQ; ++i) mbar_init(empty_q(i), 1);
-    for (int j = 0; j < NB; ++j) {
-      for (int i = 0; i < 2; ++i) mbar_init(full_s(j, i), 1), mbar_init(empty_s(j, i), kSoft);
-      mbar_init(full_p(j), kSoft);
-      mbar_init(done_pv(j), 1);
-    }
+    for (int i = 0; i < kRingK; ++i) mbar_init(full_k(i), kLoaders), mbar_init(empty_k(i), 1);
+    for (int i = 0; i < kRingV; ++i) mbar_init(full_v(i), kLoaders), mbar_init(empty_v(i), 1);
+    mbar_init(empty_q, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(full_s(b), 1), mbar_init(full_p(b), kSoft), mbar_init(done_pv(b), 1);
     mbar_init(drain, 2);
     fence_mbar_init();
   }
@@ -342,314 +334,389 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   const uint32_t tmem = tmem_base;
   volatile int* abort = &abort_flag;
 
-  Split sp;
-  Walk<NB, SLOTS> at;
-  Rows meta{};
-  const bool work = find_range<Walk<NB, SLOTS>, SLOTS, kWarps>(p, meta, sp, at, blockIdx.x, &err);
-  if (threadIdx.x == 0) {
-    if (work) p.open_row[blockIdx.x] = -1;
-    if (blockIdx.x == 0) *p.active = sp.active;
+  // A role walks over its segments (the part of a unit in the CTA's range) and a segment's visits.
+  // What only a segment's ends need lies in shared memory, a copy a warp: in registers it would push
+  // the visits' own values out to local memory, for which no L1 is left.
+  struct Place {
+    Walk<NB, SLOTS> at;
+    int64_t here, stop;   // flat indices of the segment's first visit, and of the range's end
+  };
+  __shared__ Place places[kWarps];
+  __shared__ Split split;
+  __shared__ Rows meta;
+  Walk<NB, SLOTS>& at = places[warp].at;
+  bool work;
+  {
+    Split sp;
+    Walk<NB, SLOTS> first;
+    Rows rows{};
+    work = find_range<Walk<NB, SLOTS>, SLOTS, kWarps>(p, rows, sp, first, blockIdx.x, raw, &err);
+    if (threadIdx.x == 0) {
+      if (work) p.open_row[blockIdx.x] = -1;
+      if (blockIdx.x == 0) *p.active = sp.active;
+      split = sp;
+      meta = rows;
+    }
+    if (work && lane == 0) {
+      places[warp].at = first;
+      places[warp].here = sp.first(blockIdx.x);
+      places[warp].stop = sp.first(blockIdx.x + 1);
+    }
   }
+  __syncthreads();
+  // The segment's last visit (and one more); then, on to the next segment: false at the range's end.
+  auto segment_end = [&]() { return (int32_t)min((int64_t)at.nsub, at.s + (places[warp].stop - places[warp].here)); };
+  auto next_segment = [&](int32_t v1) {
+    __syncwarp();
+    if (lane == 0) {
+      places[warp].here += v1 - at.s;
+      if (places[warp].here < places[warp].stop) at.next_unit(p, meta);
+    }
+    __syncwarp();
+    return places[warp].here < places[warp].stop;
+  };
+  // Whether the range goes on after the segment, and with the next row (else another unit of this one).
+  auto goes_on = [&](int32_t v1) { return places[warp].here + (v1 - at.s) < places[warp].stop; };
+  auto next_is_row = [&]() { return at.chunk + 1 == p.chunks && at.kv + 1 == p.kv_heads; };
   if (work) {
-    // A role walks over its segments (the part of a unit in the CTA's range) and a segment's visits.
-    int64_t here = sp.first(blockIdx.x);                  // flat index of the segment's first visit
-    const int64_t stop = sp.first(blockIdx.x + 1);
-    // registers: 512 threads are launched with 128 each; two warpgroups of 152 and two of 104 are as many
-    if (warp < 8) {
+    // registers: 512 threads are launched with 128 each; a warpgroup of 152 and three of 120 are as many
+    if (warp < 4) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
       // ------------------------------------------------------------ softmax ----
-      const int wg = warp >> 2, x = threadIdx.x & 127;      // warpgroup, tensor memory lane
-      const uint32_t bar_id = 1 + wg;
-      const uint32_t j = NB == 1 ? 0 : wg;                  // row of the group
-      const uint32_t col0 = NB == 1 ? wg * 32 : 0;          // first column
-      const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // this warp's 32 lanes
-      const uint32_t p_row = smem + L::p + j * kPBytes + (uint32_t)x * 128;
-      const float c = p.scale_log2;
-      float sum[kMine];
-      float mine_ref[kMine / 32];    // lane i: the reference of column 32 h + i, -inf if unset
-      bool unset[kMine / 32];
-      uint32_t n = 0;                // visits of this row so far
-      bool ok = true, dead = false;
-      // (slots) the slot of this thread's position of the next visit, asked for a visit ahead
-      int32_t slot = -1;
+      const int x = threadIdx.x;                       // matrix row, tensor memory lane
+      const uint32_t part_of = (uint32_t)warp >> 1;    // half of the matrix: the row of the group, or the positions' half
+      constexpr uint32_t kAll = 1;                     // barrier of the warpgroup
+      constexpr int CH = SPLIT ? 2 : 4;                // 32 positions each: what a thread weighs of a tile
+      const int c0 = SPLIT ? (int)part_of * 2 : 0;
+      const uint32_t lanes = (uint32_t)warp << 21;     // this warp's 32 lanes
+      const uint32_t out_a = tmem + lanes + kOut + (SPLIT ? part_of * kHead : 0), out_b = tmem + lanes + kOut + kHead;
+      uint32_t n = 0;                // visits so far
+      bool ok = true;
+      bool more = true;
+      // (slots) the slots of the next visit's positions, asked for a visit ahead
+      int32_t slot[CH];
+      const int32_t* list = nullptr;
+      auto ask = [&](int32_t v) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          const int32_t pos = v * kPos + (c0 + k) * 32 + lane;
+          slot[k] = pos < p.n_slots ? list[pos] : -1;
+        }
+      };
       if constexpr (SLOTS) {
-        const int32_t pos = at.s * kPos + x;
-        if (pos < p.n_slots) slot = p.slots[(int64_t)at.row0 * p.n_slots + pos];
+        list = p.slots + (int64_t)at.row0 * p.n_slots;
+        ask(at.s);
       }
-      while (here < stop && !dead) {
-        const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
-        const bool cut_front = v0 > 0;
-        const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;   // first query head
-        const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
-        int32_t win_a = at.a[0], win_b = at.b[0];                        // this row's window
-        if (NB == 2 && j == 1) win_a = at.a[NB - 1], win_b = at.b[NB - 1];
-        const bool live = win_b > win_a;
-        bool visited = false, seen = false;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) sum[i] = 0.f;
-#pragma unroll
-        for (int h = 0; h < kMine / 32; ++h) mine_ref[h] = kNegInf, unset[h] = true;
-        const int32_t* list = nullptr;
-        if constexpr (SLOTS) list = p.slots + (int64_t)at.row0 * p.n_slots;
-        for (int32_t v = v0; v < v1; ++v) {
+      while (more) {
+        const int32_t v1 = segment_end();
+        float ref = kNegInf, sum[4] = {0.f, 0.f, 0.f, 0.f};
+        bool had_a = false, had_b = false;   // the accumulators hold something of this matrix row
+        bool foreign = false;                // the first accumulator holds the other row's tiles alone in this row's lanes
+        bool seen = false;
+        for (int32_t v = at.s; v < v1; ++v, ++n) {
+          const uint32_t b = n & 1;
           int32_t tile;
           uint32_t rows;
           at.visit(v, tile, rows);
-          if (NB == 2 && !(rows >> j & 1)) continue;
-          const int32_t pos = tile * kPos + x;
-          bool on;
+          const bool mine = SPLIT || (rows >> part_of & 1);
+          // which of the positions this row sees
+          uint32_t on[CH];
+#pragma unroll
+          for (int k = 0; k < CH; ++k) on[k] = ~0u;
           if constexpr (SLOTS) {
-            on = slot >= 0 && slot < p.num_pages * kPage;
-            slot = -1;
-            if (v + 1 < v1) {
-              if (pos + kPos < p.n_slots) slot = list[pos + kPos];
-            } else if (here + (v1 - v0) < stop) {
-              // the next unit's first: of this row, or of the next
-              if (at.chunk + 1 == p.chunks && at.kv + 1 == p.kv_heads) list += p.n_slots;
-              if (x < p.n_slots) slot = list[x];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) on[k] = __ballot_sync(~0u, slot[k] >= 0 && slot[k] < p.num_pages * kPage);
+            if (v + 1 < v1) ask(v + 1);
+          } else if (rows != 3) {
+            const int32_t a = at.a[SPLIT ? 0 : part_of], z = at.b[SPLIT ? 0 : part_of];
+            if (tile * kPos < a || tile * kPos + kPos > z) {
+#pragma unroll
+              for (int k = 0; k < CH; ++k) {
+                const int32_t pos = tile * kPos + (c0 + k) * 32 + lane;
+                on[k] = __ballot_sync(~0u, pos >= a && pos < z);
+              }
             }
-          } else {
-            on = pos >= win_a && pos < win_b;
           }
-          const bool had = visited;   // the segment's output of this row has been begun
-          visited = true;
-          seen |= on;
-          const uint32_t lanes_on = __ballot_sync(~0u, on);
-          ok &= wait(full_s(j, n & 1), n >> 1 & 1, abort, &err);
+          ok &= wait(full_s(b), n >> 1 & 1, abort, &err);
           tc_fence_after();
-#pragma unroll
-          for (int h = 0; h < kMine / 32; ++h) {
-            uint32_t rs[32];
-            tmem_ld32(tmem + lanes + (j * 2 + (n & 1)) * kCols + col0 + h * 32, rs);
-            tmem_wait_ld32(rs);
-            if (h == kMine / 32 - 1) {
-              tc_fence_before();
-              mbar_arrive(empty_s(j, n & 1));
-            }
-            float d[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) d[i] = __uint_as_float(rs[i]);
-            if (lanes_on != ~0u) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) d[i] = on ? d[i] : kNegInf;
-            }
-            if constexpr (!SLOTS) {
-              if (p.logits && on) {
-                const int64_t width = (int64_t)p.max_pages * kPage;
-                float* dst = p.logits + ((int64_t)(at.row0 + j) * p.q_heads + h0 + col0 + h * 32) * width + pos;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if ((int)col0 + h * 32 + i < heads) dst[i * width] = d[i];
-              }
-            }
+          const uint32_t s = tmem + lanes + b * kPos + c0 * 32, w_at = tmem + lanes + b * kPos + c0 * 16;
+          if (mine) {
+            uint32_t r[2][32];
+            // chunk k's maximum (its scores put down first, where the weights are to be added up)
             float top = kNegInf, top2 = kNegInf;
+            auto look = [&](int k, uint32_t (&r)[32]) {
+              if constexpr (!SLOTS) {
+                if (p.logits) {
+                  const int64_t width = (int64_t)p.max_pages * kPage;
+                  const int32_t pos = tile * kPos + (c0 + k) * 32, h = at.chunk * p.chunk_heads + (x & (kCols - 1));
+                  if ((x & (kCols - 1)) < p.chunk_heads && h < p.group && pos < width) {
+                    float4* dst = (float4*)(p.logits +
+                                            ((int64_t)(at.row0 + (SPLIT ? 0 : part_of)) * p.q_heads + at.kv * p.group + h) *
+                                                width + pos);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (!unset[h]) r = *(const float4*)&ref[wg][h * 32 + i];   // the negated references
-              fma2(d[i], d[i + 1], c, r.x, r.y);
-              fma2(d[i + 2], d[i + 3], c, r.z, r.w);
-              top = max3(top, d[i], d[i + 1]);
-              top2 = max3(top2, d[i + 2], d[i + 3]);
-            }
-            top = fmaxf(top, top2);
-            for (int attempt = 0; attempt < 2; ++attempt) {
-              if (!bar_red_or(bar_id, 128, unset[h] || top > kRaise<BF16> || !ok)) break;
-              // a reference is to be set or raised (or a wait gave up): in bf16 first to the first
-              // position's score, and where that leaves too large a weight, as always in fp16, to the maximum
-              if (had) {
-                ok &= wait(done_pv(j), (n - 1) & 1, abort, &err);
-                tc_fence_after();
-              }
-              // lane i of every warp: what column i is compared with
-              const bool first = BF16 && attempt == 0 && unset[h];
-              if (lane == 0) valid[wg][warp & 3] = lanes_on;
-              if (first) {
-                if (lane == __ffs(lanes_on) - 1) {
-#pragma unroll
-                  for (int i = 0; i < 32; i += 4)
-                    *(float4*)&red[wg][warp & 3][i] = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
-                }
-              } else {
-                float t[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) t[i] = d[i];
-                red[wg][warp & 3][lane] = over_lanes<true>(t);
-              }
-              if (bar_red_or(bar_id, 128, !ok)) {
-                dead = true;
-                break;
-              }
-              float m = kNegInf;
-#pragma unroll
-              for (int i = 3; i >= 0; --i) {
-                const float y = red[wg][i][lane];
-                if (valid[wg][i]) m = first ? y : fmaxf(m, y);
-              }
-              const bool was = mine_ref[h] != kNegInf;
-              const float base = was ? mine_ref[h] : 0.f;
-              // never lowered; set at the first finite score
-              const bool set = m != kNegInf && (m > 0.f || !was);
-              const float raised = set ? base + m : base;
-              if (set) mine_ref[h] = raised;
-              if ((warp & 3) == 0) {
-                ref[wg][h * 32 + lane] = mine_ref[h] == kNegInf ? 0.f : -mine_ref[h];
-                raise[wg][lane] = __fsub_rn(raised, base);
-              }
-              unset[h] = __any_sync(~0u, mine_ref[h] == kNegInf);
-              bar_sync(bar_id, 128);
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                uint32_t r[16];
-                const uint32_t o = tmem + lanes + kO + j * kCols + col0 + h * 32 + y * 16;
-                if (had) {
-                  tmem_ld16(o, r);
-                  tmem_wait_ld16(r);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float by = raise[wg][y * 16 + i];
-                  d[y * 16 + i] -= by;
-                  top = y + i == 0 ? d[0] : fmaxf(top, d[y * 16 + i]);
-                  if (had) {
-                    const float f = ex2(-by);
-                    sum[h * 32 + y * 16 + i] *= f;
-                    r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                    for (int i = 0; i < 8; ++i)
+                      dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                           __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
                   }
                 }
-                if (had) tmem_st16(o, r);
               }
-              if (had) tmem_wait_st();
-              if (!first) break;
-            }
-            if (dead) break;   // a wait gave up: the whole warpgroup has voted
-            if (h == 0 && n > 0) ok &= wait(done_pv(j), (n - 1) & 1, abort, &err);
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float e0 = ex2(d[i + 2 * y]), e1 = ex2(d[i + 2 * y + 1]);
-                add2(sum[h * 32 + i + 2 * y], sum[h * 32 + i + 2 * y + 1], e0, e1);
-                w[y] = pack2<BF16>(e0, e1);
-              }
-              const uint32_t piece = (col0 + h * 32 + i) / 8;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + ((piece ^ (x & 7)) << 4)), "r"(w[0]),
-                           "r"(w[1]), "r"(w[2]), "r"(w[3])
-                           : "memory");
-            }
-          }
-          if (dead) break;
-          fence_proxy_async_smem();
-          tc_fence_before();
-          mbar_arrive(full_p(j));
-          ++n;
-        }
-        here += v1 - v0;
-        if (!dead) {
-          const bool unit_end = v1 == at.nsub;
-          const bool whole = unit_end && !cut_front;
-          const int which = cut_front ? 0 : 1;
-          if (!unit_end && !cut_front && threadIdx.x == 0) {
-            p.open_row[blockIdx.x] = at.row0;
-            p.open_info[blockIdx.x] =
-                make_int4(at.nrows, at.kv * p.chunks + at.chunk, sp.holder(here + (at.nsub - v1) - 1), 0);
-          }
-          if (visited) ok &= wait(done_pv(j), (n - 1) & 1, abort, &err);
-          tc_fence_after();
-          if constexpr (SLOTS) seen = bar_red_or(bar_id, 128, seen);
-          const int64_t row = at.row0 + j;
-#pragma unroll
-          for (int h = 0; h < kMine / 32; ++h) {
-            float t[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) t[i] = sum[h * 32 + i];
-            red[wg][warp & 3][lane] = over_lanes<false>(t);
-            if (bar_red_or(bar_id, 128, !ok)) {
-              dead = true;
-              break;
-            }
-            const float l = (red[wg][0][lane] + red[wg][1][lane]) + (red[wg][2][lane] + red[wg][3][lane]);
-            const int32_t first = col0 + h * 32;
-            const int32_t cols = min(32, heads - first);
-            const float inv = SLOTS && !seen ? 0.f : 1.f / l;
-            if ((warp & 3) == 0) raise[wg][lane] = whole ? inv : 1.f;
-            bar_sync(bar_id, 128);
-            const int64_t part = ((int64_t)blockIdx.x * 2 + which) * (NB * kCols) + j * kCols + first;
-            if ((warp & 3) == 0 && lane < cols && live) {
-              const float m = mine_ref[h];
-              if (!whole) {
-                p.part_ml[part + lane] = make_float2(m, !visited || (SLOTS && !seen) ? -1.f : l);
-              } else {
-                const int64_t i = row * p.q_heads + h0 + first + lane;
-                if (p.lse) p.lse[i] = (m + log2f(l)) * 0.6931471805599453f;
-                if (p.row_stat) p.row_stat[i] = make_float2(m == kNegInf ? 0.f : m, inv);
-              }
-            }
-            if (live && (whole || visited)) {
-              const uint32_t o = tmem + lanes + kO + j * kCols + first;
-              uint32_t r[32];
-              tmem_ld32(o, r);
-              tmem_wait_ld32(r);
-              if (whole) {
-                T* out = (T*)p.out + row * p.out_row + (int64_t)(h0 + first) * p.out_head + x;
-#pragma unroll
-                for (int i = 0; i < 32; ++i, out += p.out_head)
-                  if (i < cols) *out = (T)(__uint_as_float(r[i]) * raise[wg][i]);
-              } else {
-                float* po = p.part_o + part * kHead + x;
+              if (on[k] != ~0u) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (i < cols) po[i * kHead] = __uint_as_float(r[i]);
+                  if (!(on[k] >> i & 1)) r[i] = __float_as_uint(kNegInf);
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                top = max3(top, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                top2 = max3(top2, __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+              }
+              seen |= on[k] != 0;
+            };
+            if constexpr (CH == 2) {
+              // both chunks stay in registers
+              tmem_ld32(s, r[0]);
+              tmem_ld32(s + 32, r[1]);
+              tmem_wait_ld32(r[0]);
+              tmem_wait_ld32(r[1]);
+              look(0, r[0]);
+              look(1, r[1]);
+            } else {
+              // the next one is on its way meanwhile
+              tmem_ld32(s, r[0]);
+#pragma unroll
+              for (int k = 0; k < CH; ++k) {
+                tmem_wait_ld32(r[k & 1]);
+                tmem_ld32(s + (k + 1) % CH * 32, r[k & 1 ^ 1]);   // (last: the first again)
+                look(k, r[k & 1]);
               }
             }
-            bar_sync(bar_id, 128);   // red is free again
+            top = __fmul_rn(fmaxf(top, top2), p.scale_log2);
+            // does its weights' reference have to follow?
+            if (__any_sync(~0u, top > ref + kRaise || (ref == kNegInf && top > kNegInf))) {
+              const float raised = fmaxf(ref, top), f = ref == kNegInf ? (raised == kNegInf ? 1.f : 0.f) : ex2(ref - raised);
+              ref = raised;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum[i] *= f;
+              if (had_a || had_b) {
+                ok &= wait(done_pv(b ^ 1), (n - 1) >> 1 & 1, abort, &err);   // the last visit that added to them
+                tc_fence_after();
+#pragma unroll 1
+                for (int y = 0; y < 2 * kHead; y += 8) {
+                  if (y < kHead ? !had_a : !had_b) continue;
+                  const uint32_t o = (y < kHead ? out_a : out_b - kHead) + y;
+                  float z[8];
+                  tmem_load8(o, z);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) z[i] *= f;
+                  tmem_store8(o, z);
+                }
+                tmem_wait_st();
+              }
+            }
+            // the weights, over the scores
+            const float base = ref == kNegInf ? 0.f : -ref;
+            auto weigh = [&](int k, const uint32_t (&r)[32]) {
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float d0 = __uint_as_float(r[i]), d1 = __uint_as_float(r[i + 1]);
+                fma2(d0, d1, p.scale_log2, base, base);
+                const float e0 = ex2(d0), e1 = ex2(d1);
+                add2(sum[i & 2], sum[(i & 2) + 1], e0, e1);
+                w[i / 2] = pack2<BF16>(e0, e1);
+              }
+              tmem_st16(w_at + k * 16, w);
+            };
+            if constexpr (CH == 2) {
+              weigh(0, r[0]);
+              weigh(1, r[1]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < CH; ++k) {
+                uint32_t(&now)[32] = r[k & 1];
+                tmem_wait_ld32(now);
+                if (k + 1 < CH) tmem_ld32(s + (k + 1) * 32, r[k & 1 ^ 1]);
+                if (on[k] != ~0u) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (!(on[k] >> i & 1)) now[i] = __float_as_uint(kNegInf);
+                }
+                weigh(k, now);
+              }
+            }
+            if (!SPLIT && rows == 2) {
+              had_b = true;
+            } else {
+              had_a = true;
+            }
           }
+          if (!SPLIT) {
+            // the first row's own tiles end: what they left in the second row's lanes means nothing
+            if (!mine && rows == 1) foreign = true;
+            if (foreign && rows == 3) {
+              foreign = false;
+              if (n > 0) ok &= wait(done_pv(b ^ 1), (n - 1) >> 1 & 1, abort, &err);
+              tc_fence_after();
+              const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+              for (int y = 0; y < kHead; y += 8) tmem_store8(out_a + y, zero);
+            }
+          }
+          tmem_wait_st();
           tc_fence_before();
+          mbar_arrive(full_p(b));
+          if (!__all_sync(~0u, ok)) break;
         }
-        if (here < stop && !dead) at.next_unit(p, meta);
+
+        if constexpr (SLOTS) {
+          // the next unit's first: of this row, or of the next
+          if (goes_on(v1)) {
+            if (next_is_row()) list += p.n_slots;
+            ask(0);
+          }
+        }
+
+        // the segment ends: finish the unit, or leave its part
+        const bool cut_front = at.s > 0, unit_end = v1 == at.nsub, whole = unit_end && !cut_front;
+        const int which = cut_front ? 0 : 1;
+        if (!unit_end && !cut_front && threadIdx.x == 0) {
+          p.open_row[blockIdx.x] = at.row0;
+          p.open_info[blockIdx.x] = make_int4(at.nrows, at.kv * p.chunks + at.chunk,
+                                              split.holder(places[warp].here + (at.nsub - at.s) - 1), 0);
+        }
+        // the last visit of each tile of scores that this segment (or one before it) had
+        if (n > 0) ok &= wait(done_pv((n - 1) & 1), (n - 1) >> 1 & 1, abort, &err);
+        if (n > 1) ok &= wait(done_pv(n & 1), (n - 2) >> 1 & 1, abort, &err);
+        tc_fence_after();
+        float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const bool has = (had_a || had_b) && (!SLOTS || seen);
+        if constexpr (SPLIT) half_ml[part_of][x & (kCols - 1)] = make_float2(ref, has ? l : -1.f);
+        // every softmax thread votes on the waits, so that all leave together
+        if (bar_red_or(kAll, 128, !ok)) break;
+
+        const int32_t row_in = SPLIT ? 0 : (int32_t)part_of, col = x & (kCols - 1);
+        const int32_t head = at.chunk * p.chunk_heads + col;
+        const bool live = col < p.chunk_heads && head < p.group && at.b[row_in] > at.a[row_in];
+        const int64_t row = at.row0 + row_in;
+        const int32_t qh = at.kv * p.group + head;
+        const int64_t part = ((int64_t)blockIdx.x * 2 + which) * (NB * kCols) + row_in * kCols + col;
+        float top = ref, f = 1.f;
+        bool any = has;
+        if constexpr (SPLIT) {
+          const float2 o = half_ml[part_of ^ 1][col];
+          const bool other = o.y != -1.f;
+          top = fmaxf(has ? ref : kNegInf, other ? o.x : kNegInf);
+          const float base = top == kNegInf ? 0.f : top;
+          f = has ? ex2(ref - base) : 0.f;
+          l = (has ? l * f : 0.f) + (other ? o.y * ex2(o.x - base) : 0.f);
+          any = has || other;
+        }
+        const float inv = any ? 1.f / l : 0.f;
+        if (live && (!SPLIT || part_of == 0)) {
+          if (!whole) {
+            p.part_ml[part] = make_float2(top, any ? l : -1.f);
+          } else {
+            const int64_t i = row * p.q_heads + qh;
+            if (p.lse) p.lse[i] = (top + log2f(l)) * 0.6931471805599453f;
+            if (p.row_stat) p.row_stat[i] = make_float2(top == kNegInf ? 0.f : top, inv);
+          }
+        }
+        if (whole) f *= inv;
+        T* out = (T*)p.out + row * p.out_row + (int64_t)qh * p.out_head;
+        float* po = p.part_o + part * kHead;
+        auto emit = [&](int c, const float (&z)[8]) {   // 8 columns of the thread's row
+          if (!live) return;
+          if (whole) {
+            uint4 u;
+            u.x = pack2<BF16>(z[0], z[1]), u.y = pack2<BF16>(z[2], z[3]);
+            u.z = pack2<BF16>(z[4], z[5]), u.w = pack2<BF16>(z[6], z[7]);
+            *(uint4*)(out + c) = u;
+          } else if (any) {
+            *(float4*)(po + c) = make_float4(z[0], z[1], z[2], z[3]);
+            *(float4*)(po + c + 4) = make_float4(z[4], z[5], z[6], z[7]);
+          }
+        };
+        if constexpr (SPLIT) {
+          // each half finishes 64 columns; the other's share of them comes through shared memory, 32 at a time
+          float* stage = (float*)(raw + (smem - smem_addr(raw)) + kStage);
+          float* give = stage + (part_of * kCols + col) * kStageRow;
+          const float* take = stage + ((part_of ^ 1) * kCols + col) * kStageRow;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 8) {
+              float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+              if (has) tmem_load8(out_a + (part_of ^ 1) * 64 + c0 + c, r);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) give[c + i] = has ? r[i] * f : 0.f;
+            }
+            bar_sync(kAll, 128);
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 8) {
+              float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+              if (has) tmem_load8(out_a + part_of * 64 + c0 + c, r);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) r[i] = (has ? r[i] * f : 0.f) + take[c + i];
+              emit((int)part_of * 64 + c0 + c, r);
+            }
+            bar_sync(kAll, 128);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kHead; c += 8) {
+            float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, s[8];
+            if (had_a) tmem_load8(out_a + c, r);
+            if (had_b) {
+              tmem_load8(out_b + c, s);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) r[i] += s[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] *= f;
+            emit(c, r);
+          }
+        }
+        tc_fence_before();
+        more = next_segment(v1);
       }
     } else if (warp < 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
       // ------------------------------------------------------------- copies ----
-      const bool values = warp >= 10;
-      const int half = (warp - 8) & 1, t = threadIdx.x & (kLoaders - 1);
-      const uint32_t depth = values ? L::kRingV : L::kRingK;
-      const uint32_t ring = smem + (values ? L::v : L::k);
+      const bool values = warp >= 8;
+      const int quarter = warp & 3, t = threadIdx.x & (kLoaders - 1);
+      const uint32_t depth = values ? kRingV : kRingK;
+      const uint32_t ring = smem + (values ? kValues : kKeys);
       const T* cache = (const T*)(values ? p.v : p.k);
       const int64_t s_page = values ? p.v_page : p.k_page, s_slot = values ? p.v_slot : p.k_slot,
                     s_head = values ? p.v_head : p.k_head;
       // Offsets are in units of 16 bytes (the caches span less than 64 GB).
       const uint32_t page16 = (uint32_t)(s_page / 8), slot16 = (uint32_t)(s_slot / 8);
-      const int x = lane & 15, r0 = lane / 16;   // this lane's piece of a head, and its rows r0 + 2 i of the warp's 64
+      const int x = lane & 15, r0 = lane / 16;   // this lane's piece of a head, and its rows r0 + 2 i of the warp's 32
       uint32_t n = 0, seg = 0;                   // tiles, segments
       bool ok = true;
       uint32_t bad = kOk;
-      // the slots of this thread's two positions, or the page of the warp's 64, of the next visit: asked
-      // for a visit ahead (and a row's slots brought to L2 a row ahead)
-      int32_t entry[2];
+      // the slot of this thread's position, or the page of the warp's 32, of the next visit: asked for a
+      // visit ahead (and a row's slots brought to L2 a row ahead)
+      int32_t entry;
       auto ask = [&](const int32_t* list, int32_t tile) {
         if constexpr (SLOTS) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int32_t pos = tile * kPos + half * 64 + e * 32 + lane;
-            entry[e] = pos < p.n_slots ? list[pos] : -1;
-          }
+          const int32_t pos = tile * kPos + quarter * 32 + lane;
+          entry = pos < p.n_slots ? list[pos] : -1;
         } else {
-          const int32_t i = tile * 2 + half;
-          entry[0] = i < p.max_pages ? list[i] : -1;
+          const int32_t i = tile * 2 + quarter / 2;
+          entry = i < p.max_pages ? list[i] : -1;
         }
       };
-      const int32_t* list = nullptr;
       if constexpr (SLOTS) ask(p.slots + (int64_t)at.row0 * p.n_slots, at.s);
-      while (here < stop && ok) {
-        const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
-        here += v1 - v0;
+      bool more = true;
+      while (more) {
+        const int32_t v0 = at.s, v1 = segment_end();
         int32_t tile;
         uint32_t rows;
+        const int32_t* list;
         if constexpr (SLOTS) {
           list = p.slots + (int64_t)at.row0 * p.n_slots;
-          if (warp == 10 && at.row0 + 1 < p.rows)
+          if (warp == 8 && at.row0 + 1 < p.rows)
             for (int32_t i = lane * 32; i < p.n_slots; i += 32 * 32)
               asm volatile("prefetch.global.L2 [%0];" ::"l"(list + p.n_slots + i));
         } else {
@@ -658,63 +725,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           ask(list, tile);
         }
         if (!values) {
-          // the queries, with the segment's first tile of keys
-          const uint32_t b = seg % L::kQ;
-          ok = __all_sync(~0u, wait(empty_q(b), (seg / L::kQ & 1) ^ 1, abort, &err));
+          // the queries, with the segment's first tile of keys (one row's stand in both halves)
+          ok = __all_sync(~0u, wait(empty_q, (seg & 1) ^ 1, abort, &err));
           if (!ok) break;
           const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
           const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
-          const uint32_t dst = smem + L::q + b * (NB * kQBytes);
-#pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            const bool live = at.b[j] > at.a[j];
-            const T* q = (const T*)p.q + (int64_t)(at.row0 + (live ? j : 0)) * p.q_row + (int64_t)h0 * p.q_head;
 #pragma unroll 4
-            for (int i = t; i < kCols * 16; i += kLoaders) {
-              const int r = i / 16, y = i % 16;
-              const bool in = live && r < heads;
-              copy16(dst + j * kQBytes + (y / 8) * kQHalf + r * 128 + (((y & 7) ^ (r & 7)) << 4),
-                     q + (in ? (int64_t)r * p.q_head : 0) + y * 8, in ? 16u : 0u);
-            }
+          for (int i = t; i < 128 * 16; i += kLoaders) {
+            const int r = i / 16, y = i % 16, j = SPLIT ? 0 : r / kCols, h = r % kCols;
+            const bool in = at.b[j] > at.a[j] && h < heads;
+            const T* q = (const T*)p.q + (in ? (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head : 0);
+            copy16(smem + kQueries + (y / 8) * kHalfTile + r * 128 + (((y & 7) ^ (r & 7)) << 4), q + y * 8, in ? 16u : 0u);
           }
           ++seg;
         }
         const char* base = (const char*)(cache + at.kv * s_head + x * 8);
         for (int32_t v = v0; v < v1; ++v) {
           at.visit(v, tile, rows);
-          // where the warp's 64 positions lie; `all`: every one of them is read
-          uint32_t from[2];
-          bool all = true;
+          uint32_t from;   // where this lane's position lies, or ~0
           if constexpr (SLOTS) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool on = entry[e] >= 0 && entry[e] < p.num_pages * kPage;
-              if (!on && entry[e] != -1) bad = kErrInvalidPage;
-              from[e] = on ? (uint32_t)(entry[e] / kPage) * page16 + (uint32_t)(entry[e] % kPage) * slot16 : ~0u;
-              all &= on;
-            }
+            const bool on = entry >= 0 && entry < p.num_pages * kPage;
+            if (!on && entry != -1) bad = kErrInvalidPage;
+            from = on ? (uint32_t)(entry / kPage) * page16 + (uint32_t)(entry % kPage) * slot16 : ~0u;
             if (v + 1 < v1) {
               ask(list, v + 1);
-            } else if (here < stop) {
+            } else if (goes_on(v1)) {
               // the next unit's first: of this row, or of the next
-              ask(list + (at.chunk + 1 == p.chunks && at.kv + 1 == p.kv_heads ? p.n_slots : 0), 0);
+              ask(list + (next_is_row() ? p.n_slots : 0), 0);
             }
           } else {
             int32_t lo = 0, hi = INT32_MAX;   // seen by every row of the visit
 #pragma unroll
             for (int j = 0; j < NB; ++j)
               if (rows >> j & 1) lo = max(lo, at.a[j]), hi = min(hi, at.b[j]);
-            const int32_t first = tile * kPos + half * 64;
-            const bool any = first < hi && first + 64 > lo, there = entry[0] >= 0 && entry[0] < p.num_pages;
+            const int32_t first = tile * kPos + quarter * 32;
+            const bool any = first < hi && first + 32 > lo, there = entry >= 0 && entry < p.num_pages;
             if (any && !there) bad = kErrInvalidPage;
-            const uint32_t page = there ? (uint32_t)entry[0] * page16 : 0u;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int32_t pos = first + e * 32 + lane;
-              const bool on = there && pos >= lo && pos < hi;
-              from[e] = on ? page + (uint32_t)(e * 32 + lane) * slot16 : ~0u;
-              all &= on;
-            }
+            const bool on = there && first + lane >= lo && first + lane < hi;
+            from = on ? (uint32_t)entry * page16 + (uint32_t)((quarter & 1) * 32 + lane) * slot16 : ~0u;
             if (v + 1 < v1) {
               int32_t next_tile;
               uint32_t next_rows;
@@ -722,27 +770,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               ask(list, next_tile);
             }
           }
-          all = __all_sync(~0u, all);
+          const bool all = __all_sync(~0u, from != ~0u);
           const uint32_t slot = n % depth;
           ok = __all_sync(~0u, wait(values ? empty_v(slot) : empty_k(slot), (n / depth & 1) ^ 1, abort, &err));
           if (!ok) break;
-          const uint32_t dst = ring + slot * kTileBytes + (x / 8) * kHalfTile + (uint32_t)half * (64 * 128);
+          const uint32_t dst = ring + slot * kTileBytes + (x / 8) * kHalfTile + (uint32_t)quarter * (32 * 128);
           uint32_t to[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) to[i] = dst + (2 * i + r0) * 128 + (((x & 7) ^ (2 * i + r0)) << 4);
-          if (!SLOTS && all) {
-            const char* src = base + (uint64_t)__shfl_sync(~0u, from[0], 0) * 16 + (int64_t)r0 * s_slot * 2;
+          if (all) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i, src += 4 * s_slot) copy16(to[i & 3] + (i >> 2) * 1024, src, 16u);
-          } else if (all) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              copy16(to[i & 3] + (i >> 2) * 1024,
-                     base + (uint64_t)__shfl_sync(~0u, from[i / 16], (2 * i + r0) & 31) * 16, 16u);
+            for (int i = 0; i < 16; ++i)
+              copy16(to[i & 3] + (i >> 2) * 1024, base + (uint64_t)__shfl_sync(~0u, from, 2 * i + r0) * 16, 16u);
           } else {
-#pragma unroll 8
-            for (int i = 0; i < 32; ++i) {
-              const uint32_t o = __shfl_sync(~0u, i < 16 ? from[0] : from[1], (2 * i + r0) & 31);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t o = __shfl_sync(~0u, from, 2 * i + r0);
               const bool in = o != ~0u;
               copy16(to[i & 3] + (i >> 2) * 1024, base + (uint64_t)(in ? o : 0u) * 16, in ? 16u : 0u);
             }
@@ -750,104 +793,82 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           arrive_when_copied(values ? full_v(slot) : full_k(slot));
           ++n;
         }
-        if (here < stop && ok) at.next_unit(p, meta);
+        if (!ok) break;
+        more = next_segment(v1);
       }
       copy_wait_all();
       bad = __reduce_max_sync(~0u, bad);
       if (lane == 0 && bad != kOk) atomicMax(&err, bad);
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-      // ----------------------------------------------------------- products ----
-      // One warp issues the scores' products and one the outputs', each its own waits in order; the
-      // other two warps have no work.
-      bool ok = true;
-      uint32_t n = 0;                   // visits
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
       if (warp == 12) {
-        constexpr uint32_t kQK = idesc_f16<BF16>(128, kCols, false);
-        uint32_t seg = 0, ns[NB];       // segments; visits of each row
+      // ----------------------------------------------------- scores' products ----
+      constexpr uint32_t kQK = idesc_f16<BF16>(128, kPos, false);
+      const uint64_t q = desc128(smem + kQueries, 16, 1024);
+      uint32_t n = 0;
+      bool ok = true, more = true;
+      while (more) {
+        const int32_t v1 = segment_end();
+        for (int32_t v = at.s; v < v1; ++v, ++n) {
+          const uint32_t slot = n % kRingK, b = n & 1;
+          ok = __all_sync(~0u, wait(full_k(slot), n / kRingK & 1, abort, &err));
+          ok = ok && __all_sync(~0u, wait(done_pv(b), (n >> 1 & 1) ^ 1, abort, &err));
+          if (!ok) break;
+          fence_proxy_async_smem();   // the copies' writes before the products' reads
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t k = desc128(smem + kKeys + slot * kTileBytes, 16, 1024);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) ns[j] = 0;
-        while (here < stop && ok) {
-          const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
-          here += v1 - v0;
-          const uint32_t qb = seg % L::kQ;
-          const uint64_t q = desc128(smem + L::q + qb * (NB * kQBytes), 16, 1024);
-          for (int32_t v = v0; v < v1; ++v) {
-            int32_t tile;
-            uint32_t rows;
-            at.visit(v, tile, rows);
-            const uint32_t slot = n % L::kRingK;
-            ok = __all_sync(~0u, wait(full_k(slot), n / L::kRingK & 1, abort, &err));
-            fence_proxy_async_smem();   // the copies' writes before the products' reads
-            const uint64_t a = desc128(smem + L::k + slot * kTileBytes, 16, 1024);
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-              if (!(rows >> j & 1)) continue;
-              const uint32_t b = ns[j] & 1;
-              ok = ok && __all_sync(~0u, wait(empty_s(j, b), (ns[j] >> 1 & 1) ^ 1, abort, &err));
-              tc_fence_after();
-              if (ok && elect_one()) {
-#pragma unroll
-                for (int k = 0; k < kHead / 16; ++k)   // 16 elements: 32 bytes of a row
-                  mma_f16(tmem + (j * 2 + b) * kCols, a + (k / 4) * (kHalfTile >> 4) + (k % 4) * 2,
-                          q + j * (kQBytes >> 4) + (k / 4) * (kQHalf >> 4) + (k % 4) * 2, kQK, k > 0);
-                tc_commit(full_s(j, b));
-              }
-              __syncwarp();
-              ++ns[j];
-            }
-            if (!ok) break;
-            if (elect_one()) tc_commit(empty_k(slot));
-            __syncwarp();
-            ++n;
+            for (int i = 0; i < kHead / 16; ++i)   // 16 elements: 32 bytes of a row
+              mma_ss(tmem + b * kPos, q + (i / 4) * (kHalfTile >> 4) + (i % 4) * 2, k + (i / 4) * (kHalfTile >> 4) + (i % 4) * 2,
+                     kQK, i > 0);
+            tc_commit(full_s(b));
+            tc_commit(empty_k(slot));
           }
-          if (ok && elect_one()) tc_commit(empty_q(qb));
           __syncwarp();
-          ++seg;
-          if (here < stop && ok) at.next_unit(p, meta);
         }
+        if (!ok) break;
+        if (elect_one()) tc_commit(empty_q);
+        __syncwarp();
+        more = next_segment(v1);
+      }
       } else if (warp == 13) {
-        constexpr uint32_t kPV = idesc_f16<BF16>(128, kCols, true);
-        uint32_t np[NB];                // visits of each row
-        bool fresh[NB];                 // the row's output is to be begun anew
+      // ---------------------------------------------------- outputs' products ----
+      constexpr uint32_t kPV = idesc_f16<BF16>(128, kHead, true);
+      uint32_t n = 0;
+      bool ok = true, more = true;
+      while (more) {
+        const int32_t v1 = segment_end();
+        bool fresh[2] = {true, true};   // the accumulator is to be begun anew
+        for (int32_t v = at.s; v < v1; ++v, ++n) {
+          int32_t tile;
+          uint32_t rows;
+          at.visit(v, tile, rows);
+          const uint32_t slot = n % kRingV, b = n & 1;
+          const uint32_t to = !SPLIT && rows == 2 ? 1u : 0u;
+          ok = __all_sync(~0u, wait(full_v(slot), n / kRingV & 1, abort, &err));
+          ok = ok && __all_sync(~0u, wait(full_p(b), n >> 1 & 1, abort, &err));
+          if (!ok) break;
+          fence_proxy_async_smem();   // the copies' writes before the products' reads
+          tc_fence_after();
+          const bool anew = to ? fresh[1] : fresh[0];
+          // 16 positions a product: 8 columns of weights, 2048 bytes of values
+          if (elect_one()) {
+            const uint64_t val = desc128(smem + kValues + slot * kTileBytes, kHalfTile, 1024);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) np[j] = 0, fresh[j] = true;
-        while (here < stop && ok) {
-          const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
-          here += v1 - v0;
-#pragma unroll
-          for (int j = 0; j < NB; ++j) fresh[j] = true;
-          for (int32_t v = v0; v < v1; ++v) {
-            int32_t tile;
-            uint32_t rows;
-            at.visit(v, tile, rows);
-            const uint32_t slot = n % L::kRingV;
-            ok = __all_sync(~0u, wait(full_v(slot), n / L::kRingV & 1, abort, &err));
-            fence_proxy_async_smem();   // the copies' writes before the products' reads
-            const uint64_t a = desc128(smem + L::v + slot * kTileBytes, kHalfTile, 1024);
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-              if (!(rows >> j & 1)) continue;
-              ok = ok && __all_sync(~0u, wait(full_p(j), np[j] & 1, abort, &err));
-              tc_fence_after();
-              if (ok && elect_one()) {
-                const uint64_t b = desc128(smem + L::p + j * kPBytes, 1024, 1024);
-#pragma unroll
-                for (int k = 0; k < kPos / 16; ++k)   // 16 positions: 2048 bytes of either
-                  mma_f16(tmem + kO + j * kCols, a + k * (2048 >> 4), b + k * (2048 >> 4), kPV, !fresh[j] || k > 0);
-                tc_commit(done_pv(j));
-              }
-              __syncwarp();
-              fresh[j] = false;
-              ++np[j];
+            for (int i = 0; i < kPos / 16; ++i) {
+              const uint32_t out = tmem + kOut + (SPLIT ? i / 4 : to) * kHead;
+              mma_ts(out, tmem + b * kPos + i * 8, val + i * (2048 >> 4), kPV, !anew || (SPLIT ? i % 4 : i) > 0);
             }
-            if (!ok) break;
-            if (elect_one()) tc_commit(empty_v(slot));
-            __syncwarp();
-            ++n;
+            tc_commit(done_pv(b));
+            tc_commit(empty_v(slot));
           }
-          if (here < stop && ok) at.next_unit(p, meta);
+          __syncwarp();
+          if (to) fresh[1] = false; else fresh[0] = false;
         }
+        if (!ok) break;
+        more = next_segment(v1);
+      }
       }
     }
   }
@@ -883,9 +904,9 @@ template <bool BF16, int NB, bool SLOTS>
 cudaError_t launch(const AttnParams& p, int sm_count, cudaStream_t stream) {
   auto* kernel = attn_tc_kernel<BF16, NB, SLOTS>;
   static std::atomic<bool> done[64];
-  cudaError_t e = set_smem_once(kernel, Smem<NB>::bytes, done);
+  cudaError_t e = set_smem_once(kernel, kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  kernel<<<sm_count, kThreads, Smem<NB>::bytes, stream>>>(p);
+  kernel<<<sm_count, kThreads, kSmemBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
