@@ -7,9 +7,9 @@
 //   S [128 x 128 positions] = Q K^T      (queries and keys in shared memory, K-major)
 //   O [128 x 128] += P V                 (weights in tensor memory, values as they lie in the cache)
 //
-// A matrix row is a tensor memory lane and a thread of the softmax warpgroup: its maximum, its sum
-// and its weights need no other thread, the weights are written over the scores they come from, and
-// nothing of a visit but the barriers passes through shared memory, whose bandwidth (keys and values
+// A matrix row is a tensor memory lane and a thread of each softmax warpgroup: its sum and its
+// weights need no other thread, the weights are written over the scores they come from, and next to
+// nothing of a visit passes through shared memory, whose bandwidth (keys and values
 // in once, operands out to the products) is what bounds the kernel after HBM.  O is scaled only when
 // a row's maximum exceeds the reference of its weights by 2^kRaise.
 //
@@ -23,7 +23,8 @@
 // positions of every tile, the upper half the others, each with its own reference and accumulator;
 // they are joined at the segment's end.
 //
-// Roles: one warpgroup of softmax, one that copies keys (and the queries), one that copies values
+// Roles: two warpgroups of softmax (the same rows, half of the positions each; a row's maximum is
+// the only thing that its two threads exchange), one that copies keys (and the queries), one that copies values
 // (16-byte asynchronous copies into the 128-byte swizzle, any stride, page or slot), one warp that
 // issues the scores' products and one the outputs'.  Every wait is bounded.
 #pragma once
@@ -40,7 +41,7 @@ constexpr int kCols = 64;                 // matrix rows of one row of the call 
 constexpr int kHead = 128;                // head dimension
 constexpr uint32_t kHalfTile = kPos * 128;      // 64 of the dimension's elements of 128 rows
 constexpr uint32_t kTileBytes = 2 * kHalfTile;  // a tile of keys, of values or of queries
-constexpr int kWarps = 16;
+constexpr int kWarps = 20;
 constexpr int kThreads = kWarps * 32;
 constexpr int kLoaders = 128;             // threads that copy keys (and as many values)
 constexpr float kRaise = 8.f;             // weights are at most 2^kRaise
@@ -49,8 +50,8 @@ constexpr uint32_t kOut = 256;            // first column of the accumulators, a
 constexpr int kRingK = 2, kRingV = 3;     // tiles of keys and of values in shared memory
 constexpr uint32_t kKeys = 0, kValues = kKeys + kRingK * kTileBytes, kQueries = kValues + kRingV * kTileBytes,
                    kStage = kQueries + kTileBytes;   // offsets; then room to pass sums between the halves
-constexpr int kStageRow = 33;             // floats
-constexpr int kSmemBytes = (int)kStage + 2 * kCols * kStageRow * 4 + 1024;   // the base is aligned to 1024 by hand
+constexpr int kStageRow = 17;             // floats
+constexpr int kSmemBytes = (int)kStage + 4 * kCols * kStageRow * 4 + 1024;   // the base is aligned to 1024 by hand
 
 // D += A B^T with both operands in shared memory, or A in tensor memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -268,6 +269,7 @@ __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_al
 // A bounded wait: false when it gave up (after kWaitLimitNs, or because another role did).
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   uint64_t t0 = 0;
+  if (*abort) return false;
   for (uint32_t i = 0;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 63u) {
@@ -292,13 +294,15 @@ template <bool BF16, int NB, bool SLOTS>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr bool SPLIT = NB == 1;           // one row: either half of the matrix takes half of a tile's positions
-  constexpr int kSoft = 128;                // softmax threads
+  constexpr int kSoft = 256;                // softmax threads
 
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ uint32_t err, tmem_base;
   __shared__ int abort_flag;
   __shared__ __align__(8) uint64_t bars[2 * kRingK + 2 * kRingV + 1 + 3 * 2 + 1];
   __shared__ float2 half_ml[2][kCols];      // (one row) reference and sum of either half, -1 where nothing was seen
+  __shared__ float row_max[2][2][128];      // by visit and warpgroup
+  __shared__ float row_sum[2][128];         // by warpgroup, -1 where nothing was seen
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_addr(bars);
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     mbar_init(drain, 2);
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(smem_addr(&tmem_base), kTmemCols);
     tmem_relinquish();
   }
@@ -379,16 +383,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   auto goes_on = [&](int32_t v1) { return places[warp].here + (v1 - at.s) < places[warp].stop; };
   auto next_is_row = [&]() { return at.chunk + 1 == p.chunks && at.kv + 1 == p.kv_heads; };
   if (work) {
-    // registers: 512 threads are launched with 128 each; a warpgroup of 152 and three of 120 are as many
-    if (warp < 4) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    // registers: 640 threads are launched with 96 each; two warpgroups of 120 and three of 80 are as many
+    if (warp < 8) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
       // ------------------------------------------------------------ softmax ----
-      const int x = threadIdx.x;                       // matrix row, tensor memory lane
-      const uint32_t part_of = (uint32_t)warp >> 1;    // half of the matrix: the row of the group, or the positions' half
-      constexpr uint32_t kAll = 1;                     // barrier of the warpgroup
-      constexpr int CH = SPLIT ? 2 : 4;                // 32 positions each: what a thread weighs of a tile
-      const int c0 = SPLIT ? (int)part_of * 2 : 0;
-      const uint32_t lanes = (uint32_t)warp << 21;     // this warp's 32 lanes
+      const int x = threadIdx.x & 127;                 // matrix row, tensor memory lane
+      const int g = warp >> 2;                         // warpgroup
+      const uint32_t pair = 2 + (warp & 3);            // barrier of the two warps that have the same rows
+      const uint32_t part_of = (uint32_t)(warp & 3) >> 1;   // half of the matrix: the row of the group, or the positions' half
+      constexpr uint32_t kAll = 1;                     // barrier of all softmax threads
+      constexpr int CH = SPLIT ? 1 : 2;                // 32 positions each: what a thread weighs of a tile
+      const int c0 = SPLIT ? (int)part_of * 2 + g : 2 * g;
+      const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // this warp's 32 lanes
       const uint32_t out_a = tmem + lanes + kOut + (SPLIT ? part_of * kHead : 0), out_b = tmem + lanes + kOut + kHead;
       uint32_t n = 0;                // visits so far
       bool ok = true;
@@ -441,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           tc_fence_after();
           const uint32_t s = tmem + lanes + b * kPos + c0 * 32, w_at = tmem + lanes + b * kPos + c0 * 16;
           if (mine) {
-            uint32_t r[2][32];
+            uint32_t r[CH][32];
             // chunk k's maximum (its scores put down first, where the weights are to be added up)
             float top = kNegInf, top2 = kNegInf;
             auto look = [&](int k, uint32_t (&r)[32]) {
@@ -472,25 +478,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               }
               seen |= on[k] != 0;
             };
-            if constexpr (CH == 2) {
-              // both chunks stay in registers
-              tmem_ld32(s, r[0]);
-              tmem_ld32(s + 32, r[1]);
-              tmem_wait_ld32(r[0]);
-              tmem_wait_ld32(r[1]);
-              look(0, r[0]);
-              look(1, r[1]);
-            } else {
-              // the next one is on its way meanwhile
-              tmem_ld32(s, r[0]);
 #pragma unroll
-              for (int k = 0; k < CH; ++k) {
-                tmem_wait_ld32(r[k & 1]);
-                tmem_ld32(s + (k + 1) % CH * 32, r[k & 1 ^ 1]);   // (last: the first again)
-                look(k, r[k & 1]);
-              }
-            }
-            top = __fmul_rn(fmaxf(top, top2), p.scale_log2);
+            for (int k = 0; k < CH; ++k) tmem_ld32(s + k * 32, r[k]);
+#pragma unroll
+            for (int k = 0; k < CH; ++k) tmem_wait_ld32(r[k]);
+#pragma unroll
+            for (int k = 0; k < CH; ++k) look(k, r[k]);
+            // of the whole row: the other warpgroup's thread has seen the other positions
+            top = fmaxf(top, top2);
+            row_max[b][g][x] = top;
+            bar_sync(pair, 64);
+            top = __fmul_rn(fmaxf(top, row_max[b][g ^ 1][x]), p.scale_log2);
             // does its weights' reference have to follow?
             if (__any_sync(~0u, top > ref + kRaise || (ref == kNegInf && top > kNegInf))) {
               const float raised = fmaxf(ref, top), f = ref == kNegInf ? (raised == kNegInf ? 1.f : 0.f) : ex2(ref - raised);
@@ -500,10 +498,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               if (had_a || had_b) {
                 ok &= wait(done_pv(b ^ 1), (n - 1) >> 1 & 1, abort, &err);   // the last visit that added to them
                 tc_fence_after();
+                // a half of the columns each
 #pragma unroll 1
-                for (int y = 0; y < 2 * kHead; y += 8) {
-                  if (y < kHead ? !had_a : !had_b) continue;
-                  const uint32_t o = (y < kHead ? out_a : out_b - kHead) + y;
+                for (int y = 0; y < kHead; y += 8) {
+                  if (y < 64 ? !had_a : !had_b) continue;
+                  const uint32_t o = (y < 64 ? out_a : out_b - 64) + g * 64 + y;
                   float z[8];
                   tmem_load8(o, z);
 #pragma unroll
@@ -527,23 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               }
               tmem_st16(w_at + k * 16, w);
             };
-            if constexpr (CH == 2) {
-              weigh(0, r[0]);
-              weigh(1, r[1]);
-            } else {
 #pragma unroll
-              for (int k = 0; k < CH; ++k) {
-                uint32_t(&now)[32] = r[k & 1];
-                tmem_wait_ld32(now);
-                if (k + 1 < CH) tmem_ld32(s + (k + 1) * 32, r[k & 1 ^ 1]);
-                if (on[k] != ~0u) {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    if (!(on[k] >> i & 1)) now[i] = __float_as_uint(kNegInf);
-                }
-                weigh(k, now);
-              }
-            }
+            for (int k = 0; k < CH; ++k) weigh(k, r[k]);
             if (!SPLIT && rows == 2) {
               had_b = true;
             } else {
@@ -559,13 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               tc_fence_after();
               const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-              for (int y = 0; y < kHead; y += 8) tmem_store8(out_a + y, zero);
+              for (int y = 0; y < 64; y += 8) tmem_store8(out_a + g * 64 + y, zero);
             }
           }
           tmem_wait_st();
           tc_fence_before();
+          // (after a wait that gave up the visits go on, without further waiting, to the vote below)
           mbar_arrive(full_p(b));
-          if (!__all_sync(~0u, ok)) break;
         }
 
         if constexpr (SLOTS) {
@@ -589,10 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (n > 1) ok &= wait(done_pv(n & 1), (n - 2) >> 1 & 1, abort, &err);
         tc_fence_after();
         float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        const bool has = (had_a || had_b) && (!SLOTS || seen);
-        if constexpr (SPLIT) half_ml[part_of][x & (kCols - 1)] = make_float2(ref, has ? l : -1.f);
+        // of the whole row
+        row_sum[g][x] = (had_a || had_b) && (!SLOTS || seen) ? l : -1.f;
+        bar_sync(pair, 64);
+        const float l0 = row_sum[0][x], l1 = row_sum[1][x];
+        const bool has = l0 != -1.f || l1 != -1.f;
+        l = (l0 != -1.f ? l0 : 0.f) + (l1 != -1.f ? l1 : 0.f);
+        if (SPLIT && g == 0) half_ml[part_of][x & (kCols - 1)] = make_float2(ref, has ? l : -1.f);
         // every softmax thread votes on the waits, so that all leave together
-        if (bar_red_or(kAll, 128, !ok)) break;
+        if (bar_red_or(kAll, kSoft, !ok)) break;
 
         const int32_t row_in = SPLIT ? 0 : (int32_t)part_of, col = x & (kCols - 1);
         const int32_t head = at.chunk * p.chunk_heads + col;
@@ -612,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           any = has || other;
         }
         const float inv = any ? 1.f / l : 0.f;
-        if (live && (!SPLIT || part_of == 0)) {
+        if (live && g == 0 && (!SPLIT || part_of == 0)) {
           if (!whole) {
             p.part_ml[part] = make_float2(top, any ? l : -1.f);
           } else {
@@ -637,33 +626,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
         };
         if constexpr (SPLIT) {
-          // each half finishes 64 columns; the other's share of them comes through shared memory, 32 at a time
+          // each half finishes 64 columns, 32 a thread; the other half's share of them comes through shared
+          // memory, 16 at a time
           float* stage = (float*)(raw + (smem - smem_addr(raw)) + kStage);
-          float* give = stage + (part_of * kCols + col) * kStageRow;
-          const float* take = stage + ((part_of ^ 1) * kCols + col) * kStageRow;
+          float* give = stage + ((part_of * 2 + g) * kCols + col) * kStageRow;
+          const float* take = stage + (((part_of ^ 1) * 2 + g) * kCols + col) * kStageRow;
 #pragma unroll 1
-          for (int c0 = 0; c0 < 64; c0 += 32) {
+          for (int at_col = 0; at_col < 32; at_col += 16) {
 #pragma unroll 1
-            for (int c = 0; c < 32; c += 8) {
+            for (int c = 0; c < 16; c += 8) {
               float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-              if (has) tmem_load8(out_a + (part_of ^ 1) * 64 + c0 + c, r);
+              if (has) tmem_load8(out_a + (part_of ^ 1) * 64 + g * 32 + at_col + c, r);
 #pragma unroll
               for (int i = 0; i < 8; ++i) give[c + i] = has ? r[i] * f : 0.f;
             }
-            bar_sync(kAll, 128);
+            bar_sync(kAll, kSoft);
 #pragma unroll 1
-            for (int c = 0; c < 32; c += 8) {
+            for (int c = 0; c < 16; c += 8) {
               float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-              if (has) tmem_load8(out_a + part_of * 64 + c0 + c, r);
+              if (has) tmem_load8(out_a + part_of * 64 + g * 32 + at_col + c, r);
 #pragma unroll
               for (int i = 0; i < 8; ++i) r[i] = (has ? r[i] * f : 0.f) + take[c + i];
-              emit((int)part_of * 64 + c0 + c, r);
+              emit((int)part_of * 64 + g * 32 + at_col + c, r);
             }
-            bar_sync(kAll, 128);
+            bar_sync(kAll, kSoft);
           }
         } else {
 #pragma unroll 1
-          for (int c = 0; c < kHead; c += 8) {
+          for (int c = g * 64; c < g * 64 + 64; c += 8) {
             float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, s[8];
             if (had_a) tmem_load8(out_a + c, r);
             if (had_b) {
@@ -679,10 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         tc_fence_before();
         more = next_segment(v1);
       }
-    } else if (warp < 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    } else if (warp < 16) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       // ------------------------------------------------------------- copies ----
-      const bool values = warp >= 8;
+      const bool values = warp >= 12;
       const int quarter = warp & 3, t = threadIdx.x & (kLoaders - 1);
       const uint32_t depth = values ? kRingV : kRingK;
       const uint32_t ring = smem + (values ? kValues : kKeys);
@@ -716,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int32_t* list;
         if constexpr (SLOTS) {
           list = p.slots + (int64_t)at.row0 * p.n_slots;
-          if (warp == 8 && at.row0 + 1 < p.rows)
+          if (warp == 12 && at.row0 + 1 < p.rows)
             for (int32_t i = lane * 32; i < p.n_slots; i += 32 * 32)
               asm volatile("prefetch.global.L2 [%0];" ::"l"(list + p.n_slots + i));
         } else {
@@ -800,8 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       bad = __reduce_max_sync(~0u, bad);
       if (lane == 0 && bad != kOk) atomicMax(&err, bad);
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-      if (warp == 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      if (warp == 16) {
       // ----------------------------------------------------- scores' products ----
       constexpr uint32_t kQK = idesc_f16<BF16>(128, kPos, false);
       const uint64_t q = desc128(smem + kQueries, 16, 1024);
@@ -832,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         __syncwarp();
         more = next_segment(v1);
       }
-      } else if (warp == 13) {
+      } else if (warp == 17) {
       // ---------------------------------------------------- outputs' products ----
       constexpr uint32_t kPV = idesc_f16<BF16>(128, kHead, true);
       uint32_t n = 0;
@@ -886,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
   }
   // the products in flight end before the tensor memory is given back
-  if (warp == 12 || warp == 13) {
+  if (warp == 16 || warp == 17) {
     __syncwarp();
     if (elect_one()) tc_commit(drain);
     __syncwarp();
@@ -897,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0) p.cta_status[blockIdx.x] = err;
-  if (warp == 12) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 16) tmem_dealloc(tmem, kTmemCols);
 }
 
 template <bool BF16, int NB, bool SLOTS>
