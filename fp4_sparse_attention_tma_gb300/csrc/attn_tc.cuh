@@ -47,7 +47,7 @@ constexpr int kLoaders = 128;             // threads that copy keys (and as many
 constexpr float kRaise = 8.f;             // weights are at most 2^kRaise
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOut = 256;            // first column of the accumulators, after two tiles of scores
-constexpr int kRingK = 2, kRingV = 3;     // tiles of keys and of values in shared memory
+constexpr int kRingK = 3, kRingV = 2;     // tiles of keys and of values in shared memory
 constexpr uint32_t kKeys = 0, kValues = kKeys + kRingK * kTileBytes, kQueries = kValues + kRingV * kTileBytes,
                    kStage = kQueries + kTileBytes;   // offsets; then room to pass sums between the halves
 constexpr int kStageRow = 17;             // floats
