@@ -43,14 +43,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
   Split sp;
   Cursor<SLOTS> at;
   Rows rows{};
-  const bool work = find_range<Cursor<SLOTS>, SLOTS, WARPS>(p, rows, sp, at, worker, ring, &err);
-  if (work && lane == 0) p.open_row[worker] = -1;
+  int64_t end;   // of the worker's range, counted from the unit's first subtile
+  const bool work = find_range<Cursor<SLOTS>, SLOTS, WARPS>(p, rows, sp, at, end, worker, ring, &err);
+  if (worker < sp.active && lane == 0) p.open_parts[worker] = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.active = sp.active;
   uint32_t warp_err = kOk;
   if (work) {
     const uint32_t my_ring = smem_addr(ring) + (uint32_t)warp * (STAGES * 2 * kHalf);
-    int64_t here = sp.first(worker);                 // flat index of the segment's first subtile
-    const int64_t stop = sp.first(worker + 1);
 
     // ---- fetching side: runs STAGES - 1 subtiles ahead, over the ends of segments ----
     constexpr int ROWS = 32 / CH > 0 ? 32 / CH : 1;   // positions that one copy of the warp covers
@@ -64,7 +63,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
       to[i] = (uint32_t)(r * (D * 2) + ((piece ^ (r & 7)) << 4));
     }
     Cursor<SLOTS> f = at;
-    int64_t f_left = stop - here;                     // subtiles still to be fetched
+    int64_t f_end = end;                              // as `end`; 0 when everything has been fetched
     const T *f_k, *f_v;                               // the head's keys and values, at this lane's piece
     const int32_t* f_list;                            // the request's pages, or the row's slots
     int32_t entry;                                    // page of the next subtile, or slot of its position lane % 16
@@ -85,7 +84,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
     };
     begin_fetch();
     auto fetch = [&](int stage) {
-      if (f_left > 0) {
+      if (f_end > 0) {
         const uint32_t dk = my_ring + (uint32_t)stage * (2 * kHalf), dv = dk + kHalf;
         auto place = [&](int i) { return to[i % TO] + (uint32_t)(i / TO) * (8 * D * 2); };
         if constexpr (SLOTS) {
@@ -139,10 +138,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
             }
           }
         }
-        if (--f_left > 0) {
-          if (++f.s < f.nsub) {
-            look_up();
-          } else {
+        if (++f.s < min((int64_t)f.nsub, f_end)) {
+          look_up();
+        } else {
+          f_end = max((int64_t)0, f_end - f.nsub - kUnitCost);
+          if (f_end > 0) {
             f.next_unit(p, rows);
             begin_fetch();
           }
@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
     // ---- computing side ----
     int stage = 0;
     const float c = p.scale_log2;
-    while (here < stop) {
-      const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, v0 + (stop - here));
+    while (end > 0) {
+      const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, end);
       const bool cut_front = v0 > 0;      // the segment starts inside its unit
       const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
       const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
@@ -380,14 +380,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
       }
 
       // the segment ends: finish the unit, or leave its part
-      here += v1 - v0;
       {
         const bool unit_end = v1 == at.nsub, whole = unit_end && !cut_front;
         const int which = cut_front ? 0 : 1;
         if (!unit_end && !cut_front && lane == 0) {
-          p.open_row[worker] = at.row0;
-          p.open_info[worker] =
-              make_int4(at.nrows, at.kv * p.chunks + at.chunk, sp.holder(here + (at.nsub - v1) - 1), 0);
+          p.open_parts[worker] = sp.holder(sp.first(worker + 1) - end + at.nsub - 1) - worker + 1;
+          p.open_info[worker] = make_int4(at.row0, at.nrows, at.kv * p.chunks + at.chunk, 0);
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -424,7 +422,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
             }
           }
       }
-      if (here < stop) at.next_unit(p, rows);
+      end -= at.nsub + kUnitCost;
+      if (end > 0) at.next_unit(p, rows);
     }
     copy_wait<0>();
   }

@@ -8,7 +8,8 @@
 // their cached positions are read once.  A unit is cut into subtiles of kSub
 // positions; the units' subtiles, one after another, are dealt to the workers (one
 // warp each; in attn_tc.cuh one CTA each, with tiles of 128 positions) in equal
-// contiguous ranges.  A unit that lies inside one worker's range
+// contiguous ranges, each unit counted as kUnitCost subtiles more than it has (its
+// beginning and end take a worker's time too; they precede its own).  A unit that lies inside one worker's range
 // is finished there; one that is cut leaves partial sums (the maximum, the sum of
 // the exponentials and the weighted values, all fp32), which attn_join_kernel
 // combines.  A worker's range cuts at most two units, so the workspace is bounded by
@@ -25,6 +26,9 @@
 namespace idxk {
 
 constexpr int kSub = 16;           // cached positions per subtile
+// 48 ragged requests x 3 rows x 16 heads, one of them of one position: 61 us with 0, 51 with 1 or 2, 49 with 3;
+// 32 requests x 2 rows x 64 heads on one (tiles of 128 positions): 113, 111, 110, 110.
+constexpr int kUnitCost = 2;
 
 struct AttnParams {
   const void *q, *k, *v;
@@ -46,14 +50,13 @@ struct AttnParams {
   int32_t tensor_core;              // 1: the kernel of attn_tc.cuh
   int32_t far;                      // 1: a cache spans 64 GB or more
   int32_t workers;                  // warps of the grid
-  int32_t min_sub;                  // a worker's range holds at least this many subtiles
   float scale_log2;                 // softmax scale x log2(e)
   // workspace
   uint32_t* cta_status;             // [CTAs] first error that the CTA saw
   int32_t n_cta;
   int32_t* active;                  // workers that have a range (the first so many)
-  int32_t* open_row;                // [active] first row of the unit cut at the range's end, or -1
-  int4* open_info;                  // [workers] {rows of its group, unit index in the group, last worker, 0}
+  int32_t* open_parts;              // [active] parts of the unit that the range's end cuts first, or 0
+  int4* open_info;                  // [workers] {first row of its group, rows, unit index in the group, 0}
   float2* part_ml;                  // [workers][2][tile] maximum (in units of log2, scaled) and sum
   float* part_o;                    // [workers][2][tile][dim]
   int32_t tile;                     // tile rows of a unit: 16 or 32; tensor_core: 64 or 128
@@ -68,7 +71,7 @@ struct AttnParams {
 
 // Byte offsets of a call's workspace.
 struct AttnLayout {
-  size_t cta_status, active, open_row, open_info, part_ml, part_o, row_stat, logits, total;
+  size_t cta_status, active, open_parts, open_info, part_ml, part_o, row_stat, logits, total;
 };
 
 inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int64_t dim, int64_t stat_rows,
@@ -77,7 +80,7 @@ inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int6
   size_t off = 0;
   L.cta_status = off; off = align_up(off + (size_t)n_cta * 4, 256);
   L.active = off;     off = align_up(off + 4, 256);
-  L.open_row = off;   off = align_up(off + (size_t)workers * 4, 256);
+  L.open_parts = off; off = align_up(off + (size_t)workers * 4, 256);
   L.open_info = off;  off = align_up(off + (size_t)workers * 16, 256);
   L.part_ml = off;    off = align_up(off + (size_t)workers * 2 * tile * 8, 256);
   L.part_o = off;     off = align_up(off + (size_t)workers * 2 * tile * dim * 4, 256);

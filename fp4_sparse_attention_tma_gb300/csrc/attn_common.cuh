@@ -78,8 +78,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 // Divides the units' subtiles among the workers.
 struct Split {
-  int64_t total = 0;    // subtiles of all units
+  int64_t total = 0;    // subtiles of all units, and what they are counted more
   int32_t active = 0;   // workers with a range
+  __device__ void divide(const AttnParams& p, int64_t subtiles) {
+    total = subtiles;
+    active = (int32_t)(total < p.workers ? total : p.workers);
+  }
   __device__ int64_t first(int64_t w) const { return total * w / active; }
   // the worker whose range holds subtile x
   __device__ int32_t holder(int64_t x) const { return (int32_t)(((x + 1) * active - 1) / total); }
@@ -135,19 +139,27 @@ struct Cursor {
     }
     nsub = hi > lo ? (hi + kSub - 1) / kSub - base : 0;
   }
-  // Subtiles of the group that starts at row r; 0 where none does.
+  // What a unit of the group that starts at row r counts; 0 where none does, or it sees nothing.
   __device__ static int32_t count(const AttnParams& p, const Rows& rows, int32_t r) {
     if (!starts_group(p, rows, r)) return 0;
-    const int32_t req = rows.req[r];
+    const int32_t req = rows.req[r], stop = min(p.rows, (r / p.group_rows + 1) * p.group_rows);
     int32_t a = INT32_MAX, b = 0;
-    for (int32_t i = r; i < p.rows && (i == r || (i % p.group_rows != 0 && rows.req[i] == req)); ++i) {
+    for (int32_t i = r; i < stop && rows.req[i] == req; ++i) {
       const int32_t a0 = rows.start[i], b0 = rows.end[i];
       if (b0 > a0) a = min(a, a0), b = max(b, b0);
     }
-    return b > a ? (b + kSub - 1) / kSub - a / kSub : 0;
+    return b > a ? (b + kSub - 1) / kSub - a / kSub + kUnitCost : 0;
   }
-  // Subtiles of every row of a call over slots.
-  __device__ static int32_t row_count(const AttnParams& p) { return (p.n_slots + kSub - 1) / kSub; }
+  // The same for a row of a call over slots.
+  __device__ static int32_t row_count(const AttnParams& p) { return (p.n_slots + kSub - 1) / kSub + kUnitCost; }
+  // Place t of the group's units, one after another; returns how far it is behind the unit's first subtile.
+  __device__ int32_t place(const AttnParams& p, int64_t t) {
+    const int32_t n = nsub + kUnitCost, u = (int32_t)(t / n), off = (int32_t)(t - (int64_t)u * n) - kUnitCost;
+    s = max(0, off);
+    kv = u / p.chunks;
+    chunk = u % p.chunks;
+    return off;
+  }
   // The next unit, at its first subtile; the caller has not passed the end of the list.
   __device__ void next_unit(const AttnParams& p, const Rows& rows) {
     s = 0;
@@ -163,27 +175,23 @@ struct Cursor {
 
 // Checks the rows' metadata (all of it, by every CTA, so that all agree), counts the
 // subtiles, and leaves the place where the worker's range starts in `cur` (`worker` may
-// differ from warp to warp).  Called by the whole CTA.  False: an error (recorded in *err)
-// or nothing to do for this warp.  `room`: 8 bytes of shared memory a thread.
+// differ from warp to warp), and where it ends, counted from the unit's first subtile, in
+// `end`.  Called by the whole CTA.  False: an error (recorded in *err) or nothing to do for
+// this warp.  `room`: 8 bytes of shared memory a thread.
 template <class Cur, bool SLOTS, int WARPS>
-__device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur, int32_t worker, void* room, uint32_t* err) {
+__device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur, int64_t& end, int32_t worker, void* room,
+                           uint32_t* err) {
   const int32_t units = p.kv_heads * p.chunks;
   if constexpr (SLOTS) {
     const int32_t n = Cur::row_count(p);
-    sp.total = (int64_t)p.rows * units * n;
-    const int64_t most = (sp.total + p.min_sub - 1) / p.min_sub;
-    sp.active = (int32_t)(most < p.workers ? most : p.workers);
+    sp.divide(p, (int64_t)p.rows * units * n);
     if (worker >= sp.active) return false;
     const int64_t t = sp.first(worker);
     const int64_t per_row = (int64_t)units * n;
     const int32_t row = (int32_t)(t / per_row);
-    const int64_t rest = t - row * per_row;
     cur.load(p, rows, row);
-    const int32_t u = (int32_t)(rest / n);
-    cur.s = (int32_t)(rest - (int64_t)u * n);
-    cur.kv = u / p.chunks;
-    cur.chunk = u % p.chunks;
-    return true;
+    end = sp.first(worker + 1) - t + cur.place(p, t - row * per_row);
+    return end > cur.s;
   } else {
     constexpr int N = WARPS * 32;
     __shared__ int64_t warp_sum[WARPS];
@@ -212,9 +220,7 @@ __device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur,
     sum = 0;
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) sum += warp_sum[i];
-    sp.total = sum * units;
-    const int64_t most = (sp.total + p.min_sub - 1) / p.min_sub;
-    sp.active = (int32_t)(most < p.workers ? most : p.workers);
+    sp.divide(p, sum * units);
     const bool some = worker < sp.active;
     const int64_t t = some ? sp.first(worker) : 0;
     bool found = false;
@@ -245,18 +251,14 @@ __device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur,
         for (int32_t i = lane; i < n; i += 32)
           if ((before + pre[i]) * units <= t) at = i;   // pre is non-decreasing
         at = __reduce_max_sync(~0u, at);
-        const int64_t rest = t - (before + pre[at]) * units;
         cur.load(p, rows, r0 + at);
-        const int32_t u = (int32_t)(rest / cur.nsub);
-        cur.s = (int32_t)(rest - (int64_t)u * cur.nsub);
-        cur.kv = u / p.chunks;
-        cur.chunk = u % p.chunks;
+        end = sp.first(worker + 1) - t + cur.place(p, t - (before + pre[at]) * units);
         found = true;
       }
       before += all;
     }
     __syncthreads();   // `room` is free again
-    return found;
+    return found && end > cur.s;
   }
 }
 

@@ -352,14 +352,13 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   p.far = far;
   p.workers = R > 0 ? a.workers : 0;
   p.n_cta = R > 0 ? m.sm : 0;
-  p.min_sub = 1;
   p.scale_log2 = c.scale * 1.4426950408889634f;
   p.tile = a.tile, p.dim = (int32_t)D;
   const bool bf16 = c.q->dtype == IDX_BF16;
   return with_space(space, L.total, m, stream, [&](char* base, uint32_t* status) -> cudaError_t {
     p.cta_status = (uint32_t*)(base + L.cta_status);
     p.active = (int32_t*)(base + L.active);
-    p.open_row = (int32_t*)(base + L.open_row);
+    p.open_parts = (int32_t*)(base + L.open_parts);
     p.open_info = (int4*)(base + L.open_info);
     p.part_ml = (float2*)(base + L.part_ml);
     p.part_o = (float*)(base + L.part_o);

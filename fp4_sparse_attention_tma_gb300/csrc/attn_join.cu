@@ -39,12 +39,12 @@ __device__ uint32_t call_status(const AttnParams& p) {
   return all;
 }
 
-constexpr int kJoinWarps = 8;
 constexpr int kFewParts = 8;   // units of at most so many parts are joined by one warp a tile row
+constexpr int kLooks = 5;      // ranges that a thread looks at together
 
 struct OpenUnit {
-  uint16_t w0, n;            // first worker and parts
-  int32_t row0;              // its group's first row
+  uint16_t w0, n;               // first worker and parts
+  int32_t row0;                 // its group's first row
   uint32_t nrows : 8, u : 24;   // its group's rows and its index in the group
 };
 
@@ -105,18 +105,28 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const OpenUnit& 
 //   M = max m_i, l = sum l_i 2^(m_i - M), out = sum o_i 2^(m_i - M) / l.
 // Where a unit has few parts, each warp joins a row by itself; where it has many (few rows
 // over a long context), the warps of a CTA take the row's parts in turn, in a fixed order,
-// and their sums are joined in the same way.  Bound by the parts' bytes in L2.
-template <bool BF16, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p) {
+// and their sums are joined in the same way.  Bound by the latency of a chain of loads: the ranges' ends,
+// the parts.  CTAs of 16 warps look over the 1216 ranges and more of attn.cuh, CTAs of 8 the one an SM of
+// attn_tc.cuh (48 requests x 3 rows x 16 heads: 61 us with 16 warps, 64 with 8; 32 requests x 2 rows x 64
+// heads on one: 115 and 113).
+template <bool BF16, int D, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_kernel(const __grid_constant__ AttnParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr int V = D / 32;   // columns of a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   extern __shared__ OpenUnit open[];   // [workers]: units of few parts from the front, others from the back
-  __shared__ int32_t warp_n[kJoinWarps][2];
+  __shared__ uint32_t warp_n[kLooks][kJoinWarps];
   __shared__ float wm[kJoinWarps], wl[kJoinWarps];
   __shared__ float wo[kJoinWarps][D];
   allow_launch_after();
   wait_for_launch_before();
+  // the first ranges' ends (what lies beyond the workers that had a range is read too, and means nothing)
+  constexpr int N = kJoinWarps * 32;
+  int n[kLooks];
+#pragma unroll
+  for (int i = 0; i < kLooks; ++i) n[i] = (int)threadIdx.x + i * N < p.workers ? p.open_parts[threadIdx.x + i * N] : 0;
+  int4 info = (int)threadIdx.x < p.workers ? p.open_info[threadIdx.x] : make_int4(0, 0, 0, 0);
+  const int active = p.n_cta > 0 ? *p.active : 0;
   const uint32_t status = call_status(p);
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.status_out) *p.status_out = status;
   if (status != kOk) {
@@ -130,32 +140,36 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     }
     return;
   }
-  // the cut units
-  int few = 0, many = 0;
-  const int active = p.n_cta > 0 ? *p.active : 0;
-  for (int w0 = 0; w0 < active; w0 += kJoinWarps * 32) {
-    const int w = w0 + (int)threadIdx.x;
-    OpenUnit un{};
-    un.row0 = w < active ? p.open_row[w] : -1;
-    const int4 info = w < active ? p.open_info[w] : make_int4(0, 0, 0, 0);   // (means nothing where no unit is open)
-    un.w0 = (uint16_t)w, un.nrows = info.x, un.u = info.y, un.n = (uint16_t)(info.z - w + 1);
-    const bool on = un.row0 >= 0;
-    const int n = un.n;
-    const bool is_few = on && n <= kFewParts, is_many = on && !is_few;
-    const uint32_t bf = __ballot_sync(~0u, is_few), bm = __ballot_sync(~0u, is_many);
-    if (lane == 0) warp_n[warp][0] = __popc(bf), warp_n[warp][1] = __popc(bm);
-    __syncthreads();
-    int at_few = few, at_many = many;
+  // the cut units, in the same order in every CTA
+  uint32_t below[kLooks][2];
 #pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) {
-      if (i < warp) at_few += warp_n[i][0], at_many += warp_n[i][1];
-      few += warp_n[i][0], many += warp_n[i][1];
-    }
-    const uint32_t below = (1u << lane) - 1;
-    if (is_few) open[at_few + __popc(bf & below)] = un;
-    if (is_many) open[p.workers - 1 - at_many - __popc(bm & below)] = un;
-    __syncthreads();
+  for (int i = 0; i < kLooks; ++i) {
+    if ((int)threadIdx.x + i * N >= active) n[i] = 0;
+    const uint32_t bf = __ballot_sync(~0u, n[i] > 0 && n[i] <= kFewParts), bm = __ballot_sync(~0u, n[i] > kFewParts);
+    if (lane == 0) warp_n[i][warp] = (uint32_t)__popc(bf) | (uint32_t)__popc(bm) << 16;
+    below[i][0] = __popc(bf & ((1u << lane) - 1)), below[i][1] = __popc(bm & ((1u << lane) - 1));
   }
+  __syncthreads();
+  uint32_t all = 0;   // few, and 65536 times the others
+#pragma unroll
+  for (int i = 0; i < kLooks; ++i) {
+    if (i * N >= active) break;
+    uint32_t before = all;
+#pragma unroll
+    for (int x = 0; x < kJoinWarps; ++x) {
+      const uint32_t c = warp_n[i][x];
+      if (x < warp) before += c;
+      all += c;
+    }
+    if (n[i] == 0) continue;
+    const int w = (int)threadIdx.x + i * N;
+    if (i > 0) info = p.open_info[w];
+    OpenUnit un;
+    un.w0 = (uint16_t)w, un.n = (uint16_t)n[i], un.row0 = info.x, un.nrows = info.y, un.u = info.z;
+    open[n[i] <= kFewParts ? (before & 0xFFFF) + below[i][0] : p.workers - 1 - (before >> 16) - below[i][1]] = un;
+  }
+  __syncthreads();
+  const int few = all & 0xFFFF, many = all >> 16;
   // the output row of tile row m: false where it is none, or sees nothing
   auto row_of = [&](const OpenUnit& un, int m, int64_t& row, int& qh) {
     const int j = m / p.row_cols, h = m - j * p.row_cols;
@@ -164,10 +178,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     qh = un.u / p.chunks * p.group + in_group;
     return j < un.nrows && h < p.chunk_heads && in_group < p.group;
   };
-  const int per = p.tile / kJoinWarps;
-  for (int job = blockIdx.x; job < few * per; job += gridDim.x) {
-    const OpenUnit un = open[job / per];
-    const int m = job % per * kJoinWarps + warp;
+  for (int job = blockIdx.x * kJoinWarps + warp; job < few * p.tile; job += gridDim.x * kJoinWarps) {
+    const int m = job / few;   // (a group's first rows first: its last are often not there)
+    const OpenUnit un = open[job - m * few];
     int64_t row;
     int qh;
     if (!row_of(un, m, row, qh)) continue;
@@ -187,14 +200,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     }
   }
   for (int job = blockIdx.x; job < many * p.tile; job += gridDim.x) {
-    const OpenUnit un = open[p.workers - 1 - job / p.tile];
+    const int m = job / many;
+    const OpenUnit un = open[p.workers - 1 - (job - m * many)];
     int64_t row;
     int qh;
     // the same for the whole CTA
-    if (!row_of(un, job % p.tile, row, qh) || (!p.slots && p.row_end[row] <= p.row_start[row])) continue;
+    if (!row_of(un, m, row, qh) || (!p.slots && p.row_end[row] <= p.row_start[row])) continue;
     float M, l, acc[V];
     bool seen;
-    join_parts<D>(p, un, job % p.tile, warp, kJoinWarps, M, l, acc, seen);
+    join_parts<D>(p, un, m, warp, kJoinWarps, M, l, acc, seen);
     if (lane == 0) wm[warp] = M, wl[warp] = seen ? l : -1.f;
 #pragma unroll
     for (int x = 0; x < V; ++x) wo[warp][lane * V + x] = acc[x];
@@ -303,16 +317,23 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __gr
 
 }  // namespace
 
+template <bool BF16, int D, int WARPS>
+static cudaError_t launch_join(const AttnParams& p, int sm_count, cudaStream_t stream) {
+  if (p.workers > kLooks * WARPS * 32) return cudaErrorInvalidValue;
+  return launch_overlapped(attn_join_kernel<BF16, D, WARPS>, dim3(sm_count * (32 / WARPS)), dim3(WARPS * 32),
+                           (size_t)p.workers * sizeof(OpenUnit), stream, p);
+}
+
 template <bool BF16>
-static cudaError_t pick_join(const AttnParams& p, int grid, cudaStream_t stream) {
-  const size_t smem = (size_t)p.workers * sizeof(OpenUnit);
-  if (p.dim == 64) return launch_overlapped(attn_join_kernel<BF16, 64>, dim3(grid), dim3(kJoinWarps * 32), smem, stream, p);
-  if (p.dim == 128) return launch_overlapped(attn_join_kernel<BF16, 128>, dim3(grid), dim3(kJoinWarps * 32), smem, stream, p);
-  return launch_overlapped(attn_join_kernel<BF16, 256>, dim3(grid), dim3(kJoinWarps * 32), smem, stream, p);
+static cudaError_t pick_join(const AttnParams& p, int sm_count, cudaStream_t stream) {
+  if (p.tensor_core) return launch_join<BF16, 128, 8>(p, sm_count, stream);
+  if (p.dim == 64) return launch_join<BF16, 64, 16>(p, sm_count, stream);
+  if (p.dim == 128) return launch_join<BF16, 128, 16>(p, sm_count, stream);
+  return launch_join<BF16, 256, 16>(p, sm_count, stream);
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream) {
-  return bf16 ? pick_join<true>(p, sm_count * 4, stream) : pick_join<false>(p, sm_count * 4, stream);
+  return bf16 ? pick_join<true>(p, sm_count, stream) : pick_join<false>(p, sm_count, stream);
 }
 
 cudaError_t launch_attn_weights(const AttnParams& p, cudaStream_t stream) {

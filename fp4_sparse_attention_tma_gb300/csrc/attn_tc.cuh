@@ -161,9 +161,10 @@ struct Walk {
       a[j] = in ? rows.start[i] : 0;
       b[j] = in ? rows.end[i] : 0;
     }
-    return visits(a, b, c0, c1);
+    const int32_t n = visits(a, b, c0, c1);
+    return n ? n + kUnitCost : 0;
   }
-  __device__ static int32_t row_count(const AttnParams& p) { return hi(p.n_slots); }
+  __device__ static int32_t row_count(const AttnParams& p) { return hi(p.n_slots) + kUnitCost; }
 
   __device__ void load(const AttnParams& p, const Rows& rows, int32_t row) {
     row0 = row;
@@ -184,6 +185,14 @@ struct Walk {
       }
     }
     nsub = visits(a, b, c0, c1);
+  }
+  // Place t of the group's units, one after another; returns how far it is behind the unit's first visit.
+  __device__ int32_t place(const AttnParams& p, int64_t t) {
+    const int32_t n = nsub + kUnitCost, u = (int32_t)(t / n), off = (int32_t)(t - (int64_t)u * n) - kUnitCost;
+    s = max(0, off);
+    kv = u / p.chunks;
+    chunk = u % p.chunks;
+    return off;
   }
   // The next unit, at its first visit; the caller has not passed the end of the list.
   __device__ void next_unit(const AttnParams& p, const Rows& rows) {
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   // the visits' own values out to local memory, for which no L1 is left.
   struct Place {
     Walk<NB, SLOTS> at;
-    int64_t here, stop;   // flat indices of the segment's first visit, and of the range's end
+    int64_t end;   // of the CTA's range, counted from the unit's first visit
   };
   __shared__ Place places[kWarps];
   __shared__ Split split;
@@ -354,33 +363,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     Split sp;
     Walk<NB, SLOTS> first;
     Rows rows{};
-    work = find_range<Walk<NB, SLOTS>, SLOTS, kWarps>(p, rows, sp, first, blockIdx.x, raw, &err);
+    int64_t end;
+    work = find_range<Walk<NB, SLOTS>, SLOTS, kWarps>(p, rows, sp, first, end, blockIdx.x, raw, &err);
     if (threadIdx.x == 0) {
-      if (work) p.open_row[blockIdx.x] = -1;
+      if ((int32_t)blockIdx.x < sp.active) p.open_parts[blockIdx.x] = 0;
       if (blockIdx.x == 0) *p.active = sp.active;
       split = sp;
       meta = rows;
     }
     if (work && lane == 0) {
       places[warp].at = first;
-      places[warp].here = sp.first(blockIdx.x);
-      places[warp].stop = sp.first(blockIdx.x + 1);
+      places[warp].end = end;
     }
   }
   __syncthreads();
   // The segment's last visit (and one more); then, on to the next segment: false at the range's end.
-  auto segment_end = [&]() { return (int32_t)min((int64_t)at.nsub, at.s + (places[warp].stop - places[warp].here)); };
-  auto next_segment = [&](int32_t v1) {
+  auto segment_end = [&]() { return (int32_t)min((int64_t)at.nsub, places[warp].end); };
+  auto next_segment = [&]() {
     __syncwarp();
     if (lane == 0) {
-      places[warp].here += v1 - at.s;
-      if (places[warp].here < places[warp].stop) at.next_unit(p, meta);
+      places[warp].end -= at.nsub + kUnitCost;
+      if (places[warp].end > 0) at.next_unit(p, meta);
     }
     __syncwarp();
-    return places[warp].here < places[warp].stop;
+    return places[warp].end > 0;
   };
   // Whether the range goes on after the segment, and with the next row (else another unit of this one).
-  auto goes_on = [&](int32_t v1) { return places[warp].here + (v1 - at.s) < places[warp].stop; };
+  auto goes_on = [&]() { return places[warp].end > at.nsub + kUnitCost; };
   auto next_is_row = [&]() { return at.chunk + 1 == p.chunks && at.kv + 1 == p.kv_heads; };
   if (work) {
     // registers: 640 threads are launched with 96 each; two warpgroups of 120 and three of 80 are as many
@@ -554,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 
         if constexpr (SLOTS) {
           // the next unit's first: of this row, or of the next
-          if (goes_on(v1)) {
+          if (goes_on()) {
             if (next_is_row()) list += p.n_slots;
             ask(0);
           }
@@ -564,9 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const bool cut_front = at.s > 0, unit_end = v1 == at.nsub, whole = unit_end && !cut_front;
         const int which = cut_front ? 0 : 1;
         if (!unit_end && !cut_front && threadIdx.x == 0) {
-          p.open_row[blockIdx.x] = at.row0;
-          p.open_info[blockIdx.x] = make_int4(at.nrows, at.kv * p.chunks + at.chunk,
-                                              split.holder(places[warp].here + (at.nsub - at.s) - 1), 0);
+          p.open_parts[blockIdx.x] =
+              split.holder(split.first(blockIdx.x + 1) - places[warp].end + at.nsub - 1) - (int32_t)blockIdx.x + 1;
+          p.open_info[blockIdx.x] = make_int4(at.row0, at.nrows, at.kv * p.chunks + at.chunk, 0);
         }
         // the last visit of each tile of scores that this segment (or one before it) had
         if (n > 0) ok &= wait(done_pv((n - 1) & 1), (n - 1) >> 1 & 1, abort, &err);
@@ -667,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
         }
         tc_fence_before();
-        more = next_segment(v1);
+        more = next_segment();
       }
     } else if (warp < 16) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -739,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             from = on ? (uint32_t)(entry / kPage) * page16 + (uint32_t)(entry % kPage) * slot16 : ~0u;
             if (v + 1 < v1) {
               ask(list, v + 1);
-            } else if (goes_on(v1)) {
+            } else if (goes_on()) {
               // the next unit's first: of this row, or of the next
               ask(list + (next_is_row() ? p.n_slots : 0), 0);
             }
@@ -784,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           ++n;
         }
         if (!ok) break;
-        more = next_segment(v1);
+        more = next_segment();
       }
       copy_wait_all();
       bad = __reduce_max_sync(~0u, bad);
@@ -820,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (!ok) break;
         if (elect_one()) tc_commit(empty_q);
         __syncwarp();
-        more = next_segment(v1);
+        more = next_segment();
       }
       } else if (warp == 17) {
       // ---------------------------------------------------- outputs' products ----
@@ -857,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           if (to) fresh[1] = false; else fresh[0] = false;
         }
         if (!ok) break;
-        more = next_segment(v1);
+        more = next_segment();
       }
       }
     }
