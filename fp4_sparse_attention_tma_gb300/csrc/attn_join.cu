@@ -39,8 +39,10 @@ __device__ uint32_t call_status(const AttnParams& p) {
   return all;
 }
 
-constexpr int kFewParts = 8;   // units of at most so many parts are joined by one warp a tile row
-constexpr int kLooks = 5;      // ranges that a thread looks at together
+// Units of at most so many parts are joined by one warp a tile row (32 requests x 2 rows x 64 heads on one:
+// 116 us with 4, 110 with 8, 107 with 16, 106 with 32).
+constexpr int kFewParts = 16;
+constexpr int kLooks = 5;   // ranges that a thread looks at together
 
 struct OpenUnit {
   uint16_t w0, n;               // first worker and parts
@@ -242,18 +244,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_ke
 
 // weight_out[i, s] = weight_in[i, s] + the sum over request i's rows (in order) and
 // query heads of 2^(logit - M) / l.  Reads every logit once; a thread owns 4
-// positions, so the sum's order is fixed.  Bound by the logits' traffic.
-constexpr int kWeightThreads = 128;
-constexpr int kRowList = 256;
+// positions and a quarter of the heads, and the quarters are added up in order, so
+// the sum's order is fixed.  Bound by the logits' traffic and, with few requests, the
+// latency of a thread's loads (16 requests x 32 heads of up to 32768 positions: 230 us of the
+// whole call with all heads in one thread, 225 so).
+constexpr int kWeightPos = 128;                       // threads that share a quarter of the heads
+constexpr int kWeightParts = 4;
+constexpr int kWeightThreads = kWeightPos * kWeightParts;
+constexpr int kRowList = 2 * kWeightThreads;
 
 __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __grid_constant__ AttnParams p) {
   const int64_t width = (int64_t)p.max_pages * kPage;
-  const int64_t pos = ((int64_t)blockIdx.x * kWeightThreads + threadIdx.x) * 4;
+  const int part = threadIdx.x / kWeightPos, at_pos = threadIdx.x % kWeightPos;
+  const int h0 = p.q_heads * part / kWeightParts, h1 = p.q_heads * (part + 1) / kWeightParts;
+  const int64_t pos = ((int64_t)blockIdx.x * kWeightPos + at_pos) * 4;
   const bool in = pos < width;
   wait_for_launch_before();
   const bool failed = call_status(p) != kOk;
   __shared__ int32_t list[kRowList];
   __shared__ int32_t warp_n[kWeightThreads / 32];
+  __shared__ float4 sums[kWeightParts - 1][kWeightPos];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float c = p.scale_log2;
   for (int32_t req = blockIdx.y; req < p.num_req; req += gridDim.y) {
@@ -261,13 +271,13 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __gr
     if (failed) {
       // totals kept in place stay as they were
       const float nan = __uint_as_float(0x7FC00000u);
-      if (in && p.weight_in != p.weight_out) *(float4*)(p.weight_out + at) = make_float4(nan, nan, nan, nan);
+      if (in && part == 0 && p.weight_in != p.weight_out) *(float4*)(p.weight_out + at) = make_float4(nan, nan, nan, nan);
       continue;
     }
     float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (in && p.weight_in) w = *(const float4*)(p.weight_in + at);
+    if (in && part == 0 && p.weight_in) w = *(const float4*)(p.weight_in + at);
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t b0 = (int64_t)blockIdx.x * kWeightThreads * 4, b1 = b0 + kWeightThreads * 4;
+    const int64_t b0 = (int64_t)blockIdx.x * kWeightPos * 4, b1 = b0 + kWeightPos * 4;
     int n = 0;
     auto flush = [&]() {
       for (int i = 0; i < n; ++i) {
@@ -278,7 +288,7 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __gr
         const float2* st = p.row_stat + (int64_t)r * p.q_heads;
         const bool m0 = pos >= a, m1 = pos + 1 >= a && pos + 1 < b, m2 = pos + 2 >= a && pos + 2 < b, m3 = pos + 3 < b;
 #pragma unroll 8
-        for (int h = 0; h < p.q_heads; ++h) {
+        for (int h = h0; h < h1; ++h) {
           const float4 x = __ldcs((const float4*)(lg + h * width));
           const float2 s = st[h];
           if (m0) sum.x += pow2(fmaf(x.x, c, -s.x)) * s.y;
@@ -310,7 +320,16 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __gr
       }
     }
     flush();
-    if (in) *(float4*)(p.weight_out + at) = make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
+    if (part > 0) sums[part - 1][at_pos] = sum;
+    __syncthreads();
+    if (part == 0 && in) {
+#pragma unroll
+      for (int i = 0; i < kWeightParts - 1; ++i) {
+        const float4 s = sums[i][at_pos];
+        sum.x += s.x, sum.y += s.y, sum.z += s.z, sum.w += s.w;
+      }
+      *(float4*)(p.weight_out + at) = make_float4(w.x + sum.x, w.y + sum.y, w.z + sum.z, w.w + sum.w);
+    }
     __syncthreads();
   }
 }
@@ -337,7 +356,7 @@ cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int sm_count, cudaS
 }
 
 cudaError_t launch_attn_weights(const AttnParams& p, cudaStream_t stream) {
-  const int64_t per = kWeightThreads * 4;
+  const int64_t per = kWeightPos * 4;
   const int64_t x = ((int64_t)p.max_pages * kPage + per - 1) / per;
   const dim3 grid((unsigned)x, (unsigned)(p.num_req < 65535 ? p.num_req : 65535));
   return launch_overlapped(attn_weights_kernel, grid, dim3(kWeightThreads), 0, stream, p);
