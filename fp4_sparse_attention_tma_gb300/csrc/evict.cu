@@ -60,6 +60,10 @@ __device__ void check_fresh(const EvictParams& p, int C, int rank, uint32_t* sha
   }
 }
 
+__device__ __forceinline__ uint4 keys_of(float4 w) {
+  return make_uint4(score_key(w.x), score_key(w.y), score_key(w.z), score_key(w.w));
+}
+
 // Barrier of the cluster (of the CTA, where that is all of it).
 __device__ __forceinline__ void sync_all(cooperative_groups::cluster_group& cluster, int C) {
   if (C == 1)
@@ -69,7 +73,7 @@ __device__ __forceinline__ void sync_all(cooperative_groups::cluster_group& clus
 }
 
 // The selection.  Every CTA of a request's cluster holds a slice of its positions (their
-// weights in shared memory where they fit); three passes over 11, 11 and 10 bits of the key
+// keys in shared memory where they fit); three passes over 11, 11 and 10 bits of the key
 // each count the slice's keys by digit, find in the whole cluster's counts (first by groups of
 // 64 digits, then in one group) the digit that holds the last key to be kept, and go on with
 // the keys of that digit.  (Of the first 11 bits 9 are sign and exponent: fewer bits would send
@@ -114,10 +118,18 @@ __device__ void select(const EvictParams& p, cooperative_groups::cluster_group& 
   const int32_t s0 = min((int64_t)n, (int64_t)rank * slice), s1 = min((int64_t)n, (int64_t)s0 + slice);
   const bool held = slice <= p.slice_cap;
   if (cut && held) {
+    const int32_t fours = ((uintptr_t)weight & 15) == 0 ? (s1 - s0) / 4 : 0;
 #pragma unroll 8
-    for (int32_t i = s0 + tid; i < s1; i += kSelThreads) bits[i - s0] = __float_as_uint(weight[i]);
+    for (int32_t i = tid; i < fours; i += kSelThreads) ((uint4*)bits)[i] = keys_of(((const float4*)(weight + s0))[i]);
+#pragma unroll 8
+    for (int32_t i = s0 + 4 * fours + tid; i < s1; i += kSelThreads) bits[i - s0] = score_key(weight[i]);
   }
-  auto weight_at = [&](int32_t i) { return held ? __uint_as_float(bits[i - s0]) : weight[i]; };
+  // the keys of positions i .. i + 3 (i - s0 a multiple of 4; what lies behind the slice means nothing)
+  auto keys_at = [&](int32_t i) {
+    if (held) return *(const uint4*)(bits + (i - s0));
+    return keys_of(make_float4(weight[i], i + 1 < s1 ? weight[i + 1] : 0.f, i + 2 < s1 ? weight[i + 2] : 0.f,
+                               i + 3 < s1 ? weight[i + 3] : 0.f));
+  };
   for (int i = tid; i < 2 * kBins; i += kSelThreads) hist[0][i] = 0;
 
   // the pages of the request, its new table, and what lies behind the kept positions
@@ -148,10 +160,18 @@ __device__ void select(const EvictParams& p, cooperative_groups::cluster_group& 
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, buf = pass & 1;
       const uint32_t digits = pass == 2 ? 1024u : (uint32_t)kBins;
       const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFFFFFFFu << 21 : 0xFFFFFFFFu << 10;
-#pragma unroll 4
-      for (int32_t i = max(s0, lo) + tid; i < min(s1, hi); i += kSelThreads) {
-        const uint32_t k = score_key(weight_at(i));
-        if ((k & mask) == prefix) atomicAdd(&hist[buf][k >> shift & (digits - 1)], 1u);
+      const int32_t x0 = max(s0, lo), x1 = min(s1, hi);
+#pragma unroll 2
+      for (int32_t i = s0 + 4 * tid; i < x1; i += 4 * kSelThreads) {
+        const uint4 k4 = keys_at(i);
+        const uint32_t four[4] = {k4.x, k4.y, k4.z, k4.w};
+        const bool inside = i >= x0 && i + 4 <= x1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t k = four[j];
+          if ((k & mask) == prefix && (inside || (i + j >= x0 && i + j < x1)))
+            atomicAdd(&hist[buf][k >> shift & (digits - 1)], 1u);
+        }
       }
       __syncthreads();
       const uint2 mine = ((const uint2*)&hist[buf][warp * 64])[lane];
@@ -198,31 +218,41 @@ __device__ void select(const EvictParams& p, cooperative_groups::cluster_group& 
     thr = prefix;
   }
 
-  // what every warp keeps of its part of the slice
-  const int32_t part = (slice / 32 + kWarps - 1) / kWarps * 32;
+  // what every warp keeps of its part of the slice, four positions a lane at a time
+  const int32_t part = (slice + kWarps * 128 - 1) / (kWarps * 128) * 128;
   const int32_t w0 = min(s1, s0 + warp * part), w1 = min(s1, w0 + part);
   const uint32_t take = want;   // of the keys equal to thr
-  auto classify = [&](int32_t i, float& w, bool& gt, bool& eq) {
-    gt = eq = false;
+  const bool some = p.budget > p.keep_first + p.keep_last;
+  // positions i .. i + 3: bit j of gt, of eq
+  auto classify = [&](int32_t i, uint32_t (&four)[4], uint32_t& gt, uint32_t& eq) {
+    gt = eq = 0;
     if (i >= w1) return;
-    w = weight_at(i);
-    if (i < lo || i >= hi) {
-      gt = true;
-    } else if (p.budget > p.keep_first + p.keep_last) {
-      const uint32_t k = score_key(w);
-      gt = k > thr;
-      eq = k == thr;
+    const uint4 k4 = keys_at(i);
+    four[0] = k4.x, four[1] = k4.y, four[2] = k4.z, four[3] = k4.w;
+    if (some && i >= lo && i + 4 <= min(hi, w1)) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) gt |= (four[j] > thr) << j, eq |= (four[j] == thr) << j;
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t k = four[j];
+      const bool in = i + j < w1, always = i + j < lo || i + j >= hi;
+      if (in && (always || (some && k > thr))) gt |= 1u << j;
+      if (in && !always && some && k == thr) eq |= 1u << j;
     }
   };
   uint32_t n_gt = 0, n_eq = 0;
-#pragma unroll 4
-  for (int32_t i0 = w0; i0 < w1; i0 += 32) {
-    bool gt, eq;
-    float w;
-    classify(i0 + lane, w, gt, eq);
-    n_gt += __popc(__ballot_sync(~0u, gt));
-    n_eq += __popc(__ballot_sync(~0u, eq));
+#pragma unroll 2
+  for (int32_t i0 = w0; i0 < w1; i0 += 128) {
+    uint32_t gt, eq;
+    uint32_t four[4];
+    classify(i0 + 4 * lane, four, gt, eq);
+    n_gt += __popc(gt);
+    n_eq += __popc(eq);
   }
+  n_gt = __reduce_add_sync(~0u, n_gt);
+  n_eq = __reduce_add_sync(~0u, n_eq);
   if (lane == 0) warp_gt[warp] = n_gt, warp_eq[warp] = n_eq;
   __syncthreads();
   if (warp == 0) {
@@ -238,21 +268,33 @@ __device__ void select(const EvictParams& p, cooperative_groups::cluster_group& 
   }
   gt0 = __reduce_add_sync(~0u, gt0);
   eq0 = __reduce_add_sync(~0u, eq0);
-#pragma unroll 4
-  for (int32_t i0 = w0; i0 < w1; i0 += 32) {
-    bool gt, eq;
-    float w;
-    classify(i0 + lane, w, gt, eq);
-    const uint32_t bg = __ballot_sync(~0u, gt), be = __ballot_sync(~0u, eq);
-    const uint32_t below = (1u << lane) - 1;
-    const uint32_t e = eq0 + __popc(be & below);
-    if (gt || (eq && e < take)) {
-      const uint32_t at = gt0 + __popc(bg & below) + min(e, take);
-      keep[at] = i0 + lane;
-      new_weight[at] = w;
+#pragma unroll 2
+  for (int32_t i0 = w0; i0 < w1; i0 += 128) {
+    uint32_t gt, eq;
+    uint32_t four[4];
+    classify(i0 + 4 * lane, four, gt, eq);
+    const uint32_t mine = __popc(gt) | __popc(eq) << 16;   // at most 128 of each in a warp
+    uint32_t inc = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += y;
     }
-    gt0 += __popc(bg);
-    eq0 += __popc(be);
+    const uint32_t all = __shfl_sync(~0u, inc, 31);
+    inc -= mine;
+    uint32_t g0 = gt0 + (inc & 0xFFFF), e0 = eq0 + (inc >> 16);   // before this position
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool is_gt = gt >> j & 1, is_eq = eq >> j & 1;
+      if (is_gt || (is_eq && e0 < take)) {
+        const uint32_t at = g0 + min(e0, take);
+        keep[at] = i0 + 4 * lane + j;
+        new_weight[at] = four[j] ? key_score((uint64_t)four[j] << 32) : weight[i0 + 4 * lane + j];   // (0: some NaN, as it was)
+      }
+      g0 += is_gt;
+      e0 += is_eq;
+    }
+    gt0 += all & 0xFFFF;
+    eq0 += all >> 16;
   }
 }
 
