@@ -219,19 +219,38 @@ struct AttnPlan {
   bool tensor_core;
 };
 
-// Which kernel, and how the query heads of a key-value head are laid on its tiles.
-//
-// More than 16 query heads per key-value head at head dimension 128: attn_tc.cuh, 64
-// columns a row, two rows of a request together where requests have several.  Otherwise
-// attn.cuh: a tile holds 16 (query head, row) pairs; where a group, or its rows that share
-// the cache, need more, 32 (two tiles that share every key and value read), up to head
-// dimension 128 (beyond it two tiles' sums do not fit a thread's registers).  `far`: a cache
-// spans 64 GB or more, where attn_tc.cuh's offsets (32 bits, in units of 16 bytes) end.
-AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_heads, int64_t dim, bool far, int sm) {
+// Which of the two kernels, at head dimension 128 (attn_tc.cuh knows no other; and its offsets
+// end where a cache spans 64 GB, `far`).  attn_tc.cuh loads with fewer instructions and holds 64
+// query heads a row, but two rows of a request at the most, and a unit's end costs it 3 us;
+// attn.cuh holds 16 or 32 pairs of query head and row.  Measured (us; attn_tc.cuh, attn.cuh):
+//   one or two rows a request, long: 64 heads on 8, 32 requests of 4096..65536, 1 row 648, 672,
+//     2 rows 652, 677; 32 heads on 8 184, 192; 8 on 8 184, 192; 64 on 1, 2 rows 105, 402
+//   up to 2000 positions: 64 on 8 76, 76; up to 1000: 32 on 8 110, 105; 64 on 1 36, 69
+//   more rows than two: 64 on 8, 3 rows 1271, 1008; 8 on 1, 4 rows 165, 145; but 16 on 1, 4 rows
+//     166, 237 (with 11 heads or more attn.cuh's tile holds two rows as well)
+//   slots: 2048 rows of 1024, 32 on 4 480, 516; 64 rows of 1024, 32 on 8 46, 49; 2048 of 512,
+//     16 on 1 87, 80, 24 on 1 88, 137; 4096 of 128, 16 on 1 96, 56
+// `positions`: what a row sees at most, as far as the host knows (the page table's width).
+bool tensor_core_for(int64_t group, int64_t per_req, int64_t dim, int64_t positions, bool slots, bool far) {
+  if (dim != 128 || far) return false;
+  if (group > 16) return true;
+  if (slots) return positions >= 1024;
+  if (group > 10 && group * per_req > 16) return true;
+  return per_req <= 2 && positions >= 2048;
+}
+
+// How the query heads of a key-value head are laid on the kernel's tiles.  attn_tc.cuh: 64 columns
+// a row, two rows of a request together where requests have several (32 requests x 2 rows x 64
+// heads on one: 105 us, 166 one by one).  attn.cuh: a tile holds 16 (query head, row) pairs; where
+// a group, or its rows that share the cache, need more, 32 (two tiles that share every key and
+// value read; 32 requests x 4 rows x 64 heads on 8: 757 us, 1295 with 16), up to head dimension
+// 128 (beyond it two tiles' sums do not fit a thread's registers).
+AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t positions,
+                 bool slots, bool far, int sm) {
   AttnPlan a{};
   a.group = (int32_t)(q_heads / kv_heads);
   const int64_t per_req = num_req > 0 ? (rows + num_req - 1) / num_req : 1;
-  a.tensor_core = dim == 128 && a.group > 16 && !far;
+  a.tensor_core = tensor_core_for(a.group, per_req, dim, positions, slots, far);
   const int32_t most = a.tensor_core ? 64 : dim <= 128 && (int64_t)a.group * per_req > 16 ? 32 : 16;
   a.chunks = (a.group + most - 1) / most;
   a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
@@ -323,7 +342,8 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   if ((st = check_arch(&m))) return st;
   const bool weights = c.weight_out != nullptr && numel_of(c.weight_out) > 0;
   const bool far = span_of(c.k) >= kFar || span_of(c.v) >= kFar;
-  const AttnPlan a = plan_of(R, c.slots ? R : NR, Hq, Hk, D, far, m.sm);
+  const AttnPlan a = c.slots ? plan_of(R, R, Hq, Hk, D, c.slots->shape[1], true, far, m.sm)
+                             : plan_of(R, NR, Hq, Hk, D, MP * kPage, false, far, m.sm);
   int64_t logit_rows, logit_bytes;
   if (weights && (!mul_ok(R * Hq, MP * kPage, &logit_rows) || !mul_ok(logit_rows, 4, &logit_bytes) ||
                   logit_bytes > (INT64_MAX >> 2)))
@@ -377,7 +397,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
 }
 
 int attn_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t num_req, int64_t max_pages,
-               bool weights, int32_t device, uint64_t* bytes) {
+               int64_t selected, bool weights, int32_t device, uint64_t* bytes) {
   if (!bytes || rows < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || max_pages < 0)
     return IDX_ERR_INVALID_ARGUMENT;
   if (dim != 64 && dim != 128 && dim != 256) return IDX_ERR_UNSUPPORTED;
@@ -389,7 +409,8 @@ int attn_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim, int
   // whichever kernel the cache's extent allows
   *bytes = 0;
   for (bool far : {false, true}) {
-    const AttnPlan a = plan_of(rows, num_req, q_heads, kv_heads, dim, far, sm);
+    const AttnPlan a = plan_of(rows, num_req, q_heads, kv_heads, dim, selected ? selected : max_pages * kPage,
+                               selected != 0, far, sm);
     const uint64_t n = layout_of(a, sm, rows, q_heads, dim, max_pages, weights).total;
     if (n > *bytes) *bytes = n;
   }
@@ -521,7 +542,7 @@ int idx_attn_paged_async(const idx_tensor_t* q, const idx_tensor_t* k_cache, con
 
 int idx_attn_paged_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t num_req,
                                  int32_t max_pages, int32_t with_weights, int32_t device, uint64_t* bytes) {
-  return attn_bytes(rows, q_heads, kv_heads, head_dim, num_req, max_pages, with_weights != 0, device, bytes);
+  return attn_bytes(rows, q_heads, kv_heads, head_dim, num_req, max_pages, 0, with_weights != 0, device, bytes);
 }
 
 int idx_attn_selected(const idx_tensor_t* q, const idx_tensor_t* k_cache, const idx_tensor_t* v_cache,
@@ -546,7 +567,7 @@ int idx_attn_selected_async(const idx_tensor_t* q, const idx_tensor_t* k_cache, 
 int idx_attn_selected_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                     int32_t selected, int32_t device, uint64_t* bytes) {
   if (selected < 1) return IDX_ERR_INVALID_ARGUMENT;
-  return attn_bytes(rows, q_heads, kv_heads, head_dim, rows, 0, false, device, bytes);
+  return attn_bytes(rows, q_heads, kv_heads, head_dim, rows, 0, selected, false, device, bytes);
 }
 
 int idx_cache_evict(const idx_tensor_t* k_cache, const idx_tensor_t* v_cache, const idx_tensor_t* page_table,

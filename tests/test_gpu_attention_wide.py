@@ -230,3 +230,67 @@ def test_same_bits_again_and_in_a_graph():
         torch.cuda.synchronize()
         assert int(st.item()) == 0
         assert bool((c.out == out).all()) and bool((c.lse == lse).all()) and bool((w == w0).all())
+
+
+@pytest.mark.parametrize("heads", [(8, 8), (4, 1), (32, 8), (16, 1), (10, 2)])
+@pytest.mark.parametrize("dtype,layout", [("bf16", "slot"), ("f16", "joint"), ("bf16", "head")])
+def test_few_heads_over_long_contexts(heads, dtype, layout):
+    """Up to 16 query heads per key-value head, one and two rows a request, where the context is long
+    enough for the wide tiles; three rows, where it is not the context that decides."""
+    lens = [3000, 2200, 1, 0, 130]
+    wins = [(0, 0, 2999), (0, 7, 3000), (1, 1000, 2199), (1, 0, 900), (2, 0, 1), (2, 0, 0), (3, 0, 0), (3, 0, 0), (4, 0, 129),
+            (4, 0, 130)]
+    for w in (wins, wins[::2], wins + [(0, 100, 2500), (1, 2000, 2200), (4, 64, 128), (2, 0, 1), (3, 0, 0)]):
+        c = B.Case(lens, w, *heads, 128, dtype, layout, q_strided=True)
+        assert B.run_paged(c) == 0
+        c.check()
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (16, 1), (3, 3)])
+def test_weights_of_few_heads_over_long_contexts(heads):
+    import torch
+    wins = [(0, 0, 2500), (1, 100, 2100), (0, 2400, 2500), (2, 0, 0), (1, 0, 50)]
+    c = B.Case([2500, 2100, 5], wins, *heads, 128)
+    win = torch.rand(3, c.mp * PAGE, device="cuda")
+    wout = torch.full_like(win, 7.0)
+    assert B.run_paged(c, weight_in=win, weight_out=wout) == 0
+    c.check()
+    tot, bound = B._want_weights(c, win)
+    assert bool(((wout.double() - tot).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (16, 1), (32, 8), (2, 2)])
+@pytest.mark.parametrize("n", [1023, 1024, 1100])
+def test_selected_few_heads_of_long_lists(heads, n):
+    import torch
+    import fp4_sparse_attention_tma_gb300 as m
+    for dtype, layout in (("bf16", "slot"), ("f16", "head"), ("bf16", "joint")):
+        c, slots = B._slot_case(40, n, *heads, 128, dtype, layout)
+        slots[3, :700] = -1
+        m.idx_attn_selected(c.q, c.k, c.v, slots, c.scale, c.out, out_lse=c.lse)
+        torch.cuda.synchronize()
+        B._check_selected(c, slots)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("heads", [(8, 1), (32, 8)])
+def test_few_heads_and_what_one_row_sees(bad, heads):
+    import torch
+    c = B.Case([2500, 2400], [(0, 3, 2498), (0, 3, 2500), (1, 200, 2000), (1, 100, 1900)], *heads, 128)
+    t = c.table.cpu()
+    assert B.run_paged(c) == 0
+    want = c.out.clone()
+    for req, row, only in ((0, 1, range(2498, 2500)), (1, 2, range(1900, 2000)), (1, 3, range(100, 200)), (0, None, range(0, 3))):
+        k0, v0 = c.k.clone(), c.v.clone()
+        pos = torch.tensor(list(only))
+        page, off = t[req][pos // PAGE].long().cuda(), (pos % PAGE).cuda()
+        c.k[page, off] = bad
+        c.v[page, off] = bad
+        assert B.run_paged(c) == 0
+        for r in range(4):
+            if r == row:
+                assert not bool(c.out[r].isfinite().all())
+            else:
+                assert bool((c.out[r] == want[r]).all())
+        c.k.copy_(k0)
+        c.v.copy_(v0)
