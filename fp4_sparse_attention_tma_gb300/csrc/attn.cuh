@@ -9,13 +9,16 @@
 // not), which costs as much as the rounding of the output.
 //
 // What bounds it is the cache's traffic: a key and a value are read for 4 flops per
-// query head of their group and element, so up to about 70 query heads per key-value
-// head are below the tensor cores' ratio to HBM.  Hence warps that never wait for one
+// query head of their group and element, far below the tensor cores' ratio to HBM for
+// the 16 or 32 (query head, row) pairs of a tile.  Hence warps that never wait for one
 // another: every warp owns a ring of asynchronous 16-byte copies (kSub positions of
 // keys and values a stage) and a range of subtiles (attn.h), and one warp-level matrix
 // instruction chain consumes a stage while the others are in flight.  The copies take
 // any page, slot and head stride and any list of slots, and fill with zero what no row
-// sees, so that what lies there cannot reach a sum.
+// sees, so that what lies there cannot reach a sum.  As many warps as the shared memory
+// has rings for (3 stages of 16 positions).  48 requests x 3 rows x 16 heads of dimension
+// 64 over up to 1002 positions: 160 MB in 49 us, of which 5 us pass before the first copy
+// and 8 in the join; 32 requests x 3 rows x 64 heads on 8: 4.45 GB in 1008 us.
 #pragma once
 
 #include "attn_common.cuh"
