@@ -226,17 +226,20 @@ struct AttnPlan {
 //   one or two rows a request, long: 64 heads on 8, 32 requests of 4096..65536, 1 row 648, 672,
 //     2 rows 652, 677; 32 heads on 8 184, 192; 8 on 8 184, 192; 64 on 1, 2 rows 105, 402
 //   up to 2000 positions: 64 on 8 76, 76; up to 1000: 32 on 8 110, 105; 64 on 1 36, 69
+//   windows of 100 under a table of 4000, 32 on 8: 256 requests 74, 37, 76 requests 33, 21, 38 requests
+//     25, 20; of 2000: 256 requests 324, 333 (hence: many units, which may be short, are attn.cuh's)
 //   more rows than two: 64 on 8, 3 rows 1271, 1008; 8 on 1, 4 rows 165, 145; but 16 on 1, 4 rows
 //     166, 237 (with 11 heads or more attn.cuh's tile holds two rows as well)
 //   slots: 2048 rows of 1024, 32 on 4 480, 516; 64 rows of 1024, 32 on 8 46, 49; 2048 of 512,
 //     16 on 1 87, 80, 24 on 1 88, 137; 4096 of 128, 16 on 1 96, 56
 // `positions`: what a row sees at most, as far as the host knows (the page table's width).
-bool tensor_core_for(int64_t group, int64_t per_req, int64_t dim, int64_t positions, bool slots, bool far) {
+bool tensor_core_for(int64_t group, int64_t rows, int64_t per_req, int64_t kv_heads, int64_t dim, int64_t positions,
+                     bool slots, bool far, int sm) {
   if (dim != 128 || far) return false;
   if (group > 16) return true;
   if (slots) return positions >= 1024;
   if (group > 10 && group * per_req > 16) return true;
-  return per_req <= 2 && positions >= 2048;
+  return per_req <= 2 && positions >= 2048 && (rows + per_req - 1) / per_req * kv_heads <= 2 * sm;
 }
 
 // How the query heads of a key-value head are laid on the kernel's tiles.  attn_tc.cuh: 64 columns
@@ -249,8 +252,8 @@ AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_head
                  bool slots, bool far, int sm) {
   AttnPlan a{};
   a.group = (int32_t)(q_heads / kv_heads);
-  const int64_t per_req = num_req > 0 ? (rows + num_req - 1) / num_req : 1;
-  a.tensor_core = tensor_core_for(a.group, per_req, dim, positions, slots, far);
+  const int64_t per_req = rows > num_req && num_req > 0 ? (rows + num_req - 1) / num_req : 1;
+  a.tensor_core = tensor_core_for(a.group, rows, per_req, kv_heads, dim, positions, slots, far, sm);
   const int32_t most = a.tensor_core ? 64 : dim <= 128 && (int64_t)a.group * per_req > 16 ? 32 : 16;
   a.chunks = (a.group + most - 1) / most;
   a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;

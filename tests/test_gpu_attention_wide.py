@@ -294,3 +294,26 @@ def test_few_heads_and_what_one_row_sees(bad, heads):
                 assert bool((c.out[r] == want[r]).all())
         c.k.copy_(k0)
         c.v.copy_(v0)
+
+
+def test_no_rows_over_a_wide_table():
+    import torch
+    import fp4_sparse_attention_tma_gb300 as m
+    c = B.Case([3000], [(0, 0, 3000)], 8, 2, 128)
+    win = torch.rand(1, c.mp * PAGE, device="cuda")
+    wout = torch.zeros_like(win)
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert m.idx_attn_paged(c.q[:0], c.k, c.v, c.table, e, e, e, 0.1, c.out[:0], weight_in=win, weight_out=wout) == 0
+    torch.cuda.synchronize()
+    assert bool((wout == win).all())
+    for rows in (0, 1, 5):
+        assert m.idx_attn_paged_scratch_bytes(rows, 8, 2, 128, 2, 1000) > 0
+
+
+@pytest.mark.parametrize("requests", [3, 200])
+def test_short_windows_under_a_wide_table(requests):
+    """Few units, and many, where the table alone says that rows may be long."""
+    wins = [(i, 2300 - 7 * i, 2400 - 5 * i) for i in range(requests)]
+    c = B.Case([2400] * requests, wins, 16, 4, 128, "f16")
+    assert B.run_paged(c) == 0
+    c.check()
