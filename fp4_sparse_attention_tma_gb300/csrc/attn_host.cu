@@ -400,7 +400,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
 }
 
 int attn_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t num_req, int64_t max_pages,
-               int64_t selected, bool weights, int32_t device, uint64_t* bytes) {
+               bool slots, bool weights, int32_t device, uint64_t* bytes) {
   if (!bytes || rows < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || max_pages < 0)
     return IDX_ERR_INVALID_ARGUMENT;
   if (dim != 64 && dim != 128 && dim != 256) return IDX_ERR_UNSUPPORTED;
@@ -409,14 +409,14 @@ int attn_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim, int
   if (st) return st;
   int64_t n;
   if (weights && (!mul_ok(rows * q_heads, max_pages * kPage, &n) || n > (INT64_MAX >> 4))) return IDX_ERR_OVERFLOW;
-  // whichever kernel the cache's extent allows
+  // whichever kernel the caches' extent and the rows' length choose
   *bytes = 0;
-  for (bool far : {false, true}) {
-    const AttnPlan a = plan_of(rows, num_req, q_heads, kv_heads, dim, selected ? selected : max_pages * kPage,
-                               selected != 0, far, sm);
-    const uint64_t n = layout_of(a, sm, rows, q_heads, dim, max_pages, weights).total;
-    if (n > *bytes) *bytes = n;
-  }
+  for (bool far : {false, true})
+    for (int64_t positions : {(int64_t)1, kMostPositions}) {
+      const AttnPlan a = plan_of(rows, num_req, q_heads, kv_heads, dim, positions, slots, far, sm);
+      const uint64_t n = layout_of(a, sm, rows, q_heads, dim, max_pages, weights).total;
+      if (n > *bytes) *bytes = n;
+    }
   return IDX_OK;
 }
 
@@ -545,7 +545,7 @@ int idx_attn_paged_async(const idx_tensor_t* q, const idx_tensor_t* k_cache, con
 
 int idx_attn_paged_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t num_req,
                                  int32_t max_pages, int32_t with_weights, int32_t device, uint64_t* bytes) {
-  return attn_bytes(rows, q_heads, kv_heads, head_dim, num_req, max_pages, 0, with_weights != 0, device, bytes);
+  return attn_bytes(rows, q_heads, kv_heads, head_dim, num_req, max_pages, false, with_weights != 0, device, bytes);
 }
 
 int idx_attn_selected(const idx_tensor_t* q, const idx_tensor_t* k_cache, const idx_tensor_t* v_cache,
@@ -570,7 +570,7 @@ int idx_attn_selected_async(const idx_tensor_t* q, const idx_tensor_t* k_cache, 
 int idx_attn_selected_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                     int32_t selected, int32_t device, uint64_t* bytes) {
   if (selected < 1) return IDX_ERR_INVALID_ARGUMENT;
-  return attn_bytes(rows, q_heads, kv_heads, head_dim, rows, 0, selected, false, device, bytes);
+  return attn_bytes(rows, q_heads, kv_heads, head_dim, rows, 0, true, false, device, bytes);
 }
 
 int idx_cache_evict(const idx_tensor_t* k_cache, const idx_tensor_t* v_cache, const idx_tensor_t* page_table,

@@ -317,3 +317,20 @@ def test_short_windows_under_a_wide_table(requests):
     c = B.Case([2400] * requests, wins, 16, 4, 128, "f16")
     assert B.run_paged(c) == 0
     c.check()
+
+
+@pytest.mark.parametrize("heads", [(8, 8), (32, 8), (64, 1), (96, 2)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_workspace_does_not_depend_on_the_context(heads, dim):
+    """One workspace serves every width of the page table and every length of the lists."""
+    import fp4_sparse_attention_tma_gb300 as m
+    for rows, reqs in ((1, 1), (7, 3), (64, 32), (3000, 1500)):
+        assert len({m.idx_attn_paged_scratch_bytes(rows, *heads, dim, reqs, mp) for mp in (1, 31, 32, 5000)}) == 1
+        assert len({m.idx_attn_selected_scratch_bytes(rows, *heads, dim, n) for n in (1, 512, 1024, 100000)}) == 1
+    c = B.Case([2500, 100], [(0, 0, 2500), (1, 0, 100), (0, 5, 2400)], *heads, dim)
+    ws, st = B._space(c)
+    assert m.idx_attn_paged_async(*c.args(), ws, st, out_lse=c.lse) == 0
+    import torch
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    c.check()
