@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
       }
 
       // running maximum; the sums are scaled where it moved
-      float mc[MT][2];
+      float ref[MT][2];
       bool moved = false;
       float alpha[MT][2];
 #pragma unroll
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
           m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
           m = fmaxf(m, mx[t][e]);
           // a row without a finite score so far keeps 0 in its maximum's place
-          mc[t][e] = m == kNegInf ? 0.f : __fmul_rn(m, c);
-          alpha[t][e] = ex2(__fsub_rn(__fmul_rn(mx[t][e], c), mc[t][e]));
+          ref[t][e] = m == kNegInf ? 0.f : m;
+          alpha[t][e] = ex2(exponent(mx[t][e], ref[t][e], c));
           moved |= m != mx[t][e];
           mx[t][e] = m;
         }
@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float a = ex2(fmaf(s[t][n][2 * e], c, -mc[t][e]));
-            const float b = ex2(fmaf(s[t][n][2 * e + 1], c, -mc[t][e]));
+            const float a = ex2(exponent(s[t][n][2 * e], ref[t][e], c));
+            const float b = ex2(exponent(s[t][n][2 * e + 1], ref[t][e], c));
             sum[t][e] += a + b;
             pf[t][n * 2 + e] = pack2<BF16>(a, b);
           }
@@ -400,12 +400,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
             const int m = t * 16 + e * 8 + lane / 4;
             const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
             const bool on = live >> (2 * t + e) & 1;
-            const float mcs = __fmul_rn(mx[t][e], c);
             if (!whole) {
               const int64_t at_part = ((int64_t)worker * 2 + which) * TILE + m;
               if (on) {
                 // a sum of -1: the part saw no position at all
-                if ((lane & 3) == 0) p.part_ml[at_part] = make_float2(mcs, SLOTS && !seen ? -1.f : l);
+                if ((lane & 3) == 0) p.part_ml[at_part] = make_float2(mx[t][e], SLOTS && !seen ? -1.f : l);
                 float2* dst = (float2*)(p.part_o + at_part * D) + (lane & 3);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) dst[n * 4] = make_float2(o[t][n][2 * e], o[t][n][2 * e + 1]);
@@ -419,8 +418,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
               for (int n = 0; n < NT; ++n)
                 *(uint32_t*)(dst + n * 8) = pack2<BF16>(o[t][n][2 * e] * inv, o[t][n][2 * e + 1] * inv);
               if ((lane & 3) == 0) {
-                if (p.lse) p.lse[row * p.q_heads + qh] = (mcs + log2f(l)) * 0.6931471805599453f;
-                if (p.row_stat) p.row_stat[row * p.q_heads + qh] = make_float2(mcs == kNegInf ? 0.f : mcs, inv);
+                if (p.lse) p.lse[row * p.q_heads + qh] = (__fmul_rn(mx[t][e], c) + log2f(l)) * 0.6931471805599453f;
+                if (p.row_stat) p.row_stat[row * p.q_heads + qh] = make_float2(mx[t][e] == kNegInf ? 0.f : mx[t][e], inv);
               }
             }
           }

@@ -57,13 +57,13 @@ struct AttnParams {
   int32_t* active;                  // workers that have a range (the first so many)
   int32_t* open_parts;              // [active] parts of the unit that the range's end cuts first, or 0
   int4* open_info;                  // [workers] {first row of its group, rows, unit index in the group, 0}
-  float2* part_ml;                  // [workers][2][tile] maximum (in units of log2, scaled) and sum
+  float2* part_ml;                  // [workers][2][tile] maximum (of the products, not scaled) and sum
   float* part_o;                    // [workers][2][tile][dim]
   int32_t tile;                     // tile rows of a unit: 16 or 32; tensor_core: 64 or 128
   int32_t dim;
   // accumulated weights
   float* logits;                    // [rows * q_heads][max_pages * 64] or null
-  float2* row_stat;                 // [rows * q_heads] maximum (scaled) and 1 / sum, or null
+  float2* row_stat;                 // [rows * q_heads] maximum (not scaled) and 1 / sum, or null
   const float* weight_in;           // [num_req][max_pages * 64] or null
   float* weight_out;
   uint32_t* status_out;
@@ -93,6 +93,17 @@ inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int6
 // Warps of a CTA of the kernel of attn.cuh (with its ring stages, what fits the shared
 // memory of an SM).
 inline int attn_warps(int32_t dim, int32_t tile) { return dim == 256 ? 4 : dim == 128 ? 8 : tile == 32 ? 12 : 16; }
+
+#ifdef __CUDACC__
+// The exponent of a product of a row, counted from the row's reference `ref` (finite; c the scale in
+// units of log2).  The difference is formed before it is scaled: it is 0 where the two are equal, and
+// not above 0 where the product is not above the reference.  (Formed after it, in one fused
+// operation, it would keep the rounding of the scaled reference, which beyond 2^31 can be more than
+// fp32's exponents hold: the largest weight would be infinite or 0.)
+__device__ __forceinline__ float exponent(float product, float ref, float c) {
+  return __fmul_rn(__fsub_rn(product, ref), c);
+}
+#endif
 
 // The attention kernel; bf16: the inputs' type (else fp16).
 cudaError_t launch_attn(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);

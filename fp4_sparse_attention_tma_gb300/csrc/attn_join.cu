@@ -85,7 +85,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const OpenUnit& 
     for (int u = 0; u < U; ++u)
       if (ml[u].y != -1.f) top = fmaxf(top, ml[u].x);
     const float base = top == -INFINITY ? 0.f : top;
-    const float a = pow2(M - base);
+    const float a = pow2(exponent(M, base, p.scale_log2));
     l *= a;
 #pragma unroll
     for (int x = 0; x < V; ++x) acc[x] *= a;
@@ -93,7 +93,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const OpenUnit& 
     for (int u = 0; u < U; ++u) {
       if (ml[u].y == -1.f) continue;
       seen = true;
-      const float e = pow2(ml[u].x - base);
+      const float e = pow2(exponent(ml[u].x, base, p.scale_log2));
       l += ml[u].y * e;
 #pragma unroll
       for (int x = 0; x < V; ++x) acc[x] += o[u][x] * e;
@@ -104,7 +104,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const OpenUnit& 
 
 // One tile row (query head x row) of one cut unit at a time: its parts lie with the worker
 // that opened the unit (part 1) and the workers after it (part 0), and
-//   M = max m_i, l = sum l_i 2^(m_i - M), out = sum o_i 2^(m_i - M) / l.
+//   M = max m_i, l = sum l_i 2^(c (m_i - M)), out = sum o_i 2^(c (m_i - M)) / l.
 // Where a unit has few parts, each warp joins a row by itself; where it has many (few rows
 // over a long context), the warps of a CTA take the row's parts in turn, in a fixed order,
 // and their sums are joined in the same way.  Bound by the latency of a chain of loads: the ranges' ends,
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_ke
     for (int x = 0; x < V; ++x) dst[x] = (T)(acc[x] * inv);
     if (lane == 0) {
       const int64_t at = row * p.q_heads + qh;
-      if (p.lse) p.lse[at] = (M + log2f(l)) * 0.6931471805599453f;
+      if (p.lse) p.lse[at] = (__fmul_rn(M, p.scale_log2) + log2f(l)) * 0.6931471805599453f;
       if (p.row_stat) p.row_stat[at] = make_float2(M == -INFINITY ? 0.f : M, inv);
     }
   }
@@ -223,19 +223,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_ke
     bool any = false;
 #pragma unroll
     for (int i = 0; i < kJoinWarps; ++i)
-      if (wl[i] != -1.f) any = true, total += wl[i] * pow2(wm[i] - base);
+      if (wl[i] != -1.f) any = true, total += wl[i] * pow2(exponent(wm[i], base, p.scale_log2));
     const float inv = any ? 1.f / total : 0.f;
     T* dst = (T*)p.out + row * p.out_row + (int64_t)qh * p.out_head;
     for (int x = threadIdx.x; x < D; x += kJoinWarps * 32) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < kJoinWarps; ++i)
-        if (wl[i] != -1.f) sum += wo[i][x] * pow2(wm[i] - base);
+        if (wl[i] != -1.f) sum += wo[i][x] * pow2(exponent(wm[i], base, p.scale_log2));
       dst[x] = (T)(sum * inv);
     }
     if (threadIdx.x == 0) {
       const int64_t at = row * p.q_heads + qh;
-      if (p.lse) p.lse[at] = (top + log2f(total)) * 0.6931471805599453f;
+      if (p.lse) p.lse[at] = (__fmul_rn(top, p.scale_log2) + log2f(total)) * 0.6931471805599453f;
       if (p.row_stat) p.row_stat[at] = make_float2(base, inv);
     }
     __syncthreads();
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_ke
 }
 
 // weight_out[i, s] = weight_in[i, s] + the sum over request i's rows (in order) and
-// query heads of 2^(logit - M) / l.  Reads every logit once; a thread owns 4
+// query heads of 2^(c (logit - M)) / l.  Reads every logit once; a thread owns 4
 // positions and a quarter of the heads, and the quarters are added up in order, so
 // the sum's order is fixed.  Bound by the logits' traffic and, with few requests, the
 // latency of a thread's loads (16 requests x 32 heads of up to 32768 positions: a call of 209 us,
@@ -291,10 +291,10 @@ __global__ void __launch_bounds__(kWeightThreads) attn_weights_kernel(const __gr
         for (int h = h0; h < h1; ++h) {
           const float4 x = __ldcs((const float4*)(lg + h * width));
           const float2 s = st[h];
-          if (m0) sum.x += pow2(fmaf(x.x, c, -s.x)) * s.y;
-          if (m1) sum.y += pow2(fmaf(x.y, c, -s.x)) * s.y;
-          if (m2) sum.z += pow2(fmaf(x.z, c, -s.x)) * s.y;
-          if (m3) sum.w += pow2(fmaf(x.w, c, -s.x)) * s.y;
+          if (m0) sum.x += pow2(exponent(x.x, s.x, c)) * s.y;
+          if (m1) sum.y += pow2(exponent(x.y, s.x, c)) * s.y;
+          if (m2) sum.z += pow2(exponent(x.z, s.x, c)) * s.y;
+          if (m3) sum.w += pow2(exponent(x.w, s.x, c)) * s.y;
         }
       }
     };

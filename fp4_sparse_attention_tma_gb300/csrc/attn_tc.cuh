@@ -247,13 +247,14 @@ struct Walk {
   }
 };
 
-// Two fp32 operations in one instruction, and a maximum of three.
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float bx, float by) {
+// Two fp32 operations in one instruction, and a maximum of three.  exponent2: `exponent` of two products
+// (minus the reference is given).
+__device__ __forceinline__ void exponent2(float& x, float& y, float minus_ref, float c) {
   asm("{\n\t.reg .b64 v, m, s;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmov.b64 s, {%3, %4};\n\t"
-      "fma.rn.f32x2 v, v, m, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 m, {%3, %3};\n\t"
+      "add.rn.f32x2 v, v, s;\n\tmul.rn.f32x2 v, v, m;\n\tmov.b64 {%0, %1}, v;\n\t}"
       : "+f"(x), "+f"(y)
-      : "f"(a), "f"(bx), "f"(by));
+      : "f"(minus_ref), "f"(c));
 }
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
   asm("{\n\t.reg .b64 v, s;\n\t"
@@ -514,10 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             top = fmaxf(top, top2);
             row_max[b][g][x] = top;
             bar_sync(pair, 64);
-            top = __fmul_rn(fmaxf(top, row_max[b][g ^ 1][x]), p.scale_log2);
+            top = fmaxf(top, row_max[b][g ^ 1][x]);
             // does its weights' reference have to follow?
-            if (__any_sync(~0u, top > ref + kRaise || (ref == kNegInf && top > kNegInf))) {
-              const float raised = fmaxf(ref, top), f = ref == kNegInf ? (raised == kNegInf ? 1.f : 0.f) : ex2(ref - raised);
+            if (__any_sync(~0u, exponent(top, ref, p.scale_log2) > kRaise)) {   // (false where both are -infinity)
+              const float raised = fmaxf(ref, top), f = raised == ref ? 1.f : ex2(exponent(ref, raised, p.scale_log2));
               ref = raised;
 #pragma unroll
               for (int i = 0; i < 4; ++i) sum[i] *= f;
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
                 float d0 = __uint_as_float(r[i]), d1 = __uint_as_float(r[i + 1]);
-                fma2(d0, d1, p.scale_log2, base, base);
+                exponent2(d0, d1, base, p.scale_log2);
                 const float e0 = ex2(d0), e1 = ex2(d1);
                 add2(sum[i & 2], sum[(i & 2) + 1], e0, e1);
                 w[i / 2] = pack2<BF16>(e0, e1);
@@ -622,8 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           const bool other = o.y != -1.f;
           top = fmaxf(has ? ref : kNegInf, other ? o.x : kNegInf);
           const float base = top == kNegInf ? 0.f : top;
-          f = has ? ex2(ref - base) : 0.f;
-          l = (has ? l * f : 0.f) + (other ? o.y * ex2(o.x - base) : 0.f);
+          f = has ? ex2(exponent(ref, base, p.scale_log2)) : 0.f;
+          l = (has ? l * f : 0.f) + (other ? o.y * ex2(exponent(o.x, base, p.scale_log2)) : 0.f);
           any = has || other;
         }
         const float inv = any ? 1.f / l : 0.f;
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             p.part_ml[part] = make_float2(top, any ? l : -1.f);
           } else {
             const int64_t i = row * p.q_heads + qh;
-            if (p.lse) p.lse[i] = (top + log2f(l)) * 0.6931471805599453f;
+            if (p.lse) p.lse[i] = (__fmul_rn(top, p.scale_log2) + log2f(l)) * 0.6931471805599453f;
             if (p.row_stat) p.row_stat[i] = make_float2(top == kNegInf ? 0.f : top, inv);
           }
         }
