@@ -6,7 +6,8 @@
 //
 // products in 16 bits with fp32 accumulation, everything else in fp32; the weights
 // 2^(s - m) are rounded to the inputs' type for the second product (their sum is
-// not), which costs as much as the rounding of the output.
+// not), which the matrix instruction asks for: an error of u sum p |v| at most beside the
+// output's own u |out| (u half a unit in the last place; fp16's range: kShift in attn.h).
 //
 // What bounds it is the cache's traffic: a key and a value are read for 4 flops per
 // query head of their group and element, far below the tensor cores' ratio to HBM for
@@ -328,8 +329,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float a = ex2(exponent(s[t][n][2 * e], ref[t][e], c));
-            const float b = ex2(exponent(s[t][n][2 * e + 1], ref[t][e], c));
+            const float a = ex2(fmaf(__fsub_rn(s[t][n][2 * e], ref[t][e]), c, kShift<BF16>));
+            const float b = ex2(fmaf(__fsub_rn(s[t][n][2 * e + 1], ref[t][e]), c, kShift<BF16>));
             sum[t][e] += a + b;
             pf[t][n * 2 + e] = pack2<BF16>(a, b);
           }
@@ -418,8 +419,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
               for (int n = 0; n < NT; ++n)
                 *(uint32_t*)(dst + n * 8) = pack2<BF16>(o[t][n][2 * e] * inv, o[t][n][2 * e + 1] * inv);
               if ((lane & 3) == 0) {
-                if (p.lse) p.lse[row * p.q_heads + qh] = (__fmul_rn(mx[t][e], c) + log2f(l)) * 0.6931471805599453f;
-                if (p.row_stat) p.row_stat[row * p.q_heads + qh] = make_float2(mx[t][e] == kNegInf ? 0.f : mx[t][e], inv);
+                if (p.lse) p.lse[row * p.q_heads + qh] = log_sum_exp<BF16>(mx[t][e], l, c);
+                if (p.row_stat)
+                  p.row_stat[row * p.q_heads + qh] =
+                      make_float2(mx[t][e] == kNegInf ? 0.f : mx[t][e], inv * kShiftUp<BF16>);
               }
             }
           }

@@ -57,7 +57,7 @@ struct AttnParams {
   int32_t* active;                  // workers that have a range (the first so many)
   int32_t* open_parts;              // [active] parts of the unit that the range's end cuts first, or 0
   int4* open_info;                  // [workers] {first row of its group, rows, unit index in the group, 0}
-  float2* part_ml;                  // [workers][2][tile] maximum (of the products, not scaled) and sum
+  float2* part_ml;                  // [workers][2][tile] maximum (of the products, not scaled) and sum (shifted)
   float* part_o;                    // [workers][2][tile][dim]
   int32_t tile;                     // tile rows of a unit: 16 or 32; tensor_core: 64 or 128
   int32_t dim;
@@ -102,6 +102,22 @@ inline int attn_warps(int32_t dim, int32_t tile) { return dim == 256 ? 4 : dim =
 // fp32's exponents hold: the largest weight would be infinite or 0.)
 __device__ __forceinline__ float exponent(float product, float ref, float c) {
   return __fmul_rn(__fsub_rn(product, ref), c);
+}
+
+// Weights are rounded to the inputs' type for the product with the values.  bf16 has fp32's range; fp16
+// loses bits below 2^-14 and ends at 2^-25, where a long tail under one heavy position would be lost
+// while its sum is not.  So fp16 weights, their sums and the weighted values are 2^kShift times what they
+// stand for: bits are lost below 2^-24 of a row's largest weight, nothing above 2^-35 vanishes, and n
+// positions together are off by n 2^-35 max |v| at the most.
+template <bool BF16>
+constexpr float kShift = BF16 ? 0.f : 10.f;
+template <bool BF16>
+constexpr float kShiftUp = BF16 ? 1.f : 1024.f;   // 2^kShift
+
+// The row's log sum exp from its maximum and its (shifted) sum.
+template <bool BF16>
+__device__ __forceinline__ float log_sum_exp(float top, float sum, float c) {
+  return (__fmul_rn(top, c) + log2f(sum * (1.f / kShiftUp<BF16>))) * 0.6931471805599453f;
 }
 #endif
 

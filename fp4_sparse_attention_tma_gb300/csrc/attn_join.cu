@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_ke
     for (int x = 0; x < V; ++x) dst[x] = (T)(acc[x] * inv);
     if (lane == 0) {
       const int64_t at = row * p.q_heads + qh;
-      if (p.lse) p.lse[at] = (__fmul_rn(M, p.scale_log2) + log2f(l)) * 0.6931471805599453f;
-      if (p.row_stat) p.row_stat[at] = make_float2(M == -INFINITY ? 0.f : M, inv);
+      if (p.lse) p.lse[at] = log_sum_exp<BF16>(M, l, p.scale_log2);
+      if (p.row_stat) p.row_stat[at] = make_float2(M == -INFINITY ? 0.f : M, inv * kShiftUp<BF16>);
     }
   }
   for (int job = blockIdx.x; job < many * p.tile; job += gridDim.x) {
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_ke
     }
     if (threadIdx.x == 0) {
       const int64_t at = row * p.q_heads + qh;
-      if (p.lse) p.lse[at] = (__fmul_rn(top, p.scale_log2) + log2f(total)) * 0.6931471805599453f;
-      if (p.row_stat) p.row_stat[at] = make_float2(base, inv);
+      if (p.lse) p.lse[at] = log_sum_exp<BF16>(top, total, p.scale_log2);
+      if (p.row_stat) p.row_stat[at] = make_float2(base, inv * kShiftUp<BF16>);
     }
     __syncthreads();
   }

@@ -11,9 +11,9 @@
 // A matrix row is a tensor memory lane and a thread of each softmax warpgroup: its sum and its
 // weights need no other thread, the weights are written over the scores they come from, and next to
 // nothing of a visit passes through shared memory.  O is scaled only when a row's maximum exceeds
-// the reference of its weights by kRaise (in units of log2); a weight, at most 2^kRaise then, is
-// rounded to the inputs' type for the second product (its sum is not), which costs as much as the
-// output's rounding.
+// the reference of its weights by kRaise (in units of log2); a weight, at most 2^kRaise then (fp16:
+// 2^(kRaise + kShift), within its range), is rounded to the inputs' type for the second product (its
+// sum is not), which the matrix instruction asks for: u sum p |v| at most beside the output's u |out|.
 //
 // What bounds it: HBM where the cache is long (32 requests x 2 rows x 64 heads on 8, 4096..65536
 // positions: 4.45 GB in 633 us, 7.0 TB/s; one row of 262143 positions: 160 us, 6.7 TB/s).  The same
@@ -54,7 +54,8 @@ constexpr uint32_t kTileBytes = 2 * kHalfTile;  // a tile of keys, of values or 
 constexpr int kWarps = 20;
 constexpr int kThreads = kWarps * 32;
 constexpr int kLoaders = 128;             // threads that copy keys (and as many values)
-constexpr float kRaise = 8.f;             // weights are at most 2^kRaise
+template <bool BF16>
+constexpr float kRaise = BF16 ? 8.f : 5.f;   // weights are at most 2^(kRaise + kShift)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOut = 256;            // first column of the accumulators, after two tiles of scores
 constexpr int kRingK = 3, kRingV = 2;     // tiles of keys and of values in shared memory
@@ -248,13 +249,13 @@ struct Walk {
 };
 
 // Two fp32 operations in one instruction, and a maximum of three.  exponent2: `exponent` of two products
-// (minus the reference is given).
-__device__ __forceinline__ void exponent2(float& x, float& y, float minus_ref, float c) {
-  asm("{\n\t.reg .b64 v, m, s;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 m, {%3, %3};\n\t"
-      "add.rn.f32x2 v, v, s;\n\tmul.rn.f32x2 v, v, m;\n\tmov.b64 {%0, %1}, v;\n\t}"
+// (minus the reference is given), and the shift.
+__device__ __forceinline__ void exponent2(float& x, float& y, float minus_ref, float c, float shift) {
+  asm("{\n\t.reg .b64 v, m, s, h;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 m, {%3, %3};\n\tmov.b64 h, {%4, %4};\n\t"
+      "add.rn.f32x2 v, v, s;\n\tfma.rn.f32x2 v, v, m, h;\n\tmov.b64 {%0, %1}, v;\n\t}"
       : "+f"(x), "+f"(y)
-      : "f"(minus_ref), "f"(c));
+      : "f"(minus_ref), "f"(c), "f"(shift));
 }
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
   asm("{\n\t.reg .b64 v, s;\n\t"
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             bar_sync(pair, 64);
             top = fmaxf(top, row_max[b][g ^ 1][x]);
             // does its weights' reference have to follow?
-            if (__any_sync(~0u, exponent(top, ref, p.scale_log2) > kRaise)) {   // (false where both are -infinity)
+            if (__any_sync(~0u, exponent(top, ref, p.scale_log2) > kRaise<BF16>)) {   // (false where both are -infinity)
               const float raised = fmaxf(ref, top), f = raised == ref ? 1.f : ex2(exponent(ref, raised, p.scale_log2));
               ref = raised;
 #pragma unroll
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
                 float d0 = __uint_as_float(r[i]), d1 = __uint_as_float(r[i + 1]);
-                exponent2(d0, d1, base, p.scale_log2);
+                exponent2(d0, d1, base, p.scale_log2, kShift<BF16>);
                 const float e0 = ex2(d0), e1 = ex2(d1);
                 add2(sum[i & 2], sum[(i & 2) + 1], e0, e1);
                 w[i / 2] = pack2<BF16>(e0, e1);
@@ -633,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             p.part_ml[part] = make_float2(top, any ? l : -1.f);
           } else {
             const int64_t i = row * p.q_heads + qh;
-            if (p.lse) p.lse[i] = (__fmul_rn(top, p.scale_log2) + log2f(l)) * 0.6931471805599453f;
-            if (p.row_stat) p.row_stat[i] = make_float2(top == kNegInf ? 0.f : top, inv);
+            if (p.lse) p.lse[i] = log_sum_exp<BF16>(top, l, p.scale_log2);
+            if (p.row_stat) p.row_stat[i] = make_float2(top == kNegInf ? 0.f : top, inv * kShiftUp<BF16>);
           }
         }
         if (whole) f *= inv;

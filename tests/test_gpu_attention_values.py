@@ -1,9 +1,11 @@
-"""Attention where the scores reach the ends of their type: scores beyond 2^24.  Every kernel,
-whole and cut units, windows and lists of slots."""
+"""Attention where the scores or the softmax weights reach the ends of their types: one position
+far above a long tail (fp16 weights lose bits below 2^-14 and vanish below 2^-25), scores beyond
+2^24.  Every kernel, whole and cut units, windows and lists of slots."""
 import math
 
 import pytest
 
+from tests import attn_ref as A
 from tests import test_gpu_attention as B
 
 pytestmark = pytest.mark.gpu
@@ -45,6 +47,94 @@ def _case(n, kind, dtype, copies=1):
     c.req = torch.arange(copies, dtype=torch.int32, device="cuda").repeat_interleave(rows)
     c.wins = [(int(i), 0, n) for i in c.req.cpu()]
     return c
+
+
+def _many(kind):
+    """Requests that give every worker of the kernel more than one unit."""
+    return {(64, 1): 200, (32, 8): 38}.get(kind[0], 1300)
+
+
+# ------------------------------------------------------------- weights ----
+
+@pytest.mark.parametrize("form", ["paged", "slots"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_long_tail_under_one_position(kind, dtype, form):
+    """Position j weighs 1 and every other 2^-d: out = (v_j + (n - 1) 2^-d v) / (1 + (n - 1) 2^-d).
+
+    The scores are exact products.  A weight is rounded to the inputs' type with a relative error
+    of u; an fp16 weight is taken relative to at least 2^10 times the row's largest, so that one
+    below fp16's normal range is off by 2^-25 2^-10 of it at the most, and the output by n times
+    that: no more than 2^-17 of max |v| for the longest row here."""
+    import torch
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    many = _many(kind)
+    for n, d, copies in ((5001, 10.3, many), (5001, 17.45, many), (5001, 20.55, many), (5001, 24.7, many), (5001, 25.3, many),
+                         (5001, 26.4, many), (1900, 24.85, many), (262143, 24.6, 1), (262143, 25.4, 1)):
+        if n > 100000 and (kind[0][1] > 2 or kind[1] > 128):
+            continue
+        c = _case(n, kind, dtype, copies)
+        D = c.dim
+        # q = e_0: the score is scale * log2(e) * k_0 in units of log2
+        c.q.zero_()
+        c.q[:, :, 0] = 1.0
+        c.k.zero_()
+        j = {0: 0, 1: n - 1, 2: n // 2}[int(d * 10) % 3]
+        c.k[(*_place(c, 0, [j]), slice(None), 0)] = 64.0
+        c.scale = d * math.log(2) / 64.0
+        # signs that agree, then values that cancel; the heavy position's value is 0
+        for signs in (False, True):
+            pos = torch.arange(n)
+            page, off = _place(c, 0, pos)
+            v = torch.ones(n, device="cuda")
+            if signs:
+                v[1::2] = -0.5
+            c.v[page, off] = v.to(c.v.dtype)[:, None, None].expand(n, c.hk, D)
+            c.v[_place(c, 0, [j])] = 0.0
+            v[j] = 0.0
+            _attend(c, form)
+            w = torch.full((n,), 2.0 ** -d, dtype=torch.float64, device="cuda")
+            w[j] = 1.0
+            total = w.sum()
+            want, mag = float((w * v.double()).sum() / total), float((w * v.abs().double()).sum() / total)
+            # fp32: the scale, its product with log2(e) and the score's are rounded, as are 2^x and the sums
+            ep = 2 * (d * 3 * 2.0 ** -24 * math.log(2)) + 2.0 ** -20
+            bound = u * abs(want) + (u + ep + n * 2.0 ** -24) * mag + (n * 2.0 ** -35 if dtype == "f16" else 0.0)
+            if dtype == "f16" and abs(want) < 2.0 ** -14:
+                bound += 2.0 ** -25      # the output's own rounding
+            err = float((c.out.double() - want).abs().max())
+            assert err <= bound, (n, d, signs, want, err, bound)
+            # (n additions to the sum)
+            assert float((c.lse.double() - (d * math.log(2) + math.log(total))).abs().max()) <= 2.0 ** -17 + n * 2.0 ** -24
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_random_tail_under_one_position_f16(kind):
+    """Scores of deviation 1/2 and one position 16 to 18 above them, first, last or between."""
+    import torch
+    for n, gap in ((30000, 16.0), (30000, 17.0), (30000, 18.0)):
+        c = _case(n, kind, "f16", _many(kind) // 4)
+        j = {16.0: 0, 17.0: 31, 18.0: 1234}[gap]
+        # every head's queries are parallel to the unit vector x, whose keys carry the scores
+        x = torch.ones(c.dim, device="cuda") / 8.0
+        c.q[:] = x.half()
+        g = torch.Generator(device="cuda")
+        g.manual_seed(int(gap))
+        s = torch.randn(n, c.hk, device="cuda", generator=g) * 0.5
+        s[j] = gap
+        c.scale = 1.0
+        page, off = _place(c, 0, torch.arange(n))
+        c.k[page, off] = (s[:, :, None] * (8.0 / c.dim)).half().expand(n, c.hk, c.dim)
+        c.v[_place(c, 0, [j])] = 0.001
+        c.v.abs_()                       # values of one sign: errors of the weights add up
+        assert B.run_paged(c) == 0
+        k, v = c.rows()[0]
+        want, lse, _, _, bl, ep = A.attend(c.q[0], k, v, c.scale)     # (every row's)
+        u = 2.0 ** -11
+        bound = u * want + (u + ep[:, None] + n * 2.0 ** -24) * want + n * 2.0 ** -35 * float(v.max())   # all values are positive
+        err = (c.out.double() - want).abs()
+        assert bool((err <= bound).all()), (gap, float((err / want).max()), float((bound / want).max()))
+        assert bool(((c.lse.double() - lse).abs() <= bl + n * 2.0 ** -24).all())
 
 
 # -------------------------------------------------------- large scores ----
