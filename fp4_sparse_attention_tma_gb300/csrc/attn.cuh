@@ -302,9 +302,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_kernel(const __grid_consta
           m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
           m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
           m = fmaxf(m, mx[t][e]);
-          // a row without a finite score so far keeps 0 in its maximum's place
-          ref[t][e] = m == kNegInf ? 0.f : m;
-          alpha[t][e] = ex2(exponent(mx[t][e], ref[t][e], c));
+          ref[t][e] = reference(m);
+          alpha[t][e] = m == mx[t][e] ? 1.f : ex2(exponent(mx[t][e], ref[t][e], c));
           moved |= m != mx[t][e];
           mx[t][e] = m;
         }

@@ -95,6 +95,12 @@ inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int6
 inline int attn_warps(int32_t dim, int32_t tile) { return dim == 256 ? 4 : dim == 128 ? 8 : tile == 32 ? 12 : 16; }
 
 #ifdef __CUDACC__
+// What exponents are counted from, where a row's maximum is `top`: the maximum, or 0 where it is
+// infinite.  Below -infinity every weight is 0.  Above it a score of +infinity weighs +infinity, so
+// that the sum is infinite (NaN only with a score of NaN), log sum exp is +infinity and the outputs,
+// infinity over infinity, are NaN.
+__device__ __forceinline__ float reference(float top) { return fabsf(top) == INFINITY ? 0.f : top; }
+
 // The exponent of a product of a row, counted from the row's reference `ref` (finite; c the scale in
 // units of log2).  The difference is formed before it is scaled: it is 0 where the two are equal, and
 // not above 0 where the product is not above the reference.  (Formed after it, in one fused

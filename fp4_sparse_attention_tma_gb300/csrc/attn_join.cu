@@ -84,7 +84,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const OpenUnit& 
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (ml[u].y != -1.f) top = fmaxf(top, ml[u].x);
-    const float base = top == -INFINITY ? 0.f : top;
+    const float base = reference(top);
     const float a = pow2(exponent(M, base, p.scale_log2));
     l *= a;
 #pragma unroll
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_ke
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, wm[i]);
-    const float base = top == -INFINITY ? 0.f : top;
+    const float base = reference(top);
     float total = 0.f;
     bool any = false;
 #pragma unroll
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_ke
     if (threadIdx.x == 0) {
       const int64_t at = row * p.q_heads + qh;
       if (p.lse) p.lse[at] = log_sum_exp<BF16>(top, total, p.scale_log2);
-      if (p.row_stat) p.row_stat[at] = make_float2(base, inv * kShiftUp<BF16>);
+      if (p.row_stat) p.row_stat[at] = make_float2(top == -INFINITY ? 0.f : top, inv * kShiftUp<BF16>);
     }
     __syncthreads();
   }

@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               }
             }
             // the weights, over the scores
-            const float base = ref == kNegInf ? 0.f : -ref;
+            const float base = -reference(ref);
             auto weigh = [&](int k, const uint32_t (&r)[32]) {
               uint32_t w[16];
 #pragma unroll
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           const float2 o = half_ml[part_of ^ 1][col];
           const bool other = o.y != -1.f;
           top = fmaxf(has ? ref : kNegInf, other ? o.x : kNegInf);
-          const float base = top == kNegInf ? 0.f : top;
+          const float base = reference(top);
           f = has ? ex2(exponent(ref, base, p.scale_log2)) : 0.f;
           l = (has ? l * f : 0.f) + (other ? o.y * ex2(exponent(o.x, base, p.scale_log2)) : 0.f);
           any = has || other;

@@ -1,6 +1,6 @@
 """Attention where the scores or the softmax weights reach the ends of their types: one position
 far above a long tail (fp16 weights lose bits below 2^-14 and vanish below 2^-25), scores beyond
-2^24.  Every kernel, whole and cut units, windows and lists of slots."""
+2^24, scores of +infinity.  Every kernel, whole and cut units, windows and lists of slots."""
 import math
 
 import pytest
@@ -182,3 +182,69 @@ def test_weights_of_scores_beyond_2_to_24(kind, dtype):
             want = torch.zeros_like(w)
             want[0, 77] = c.hq * len(c.wins)
             assert bool(((w - want).abs() <= 2.0 ** -18 * want).all()), (n, e)
+
+
+# ------------------------------------------------------------ infinity ----
+
+@pytest.mark.parametrize("form", ["paged", "slots"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_scores_of_plus_infinity(kind, dtype, form):
+    """A visible score of +infinity: log sum exp is +infinity and the outputs are NaN, as in the
+    formula; with a visible score of NaN as well, both are NaN.  Other requests notice nothing."""
+    import torch
+    heads, dim, rows = kind
+    for n in (1, 40, 300, 9000):
+        for j in sorted({0, n // 2, n - 1}):
+            c = B.Case([n, 500], [(0, 0, n)] * rows + [(1, 0, 500)] * rows, *heads, dim, dtype)
+            c.q.abs_().clamp_(min=0.125)
+            _attend(c, form)
+            out, lse = c.out.clone(), c.lse.clone()
+            c.k[(*_place(c, 0, [j]), slice(None), 3)] = float("inf")
+            _attend(c, form)
+            assert bool(torch.isposinf(c.lse[:rows]).all()), (n, j)
+            assert bool(c.out[:rows].isnan().all()), (n, j)
+            assert bool((c.out[rows:] == out[rows:]).all()) and bool((c.lse[rows:] == lse[rows:]).all())
+            # one more far from it, and then a score of NaN
+            c.k[(*_place(c, 0, [n - 1 - j]), slice(None), 3)] = float("inf")
+            _attend(c, form)
+            assert bool(torch.isposinf(c.lse[:rows]).all()) and bool(c.out[:rows].isnan().all()), (n, j)
+            if n > 2:
+                for x in {1, n - 2}:
+                    k0 = c.k.clone()
+                    c.k[(*_place(c, 0, [x]), slice(None), 5)] = float("nan")
+                    _attend(c, form)
+                    assert bool(c.lse[:rows].isnan().all()) and bool(c.out[:rows].isnan().all()), (n, j, x)
+                    c.k.copy_(k0)
+
+
+@pytest.mark.parametrize("form", ["paged", "slots"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_plus_infinity_within_a_workers_range(kind, dtype, form):
+    """The same where one worker sees all of a request: before, among and after finite scores."""
+    import torch
+    for n, at in ((700, [0]), (700, [350]), (700, [699]), (2100, [5, 2000])):
+        c = _case(n, kind, dtype, _many(kind))
+        c.q.abs_().clamp_(min=0.125)
+        c.k[(*_place(c, 0, at), slice(None), 3)] = float("inf")
+        _attend(c, form)
+        assert bool(torch.isposinf(c.lse).all()) and bool(c.out.isnan().all()), (n, at)
+        c.k[(*_place(c, 0, [300]), slice(None), 5)] = float("nan")
+        _attend(c, form)
+        assert bool(c.lse.isnan().all()) and bool(c.out.isnan().all()), (n, at)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_weights_beside_a_score_of_plus_infinity(kind):
+    """exp(s - infinity) is 0 for the finite scores and NaN where the score is infinite."""
+    import torch
+    for n in (300, 9000):
+        c = _case(n, kind, "bf16")
+        c.q.abs_().clamp_(min=0.125)
+        c.k[(*_place(c, 0, [100]), slice(None), 3)] = float("inf")
+        w = torch.full((1, c.mp * PAGE), 7.0, device="cuda")
+        assert B.run_paged(c, weight_out=w) == 0
+        assert bool(w[0, 100].isnan())
+        w[0, 100] = 0.0
+        assert bool((w == 0).all())
