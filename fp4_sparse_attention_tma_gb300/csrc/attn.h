@@ -4,8 +4,8 @@
 //
 // The work of a call is a list of units.  A unit is one key-value head (or, where
 // more query heads share it than one matrix tile holds, one chunk of them) of one
-// row group: consecutive rows of one request, as many as share a tile, so that
-// their cached positions are read once.  A unit is cut into subtiles of kSub
+// row group: consecutive rows of one request that share a tile and, in attn.cuh, whose
+// windows meet, so that their cached positions are read once.  A unit is cut into subtiles of kSub
 // positions; the units' subtiles, one after another, are dealt to the workers (one
 // warp each; in attn_tc.cuh one CTA each, with tiles of 128 positions) in equal
 // contiguous ranges, each unit counted as kUnitCost subtiles more than it has (its

@@ -96,9 +96,35 @@ struct Rows {
   const int32_t *req, *start, *end;
 };
 
-// Row groups: a row starts one where the request changes, and every group_rows rows.
+// Row groups: a row starts one where the request changes, and every group_rows rows of the call (counted
+// from its first row, so a request's rows may fall into two groups).
 __device__ __forceinline__ bool starts_group(const AttnParams& p, const Rows& rows, int32_t r) {
   return r < p.rows && (r % p.group_rows == 0 || rows.req[r - 1] != rows.req[r]);
+}
+
+// Whether a row's window [a, b) does not meet the window [a0, b0) of the row before it.  Groups whose rows
+// are walked over together (Cursor) end there: their windows then have no gap between them, so that every
+// position that is read is under some row's window, and no page is asked for that none needs.
+__device__ __forceinline__ bool apart(int32_t a0, int32_t b0, int32_t a, int32_t b) {
+  return b > a && (b0 <= a0 || max(a, a0) > min(b, b0));
+}
+
+// What a unit of the group that starts at row r counts; 0 where none does, or it sees nothing.  (A call of
+// its own: within the kernel it costs the loops there registers, 51.5 us for 50.8 at 48 requests x 3 rows x
+// 16 heads of dimension 64.)
+inline __device__ __noinline__ int32_t joint_count(Rows rows, int32_t n_rows, int32_t group_rows, int32_t r) {
+  if (r >= n_rows) return 0;
+  const int32_t req = rows.req[r], stop = min(n_rows, (r / group_rows + 1) * group_rows);
+  int32_t a0 = rows.start[r], b0 = rows.end[r];
+  if (r % group_rows != 0 && rows.req[r - 1] == req && !apart(rows.start[r - 1], rows.end[r - 1], a0, b0)) return 0;
+  int32_t a = b0 > a0 ? a0 : INT32_MAX, b = b0 > a0 ? b0 : 0;
+  for (int32_t i = r + 1; i < stop && rows.req[i] == req; ++i) {
+    const int32_t a1 = rows.start[i], b1 = rows.end[i];
+    if (apart(a0, b0, a1, b1)) break;
+    if (b1 > a1) a = min(a, a1), b = max(b, b1);
+    a0 = a1, b0 = b1;
+  }
+  return b > a ? (b + kSub - 1) / kSub - a / kSub + kUnitCost : 0;
 }
 
 // A place in the list of units: subtile `s` of one unit of the group at row0.
@@ -124,14 +150,12 @@ struct Cursor {
       const int32_t stop = min(p.rows, (row / p.group_rows + 1) * p.group_rows);
       const bool in = r < stop;
       const int32_t rr = in ? rows.req[r] : -1;
+      int32_t a = in ? rows.start[r] : 0, b = in ? rows.end[r] : 0;
+      const int32_t a0 = __shfl_up_sync(~0u, a, 1), b0 = __shfl_up_sync(~0u, b, 1);
       req = __shfl_sync(~0u, rr, 0);
-      const uint32_t other = ~__ballot_sync(~0u, in && rr == req);
+      const uint32_t other = ~__ballot_sync(~0u, in && rr == req && (lane == 0 || !apart(a0, b0, a, b)));
       nrows = other ? __ffs(other) - 1 : 32;
-      int32_t a = INT32_MAX, b = 0;
-      if (lane < nrows) {
-        const int32_t a0 = rows.start[r], b0 = rows.end[r];
-        if (b0 > a0) a = a0, b = b0;
-      }
+      if (lane >= nrows || b <= a) a = INT32_MAX, b = 0;
       lo = __reduce_min_sync(~0u, a);
       hi = __reduce_max_sync(~0u, b);
       if (lo > hi) lo = hi;
@@ -139,16 +163,8 @@ struct Cursor {
     }
     nsub = hi > lo ? (hi + kSub - 1) / kSub - base : 0;
   }
-  // What a unit of the group that starts at row r counts; 0 where none does, or it sees nothing.
   __device__ static int32_t count(const AttnParams& p, const Rows& rows, int32_t r) {
-    if (!starts_group(p, rows, r)) return 0;
-    const int32_t req = rows.req[r], stop = min(p.rows, (r / p.group_rows + 1) * p.group_rows);
-    int32_t a = INT32_MAX, b = 0;
-    for (int32_t i = r; i < stop && rows.req[i] == req; ++i) {
-      const int32_t a0 = rows.start[i], b0 = rows.end[i];
-      if (b0 > a0) a = min(a, a0), b = max(b, b0);
-    }
-    return b > a ? (b + kSub - 1) / kSub - a / kSub + kUnitCost : 0;
+    return joint_count(rows, p.rows, p.group_rows, r);
   }
   // The same for a row of a call over slots.
   __device__ static int32_t row_count(const AttnParams& p) { return (p.n_slots + kSub - 1) / kSub + kUnitCost; }
