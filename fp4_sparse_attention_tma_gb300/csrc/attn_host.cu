@@ -106,6 +106,62 @@ bool same_layout(const idx_tensor_t* x, const idx_tensor_t* y) {
   return true;
 }
 
+bool same_strides(const idx_tensor_t* x, const idx_tensor_t* y) {
+  for (int i = 0; i < x->ndim; ++i)
+    if (x->shape[i] != y->shape[i] || (x->shape[i] > 1 && x->stride[i] != y->stride[i])) return false;
+  return true;
+}
+
+// Elements from the address of x to that of y.
+int64_t distance(const idx_tensor_t* x, const idx_tensor_t* y) {
+  return ((int64_t)(uintptr_t)y->data - (int64_t)(uintptr_t)x->data) / elem_bytes(x);
+}
+
+// Whether two elements of a cache whose dimensions nest (no_overlap) lie `delta` apart, other than two of
+// one position (`one_position`: those do not count).  Dimension by dimension, the largest stride first: of
+// the steps along it only one or two leave a rest that the others can reach.
+bool elements_apart(const idx_tensor_t* t, int64_t delta, bool one_position, uint32_t used = 0, bool moved = false) {
+  int best = -1;
+  int64_t inner = 0;
+  for (int i = 0; i < 4; ++i)
+    if (!(used >> i & 1) && t->shape[i] > 1 && (best < 0 || t->stride[i] > t->stride[best])) best = i;
+  if (best < 0) return delta == 0 && (moved || !one_position);
+  used |= 1u << best;
+  for (int i = 0; i < 4; ++i)
+    if (!(used >> i & 1) && t->shape[i] > 1) inner += (t->shape[i] - 1) * t->stride[i];
+  const int64_t s = t->stride[best], n = t->shape[best] - 1;
+  for (int64_t d = delta / s - 2; d <= delta / s + 2; ++d) {
+    const int64_t rest = delta - d * s;
+    if (d < -n || d > n || rest > inner || rest < -inner) continue;
+    if (elements_apart(t, rest, one_position, used, moved || (best < 2 && d != 0))) return true;
+  }
+  return false;
+}
+
+// Whether keys and values moved into k_dst and v_dst (each without overlap in itself) keep out of each
+// other's way: the two share no element, or only elements that the caches' keys and values of a position
+// share alike (a latent cache that both are views of: the same bytes are moved twice).
+bool places_agree(const idx_tensor_t* k, const idx_tensor_t* v, const idx_tensor_t* k_dst, const idx_tensor_t* v_dst) {
+  if (apart(k_dst, v_dst)) return true;
+  if (same_strides(k_dst, v_dst)) {
+    bool alike = same_strides(k, v) && distance(k, v) == distance(k_dst, v_dst);
+    for (int i = 1; i < 4; ++i) alike &= k->shape[i] <= 1 || k->stride[i] == k_dst->stride[i];
+    return !elements_apart(k_dst, distance(k_dst, v_dst), alike);
+  }
+  // laid out differently: in every page apart
+  const int64_t page = k_dst->stride[0];
+  if (k_dst->shape[0] <= 1 || v_dst->stride[0] != page || page <= 0) return false;
+  int64_t k_end = 1, v_end = 1;
+  for (int i = 1; i < 4; ++i) {
+    if (k_dst->shape[i] <= 1) continue;
+    k_end += (k_dst->shape[i] - 1) * k_dst->stride[i];
+    v_end += (v_dst->shape[i] - 1) * v_dst->stride[i];
+  }
+  int64_t at = distance(k_dst, v_dst) % page;
+  if (at < 0) at += page;
+  return at >= k_end && at + v_end <= page;
+}
+
 // The stride of dimension i (0 where it has one element: nothing steps along it).
 int64_t step(const idx_tensor_t* t, int i) { return t->shape[i] > 1 ? t->stride[i] : 0; }
 
@@ -470,7 +526,7 @@ int run_evict(const EvictCall& c, const Space& space, cudaStream_t stream) {
   // the fresh pages are pages of the same tensors, or of others that lie apart from them
   const bool same = NR > 0 && same_layout(c.k, c.k_dst) && same_layout(c.v, c.v_dst);
   if (!no_overlap(c.k_dst) || !no_overlap(c.v_dst)) return IDX_ERR_INVALID_ARGUMENT;
-  if (c.k_dst->data == c.v_dst->data && !same_layout(c.k, c.v) && NR > 0) return IDX_ERR_INVALID_ARGUMENT;
+  if (NR > 0 && !places_agree(c.k, c.v, c.k_dst, c.v_dst)) return IDX_ERR_INVALID_ARGUMENT;
   for (const idx_tensor_t* d : {c.k_dst, c.v_dst})
     for (const idx_tensor_t* s : {c.k, c.v})
       if (!same && !apart(d, s)) return IDX_ERR_INVALID_ARGUMENT;

@@ -582,7 +582,10 @@ int idx_attn_selected_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_he
  *   page_table     i32 [NR, MP], seq_len i32 [NR], weight f32 [NR, MP * 64]
  *   budget >= 1, keep_first >= 0, keep_last >= 0, keep_first + keep_last <= budget
  *   k_dst, v_dst   [DN, 64, Hk, D]: the caches themselves (same address and strides),
- *                  or tensors that lie apart from them
+ *                  or tensors that lie apart from them.  The two may interleave in one
+ *                  allocation, but share no element; only where keys and values of a
+ *                  position share elements in the caches (two views of one latent cache)
+ *                  may they share the same ones of a position here.
  *   dst_page_table i32 [NR, DP]: fresh pages, DP <= MP, DP * 64 >= min(budget, MP * 64)
  *   out_keep_idx   i32 [NR, budget]  kept positions, ascending, then -1
  *   out_len        i32 [NR]          min(seq_len, budget)
