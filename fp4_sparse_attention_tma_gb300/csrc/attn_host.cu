@@ -361,7 +361,8 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   if ((st = check_space(space))) return st;
   if ((st = check_heads(c.q, c.k, c.v, c.out))) return st;
   const int64_t R = c.q->shape[0], Hq = c.q->shape[1], D = c.q->shape[2], NP = c.k->shape[0], Hk = c.k->shape[2];
-  if (!(c.scale > 0.f) || !std::isfinite(c.scale)) return IDX_ERR_INVALID_ARGUMENT;
+  const float scale_log2 = c.scale * 1.4426950408889634f;   // what the kernels work with
+  if (!(c.scale > 0.f) || !std::isfinite(scale_log2)) return IDX_ERR_INVALID_ARGUMENT;
   if (c.lse && ((st = check_tensor(c.lse, IDX_F32, 2)))) return st;
   if (c.lse && (c.lse->shape[0] != R || c.lse->shape[1] != Hq)) return IDX_ERR_INVALID_ARGUMENT;
   int64_t NR = 1, MP = 0;
@@ -431,7 +432,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   p.far = far;
   p.workers = R > 0 ? a.workers : 0;
   p.n_cta = R > 0 ? m.sm : 0;
-  p.scale_log2 = c.scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.tile = a.tile, p.dim = (int32_t)D;
   const bool bf16 = c.q->dtype == IDX_BF16;
   return with_space(space, L.total, m, stream, [&](char* base, uint32_t* status) -> cudaError_t {

@@ -510,7 +510,7 @@ int idx_dense_topk_fp4_prefill(const idx_tensor_t* q_fp4, const idx_tensor_t* q_
  * hold; within it infinities and NaN propagate as in the formula.  Rows of one
  * request that follow one another read the cache together.
  *   page_table i32 [NR, MP], row_req / row_start / row_end i32 [R] as above
- *   scale      finite, above 0
+ *   scale      above 0, and finite also when multiplied by log2(e)
  *   out        [R, Hq, D], q's type
  *   out_lse    f32 [R, Hq] or NULL
  *   weight_in, weight_out  f32 [NR, MP * 64] or NULL: weight_out[i, s] =

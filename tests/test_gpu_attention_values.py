@@ -248,3 +248,21 @@ def test_weights_beside_a_score_of_plus_infinity(kind):
         assert bool(w[0, 100].isnan())
         w[0, 100] = 0.0
         assert bool((w == 0).all())
+
+
+def test_a_scale_beyond_the_kernels_units_is_refused():
+    """Exponents are counted in units of log2: scale * log2(e) has to be finite."""
+    import torch
+    import fp4_sparse_attention_tma_gb300 as m
+    c = B.Case([100], [(0, 0, 100)], 8, 2, 64)
+    c.q.zero_()                  # scores of 0 at any scale: out is the mean of the values
+    for scale, code in ((3.4e38, B.INVALID_ARGUMENT), (2.4e38, B.INVALID_ARGUMENT), (2.3e38, 0), (1e-45, 0)):
+        c.scale = scale
+        c.out.fill_(7.0)
+        assert B.run_paged(c) == code
+        if code:
+            assert bool((c.out == 7).all())
+            slots = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+            assert m.idx_attn_selected(c.q, c.k, c.v, slots, scale, c.out, raise_on_error=False) == code
+        else:
+            c.check()
