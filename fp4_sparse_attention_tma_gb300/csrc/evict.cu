@@ -119,7 +119,7 @@ __device__ void select(const EvictParams& p, cooperative_groups::cluster_group& 
   const int32_t s0 = min((int64_t)n, (int64_t)rank * slice), s1 = min((int64_t)n, (int64_t)s0 + slice);
   const bool held = slice <= p.slice_cap;
   if (cut && held) {
-    const int32_t fours = ((uintptr_t)weight & 15) == 0 ? (s1 - s0) / 4 : 0;
+    const int32_t fours = (s1 - s0) / 4;   // (a request's weights, 256 bytes a page, begin at 16-byte boundaries)
 #pragma unroll 8
     for (int32_t i = tid; i < fours; i += kSelThreads) ((uint4*)bits)[i] = keys_of(((const float4*)(weight + s0))[i]);
 #pragma unroll 8
