@@ -18,8 +18,9 @@
 // any page, slot and head stride and any list of slots, and fill with zero what no row
 // sees, so that what lies there cannot reach a sum.  As many warps as the shared memory
 // has rings for (3 stages of 16 positions).  48 requests x 3 rows x 16 heads of dimension
-// 64 over up to 1002 positions: 160 MB in 49 us, of which 5 us pass before the first copy
-// and 8 in the join; 32 requests x 3 rows x 64 heads on 8: 4.45 GB in 1008 us.
+// 64 over up to 1002 positions: 160 MB in 50 us, of which 5 us pass before the first copy
+// and 8 in the join; 32 requests x 3 rows x 64 heads on 8: 4.45 GB in 1008 us (groups of four rows begin at
+// every fourth row of the call, so the 32 requests are walked over 48 times).
 #pragma once
 
 #include "attn_common.cuh"

@@ -284,7 +284,8 @@ struct AttnPlan {
 //   up to 2000 positions: 64 on 8 76, 76; up to 1000: 32 on 8 110, 105; 64 on 1 36, 69
 //   windows of 100 under a table of 4000, 32 on 8: 256 requests 74, 37, 76 requests 33, 21, 38 requests
 //     25, 20; of 2000: 256 requests 324, 333 (hence: many units, which may be short, are attn.cuh's)
-//   more rows than two: 64 on 8, 3 rows 1271, 1008; 8 on 1, 4 rows 165, 145; but 16 on 1, 4 rows
+//   more rows than two: 64 on 8, 3 rows 1271, 1008 (as many walks as for 4 rows and half as many again: groups
+//     begin at fixed row numbers), 4 rows 757 (attn.cuh); 8 on 1, 4 rows 165, 145; but 16 on 1, 4 rows
 //     166, 237 (with 11 heads or more attn.cuh's tile holds two rows as well)
 //   slots: 2048 rows of 1024, 32 on 4 480, 516; 64 rows of 1024, 32 on 8 46, 49; 2048 of 512,
 //     16 on 1 87, 80, 24 on 1 88, 137; 4096 of 128, 16 on 1 96, 56
@@ -298,7 +299,10 @@ bool tensor_core_for(int64_t group, int64_t rows, int64_t per_req, int64_t kv_he
   return per_req <= 2 && positions >= 2048 && (rows + per_req - 1) / per_req * kv_heads <= 2 * sm;
 }
 
-// How the query heads of a key-value head are laid on the kernel's tiles.  attn_tc.cuh: 64 columns
+// How the query heads of a key-value head are laid on the kernel's tiles.  The page table's rows stand for
+// the number of requests, which the host does not know: under a table of more rows than the call has, rows
+// are taken for single ones (one call between events: 32 requests x 2 rows x 64 heads on one 178 us, 120
+// under a table of 32; x 4 rows x 64 heads on 8 1313, 756).  attn_tc.cuh: 64 columns
 // a row, two rows of a request together where requests have several (32 requests x 2 rows x 64
 // heads on one: 105 us, 166 one by one).  attn.cuh: a tile holds 16 (query head, row) pairs; where
 // a group, or its rows that share the cache, need more, 32 (two tiles that share every key and

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) attn_join_ke
 // query heads of 2^(c (logit - M)) / l.  Reads every logit once; a thread owns 4
 // positions and a quarter of the heads, and the quarters are added up in order, so
 // the sum's order is fixed.  Bound by the logits' traffic and, with few requests, the
-// latency of a thread's loads (16 requests x 32 heads of up to 32768 positions: a call of 209 us,
+// latency of a thread's loads (16 requests x 32 heads of up to 32768 positions: a call of 213 us,
 // 5 us more with all heads in one thread).
 constexpr int kWeightPos = 128;                       // threads that share a quarter of the heads
 constexpr int kWeightParts = 4;

@@ -16,11 +16,11 @@
 // sum is not), which the matrix instruction asks for: u sum p |v| at most beside the output's u |out|.
 //
 // What bounds it: HBM where the cache is long (32 requests x 2 rows x 64 heads on 8, 4096..65536
-// positions: 4.45 GB in 633 us, 7.0 TB/s; one row of 262143 positions: 160 us, 6.7 TB/s).  The same
-// batch with one key-value head: 0.56 GB in 104 us, of which 5 us pass before the first copies, 4 us
+// positions: 4.45 GB in 652 us, 6.8 TB/s; one row of 262143 positions: 163 us, 6.6 TB/s).  The same
+// batch with one key-value head: 0.56 GB in 105 us, of which 5 us pass before the first copies, 4 us
 // in a segment's end and 8 us in the join.  Where rows pick 1024 slots of a cache that L2 holds, the
 // copies (64 KB a visit), the products and the softmax each take 0.7 to 0.8 us a visit and overlap to
-// 1.0, and a unit of 8 visits ends in 2.5 us (8192 rows: 548 us, 500 TFLOP/s; without the copies 15 %
+// 1.0, and a unit of 8 visits ends in 2.5 us (8192 rows: 555 us, 495 TFLOP/s; without the copies 15 %
 // less, without the products 13 %).
 //
 // Two rows of one request: matrix rows 0..63 and 64..127 are theirs; both use the tiles that both

@@ -494,8 +494,11 @@ int idx_dense_topk_fp4_prefill(const idx_tensor_t* q_fp4, const idx_tensor_t* q_
  * their code with nothing enqueued and the outputs untouched.  After an error that
  * the device finds (IDX_ERR_INVALID_METADATA, IDX_ERR_INVALID_PAGE) floating
  * outputs are NaN and integer outputs -1.  Sums, maxima and weights are held in
- * fp32; outputs are rounded once, and the softmax weights are rounded to the
- * inputs' type for their product with the values.  Results do not depend on the
+ * fp32; outputs are rounded once, and the softmax weights p are rounded to the
+ * inputs' type for their product with the values: an error of u sum p |v| at most
+ * (u 2^-8 or 2^-11; fp16 weights below 2^-24 of a row's largest lose more, n of them
+ * n 2^-35 max |v|).  Values are weighted before the division by the sum of up to n
+ * weights, so |v| from 2^119 / n on (bf16) can overflow.  Results do not depend on the
  * stream, on timing, or on other calls.  More than INT32_MAX - 65536 positions or
  * slots of a request or row, or NP * 64 above INT32_MAX, are IDX_ERR_OVERFLOW.
  */
@@ -507,8 +510,10 @@ int idx_dense_topk_fp4_prefill(const idx_tensor_t* q_fp4, const idx_tensor_t* q_
  *   out_lse[r, h] = log sum_j exp(s_hj).
  * A row whose window is empty gets out 0 and out_lse -infinity.  Positions
  * outside a row's window never reach its outputs, whatever their keys and values
- * hold; within it infinities and NaN propagate as in the formula.  Rows of one
- * request that follow one another read the cache together.
+ * hold, and page entries under no window may be anything; within it infinities and
+ * NaN propagate as in the formula.  Rows of one request that follow one another may
+ * read the cache together (which of them do depends on their place among the call's
+ * rows and on the page table's height; it changes the time a call takes).
  *   page_table i32 [NR, MP], row_req / row_start / row_end i32 [R] as above
  *   scale      above 0, and finite also when multiplied by log2(e)
  *   out        [R, Hq, D], q's type
