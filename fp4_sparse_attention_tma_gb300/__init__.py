@@ -34,7 +34,9 @@ __all__ = ["IdxError", "SUPPORTED_K", "idx_topk_fp4_prefill", "idx_topk_fp4_pref
            "idx_topk_last_timings", "idx_debug_bounded_wait",
            "idx_attn_paged", "idx_attn_paged_async", "idx_attn_paged_scratch_bytes",
            "idx_attn_selected", "idx_attn_selected_async", "idx_attn_selected_scratch_bytes",
-           "idx_cache_evict", "idx_cache_evict_async", "idx_cache_evict_scratch_bytes"]
+           "idx_cache_evict", "idx_cache_evict_async", "idx_cache_evict_scratch_bytes",
+           "idx_cache_append", "idx_cache_append_async", "idx_cache_append_fp4",
+           "idx_cache_append_fp4_async", "idx_cache_gather_fp4", "idx_cache_gather_fp4_async"]
 
 STATUS = {0: "OK", 1: "INVALID_ARGUMENT", 2: "UNSUPPORTED", 3: "INVALID_METADATA",
           4: "INVALID_PAGE", 5: "OVERFLOW", 6: "CUDA_ERROR", 7: "INTERNAL", 8: "TIMEOUT",
@@ -451,6 +453,80 @@ def idx_cache_evict_scratch_bytes(num_req: int, max_pages: int, dst_pages: int, 
                                                      ctypes.byref(v))
     _check(code, "idx_cache_evict_scratch_bytes", True)
     return int(v.value)
+
+
+def _append(fn, fp4, k, v, page_table, row_req, row_pos, places, tail, q, out_q, out_q_scale,
+            q_weight, k_weight, eps, rope, rope_first, rope_pairs, raise_on_error):
+    outs = (out_q, out_q_scale) if fp4 else (out_q,)
+    keep, ds = _descs((q, k, v, page_table, row_req, row_pos, q_weight, k_weight, rope, *outs,
+                       *places))
+    code = getattr(_lib.load(), fn)(*ds[:8], float(eps), ds[8], int(rope_first),
+                                    1 if rope_pairs else 0, *ds[9:], *tail)
+    return _check(code, fn, raise_on_error)
+
+
+def idx_cache_append(k, v, page_table, row_req, row_pos, k_cache, v_cache, q=None, out_q=None,
+                     q_weight=None, k_weight=None, eps=0.0, rope=None, rope_first=0,
+                     rope_pairs=False, stream=None, raise_on_error=True) -> int:
+    """Puts each row's key and value [R, Hk, D] at position row_pos (-1: no row) of its
+    request in the paged cache.  On the way keys are normed head by head (k_weight, eps) and
+    rotated by the position's angles, rope f32 [P, 2, rot / 2] (cosines, sines); queries q
+    likewise, to out_q (which may be q).  v and v_cache may be None."""
+    return _append("idx_cache_append", False, k, v, page_table, row_req, row_pos,
+                   (k_cache, v_cache), (_stream(stream),), q, out_q, None, q_weight, k_weight,
+                   eps, rope, rope_first, rope_pairs, raise_on_error)
+
+
+def idx_cache_append_async(k, v, page_table, row_req, row_pos, k_cache, v_cache, status, q=None,
+                           out_q=None, q_weight=None, k_weight=None, eps=0.0, rope=None,
+                           rope_first=0, rope_pairs=False, stream=None,
+                           raise_on_error=True) -> int:
+    """idx_cache_append without host synchronisation or allocation (graph-capturable):
+    `status` an int32 device tensor of one element."""
+    return _append("idx_cache_append_async", False, k, v, page_table, row_req, row_pos,
+                   (k_cache, v_cache), (status.data_ptr(), _stream(stream)), q, out_q, None,
+                   q_weight, k_weight, eps, rope, rope_first, rope_pairs, raise_on_error)
+
+
+def idx_cache_append_fp4(k, v, page_table, row_req, row_pos, k_codes, k_scale, v_codes, v_scale,
+                         q=None, out_q=None, out_q_scale=None, q_weight=None, k_weight=None,
+                         eps=0.0, rope=None, rope_first=0, rope_pairs=False, stream=None,
+                         raise_on_error=True) -> int:
+    """idx_cache_append into a 4-bit cache: E2M1 codes u8 [NP, 64, Hk, D / 2] with UE8M0
+    scales u8 [NP, 64, Hk, D / 32], the format of the indexer's keys.  out_q in q's type, or
+    codes u8 [R, Hq, D / 2] with out_q_scale u8 [R, Hq, D / 32], as the indexer takes them."""
+    return _append("idx_cache_append_fp4", True, k, v, page_table, row_req, row_pos,
+                   (k_codes, k_scale, v_codes, v_scale), (_stream(stream),), q, out_q,
+                   out_q_scale, q_weight, k_weight, eps, rope, rope_first, rope_pairs,
+                   raise_on_error)
+
+
+def idx_cache_append_fp4_async(k, v, page_table, row_req, row_pos, k_codes, k_scale, v_codes,
+                               v_scale, status, q=None, out_q=None, out_q_scale=None,
+                               q_weight=None, k_weight=None, eps=0.0, rope=None, rope_first=0,
+                               rope_pairs=False, stream=None, raise_on_error=True) -> int:
+    """idx_cache_append_fp4 without host synchronisation or allocation (graph-capturable)."""
+    return _append("idx_cache_append_fp4_async", True, k, v, page_table, row_req, row_pos,
+                   (k_codes, k_scale, v_codes, v_scale), (status.data_ptr(), _stream(stream)), q,
+                   out_q, out_q_scale, q_weight, k_weight, eps, rope, rope_first, rope_pairs,
+                   raise_on_error)
+
+
+def idx_cache_gather_fp4(k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v, stream=None,
+                         raise_on_error=True) -> int:
+    """Listed physical slots [N] (-1: zeros) of a 4-bit cache as 16-bit rows [N, Hk, D];
+    v_codes, v_scale and out_v may be None."""
+    keep, ds = _descs((k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v))
+    code = _lib.load().idx_cache_gather_fp4(*ds, _stream(stream))
+    return _check(code, "idx_cache_gather_fp4", raise_on_error)
+
+
+def idx_cache_gather_fp4_async(k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v, status,
+                               stream=None, raise_on_error=True) -> int:
+    """idx_cache_gather_fp4 without host synchronisation or allocation (graph-capturable)."""
+    keep, ds = _descs((k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v))
+    code = _lib.load().idx_cache_gather_fp4_async(*ds, status.data_ptr(), _stream(stream))
+    return _check(code, "idx_cache_gather_fp4_async", raise_on_error)
 
 
 def dense_score_bytes(rows: int, context: int) -> int:

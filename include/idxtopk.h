@@ -625,6 +625,110 @@ int idx_cache_evict_async(const idx_tensor_t* k_cache, const idx_tensor_t* v_cac
 int idx_cache_evict_scratch_bytes(int32_t num_req, int32_t max_pages, int32_t dst_pages,
                                   int32_t budget, int32_t device, uint64_t* bytes);
 
+/*
+ * Writing a paged cache (no counterpart on the pages).  For every row r with a position
+ * pos = row_pos[r] >= 0 of request row_req[r]:
+ *   y = (x / sqrt(mean x^2 + eps)) * weight   head by head, of q with q_weight and of k with
+ *       k_weight (NULL: x as it is);
+ *   (a, b) -> (a cos - b sin, b cos + a sin)  for each pair of the rotated dimensions
+ *       rope_first .. rope_first + rot - 1 of y, angle i of position pos: neighbours
+ *       (rope_pairs 1: dimensions rope_first + 2 i and + 2 i + 1) or halves (0: + i and
+ *       + i + rot / 2); NULL: nothing is rotated;
+ *   out_q[r] = q's result; k's result and v[r] become slot pos % 64 of page
+ *       page_table[row_req[r], pos / 64].
+ * A row with position -1 is not there (padding): nothing of it is read or written.  Rows may
+ * come in any order.  All in fp32, in the order written, each product and sum rounded by
+ * itself and the sum of squares as if it were rounded once, so that the results do not depend
+ * on how the work is divided; results are rounded once to the output's type.
+ *   q [R, Hq, D] or NULL (then out_q is too), k [R, Hk, D], v [R, Hk, D] or NULL (then v_cache
+ *              is too); strides as above
+ *   q_weight, k_weight [D] or NULL, in q's type or IDX_F32 (both alike); eps >= 0, finite
+ *   rope       f32 [P, 2, rot / 2] or NULL: the cosines, then the sines of position p's
+ *              angles; rot <= D a multiple of 16, rope_first a multiple of 8 (0 without rope)
+ *   out_q      [R, Hq, D]; may be q itself
+ *   k_cache, v_cache [NP, 64, Hk, D]; they may interleave, but share no element
+ * Errors: a position below -1, at or above MP * 64 or (with rope) P, or a request out of range
+ * IDX_ERR_INVALID_METADATA; a page outside [0, NP), or a slot named by two rows
+ * IDX_ERR_INVALID_PAGE.  After an error that the device finds the caches, and queries in place,
+ * are as they were, and out_q is NaN.
+ */
+int idx_cache_append(const idx_tensor_t* q, const idx_tensor_t* k, const idx_tensor_t* v,
+                     const idx_tensor_t* page_table, const idx_tensor_t* row_req,
+                     const idx_tensor_t* row_pos, const idx_tensor_t* q_weight,
+                     const idx_tensor_t* k_weight, float eps, const idx_tensor_t* rope,
+                     int32_t rope_first, int32_t rope_pairs, const idx_tensor_t* out_q,
+                     const idx_tensor_t* k_cache, const idx_tensor_t* v_cache,
+                     idx_stream_t stream);
+
+/* Stream-ordered idx_cache_append (no counterpart on the pages); it needs no workspace. */
+int idx_cache_append_async(const idx_tensor_t* q, const idx_tensor_t* k, const idx_tensor_t* v,
+                           const idx_tensor_t* page_table, const idx_tensor_t* row_req,
+                           const idx_tensor_t* row_pos, const idx_tensor_t* q_weight,
+                           const idx_tensor_t* k_weight, float eps, const idx_tensor_t* rope,
+                           int32_t rope_first, int32_t rope_pairs, const idx_tensor_t* out_q,
+                           const idx_tensor_t* k_cache, const idx_tensor_t* v_cache,
+                           uint32_t* status, idx_stream_t stream);
+
+/*
+ * A cache in 4 bits (no counterpart on the pages; the format is the indexer's): E2M1 codes
+ * u8 [NP, 64, Hk, D / 2], the even element in the low half of a byte, with one UE8M0 scale e
+ * for 32 elements, u8 [NP, 64, Hk, D / 32], which stand for code * 2^(e - 127).  Codes may have
+ * any strides whose last dimension is contiguous and whose others are multiples of 16 bytes,
+ * scales of D / 32 bytes.  With Hk 1 and D 128 keys in it are the indexer's k_cache_fp4 and
+ * k_scale.
+ *
+ * idx_cache_append_fp4 is idx_cache_append into such a cache: of the normed and rotated key in
+ * fp32, and of the value, e is the smallest of 0 .. 254 such that no element of the block
+ * exceeds 6 * 2^(e - 127), and an element becomes the nearest code, ties to the even one.  A
+ * block with a NaN or an infinity gets e = 255, and codes 0.
+ *   out_q, out_q_scale  out_q [R, Hq, D] in q's type with out_q_scale NULL, or in 4 bits: codes
+ *                       u8 [R, Hq, D / 2] with scales u8 [R, Hq, D / 32] (after a device error
+ *                       codes 0 and scales 255)
+ * No element of the four (or two) cache tensors is shared; codes and scales may interleave page
+ * by page.
+ */
+int idx_cache_append_fp4(const idx_tensor_t* q, const idx_tensor_t* k, const idx_tensor_t* v,
+                         const idx_tensor_t* page_table, const idx_tensor_t* row_req,
+                         const idx_tensor_t* row_pos, const idx_tensor_t* q_weight,
+                         const idx_tensor_t* k_weight, float eps, const idx_tensor_t* rope,
+                         int32_t rope_first, int32_t rope_pairs, const idx_tensor_t* out_q,
+                         const idx_tensor_t* out_q_scale, const idx_tensor_t* k_codes,
+                         const idx_tensor_t* k_scale, const idx_tensor_t* v_codes,
+                         const idx_tensor_t* v_scale, idx_stream_t stream);
+
+/* Stream-ordered idx_cache_append_fp4 (no counterpart on the pages); it needs no workspace. */
+int idx_cache_append_fp4_async(const idx_tensor_t* q, const idx_tensor_t* k,
+                               const idx_tensor_t* v, const idx_tensor_t* page_table,
+                               const idx_tensor_t* row_req, const idx_tensor_t* row_pos,
+                               const idx_tensor_t* q_weight, const idx_tensor_t* k_weight,
+                               float eps, const idx_tensor_t* rope, int32_t rope_first,
+                               int32_t rope_pairs, const idx_tensor_t* out_q,
+                               const idx_tensor_t* out_q_scale, const idx_tensor_t* k_codes,
+                               const idx_tensor_t* k_scale, const idx_tensor_t* v_codes,
+                               const idx_tensor_t* v_scale, uint32_t* status,
+                               idx_stream_t stream);
+
+/*
+ * Listed slots of a 4-bit cache as 16-bit rows (no counterpart on the pages): what the codes
+ * stand for, rounded once to the outputs' type.
+ *   slots  i32 [N]: physical slots (page * 64 + offset) in any order, also several times; -1
+ *          gives zeros
+ *   out_k, out_v  [N, Hk, D], IDX_BF16 or IDX_F16, strides as above; v_codes, v_scale and out_v
+ *          may be NULL together
+ * A slot below -1 or at or above NP * 64 is IDX_ERR_INVALID_PAGE; its row becomes NaN, the
+ * others are as they should be.  A scale of 255 gives NaN.
+ */
+int idx_cache_gather_fp4(const idx_tensor_t* k_codes, const idx_tensor_t* k_scale,
+                         const idx_tensor_t* v_codes, const idx_tensor_t* v_scale,
+                         const idx_tensor_t* slots, const idx_tensor_t* out_k,
+                         const idx_tensor_t* out_v, idx_stream_t stream);
+
+/* Stream-ordered idx_cache_gather_fp4 (no counterpart on the pages); it needs no workspace. */
+int idx_cache_gather_fp4_async(const idx_tensor_t* k_codes, const idx_tensor_t* k_scale,
+                               const idx_tensor_t* v_codes, const idx_tensor_t* v_scale,
+                               const idx_tensor_t* slots, const idx_tensor_t* out_k,
+                               const idx_tensor_t* out_v, uint32_t* status, idx_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
