@@ -36,7 +36,10 @@ __all__ = ["IdxError", "SUPPORTED_K", "idx_topk_fp4_prefill", "idx_topk_fp4_pref
            "idx_attn_selected", "idx_attn_selected_async", "idx_attn_selected_scratch_bytes",
            "idx_cache_evict", "idx_cache_evict_async", "idx_cache_evict_scratch_bytes",
            "idx_cache_append", "idx_cache_append_async", "idx_cache_append_fp4",
-           "idx_cache_append_fp4_async", "idx_cache_gather_fp4", "idx_cache_gather_fp4_async"]
+           "idx_cache_append_fp4_async", "idx_cache_gather_fp4", "idx_cache_gather_fp4_async",
+           "idx_attn_paged_fp4", "idx_attn_paged_fp4_async", "idx_attn_paged_fp4_scratch_bytes",
+           "idx_attn_selected_fp4", "idx_attn_selected_fp4_async",
+           "idx_attn_selected_fp4_scratch_bytes"]
 
 STATUS = {0: "OK", 1: "INVALID_ARGUMENT", 2: "UNSUPPORTED", 3: "INVALID_METADATA",
           4: "INVALID_PAGE", 5: "OVERFLOW", 6: "CUDA_ERROR", 7: "INTERNAL", 8: "TIMEOUT",
@@ -527,6 +530,68 @@ def idx_cache_gather_fp4_async(k_codes, k_scale, v_codes, v_scale, slots, out_k,
     keep, ds = _descs((k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v))
     code = _lib.load().idx_cache_gather_fp4_async(*ds, status.data_ptr(), _stream(stream))
     return _check(code, "idx_cache_gather_fp4_async", raise_on_error)
+
+
+def idx_attn_paged_fp4(q, k_codes, k_scale, v_codes, v_scale, page_table, row_req, row_start,
+                       row_end, scale, out, out_lse=None, stream=None, raise_on_error=True) -> int:
+    """idx_attn_paged over a cache in 4 bits: codes u8 [NP, 64, Hk, D / 2] with scales u8
+    [NP, 64, Hk, D / 32], as idx_cache_append_fp4 writes them."""
+    keep, ds = _descs((q, k_codes, k_scale, v_codes, v_scale, page_table, row_req, row_start,
+                       row_end, out, out_lse))
+    code = _lib.load().idx_attn_paged_fp4(*ds[:9], float(scale), *ds[9:], _stream(stream))
+    return _check(code, "idx_attn_paged_fp4", raise_on_error)
+
+
+def idx_attn_paged_fp4_async(q, k_codes, k_scale, v_codes, v_scale, page_table, row_req,
+                             row_start, row_end, scale, out, workspace, status, out_lse=None,
+                             stream=None, raise_on_error=True) -> int:
+    """idx_attn_paged_fp4 without host synchronisation or allocation (graph-capturable);
+    `workspace` of idx_attn_paged_fp4_scratch_bytes bytes."""
+    keep, ds = _descs((q, k_codes, k_scale, v_codes, v_scale, page_table, row_req, row_start,
+                       row_end, out, out_lse))
+    code = _lib.load().idx_attn_paged_fp4_async(*ds[:9], float(scale), *ds[9:],
+                                                *_space(workspace, status), _stream(stream))
+    return _check(code, "idx_attn_paged_fp4_async", raise_on_error)
+
+
+def idx_attn_paged_fp4_scratch_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: int,
+                                     num_req: int, max_pages: int, device: int = 0) -> int:
+    v = ctypes.c_uint64(0)
+    code = _lib.load().idx_attn_paged_fp4_scratch_bytes(
+        int(rows), int(q_heads), int(kv_heads), int(head_dim), int(num_req), int(max_pages),
+        int(device), ctypes.byref(v))
+    _check(code, "idx_attn_paged_fp4_scratch_bytes", True)
+    return int(v.value)
+
+
+def idx_attn_selected_fp4(q, k_codes, k_scale, v_codes, v_scale, slots, scale, out, out_lse=None,
+                          stream=None, raise_on_error=True) -> int:
+    """idx_attn_selected over a cache in 4 bits."""
+    keep, ds = _descs((q, k_codes, k_scale, v_codes, v_scale, slots, out, out_lse))
+    code = _lib.load().idx_attn_selected_fp4(*ds[:6], float(scale), ds[6], ds[7],
+                                             _stream(stream))
+    return _check(code, "idx_attn_selected_fp4", raise_on_error)
+
+
+def idx_attn_selected_fp4_async(q, k_codes, k_scale, v_codes, v_scale, slots, scale, out,
+                                workspace, status, out_lse=None, stream=None,
+                                raise_on_error=True) -> int:
+    """idx_attn_selected_fp4 without host synchronisation or allocation (graph-capturable);
+    `workspace` of idx_attn_selected_fp4_scratch_bytes bytes."""
+    keep, ds = _descs((q, k_codes, k_scale, v_codes, v_scale, slots, out, out_lse))
+    code = _lib.load().idx_attn_selected_fp4_async(*ds[:6], float(scale), ds[6], ds[7],
+                                                   *_space(workspace, status), _stream(stream))
+    return _check(code, "idx_attn_selected_fp4_async", raise_on_error)
+
+
+def idx_attn_selected_fp4_scratch_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: int,
+                                        selected: int, device: int = 0) -> int:
+    v = ctypes.c_uint64(0)
+    code = _lib.load().idx_attn_selected_fp4_scratch_bytes(
+        int(rows), int(q_heads), int(kv_heads), int(head_dim), int(selected), int(device),
+        ctypes.byref(v))
+    _check(code, "idx_attn_selected_fp4_scratch_bytes", True)
+    return int(v.value)
 
 
 def dense_score_bytes(rows: int, context: int) -> int:

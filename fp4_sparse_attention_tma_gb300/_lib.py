@@ -27,7 +27,8 @@ LIB_PATH = os.path.join(_HERE, "libidxtopk.so")
 DEBUG_BUILD_DIR = os.path.join(_HERE, "_build_dbg")
 DEBUG_LIB_PATH = os.path.join(_HERE, "libidxtopk_dbg.so")
 SOURCES = ["host.cu", "plan.cu", "score.cu", "finish.cu", "attn_host.cu", "attn_paged.cu",
-           "attn_slots.cu", "attn_tc.cu", "attn_join.cu", "evict.cu", "cache_host.cu", "append.cu"]
+           "attn_slots.cu", "attn_tc.cu", "attn_join.cu", "evict.cu", "cache_host.cu", "append.cu",
+           "attn_fp4_paged.cu", "attn_fp4_slots.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "-I" + INCLUDE, "-I" + CSRC] + ARCH
@@ -153,6 +154,20 @@ EXPORTS = {
                                                  ctypes.c_void_p, ctypes.c_void_p]),
     "idx_cache_evict_scratch_bytes": (ctypes.c_int, [ctypes.c_int32] * 5 +
                                       [ctypes.POINTER(ctypes.c_uint64)]),
+    "idx_attn_paged_fp4": (ctypes.c_int, [_DESC_PTR] * 9 + [ctypes.c_float] + [_DESC_PTR] * 2 +
+                           [ctypes.c_void_p]),
+    "idx_attn_paged_fp4_async": (ctypes.c_int, [_DESC_PTR] * 9 + [ctypes.c_float] +
+                                 [_DESC_PTR] * 2 + [ctypes.c_void_p, ctypes.c_uint64,
+                                                    ctypes.c_void_p, ctypes.c_void_p]),
+    "idx_attn_paged_fp4_scratch_bytes": (ctypes.c_int, [ctypes.c_int32] * 7 +
+                                         [ctypes.POINTER(ctypes.c_uint64)]),
+    "idx_attn_selected_fp4": (ctypes.c_int, [_DESC_PTR] * 6 + [ctypes.c_float] + [_DESC_PTR] * 2 +
+                              [ctypes.c_void_p]),
+    "idx_attn_selected_fp4_async": (ctypes.c_int, [_DESC_PTR] * 6 + [ctypes.c_float] +
+                                    [_DESC_PTR] * 2 + [ctypes.c_void_p, ctypes.c_uint64,
+                                                       ctypes.c_void_p, ctypes.c_void_p]),
+    "idx_attn_selected_fp4_scratch_bytes": (ctypes.c_int, [ctypes.c_int32] * 6 +
+                                            [ctypes.POINTER(ctypes.c_uint64)]),
     "idx_cache_append": (ctypes.c_int, [_DESC_PTR] * 8 + [ctypes.c_float, _DESC_PTR] +
                          [ctypes.c_int32] * 2 + [_DESC_PTR] * 3 + [ctypes.c_void_p]),
     "idx_cache_append_async": (ctypes.c_int, [_DESC_PTR] * 8 + [ctypes.c_float, _DESC_PTR] +

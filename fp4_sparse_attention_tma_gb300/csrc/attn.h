@@ -38,6 +38,10 @@ struct AttnParams {
   int64_t k_page, k_slot, k_head;
   int64_t v_page, v_slot, v_head;
   int64_t out_row, out_head;
+  // a cache in 4 bits: k and v are its codes (strides in bytes), with these scales; else null
+  const uint8_t *k_scale, *v_scale;
+  int64_t ks_page, ks_slot, ks_head;
+  int64_t vs_page, vs_slot, vs_head;
   const int32_t *page_table, *row_req, *row_start, *row_end;
   const int32_t* slots;             // [rows, n_slots]: attention over slot lists, else null
   int32_t n_slots;
@@ -93,6 +97,9 @@ inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int6
 // Warps of a CTA of the kernel of attn.cuh (with its ring stages, what fits the shared
 // memory of an SM).
 inline int attn_warps(int32_t dim, int32_t tile) { return dim == 256 ? 4 : dim == 128 ? 8 : tile == 32 ? 12 : 16; }
+
+// The same of the kernel of attn_fp4.cuh.
+inline int attn_fp4_warps(int32_t dim, int32_t tile) { return dim == 256 ? 6 : tile == 32 ? 8 : 12; }
 
 #ifdef __CUDACC__
 // What exponents are counted from, where a row's maximum is `top`: the maximum, or 0 where it is

@@ -112,7 +112,8 @@ __device__ __forceinline__ bool apart(int32_t a0, int32_t b0, int32_t a, int32_t
 // What a unit of the group that starts at row r counts; 0 where none does, or it sees nothing.  (A call of
 // its own: within the kernel it costs the loops there registers, 51.5 us for 50.8 at 48 requests x 3 rows x
 // 16 heads of dimension 64.)
-inline __device__ __noinline__ int32_t joint_count(Rows rows, int32_t n_rows, int32_t group_rows, int32_t r) {
+template <int SUB>
+__device__ __noinline__ int32_t joint_count(Rows rows, int32_t n_rows, int32_t group_rows, int32_t r) {
   if (r >= n_rows) return 0;
   const int32_t req = rows.req[r], stop = min(n_rows, (r / group_rows + 1) * group_rows);
   int32_t a0 = rows.start[r], b0 = rows.end[r];
@@ -124,11 +125,11 @@ inline __device__ __noinline__ int32_t joint_count(Rows rows, int32_t n_rows, in
     if (b1 > a1) a = min(a, a1), b = max(b, b1);
     a0 = a1, b0 = b1;
   }
-  return b > a ? (b + kSub - 1) / kSub - a / kSub + kUnitCost : 0;
+  return b > a ? (b + SUB - 1) / SUB - a / SUB + kUnitCost : 0;
 }
 
-// A place in the list of units: subtile `s` of one unit of the group at row0.
-template <bool SLOTS>
+// A place in the list of units: subtile `s` (of SUB positions) of one unit of the group at row0.
+template <bool SLOTS, int SUB = kSub>
 struct Cursor {
   int32_t row0, nrows, req;   // the group
   int32_t lo, hi;             // positions of its rows' windows, together
@@ -159,15 +160,15 @@ struct Cursor {
       lo = __reduce_min_sync(~0u, a);
       hi = __reduce_max_sync(~0u, b);
       if (lo > hi) lo = hi;
-      base = lo / kSub;
+      base = lo / SUB;
     }
-    nsub = hi > lo ? (hi + kSub - 1) / kSub - base : 0;
+    nsub = hi > lo ? (hi + SUB - 1) / SUB - base : 0;
   }
   __device__ static int32_t count(const AttnParams& p, const Rows& rows, int32_t r) {
-    return joint_count(rows, p.rows, p.group_rows, r);
+    return joint_count<SUB>(rows, p.rows, p.group_rows, r);
   }
   // The same for a row of a call over slots.
-  __device__ static int32_t row_count(const AttnParams& p) { return (p.n_slots + kSub - 1) / kSub + kUnitCost; }
+  __device__ static int32_t row_count(const AttnParams& p) { return (p.n_slots + SUB - 1) / SUB + kUnitCost; }
   // Place t of the group's units, one after another; returns how far it is behind the unit's first subtile.
   __device__ int32_t place(const AttnParams& p, int64_t t) {
     const int32_t n = nsub + kUnitCost, u = (int32_t)(t / n), off = (int32_t)(t - (int64_t)u * n) - kUnitCost;

@@ -61,11 +61,11 @@ bool tensor_core_for(int64_t group, int64_t rows, int64_t per_req, int64_t kv_he
 // value read; 32 requests x 4 rows x 64 heads on 8: 757 us, 1295 with 16), up to head dimension
 // 128 (beyond it two tiles' sums do not fit a thread's registers).
 AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t positions,
-                 bool slots, bool far, int sm) {
+                 bool slots, bool far, bool fp4, int sm) {
   AttnPlan a{};
   a.group = (int32_t)(q_heads / kv_heads);
   const int64_t per_req = rows > num_req && num_req > 0 ? (rows + num_req - 1) / num_req : 1;
-  a.tensor_core = tensor_core_for(a.group, rows, per_req, kv_heads, dim, positions, slots, far, sm);
+  a.tensor_core = !fp4 && tensor_core_for(a.group, rows, per_req, kv_heads, dim, positions, slots, far, sm);
   const int32_t most = a.tensor_core ? 64 : dim <= 128 && (int64_t)a.group * per_req > 16 ? 32 : 16;
   a.chunks = (a.group + most - 1) / most;
   a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
@@ -78,23 +78,25 @@ AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_head
     a.group_rows = a.chunks > 1 ? 1 : most / a.group;
     a.row_cols = a.chunk_heads;
     a.tile = most;
-    a.workers = sm * attn_warps((int32_t)dim, most);
+    a.workers = sm * (fp4 ? attn_fp4_warps((int32_t)dim, most) : attn_warps((int32_t)dim, most));
   }
   return a;
 }
 
-int check_heads(const idx_tensor_t* q, const idx_tensor_t* k, const idx_tensor_t* v, const idx_tensor_t* out) {
+// `fp4`: k and v are codes, [NP, 64, Hk, D / 2].
+int check_heads(const idx_tensor_t* q, const idx_tensor_t* k, const idx_tensor_t* v, const idx_tensor_t* out, bool fp4) {
   if (!q || (q->dtype != IDX_BF16 && q->dtype != IDX_F16)) return IDX_ERR_INVALID_ARGUMENT;
   int st;
-  if ((st = check_strided(q, q->dtype, 3)) || (st = check_strided(k, q->dtype, 4)) ||
-      (st = check_strided(v, q->dtype, 4)) || (st = check_strided(out, q->dtype, 3)))
+  const int cached = fp4 ? IDX_U8 : q->dtype;
+  if ((st = check_strided(q, q->dtype, 3)) || (st = check_strided(k, cached, 4, fp4 ? 16 : 8)) ||
+      (st = check_strided(v, cached, 4, fp4 ? 16 : 8)) || (st = check_strided(out, q->dtype, 3)))
     return st;
   const int64_t D = q->shape[2], Hq = q->shape[1], Hk = k->shape[2];
   for (int i = 0; i < 4; ++i)
     if (k->shape[i] != v->shape[i]) return IDX_ERR_INVALID_ARGUMENT;
   for (int i = 0; i < 3; ++i)
     if (q->shape[i] != out->shape[i]) return IDX_ERR_INVALID_ARGUMENT;
-  if (k->shape[3] != D || Hk < 1 || Hq < 1 || Hq % Hk != 0) return IDX_ERR_INVALID_ARGUMENT;
+  if (k->shape[3] != (fp4 ? D / 2 : D) || Hk < 1 || Hq < 1 || Hq % Hk != 0) return IDX_ERR_INVALID_ARGUMENT;
   if ((D != 64 && D != 128 && D != 256) || k->shape[1] != kPage) return IDX_ERR_UNSUPPORTED;
   if (!no_overlap(out)) return IDX_ERR_INVALID_ARGUMENT;
   if (q->shape[0] > INT32_MAX || Hq > 65536 || k->shape[0] * (int64_t)kPage > INT32_MAX) return IDX_ERR_OVERFLOW;
@@ -105,7 +107,18 @@ struct AttnCall {
   const idx_tensor_t *q, *k, *v, *page_table, *row_req, *row_start, *row_end, *slots;
   float scale;
   const idx_tensor_t *out, *lse, *weight_in, *weight_out;
+  const idx_tensor_t *k_scale, *v_scale;   // a cache in 4 bits
+  bool fp4;
 };
+
+// The scales of a 4-bit cache's codes.
+int check_scales(const idx_tensor_t* codes, const idx_tensor_t* scale, int64_t D) {
+  const int st = check_strided(scale, IDX_U8, 4, D / 32);
+  if (st) return st;
+  for (int i = 0; i < 3; ++i)
+    if (scale->shape[i] != codes->shape[i]) return IDX_ERR_INVALID_ARGUMENT;
+  return scale->shape[3] == D / 32 ? IDX_OK : IDX_ERR_INVALID_ARGUMENT;
+}
 
 AttnLayout layout_of(const AttnPlan& a, int sm, int64_t rows, int64_t q_heads, int64_t dim, int64_t max_pages,
                      bool weights) {
@@ -115,7 +128,9 @@ AttnLayout layout_of(const AttnPlan& a, int sm, int64_t rows, int64_t q_heads, i
 int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   int st;
   if ((st = check_space(space))) return st;
-  if ((st = check_heads(c.q, c.k, c.v, c.out))) return st;
+  if ((st = check_heads(c.q, c.k, c.v, c.out, c.fp4))) return st;
+  if (c.fp4 && ((st = check_scales(c.k, c.k_scale, c.q->shape[2])) || (st = check_scales(c.v, c.v_scale, c.q->shape[2]))))
+    return st;
   const int64_t R = c.q->shape[0], Hq = c.q->shape[1], D = c.q->shape[2], NP = c.k->shape[0], Hk = c.k->shape[2];
   const float scale_log2 = c.scale * 1.4426950408889634f;   // what the kernels work with
   if (!(c.scale > 0.f) || !std::isfinite(scale_log2)) return IDX_ERR_INVALID_ARGUMENT;
@@ -145,21 +160,21 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   if (R > 0 && NP < 1) return IDX_ERR_INVALID_ARGUMENT;
   const bool in_place = c.weight_in && c.weight_in->data == c.weight_out->data;
   const idx_tensor_t* outs[] = {c.out, c.lse, c.weight_out};
-  const idx_tensor_t* ins[] = {c.q,       c.k,     c.v,    c.page_table, c.row_req, c.row_start,
-                               c.row_end, c.slots, in_place ? nullptr : c.weight_in};
+  const idx_tensor_t* ins[] = {c.q,       c.k,     c.v,       c.page_table, c.row_req, c.row_start,
+                               c.row_end, c.slots, c.k_scale, c.v_scale,    in_place ? nullptr : c.weight_in};
   if (!all_apart(outs, ins)) return IDX_ERR_INVALID_ARGUMENT;
-  const idx_tensor_t* all[] = {c.q,       c.k,     c.v,   c.page_table, c.row_req, c.row_start,
-                               c.row_end, c.slots, c.out, c.lse,        c.weight_in, c.weight_out};
+  const idx_tensor_t* all[] = {c.q,   c.k,   c.v,         c.page_table, c.row_req, c.row_start, c.row_end, c.slots,
+                               c.out, c.lse, c.weight_in, c.weight_out, c.k_scale, c.v_scale};
   Machine m;
-  if ((st = find_machine(all, 12, space.status, space.workspace, stream, &m))) return st;
+  if ((st = find_machine(all, 14, space.status, space.workspace, stream, &m))) return st;
   if (m.capturing && !space.async) return IDX_ERR_UNSUPPORTED;
   DeviceGuard guard(m.dev);
   if (!guard.ok()) return IDX_ERR_CUDA;
   if ((st = check_arch(&m))) return st;
   const bool weights = c.weight_out != nullptr && numel_of(c.weight_out) > 0;
   const bool far = span_of(c.k) >= kFar || span_of(c.v) >= kFar;
-  const AttnPlan a = c.slots ? plan_of(R, R, Hq, Hk, D, c.slots->shape[1], true, far, m.sm)
-                             : plan_of(R, NR, Hq, Hk, D, MP * kPage, false, far, m.sm);
+  const AttnPlan a = c.slots ? plan_of(R, R, Hq, Hk, D, c.slots->shape[1], true, far, c.fp4, m.sm)
+                             : plan_of(R, NR, Hq, Hk, D, MP * kPage, false, far, c.fp4, m.sm);
   int64_t logit_rows, logit_bytes;
   if (weights && (!mul_ok(R * Hq, MP * kPage, &logit_rows) || !mul_ok(logit_rows, 4, &logit_bytes) ||
                   logit_bytes > (INT64_MAX >> 2)))
@@ -172,6 +187,11 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   p.out_row = step(c.out, 0), p.out_head = step(c.out, 1);
   p.k_page = step(c.k, 0), p.k_slot = step(c.k, 1), p.k_head = step(c.k, 2);
   p.v_page = step(c.v, 0), p.v_slot = step(c.v, 1), p.v_head = step(c.v, 2);
+  if (c.fp4) {
+    p.k_scale = (const uint8_t*)c.k_scale->data, p.v_scale = (const uint8_t*)c.v_scale->data;
+    p.ks_page = step(c.k_scale, 0), p.ks_slot = step(c.k_scale, 1), p.ks_head = step(c.k_scale, 2);
+    p.vs_page = step(c.v_scale, 0), p.vs_slot = step(c.v_scale, 1), p.vs_head = step(c.v_scale, 2);
+  }
   if (c.slots) {
     p.slots = (const int32_t*)c.slots->data;
     p.n_slots = (int32_t)c.slots->shape[1];
@@ -213,7 +233,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
 }
 
 int attn_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t num_req, int64_t max_pages,
-               bool slots, bool weights, int32_t device, uint64_t* bytes) {
+               bool slots, bool weights, bool fp4, int32_t device, uint64_t* bytes) {
   if (!bytes || rows < 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || max_pages < 0)
     return IDX_ERR_INVALID_ARGUMENT;
   if (dim != 64 && dim != 128 && dim != 256) return IDX_ERR_UNSUPPORTED;
@@ -226,7 +246,7 @@ int attn_bytes(int64_t rows, int64_t q_heads, int64_t kv_heads, int64_t dim, int
   *bytes = 0;
   for (bool far : {false, true})
     for (int64_t positions : {(int64_t)1, kMostPositions}) {
-      const AttnPlan a = plan_of(rows, num_req, q_heads, kv_heads, dim, positions, slots, far, sm);
+      const AttnPlan a = plan_of(rows, num_req, q_heads, kv_heads, dim, positions, slots, far, fp4, sm);
       const uint64_t n = layout_of(a, sm, rows, q_heads, dim, max_pages, weights).total;
       if (n > *bytes) *bytes = n;
     }
@@ -356,7 +376,7 @@ int idx_attn_paged_async(const idx_tensor_t* q, const idx_tensor_t* k_cache, con
 
 int idx_attn_paged_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t num_req,
                                  int32_t max_pages, int32_t with_weights, int32_t device, uint64_t* bytes) {
-  return attn_bytes(rows, q_heads, kv_heads, head_dim, num_req, max_pages, false, with_weights != 0, device, bytes);
+  return attn_bytes(rows, q_heads, kv_heads, head_dim, num_req, max_pages, false, with_weights != 0, false, device, bytes);
 }
 
 int idx_attn_selected(const idx_tensor_t* q, const idx_tensor_t* k_cache, const idx_tensor_t* v_cache,
@@ -381,7 +401,56 @@ int idx_attn_selected_async(const idx_tensor_t* q, const idx_tensor_t* k_cache, 
 int idx_attn_selected_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                     int32_t selected, int32_t device, uint64_t* bytes) {
   if (selected < 1) return IDX_ERR_INVALID_ARGUMENT;
-  return attn_bytes(rows, q_heads, kv_heads, head_dim, rows, 0, true, false, device, bytes);
+  return attn_bytes(rows, q_heads, kv_heads, head_dim, rows, 0, true, false, false, device, bytes);
+}
+
+int idx_attn_paged_fp4(const idx_tensor_t* q, const idx_tensor_t* k_codes, const idx_tensor_t* k_scale,
+                       const idx_tensor_t* v_codes, const idx_tensor_t* v_scale, const idx_tensor_t* page_table,
+                       const idx_tensor_t* row_req, const idx_tensor_t* row_start, const idx_tensor_t* row_end, float scale,
+                       const idx_tensor_t* out, const idx_tensor_t* out_lse, idx_stream_t stream) {
+  return run_attn({q, k_codes, v_codes, page_table, row_req, row_start, row_end, nullptr, scale, out, out_lse, nullptr,
+                   nullptr, k_scale, v_scale, true},
+                  kSync, (cudaStream_t)stream);
+}
+
+int idx_attn_paged_fp4_async(const idx_tensor_t* q, const idx_tensor_t* k_codes, const idx_tensor_t* k_scale,
+                             const idx_tensor_t* v_codes, const idx_tensor_t* v_scale, const idx_tensor_t* page_table,
+                             const idx_tensor_t* row_req, const idx_tensor_t* row_start, const idx_tensor_t* row_end,
+                             float scale, const idx_tensor_t* out, const idx_tensor_t* out_lse, void* workspace,
+                             uint64_t workspace_bytes, uint32_t* status, idx_stream_t stream) {
+  return run_attn({q, k_codes, v_codes, page_table, row_req, row_start, row_end, nullptr, scale, out, out_lse, nullptr,
+                   nullptr, k_scale, v_scale, true},
+                  {true, workspace, workspace_bytes, status}, (cudaStream_t)stream);
+}
+
+int idx_attn_paged_fp4_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t num_req,
+                                     int32_t max_pages, int32_t device, uint64_t* bytes) {
+  return attn_bytes(rows, q_heads, kv_heads, head_dim, num_req, max_pages, false, false, true, device, bytes);
+}
+
+int idx_attn_selected_fp4(const idx_tensor_t* q, const idx_tensor_t* k_codes, const idx_tensor_t* k_scale,
+                          const idx_tensor_t* v_codes, const idx_tensor_t* v_scale, const idx_tensor_t* slots, float scale,
+                          const idx_tensor_t* out, const idx_tensor_t* out_lse, idx_stream_t stream) {
+  if (!slots) return IDX_ERR_INVALID_ARGUMENT;
+  return run_attn({q, k_codes, v_codes, nullptr, nullptr, nullptr, nullptr, slots, scale, out, out_lse, nullptr, nullptr,
+                   k_scale, v_scale, true},
+                  kSync, (cudaStream_t)stream);
+}
+
+int idx_attn_selected_fp4_async(const idx_tensor_t* q, const idx_tensor_t* k_codes, const idx_tensor_t* k_scale,
+                                const idx_tensor_t* v_codes, const idx_tensor_t* v_scale, const idx_tensor_t* slots,
+                                float scale, const idx_tensor_t* out, const idx_tensor_t* out_lse, void* workspace,
+                                uint64_t workspace_bytes, uint32_t* status, idx_stream_t stream) {
+  if (!slots) return IDX_ERR_INVALID_ARGUMENT;
+  return run_attn({q, k_codes, v_codes, nullptr, nullptr, nullptr, nullptr, slots, scale, out, out_lse, nullptr, nullptr,
+                   k_scale, v_scale, true},
+                  {true, workspace, workspace_bytes, status}, (cudaStream_t)stream);
+}
+
+int idx_attn_selected_fp4_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                        int32_t selected, int32_t device, uint64_t* bytes) {
+  if (selected < 1) return IDX_ERR_INVALID_ARGUMENT;
+  return attn_bytes(rows, q_heads, kv_heads, head_dim, rows, 0, true, false, true, device, bytes);
 }
 
 int idx_cache_evict(const idx_tensor_t* k_cache, const idx_tensor_t* v_cache, const idx_tensor_t* page_table,

@@ -729,6 +729,64 @@ int idx_cache_gather_fp4_async(const idx_tensor_t* k_codes, const idx_tensor_t* 
                                const idx_tensor_t* slots, const idx_tensor_t* out_k,
                                const idx_tensor_t* out_v, uint32_t* status, idx_stream_t stream);
 
+/*
+ * idx_attn_paged and idx_attn_selected over a cache in 4 bits (no counterpart on the pages):
+ * k[j] and v[j] are what the codes and scales of position j stand for, tensors as for
+ * idx_cache_append_fp4 (keys and values may share elements here).  Rows, windows, slots, empty
+ * rows, outputs and errors as there, and:
+ *   a scale byte above IDX_MAX_SCALE_BYTE of a position that a row sees (NaN included) is
+ *   IDX_ERR_INVALID_VALUE.
+ * Sums, maxima and weights are held in fp32; softmax weights are rounded to fp16 for their
+ * product with the values, for queries of either type: an error of 2^-11 sum p |v| at most, n
+ * weights below 2^-24 of a row's largest lose n 2^-35 max |v|.  Of keys, blocks whose scale is
+ * below 2^-26 of the largest within 128 positions, and of values, blocks below 2^-26 of the
+ * largest that the head has in the request or list, may count as 0 (their elements are below
+ * 2^-24 of what the largest block can hold); bf16 queries' elements below 2^-38 of the head's
+ * largest lose bits.
+ */
+int idx_attn_paged_fp4(const idx_tensor_t* q, const idx_tensor_t* k_codes,
+                       const idx_tensor_t* k_scale, const idx_tensor_t* v_codes,
+                       const idx_tensor_t* v_scale, const idx_tensor_t* page_table,
+                       const idx_tensor_t* row_req, const idx_tensor_t* row_start,
+                       const idx_tensor_t* row_end, float scale, const idx_tensor_t* out,
+                       const idx_tensor_t* out_lse, idx_stream_t stream);
+
+/* Stream-ordered idx_attn_paged_fp4 (no counterpart on the pages). */
+int idx_attn_paged_fp4_async(const idx_tensor_t* q, const idx_tensor_t* k_codes,
+                             const idx_tensor_t* k_scale, const idx_tensor_t* v_codes,
+                             const idx_tensor_t* v_scale, const idx_tensor_t* page_table,
+                             const idx_tensor_t* row_req, const idx_tensor_t* row_start,
+                             const idx_tensor_t* row_end, float scale, const idx_tensor_t* out,
+                             const idx_tensor_t* out_lse, void* workspace,
+                             uint64_t workspace_bytes, uint32_t* status, idx_stream_t stream);
+
+/* Workspace of idx_attn_paged_fp4_async for these sizes on `device` (no counterpart on the
+ * pages); it does not depend on the context. */
+int idx_attn_paged_fp4_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads,
+                                     int32_t head_dim, int32_t num_req, int32_t max_pages,
+                                     int32_t device, uint64_t* bytes);
+
+/* The same over each row's list of slots (no counterpart on the pages). */
+int idx_attn_selected_fp4(const idx_tensor_t* q, const idx_tensor_t* k_codes,
+                          const idx_tensor_t* k_scale, const idx_tensor_t* v_codes,
+                          const idx_tensor_t* v_scale, const idx_tensor_t* slots, float scale,
+                          const idx_tensor_t* out, const idx_tensor_t* out_lse,
+                          idx_stream_t stream);
+
+/* Stream-ordered idx_attn_selected_fp4 (no counterpart on the pages). */
+int idx_attn_selected_fp4_async(const idx_tensor_t* q, const idx_tensor_t* k_codes,
+                                const idx_tensor_t* k_scale, const idx_tensor_t* v_codes,
+                                const idx_tensor_t* v_scale, const idx_tensor_t* slots,
+                                float scale, const idx_tensor_t* out,
+                                const idx_tensor_t* out_lse, void* workspace,
+                                uint64_t workspace_bytes, uint32_t* status, idx_stream_t stream);
+
+/* Workspace of idx_attn_selected_fp4_async for these sizes on `device` (no counterpart on the
+ * pages). */
+int idx_attn_selected_fp4_scratch_bytes(int32_t rows, int32_t q_heads, int32_t kv_heads,
+                                        int32_t head_dim, int32_t selected, int32_t device,
+                                        uint64_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -186,3 +186,47 @@ def test_gather_refusals():
     a = list(base)
     a[0] = u8(5, 64, 2, 48)
     assert gather(a) == UNSUPPORTED
+
+
+def attend(a, slots=False):
+    s = Stream()
+    fn = m.idx_attn_selected_fp4 if slots else m.idx_attn_paged_fp4
+    return fn(**a, stream=s, raise_on_error=False)
+
+
+def attend_case(slots=False, dtype=torch.bfloat16, D=128, Hq=8, Hk=2, R=3, NP=5):
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    a = dict(q=torch.zeros(R, Hq, D, dtype=dtype), k_codes=u8(NP, 64, Hk, D // 2), k_scale=u8(NP, 64, Hk, D // 32),
+             v_codes=u8(NP, 64, Hk, D // 2), v_scale=u8(NP, 64, Hk, D // 32), scale=0.1, out=torch.zeros(R, Hq, D, dtype=dtype),
+             out_lse=torch.zeros(R, Hq))
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    a.update(dict(slots=i32(R, 70)) if slots else dict(page_table=i32(2, 4), row_req=i32(R), row_start=i32(R), row_end=i32(R)))
+    return a
+
+
+@pytest.mark.parametrize("slots", [False, True])
+def test_attention_refusals(slots):
+    if not torch.cuda.is_available():
+        for kw in [{}, dict(D=64), dict(D=256), dict(dtype=torch.float16), dict(R=0)]:
+            assert attend(attend_case(slots, **kw), slots) == 6, kw
+        a = attend_case(slots)
+        a["v_codes"], a["v_scale"] = a["k_codes"], a["k_scale"]      # a latent cache: both are the same
+        assert attend(a, slots) == 6
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    bad = [dict(k_scale=None), dict(v_scale=None), dict(k_codes=None), dict(k_scale=u8(5, 64, 2, 2)), dict(v_scale=u8(4, 64, 2, 4)),
+           dict(v_codes=u8(5, 64, 1, 64)), dict(k_codes=u8(5, 64, 2, 128)), dict(k_scale=torch.zeros(5, 64, 2, 4)),
+           dict(k_codes=torch.zeros(5, 64, 2, 64, dtype=torch.bfloat16)), dict(k_codes=u8(5, 64, 2, 72)[..., :64]),
+           dict(k_scale=u8(5, 64, 2, 6)[..., :4]), dict(k_scale=u8(5, 64, 2, 4).flip(0)[1:]), dict(scale=0.0), dict(scale=float("nan")),
+           dict(scale=float("inf")), dict(scale=-1.0), dict(out=torch.zeros(3, 8, 64, dtype=torch.bfloat16)), dict(out_lse=torch.zeros(3, 2)),
+           dict(q=torch.zeros(3, 7, 128, dtype=torch.bfloat16), out=torch.zeros(3, 7, 128, dtype=torch.bfloat16))]
+    bad += [dict(slots=None)] if slots else [dict(page_table=None), dict(row_end=torch.zeros(2, dtype=torch.int32))]
+    for change in bad:
+        assert attend({**attend_case(slots), **change}, slots) == INVALID, change.keys()
+    a = attend_case(slots)
+    a["out"] = a["q"]
+    assert attend(a, slots) == INVALID
+    a = attend_case(slots)
+    a["out_lse"] = a["k_scale"].flatten()[:96].view(torch.float32).view(3, 8)
+    assert attend(a, slots) == INVALID                               # the output lies in the scales
+    a = attend_case(slots, D=96)
+    assert attend(a, slots) == UNSUPPORTED
