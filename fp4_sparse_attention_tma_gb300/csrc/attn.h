@@ -54,6 +54,9 @@ struct AttnParams {
   int32_t tensor_core;              // 1: the kernel of attn_tc.cuh
   int32_t far;                      // 1: a cache spans 64 GB or more
   int32_t workers;                  // warps of the grid
+  int32_t team;                     // (attn_fp4.cuh) warps that walk over the same range, a key-value head each; else 1
+  int32_t ranges;                   // workers / team
+  int32_t kv_units;                 // kv_heads / team
   float scale_log2;                 // softmax scale x log2(e)
   // workspace
   uint32_t* cta_status;             // [CTAs] first error that the CTA saw
@@ -100,6 +103,15 @@ inline int attn_warps(int32_t dim, int32_t tile) { return dim == 256 ? 4 : dim =
 
 // The same of the kernel of attn_fp4.cuh.
 inline int attn_fp4_warps(int32_t dim, int32_t tile) { return dim == 256 ? 6 : tile == 32 ? 8 : 12; }
+
+// Warps of a team there: key-value heads whose scales (4 bytes a position at head dimension 128) may share a sector of
+// memory are read at the same time, by warps of one CTA.  32 requests x 2 rows x 64 heads on 8, slot by slot: each
+// head by itself reads twice the cache's bytes.
+inline int attn_fp4_team(int64_t kv_heads, int warps) {
+  for (int t : {4, 3, 2})
+    if (kv_heads % t == 0 && warps % t == 0) return t;
+  return 1;
+}
 
 #ifdef __CUDACC__
 // What exponents are counted from, where a row's maximum is `top`: the maximum, or 0 where it is

@@ -76,13 +76,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Divides the units' subtiles among the workers.
+// Divides the units' subtiles among the workers (or teams of them).
 struct Split {
   int64_t total = 0;    // subtiles of all units, and what they are counted more
-  int32_t active = 0;   // workers with a range
+  int32_t active = 0;   // those with a range
   __device__ void divide(const AttnParams& p, int64_t subtiles) {
     total = subtiles;
-    active = (int32_t)(total < p.workers ? total : p.workers);
+    active = (int32_t)(total < p.ranges ? total : p.ranges);
   }
   __device__ int64_t first(int64_t w) const { return total * w / active; }
   // the worker whose range holds subtile x
@@ -134,7 +134,7 @@ struct Cursor {
   int32_t row0, nrows, req;   // the group
   int32_t lo, hi;             // positions of its rows' windows, together
   int32_t base, nsub;         // first subtile (absolute) and their number
-  int32_t kv, chunk, s;       // the unit: key-value head and chunk of its query heads
+  int32_t kv, chunk, s;       // the unit: key-value head (or team's heads) and chunk of its query heads
 
   // The group that starts at `row`.  Called by the whole warp.
   __device__ void load(const AttnParams& p, const Rows& rows, int32_t row) {
@@ -182,7 +182,7 @@ struct Cursor {
     s = 0;
     if (++chunk < p.chunks) return;
     chunk = 0;
-    if (++kv < p.kv_heads) return;
+    if (++kv < p.kv_units) return;
     kv = 0;
     do {
       load(p, rows, row0 + nrows);
@@ -198,7 +198,7 @@ struct Cursor {
 template <class Cur, bool SLOTS, int WARPS>
 __device__ bool find_range(const AttnParams& p, Rows& rows, Split& sp, Cur& cur, int64_t& end, int32_t worker, void* room,
                            uint32_t* err) {
-  const int32_t units = p.kv_heads * p.chunks;
+  const int32_t units = p.kv_units * p.chunks;
   if constexpr (SLOTS) {
     const int32_t n = Cur::row_count(p);
     sp.divide(p, (int64_t)p.rows * units * n);

@@ -116,6 +116,36 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
   asm volatile("{\n\t.reg .u16 t;\n\tcvt.u16.u32 t, %1;\n\tst.shared.u16 [%0], t;\n\t}" ::"r"(a), "r"(v) : "memory");
 }
 
+// Two fp32 operations in one instruction: x * a + b and x + y of pairs.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, m, s;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmov.b64 s, {%3, %3};\n\t"
+      "fma.rn.f32x2 v, v, m, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float a) {
+  asm("{\n\t.reg .b64 v, m;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\t"
+      "mul.rn.f32x2 v, v, m;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, s;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void mma_from_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 template <bool BF16, int D, int TILE, int WARPS, int STAGES, bool SLOTS>
 __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_constant__ AttnParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
@@ -129,33 +159,60 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
 
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ uint32_t err;
+  // What only a unit's or segment's ends need lies in shared memory: in registers it would push the loops' own
+  // values out to local memory.
+  struct Walks {
+    Place fetch, at;
+    int64_t end;                         // of the worker's range, counted from at's unit's first subtile
+    int64_t f_end;                       // the same of fetch's
+  };
+  __shared__ Walks walks[WARPS];
+  __shared__ Split split;
+  __shared__ Rows meta;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = lane & 3, col = lane >> 2;
-  const int32_t worker = warp * gridDim.x + blockIdx.x;
+  // a team's warps have the same range, each with a key-value head of its own
+  const int32_t member = warp % p.team, team = warp / p.team * gridDim.x + blockIdx.x;
+  Walks& w = walks[warp];
   allow_launch_after();
   if (threadIdx.x == 0) err = kOk;
   __syncthreads();
 
-  Split sp;
-  Place at;
-  Rows rows{};
-  int64_t end;   // of the worker's range, counted from the unit's first subtile
-  const bool work = find_range<Place, SLOTS, WARPS>(p, rows, sp, at, end, worker, ring, &err);
-  if (worker < sp.active && lane == 0) p.open_parts[worker] = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.active = sp.active;
+  bool work;
+  {
+    Split sp;
+    Place at;
+    Rows rows{};
+    int64_t end;
+    work = find_range<Place, SLOTS, WARPS>(p, rows, sp, at, end, team, ring, &err);
+    // the parts of a head's units lie one after another
+    if (team < sp.active && lane == 0) p.open_parts[member * sp.active + team] = 0;
+    if (threadIdx.x == 0) {
+      if (blockIdx.x == 0) *p.active = sp.active * p.team;
+      split = sp;
+      meta = rows;
+    }
+    if (lane == 0) w.fetch = w.at = at, w.end = w.f_end = end;
+  }
+  __syncthreads();
   uint32_t warp_err = kOk;
   if (work) {
+    const int32_t worker = member * split.active + team;
     const uint32_t my_ring = smem_addr(ring) + (uint32_t)warp * (STAGES * S::kStage);
 
     // ---- fetching side: runs STAGES - 1 subtiles ahead, over the ends of segments ----
     constexpr int ROWS = 32 / CH;                     // positions that one copy of the warp covers
     constexpr int COPIES = kSub4 / ROWS;
     const int piece = lane % CH, row_in = lane / CH;
-    Place f = at;
-    int64_t f_end = end;                              // as `end`; 0 when everything has been fetched
-    bool f_first = true;                              // the next subtile fetched is a segment's first
-    const uint8_t *f_k, *f_v, *f_ks, *f_vs;           // the head's codes, at this lane's piece, and scales
+    const uint32_t kp16 = (uint32_t)(p.k_page / 16), ks16 = (uint32_t)(p.k_slot / 16), vp16 = (uint32_t)(p.v_page / 16),
+                   vs16 = (uint32_t)(p.v_slot / 16);
+    int32_t f_left;                                   // subtiles of the segment that are still to be fetched; 0: all done
+    int32_t f_sub;                                    // the next subtile, counted from position 0
+    int32_t f_lo, f_hi;                               // what the group's rows see of it
+    uint32_t f_k16, f_v16;                            // the head and this lane's piece of it, in units of 16 bytes
+    uint32_t f_ks, f_vs;                              // the head's scales, in bytes
     const int32_t* f_list;                            // the request's pages, or the row's slots
+    bool f_first;                                     // the next subtile fetched is a segment's first
     int32_t entry;                                    // page of the next subtile, or slot of its position `lane`
     uint32_t shown[STAGES];                           // (slots) which positions of the stages are one
     // the scales of this lane's position of the subtile fetched last: on their way from memory
@@ -164,43 +221,66 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
     uint32_t ref = kLowest;                           // largest scale of values so far of the segment
     auto look_up = [&]() {
       if constexpr (SLOTS) {
-        const int32_t j = f.s * kSub4 + lane;
+        const int32_t j = f_sub * kSub4 + lane;
         entry = j < p.n_slots ? f_list[j] : -1;
       } else {
-        entry = f_list[(f.base + f.s) / (kPage / kSub4)];
+        entry = f_list[f_sub / (kPage / kSub4)];
       }
     };
     auto begin_fetch = [&]() {
-      f_k = (const uint8_t*)p.k + f.kv * p.k_head + piece * 16;
-      f_v = (const uint8_t*)p.v + f.kv * p.v_head + piece * 16;
-      f_ks = p.k_scale + f.kv * p.ks_head;
-      f_vs = p.v_scale + f.kv * p.vs_head;
+      const Place& f = w.fetch;
+      f_left = (int32_t)min((int64_t)f.nsub, w.f_end) - f.s;
+      f_sub = f.base + f.s;
+      f_lo = f.lo, f_hi = f.hi;
+      f_first = true;
+      const int32_t kv = f.kv * p.team + member;
+      f_k16 = (uint32_t)(kv * (p.k_head / 16)) + piece;
+      f_v16 = (uint32_t)(kv * (p.v_head / 16)) + piece;
+      f_ks = (uint32_t)(kv * p.ks_head), f_vs = (uint32_t)(kv * p.vs_head);
       f_list = SLOTS ? p.slots + (int64_t)f.row0 * p.n_slots : p.page_table + (int64_t)f.req * p.max_pages;
       look_up();
     };
     begin_fetch();
     // factors of the subtile fetched last, into its stage
+    const uint32_t kf_to = S::kKf + (uint32_t)((2 * quad + (col & 1)) * 16 * S::H + (lane >> 3)) * 4;
+    const uint32_t vf_to = S::kVf + (uint32_t)(quad * 4 + (lane >> 3)) * 4 + (col & 1) * 2;
     auto put_scales = [&](int stage) {
       if (!pend) return;
       const uint32_t to = my_ring + (uint32_t)stage * S::kStage;
       const uint32_t ek = max(__reduce_max_sync(~0u, sk.largest()), kLowest), ev = __reduce_max_sync(~0u, sv.largest());
       if (max(ek, ev) > kMaxScaleByte) warp_err = kErrInvalidValue;
       ref = max(pend_first ? kLowest : ref, ev);
-      const int t = lane >> 3, c = lane & 3, x = (lane >> 2) & 1;
 #pragma unroll
       for (int i = 0; i < 4 * S::H; ++i)              // quarter i / H, its block i % H
-        sts32(to + S::kKf + (uint32_t)((((2 * c + x) * 4 + i / S::H) * S::H + i % S::H) * 4 + t) * 4,
-              factor2(sk.get(D == 64 ? i / 2 : i), ek));
+        sts32(to + kf_to + (uint32_t)i * 16, factor2(sk.get(D == 64 ? i / 2 : i), ek));
 #pragma unroll
-      for (int b = 0; b < S::NB; ++b)
-        sts16(to + S::kVf + (uint32_t)((b * 4 + c) * 4 + t) * 4 + x * 2, factor2(sv.get(b), ref));
+      for (int b = 0; b < S::NB; ++b) sts16(to + vf_to + (uint32_t)b * 64, factor2(sv.get(b), ref));
       if (lane == 0) sts32(to + S::kRef, ek), sts32(to + S::kRef + 4, ref);
+    };
+    // where this lane's pieces go: copy i, from the first one's place (keys of head dimension 256: every second copy
+    // is swizzled the other way)
+    const uint32_t key0 = S::key_at(row_in, piece), value0 = S::value_at(row_in, piece);
+    const uint32_t key1 = D == 256 ? S::key_at(row_in + 4, piece) : 0;
+    static_assert(ROWS % (D == 256 ? 4 : 8) == 0, "the copies of a lane lie alike");
+    auto key_to = [&](uint32_t dst, int i) {
+      return dst + (D == 256 ? (i & 1 ? key1 : key0) + (uint32_t)(i >> 1) * 8 * S::kRow : key0 + (uint32_t)(i * ROWS) * S::kRow);
+    };
+    const uint32_t ksp = (uint32_t)p.ks_page, kss = (uint32_t)p.ks_slot, vsp = (uint32_t)p.vs_page, vss = (uint32_t)p.vs_slot;
+    auto load_scales = [&](int32_t page, int32_t off) {
+      if (!p.far) {
+        sk.load(p.k_scale + (f_ks + (uint32_t)page * ksp + (uint32_t)off * kss));
+        sv.load(p.v_scale + (f_vs + (uint32_t)page * vsp + (uint32_t)off * vss));
+      } else {
+        const int64_t kv = w.fetch.kv * p.team + member;
+        sk.load(p.k_scale + kv * p.ks_head + page * p.ks_page + off * p.ks_slot);
+        sv.load(p.v_scale + kv * p.vs_head + page * p.vs_page + off * p.vs_slot);
+      }
     };
     auto fetch = [&](int stage, int stage_before) {
       put_scales(stage_before);
-      pend = f_end > 0;
-      if (f_end > 0) {
-        const uint32_t dst = my_ring + (uint32_t)stage * S::kStage;
+      pend = f_left > 0;
+      if (f_left > 0) {
+        const uint32_t dst = my_ring + (uint32_t)stage * S::kStage, dv = dst + value0;
         sk.clear(), sv.clear();
         if constexpr (SLOTS) {
           const bool on = entry >= 0 && entry < p.num_pages * kPage;
@@ -209,69 +289,68 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < STAGES; ++i)
             if (i == stage) shown[i] = mask;
-          const int64_t page = on ? entry / kPage : 0, off = on ? entry % kPage : 0;
-          if (on) {
-            sk.load(f_ks + page * p.ks_page + off * p.ks_slot);
-            sv.load(f_vs + page * p.vs_page + off * p.vs_slot);
-          }
-          const unsigned long long ok = page * p.k_page + off * p.k_slot, ov = page * p.v_page + off * p.v_slot;
+          const int32_t page = on ? entry / kPage : 0, off = on ? entry % kPage : 0;
+          if (on) load_scales(page, off);
           if (!p.far) {
-            const uint32_t ok16 = (uint32_t)(ok >> 4), ov16 = (uint32_t)(ov >> 4);
+            const uint32_t ok = (uint32_t)page * kp16 + (uint32_t)off * ks16, ov = (uint32_t)page * vp16 + (uint32_t)off * vs16;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i) {
               const int r = i * ROWS + row_in;
               const uint32_t bytes = mask >> r & 1u ? 16u : 0u;
-              copy16(dst + S::key_at(r, piece), f_k + (uint64_t)__shfl_sync(~0u, ok16, r) * 16, bytes);
-              copy16(dst + S::value_at(r, piece), f_v + (uint64_t)__shfl_sync(~0u, ov16, r) * 16, bytes);
+              copy16(key_to(dst, i), (const uint8_t*)p.k + (uint64_t)(__shfl_sync(~0u, ok, r) + f_k16) * 16, bytes);
+              copy16(dv + (uint32_t)(i * ROWS) * S::kRow, (const uint8_t*)p.v + (uint64_t)(__shfl_sync(~0u, ov, r) + f_v16) * 16, bytes);
             }
           } else {
+            const unsigned long long ok = page * p.k_page + off * p.k_slot, ov = page * p.v_page + off * p.v_slot;
+            const int64_t kv = w.fetch.kv * p.team + member;
+            const uint8_t *k = (const uint8_t*)p.k + kv * p.k_head + piece * 16, *v = (const uint8_t*)p.v + kv * p.v_head + piece * 16;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i) {
               const int r = i * ROWS + row_in;
               const uint32_t bytes = mask >> r & 1u ? 16u : 0u;
-              copy16(dst + S::key_at(r, piece), f_k + __shfl_sync(~0u, ok, r), bytes);
-              copy16(dst + S::value_at(r, piece), f_v + __shfl_sync(~0u, ov, r), bytes);
+              copy16(key_to(dst, i), k + __shfl_sync(~0u, ok, r), bytes);
+              copy16(dv + (uint32_t)(i * ROWS) * S::kRow, v + __shfl_sync(~0u, ov, r), bytes);
             }
           }
         } else {
           const bool there = entry >= 0 && entry < p.num_pages;
           if (!there) warp_err = kErrInvalidPage;
-          const int32_t pos0 = (f.base + f.s) * kSub4, off = pos0 % kPage;
-          const int64_t page = there ? entry : 0;
-          const uint8_t* k = f_k + page * p.k_page + (off + row_in) * p.k_slot;
-          const uint8_t* v = f_v + page * p.v_page + (off + row_in) * p.v_slot;
-          const int64_t ks = ROWS * p.k_slot, vs = ROWS * p.v_slot;
-          if (there && pos0 + lane >= f.lo && pos0 + lane < f.hi) {
-            sk.load(f_ks + page * p.ks_page + (off + lane) * p.ks_slot);
-            sv.load(f_vs + page * p.vs_page + (off + lane) * p.vs_slot);
-          }
-          if (there && pos0 >= f.lo && pos0 + kSub4 <= f.hi) {
+          const int32_t pos0 = f_sub * kSub4, off = pos0 % kPage, page = there ? entry : 0;
+          if (there && pos0 + lane >= f_lo && pos0 + lane < f_hi) load_scales(page, off + lane);
+          if (!p.far && there && pos0 >= f_lo && pos0 + kSub4 <= f_hi) {
+            uint32_t k = f_k16 + (uint32_t)page * kp16 + (uint32_t)(off + row_in) * ks16;
+            uint32_t v = f_v16 + (uint32_t)page * vp16 + (uint32_t)(off + row_in) * vs16;
 #pragma unroll
-            for (int i = 0; i < COPIES; ++i, k += ks, v += vs) {
-              copy16(dst + S::key_at(i * ROWS + row_in, piece), k, 16u);
-              copy16(dst + S::value_at(i * ROWS + row_in, piece), v, 16u);
+            for (int i = 0; i < COPIES; ++i, k += ROWS * ks16, v += ROWS * vs16) {
+              copy16(key_to(dst, i), (const uint8_t*)p.k + (uint64_t)k * 16, 16u);
+              copy16(dv + (uint32_t)(i * ROWS) * S::kRow, (const uint8_t*)p.v + (uint64_t)v * 16, 16u);
             }
           } else {
+            const int64_t kv = w.fetch.kv * p.team + member;
+            const uint8_t* k = (const uint8_t*)p.k + kv * p.k_head + piece * 16 + page * p.k_page + (off + row_in) * p.k_slot;
+            const uint8_t* v = (const uint8_t*)p.v + kv * p.v_head + piece * 16 + page * p.v_page + (off + row_in) * p.v_slot;
 #pragma unroll
-            for (int i = 0; i < COPIES; ++i, k += ks, v += vs) {
+            for (int i = 0; i < COPIES; ++i, k += ROWS * p.k_slot, v += ROWS * p.v_slot) {
               const int32_t pos = pos0 + i * ROWS + row_in;
-              const bool on = there && pos >= f.lo && pos < f.hi;
-              copy16(dst + S::key_at(i * ROWS + row_in, piece), on ? k : (const uint8_t*)p.k, on ? 16u : 0u);
-              copy16(dst + S::value_at(i * ROWS + row_in, piece), on ? v : (const uint8_t*)p.v, on ? 16u : 0u);
+              const bool on = there && pos >= f_lo && pos < f_hi;
+              copy16(key_to(dst, i), on ? k : (const uint8_t*)p.k, on ? 16u : 0u);
+              copy16(dv + (uint32_t)(i * ROWS) * S::kRow, on ? v : (const uint8_t*)p.v, on ? 16u : 0u);
             }
           }
         }
         pend_first = f_first;
         f_first = false;
-        if (++f.s < min((int64_t)f.nsub, f_end)) {
+        ++f_sub;
+        if (--f_left > 0) {
           look_up();
         } else {
-          f_end = max((int64_t)0, f_end - f.nsub - kUnitCost);
-          f_first = true;
-          if (f_end > 0) {
-            f.next_unit(p, rows);
-            begin_fetch();
-          }
+          Place f = w.fetch;
+          const int64_t left = w.f_end - f.nsub - kUnitCost;
+          if (left > 0) f.next_unit(p, meta);
+          __syncwarp();
+          if (lane == 0) w.fetch = f, w.f_end = left;
+          __syncwarp();
+          if (left > 0) begin_fetch();
         }
       }
       copy_commit();
@@ -284,68 +363,71 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
     // ---- computing side ----
     int stage = 0;
     const float c = p.scale_log2;
-    while (end > 0) {
-      const int32_t v0 = at.s, v1 = (int32_t)min((int64_t)at.nsub, end);
-      const bool cut_front = v0 > 0;      // the segment starts inside its unit
-      const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
-      const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
+    for (bool more = true; more;) {
+      int32_t left, sub;                  // subtiles of the segment to go, and the next one
       uint32_t qf[MT][KS][4];
       float o[MT][NT][4];
-      float mx[MT][2], sum[MT][2], unit[MT][2];   // unit: what the queries were divided by
-      int32_t w_lo[MT][2], w_hi[MT][2];   // windows of the thread's tile rows
+      float mx[MT][2], sum[MT][2][2], unit[MT][2];   // unit: what the queries were divided by
       uint32_t live = 0;                  // bit 2t + e: the thread's tile row is a row that sees something
       bool seen = false;                  // (slots) some slot of the segment was one
       uint32_t o_ref = kLowest;           // the weighted values' reference
       int32_t full_lo = 0, full_hi = INT32_MAX;   // positions that every row of the group sees
       // tile row m: row m / chunk_heads of the group, head h0 + m % chunk_heads
+      {
+        const Place at = w.at;
+        const Rows rows = meta;
+        const int32_t h0 = (at.kv * p.team + member) * p.group + at.chunk * p.chunk_heads;
+        const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
+        left = (int32_t)min((int64_t)at.nsub, w.end) - at.s;
+        sub = at.base + at.s;
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int m = t * 16 + e * 8 + col;
-          const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
-          bool on = j < at.nrows && h < heads;
-          int32_t a = at.lo, b = at.hi;
-          if constexpr (!SLOTS) {
-            if (on) {
-              a = rows.start[at.row0 + j], b = rows.end[at.row0 + j];
-              if (b <= a) on = false, a = at.lo, b = at.hi;
-            }
-          }
-          if (on) live |= 1u << (2 * t + e);
-          w_lo[t][e] = a, w_hi[t][e] = b;
-          full_lo = max(full_lo, a), full_hi = min(full_hi, b);
-          mx[t][e] = kNegInf, sum[t][e] = 0.f, unit[t][e] = 1.f;
-          // this lane's quarter of the head
-          const uint2* src = (const uint2*)((const T*)p.q + (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head +
-                                            quad * (D / 4));
-          uint32_t top = 0;
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const uint2 u = on ? src[k] : make_uint2(0, 0);
-            qf[t][k][e] = u.x;
-            qf[t][k][2 + e] = u.y;
-            if constexpr (BF16) {
-              top = max(top, max(u.x & 0x7FFFu, (u.x >> 16) & 0x7FFFu));
-              top = max(top, max(u.y & 0x7FFFu, (u.y >> 16) & 0x7FFFu));
-            }
-          }
-          if constexpr (BF16) {
-            // to a largest element in [2^14, 2^15): exact, but for what is below 2^-24 then
-            top = max(top, __shfl_xor_sync(~0u, top, 1));
-            top = max(top, __shfl_xor_sync(~0u, top, 2));
-            const int32_t by = min(268 - (int32_t)(top >> 7), 253);
-            const float up = pow2_of(by);
-            unit[t][e] = pow2_of(254 - by);
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-              for (int x = 0; x < 4; x += 2) {
-                const uint32_t u = qf[t][k][x + e];
-                qf[t][k][x + e] = pack2<false>(__uint_as_float(u << 16) * up, __uint_as_float(u & 0xFFFF0000u) * up);
+          for (int e = 0; e < 2; ++e) {
+            const int m = t * 16 + e * 8 + col;
+            const int j = m / p.chunk_heads, h = m - j * p.chunk_heads;
+            bool on = j < at.nrows && h < heads;
+            int32_t a = at.lo, b = at.hi;
+            if constexpr (!SLOTS) {
+              if (on) {
+                a = rows.start[at.row0 + j], b = rows.end[at.row0 + j];
+                if (b <= a) on = false, a = at.lo, b = at.hi;
               }
+            }
+            if (on) live |= 1u << (2 * t + e);
+            full_lo = max(full_lo, a), full_hi = min(full_hi, b);
+            mx[t][e] = kNegInf, sum[t][e][0] = sum[t][e][1] = 0.f, unit[t][e] = 1.f;
+            // this lane's quarter of the head
+            const uint2* src = (const uint2*)((const T*)p.q + (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head +
+                                              quad * (D / 4));
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              const uint2 u = on ? src[k] : make_uint2(0, 0);
+              qf[t][k][e] = u.x;
+              qf[t][k][2 + e] = u.y;
+              if constexpr (BF16) {
+                top = max(top, max(u.x & 0x7FFFu, (u.x >> 16) & 0x7FFFu));
+                top = max(top, max(u.y & 0x7FFFu, (u.y >> 16) & 0x7FFFu));
+              }
+            }
+            if constexpr (BF16) {
+              // to a largest element in [2^14, 2^15): exact, but for what is below 2^-24 then
+              top = max(top, __shfl_xor_sync(~0u, top, 1));
+              top = max(top, __shfl_xor_sync(~0u, top, 2));
+              const int32_t by = min(268 - (int32_t)(top >> 7), 253);
+              const float up = pow2_of(by);
+              unit[t][e] = pow2_of(254 - by);
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int x = 0; x < 4; x += 2) {
+                  const uint32_t u = qf[t][k][x + e];
+                  qf[t][k][x + e] = pack2<false>(__uint_as_float(u << 16) * up, __uint_as_float(u & 0xFFFF0000u) * up);
+                }
+            }
           }
-        }
+      }
       full_lo = __reduce_max_sync(~0u, full_lo);
       full_hi = __reduce_min_sync(~0u, full_hi);
 #pragma unroll
@@ -355,7 +437,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
 #pragma unroll
           for (int x = 0; x < 4; ++x) o[t][n][x] = 0.f;
 
-      for (int32_t sub = v0; sub < v1; ++sub) {
+      for (; left > 0; --left, ++sub) {
         // the next stage goes where the last one computed was
         copy_wait<STAGES - 2>();
         uint32_t on = ~0u;
@@ -373,58 +455,45 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
         stage = stage == STAGES - 1 ? 0 : stage + 1;
         const uint2 refs = lds64(st + S::kRef);
 
-        // scores of the subtile: four tiles of 8 positions
+        // scores of the subtile: four tiles of 8 positions, four chains of products
         float s[MT][4][4];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) s[t][n][x] = 0.f;
         {
-          uint4 kf[S::H];
 #pragma unroll
-          for (int i = 0; i < S::H; ++i) kf[i] = lds128(st + S::kKf + (uint32_t)((col * 4 + quad) * S::H + i) * 16);
+          for (int i = 0; i < S::H; ++i) {            // a block's 16 bytes (8 at head dimension 64)
+            uint32_t kw[4][4];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t row = st + (uint32_t)(n * 8 + col) * S::kRow;
-#pragma unroll
-            for (int i = 0; i < S::H; ++i) {          // a block's 16 bytes (8 at head dimension 64)
-              uint32_t w[4];
+            for (int n = 0; n < 4; ++n) {
+              const uint32_t row = st + (uint32_t)(n * 8 + col) * S::kRow;
               if constexpr (D == 64) {
                 const uint2 u = lds64(row + quad * 8);
-                w[0] = u.x, w[1] = u.y, w[2] = w[3] = 0;
+                kw[n][0] = u.x, kw[n][1] = u.y;
               } else {
                 const uint4 u = lds128(row + (uint32_t)((D == 256 ? (quad * 2 + i) ^ (col & 1) : quad) << 4));
-                w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+                kw[n][0] = u.x, kw[n][1] = u.y, kw[n][2] = u.z, kw[n][3] = u.w;
               }
-              const uint32_t fac = n == 0 ? kf[i].x : n == 1 ? kf[i].y : n == 2 ? kf[i].z : kf[i].w;
+            }
+            const uint4 kf = lds128(st + S::kKf + (uint32_t)((col * 4 + quad) * S::H + i) * 16);
 #pragma unroll
-              for (int k = 0; k < (D == 64 ? 2 : 4); ++k) {
+            for (int k = 0; k < (D == 64 ? 2 : 4); ++k)
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
                 uint32_t h[4];
-                from_codes(w[k], h);
+                from_codes(kw[n][k], h);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) h[x] = hmul2(h[x], fac);
+                for (int x = 0; x < 4; ++x) h[x] = hmul2(h[x], n == 0 ? kf.x : n == 1 ? kf.y : n == 2 ? kf.z : kf.w);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                  mma16816<false>(s[t][n], qf[t][(i * 4 + k) * 2], h[0], h[1]);
+                  if (i == 0 && k == 0)
+                    mma_from_zero(s[t][n], qf[t][0], h[0], h[1]);
+                  else
+                    mma16816<false>(s[t][n], qf[t][(i * 4 + k) * 2], h[0], h[1]);
                   mma16816<false>(s[t][n], qf[t][(i * 4 + k) * 2 + 1], h[2], h[3]);
                 }
               }
-            }
           }
         }
-        const float k_unit = pow2_of((int32_t)refs.x - 12);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float u = BF16 ? fminf(k_unit * unit[t][e], 0x1p127f) : k_unit;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) s[t][n][2 * e] *= u, s[t][n][2 * e + 1] *= u;
-          }
 
-        const int32_t pos0 = (at.base + sub) * kSub4;
+        const int32_t pos0 = sub * kSub4;
         if constexpr (SLOTS) {
           seen |= on != 0;
           if (on != ~0u) {
@@ -438,21 +507,28 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
                 }
           }
         } else if (pos0 < full_lo || pos0 + kSub4 > full_hi) {
+          // (windows are looked up again: the loop has no registers for them)
+          const Place& at = w.at;
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int32_t pos = pos0 + n * 8 + quad + 4 * x;
+            for (int e = 0; e < 2; ++e) {
+              const bool there = live >> (2 * t + e) & 1;
+              const int32_t row = at.row0 + (there ? (t * 16 + e * 8 + col) / p.chunk_heads : 0);
+              const int32_t a = there ? meta.start[row] : 0, b = there ? meta.end[row] : 0;
 #pragma unroll
-              for (int t = 0; t < MT; ++t)
+              for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (pos < w_lo[t][e] || pos >= w_hi[t][e]) s[t][n][2 * e + x] = kNegInf;
+                for (int x = 0; x < 2; ++x) {
+                  const int32_t pos = pos0 + n * 8 + quad + 4 * x;
+                  if (pos < a || pos >= b) s[t][n][2 * e + x] = kNegInf;
+                }
             }
         }
 
         // running maximum; the sums are scaled where it moved, the weighted values also where their reference did
-        float base[MT][2];
+        const float k_unit = pow2_of((int32_t)refs.x - 12);
+        float base[MT][2], u[MT][2];
         bool moved = refs.y != o_ref;
         float alpha[MT][2];
 #pragma unroll
@@ -464,7 +540,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
             for (int n = 1; n < 4; ++n) m = fmaxf(m, fmaxf(s[t][n][2 * e], s[t][n][2 * e + 1]));
             m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
             m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-            m = fmaxf(m, mx[t][e]);
+            // in true units (the factor a power of two, never 0: -infinity stays)
+            u[t][e] = BF16 ? fmaxf(fminf(k_unit * unit[t][e], 0x1p127f), 0x1p-126f) : k_unit;
+            m = fmaxf(m * u[t][e], mx[t][e]);
             base[t][e] = reference(m);
             alpha[t][e] = m == mx[t][e] ? 1.f : ex2(exponent(mx[t][e], base[t][e], c));
             moved |= m != mx[t][e];
@@ -477,10 +555,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
           for (int t = 0; t < MT; ++t) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              sum[t][e] *= alpha[t][e];
+              sum[t][e][0] *= alpha[t][e], sum[t][e][1] *= alpha[t][e];
               const float a = alpha[t][e] * down;
 #pragma unroll
-              for (int n = 0; n < NT; ++n) o[t][n][2 * e] *= a, o[t][n][2 * e + 1] *= a;
+              for (int n = 0; n < NT; ++n) mul2(o[t][n][2 * e], o[t][n][2 * e + 1], a);
             }
           }
         }
@@ -491,9 +569,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
           for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float a = ex2(fmaf(__fsub_rn(s[t][n][2 * e], base[t][e]), c, (float)kF16Shift));
-              const float b = ex2(fmaf(__fsub_rn(s[t][n][2 * e + 1], base[t][e]), c, (float)kF16Shift));
-              sum[t][e] += a + b;
+              // (the product with a power of two is exact: one rounding, that of the difference)
+              float &a = s[t][n][2 * e], &b = s[t][n][2 * e + 1];
+              fma2(a, b, u[t][e], -base[t][e]);
+              fma2(a, b, c, (float)kF16Shift);
+              a = ex2(a), b = ex2(b);
+              add2(sum[t][e][0], sum[t][e][1], a, b);
               pf[t][n / 2][(n & 1) * 2 + e] = pack2<false>(a, b);
             }
 
@@ -503,27 +584,27 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
         for (int g = 0; g < 2; ++g) {
           const uint32_t f0 = g ? vf.z : vf.x, f1 = g ? vf.w : vf.y;
           constexpr int W = D / 64;                  // words of a lane
-          uint32_t w[4][W];
+          uint32_t vw[4][W];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int pos = g * 16 + u * 4 + quad;
+          for (int i = 0; i < 4; ++i) {
+            const int pos = g * 16 + i * 4 + quad;
             const uint32_t row = st + S::kV + (uint32_t)pos * S::kRow;
-            const uint32_t sw = S::value_swizzle(pos);
+            const uint32_t sw = S::value_swizzle(quad);   // (the same for all four)
             if constexpr (D == 64) {
-              w[u][0] = lds32(row + col * 4);
+              vw[i][0] = lds32(row + col * 4);
             } else if constexpr (D == 128) {
               const uint2 x = lds64(row + ((((uint32_t)col >> 1) ^ sw) << 4) + (col & 1) * 8);
-              w[u][0] = x.x, w[u][1] = x.y;
+              vw[i][0] = x.x, vw[i][1] = x.y;
             } else {
               const uint4 x = lds128(row + (((uint32_t)col ^ sw) << 4));
-              w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w;
+              vw[i][0] = x.x, vw[i][1] = x.y, vw[i][2] = x.z, vw[i][3] = x.w;
             }
           }
 #pragma unroll
           for (int i = 0; i < W; ++i) {
             uint32_t b0[8], b1[8];
-            from_pairs(w[0][i], w[1][i], b0);
-            from_pairs(w[2][i], w[3][i], b1);
+            from_pairs(vw[0][i], vw[1][i], b0);
+            from_pairs(vw[2][i], vw[3][i], b1);
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
               const uint32_t y0 = hmul2(b0[x], f0), y1 = hmul2(b1[x], f1);
@@ -536,11 +617,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
 
       // the segment ends: finish the unit, or leave its part
       {
-        const bool unit_end = v1 == at.nsub, whole = unit_end && !cut_front;
+        Place at = w.at;
+        const int64_t end = w.end;
+        const int32_t kv = at.kv * p.team + member, h0 = kv * p.group + at.chunk * p.chunk_heads;
+        const bool unit_end = end >= at.nsub, cut_front = at.s > 0, whole = unit_end && !cut_front;
         const int which = cut_front ? 0 : 1;
         if (!unit_end && !cut_front && lane == 0) {
-          p.open_parts[worker] = sp.holder(sp.first(worker + 1) - end + at.nsub - 1) - worker + 1;
-          p.open_info[worker] = make_int4(at.row0, at.nrows, at.kv * p.chunks + at.chunk, 0);
+          p.open_parts[worker] = split.holder(split.first(team + 1) - end + at.nsub - 1) - team + 1;
+          p.open_info[worker] = make_int4(at.row0, at.nrows, kv * p.chunks + at.chunk, 0);
         }
         const float o_unit = pow2_of((int32_t)o_ref - 12);
         constexpr float kBack = kShiftUp<BF16> / (float)(1 << kF16Shift);   // to the shift that the join expects
@@ -548,7 +632,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float l = sum[t][e];
+            float l = sum[t][e][0] + sum[t][e][1];
             l += __shfl_xor_sync(~0u, l, 1);
             l += __shfl_xor_sync(~0u, l, 2);
             l *= kBack;
@@ -586,9 +670,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
               if (quad == 0 && p.lse) p.lse[row * p.q_heads + qh] = log_sum_exp<BF16>(mx[t][e], l, c);
             }
           }
+        const int64_t rest = end - at.nsub - kUnitCost;
+        more = rest > 0;
+        if (more) at.next_unit(p, meta);
+        __syncwarp();
+        if (lane == 0) w.at = at, w.end = rest;
+        __syncwarp();
       }
-      end -= at.nsub + kUnitCost;
-      if (end > 0) at.next_unit(p, rows);
     }
     copy_wait<0>();
   }

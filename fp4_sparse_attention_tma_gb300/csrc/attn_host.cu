@@ -23,7 +23,7 @@ constexpr int64_t kMostPositions = INT32_MAX - 65536;
 // --------------------------------------------------------------- attention ----
 
 struct AttnPlan {
-  int32_t group, chunks, chunk_heads, group_rows, row_cols, tile, workers;
+  int32_t group, chunks, chunk_heads, group_rows, row_cols, tile, workers, team;
   bool tensor_core;
 };
 
@@ -80,6 +80,7 @@ AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_head
     a.tile = most;
     a.workers = sm * (fp4 ? attn_fp4_warps((int32_t)dim, most) : attn_warps((int32_t)dim, most));
   }
+  a.team = fp4 ? attn_fp4_team(kv_heads, a.workers / sm) : 1;
   return a;
 }
 
@@ -172,7 +173,8 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   if (!guard.ok()) return IDX_ERR_CUDA;
   if ((st = check_arch(&m))) return st;
   const bool weights = c.weight_out != nullptr && numel_of(c.weight_out) > 0;
-  const bool far = span_of(c.k) >= kFar || span_of(c.v) >= kFar;
+  const bool far = span_of(c.k) >= kFar || span_of(c.v) >= kFar ||
+                   (c.fp4 && (span_of(c.k_scale) > UINT32_MAX || span_of(c.v_scale) > UINT32_MAX));
   const AttnPlan a = c.slots ? plan_of(R, R, Hq, Hk, D, c.slots->shape[1], true, far, c.fp4, m.sm)
                              : plan_of(R, NR, Hq, Hk, D, MP * kPage, false, far, c.fp4, m.sm);
   int64_t logit_rows, logit_bytes;
@@ -207,6 +209,7 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   p.row_cols = a.row_cols, p.tensor_core = a.tensor_core;
   p.far = far;
   p.workers = R > 0 ? a.workers : 0;
+  p.team = a.team, p.ranges = p.workers / a.team, p.kv_units = (int32_t)Hk / a.team;
   p.n_cta = R > 0 ? m.sm : 0;
   p.scale_log2 = scale_log2;
   p.tile = a.tile, p.dim = (int32_t)D;

@@ -210,7 +210,7 @@ struct Walk {
     s = 0;
     if (++chunk < p.chunks) return;
     chunk = 0;
-    if (++kv < p.kv_heads) return;
+    if (++kv < p.kv_units) return;
     kv = 0;
     do {
       load(p, rows, row0 + nrows);
