@@ -28,7 +28,7 @@ DEBUG_BUILD_DIR = os.path.join(_HERE, "_build_dbg")
 DEBUG_LIB_PATH = os.path.join(_HERE, "libidxtopk_dbg.so")
 SOURCES = ["host.cu", "plan.cu", "score.cu", "finish.cu", "attn_host.cu", "attn_paged.cu",
            "attn_slots.cu", "attn_tc.cu", "attn_join.cu", "evict.cu", "cache_host.cu", "append.cu",
-           "attn_fp4_paged.cu", "attn_fp4_slots.cu"]
+           "attn_fp4_paged.cu", "attn_fp4_slots.cu", "attn_tc_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "-I" + INCLUDE, "-I" + CSRC] + ARCH

@@ -111,6 +111,28 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
   return r;
 }
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// The largest byte of a word.
+__device__ __forceinline__ uint32_t largest_of(uint32_t w) {
+  return max(max(w & 255u, w >> 8 & 255u), max(w >> 16 & 255u, w >> 24));
+}
+// 8 bf16 elements, of a head that 16 lanes hold, to fp16 with the head's largest element in [2^14, 2^15): exact, but for
+// what is below 2^-24 then.  `unit`: what they were divided by.
+__device__ __forceinline__ void to_f16(uint4& u, float& unit) {
+  uint32_t w[4] = {u.x, u.y, u.z, u.w}, top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+  const int32_t by = min(268 - (int32_t)(top >> 7), 253);
+  const float up = pow2_of(by);
+  unit = pow2_of(254 - by);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack2<false>(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
+  u = make_uint4(w[0], w[1], w[2], w[3]);
+}
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
   asm volatile("{\n\t.reg .u16 t;\n\tcvt.u16.u32 t, %1;\n\tst.shared.u16 [%0], t;\n\t}" ::"r"(a), "r"(v) : "memory");

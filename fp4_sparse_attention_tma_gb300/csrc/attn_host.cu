@@ -65,7 +65,8 @@ AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_head
   AttnPlan a{};
   a.group = (int32_t)(q_heads / kv_heads);
   const int64_t per_req = rows > num_req && num_req > 0 ? (rows + num_req - 1) / num_req : 1;
-  a.tensor_core = !fp4 && tensor_core_for(a.group, rows, per_req, kv_heads, dim, positions, slots, far, sm);
+  a.tensor_core = fp4 ? dim == 128 && !far && a.group > 16
+                       : tensor_core_for(a.group, rows, per_req, kv_heads, dim, positions, slots, far, sm);
   const int32_t most = a.tensor_core ? 64 : dim <= 128 && (int64_t)a.group * per_req > 16 ? 32 : 16;
   a.chunks = (a.group + most - 1) / most;
   a.chunk_heads = (a.group + a.chunks - 1) / a.chunks;
@@ -80,7 +81,7 @@ AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_head
     a.tile = most;
     a.workers = sm * (fp4 ? attn_fp4_warps((int32_t)dim, most) : attn_warps((int32_t)dim, most));
   }
-  a.team = fp4 ? attn_fp4_team(kv_heads, a.workers / sm) : 1;
+  a.team = fp4 && !a.tensor_core ? attn_fp4_team(kv_heads, a.workers / sm) : 1;
   return a;
 }
 

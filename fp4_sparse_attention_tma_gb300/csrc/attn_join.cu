@@ -12,10 +12,12 @@ namespace idxk {
 cudaError_t launch_attn_pages(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
 cudaError_t launch_attn_slots(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
 cudaError_t launch_attn_tc(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
+cudaError_t launch_attn_tc_fp4(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
 cudaError_t launch_attn_fp4_pages(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
 cudaError_t launch_attn_fp4_slots(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream);
 
 cudaError_t launch_attn(const AttnParams& p, bool bf16, int sm_count, cudaStream_t stream) {
+  if (p.k_scale && p.tensor_core) return launch_attn_tc_fp4(p, bf16, sm_count, stream);
   if (p.k_scale)
     return p.slots ? launch_attn_fp4_slots(p, bf16, sm_count, stream) : launch_attn_fp4_pages(p, bf16, sm_count, stream);
   if (p.tensor_core) return launch_attn_tc(p, bf16, sm_count, stream);

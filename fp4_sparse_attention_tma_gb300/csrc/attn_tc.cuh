@@ -40,6 +40,7 @@
 #pragma once
 
 #include "attn_common.cuh"
+#include "attn_fp4.cuh"
 #include "idx_device.cuh"
 
 namespace idxk {
@@ -318,9 +319,10 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
   return wait_slow(bar, parity, abort, err);
 }
 
-template <bool BF16, int NB, bool SLOTS>
+template <bool BF16, int NB, bool SLOTS, bool FP4>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr bool MB = BF16 && !FP4;         // the matrices' type: bf16, or fp16
   constexpr bool SPLIT = NB == 1;           // one row: either half of the matrix takes half of a tile's positions
   constexpr int kSoft = 256;                // softmax threads
 
@@ -331,6 +333,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   __shared__ float2 half_ml[2][kCols];      // (one row) reference and sum of either half, -1 where nothing was seen
   __shared__ float row_max[2][2][128];      // by visit and warpgroup
   __shared__ float row_sum[2][128];         // by warpgroup, -1 where nothing was seen
+  // (4 bits) what the queries were divided by, by segment, and the references of keys and values by visit and quarter
+  // of the tile: the copies run no more than so far ahead of the softmax
+  constexpr int kAhead = FP4 ? 8 : 1;
+  __shared__ float q_unit[FP4 ? 4 : 1][128];
+  __shared__ __align__(16) int32_t refs[kAhead][2][4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_addr(bars);
@@ -352,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     for (int i = 0; i < kRingK; ++i) mbar_init(full_k(i), kLoaders), mbar_init(empty_k(i), 1);
     for (int i = 0; i < kRingV; ++i) mbar_init(full_v(i), kLoaders), mbar_init(empty_v(i), 1);
     mbar_init(empty_q, 1);
-    for (int b = 0; b < 2; ++b) mbar_init(full_s(b), 1), mbar_init(full_p(b), kSoft), mbar_init(done_pv(b), 1);
+    for (int b = 0; b < 2; ++b) mbar_init(full_s(b), FP4 ? 2 : 1), mbar_init(full_p(b), kSoft), mbar_init(done_pv(b), 1);
     mbar_init(drain, 2);
     fence_mbar_init();
   }
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const int c0 = SPLIT ? (int)part_of * 2 + g : 2 * g;
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // this warp's 32 lanes
       const uint32_t out_a = tmem + lanes + kOut + (SPLIT ? part_of * kHead : 0), out_b = tmem + lanes + kOut + kHead;
-      uint32_t n = 0;                // visits so far
+      uint32_t n = 0, seg = 0;       // visits, segments so far
       bool ok = true;
       bool more = true;
       // (slots) the slots of the next visit's positions, asked for a visit ahead
@@ -447,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         bool had_a = false, had_b = false;   // the accumulators hold something of this matrix row
         bool foreign = false;                // the first accumulator holds the other row's tiles alone in this row's lanes
         bool seen = false;
+        int32_t o_ref = (int32_t)fp4::kLowest;   // (4 bits) the weighted values' reference
         for (int32_t v = at.s; v < v1; ++v, ++n) {
           const uint32_t b = n & 1;
           int32_t tile;
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             // chunk k's maximum (its scores put down first, where the weights are to be added up)
             float top = kNegInf, top2 = kNegInf;
             auto look = [&](int k, uint32_t (&r)[32]) {
-              if constexpr (!SLOTS) {
+              if constexpr (!SLOTS && !FP4) {
                 if (p.logits) {
                   const int64_t width = (int64_t)p.max_pages * kPage;
                   const int32_t pos = tile * kPos + (c0 + k) * 32, h = at.chunk * p.chunk_heads + (x & (kCols - 1));
@@ -510,19 +518,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             for (int k = 0; k < CH; ++k) tmem_ld32(s + k * 32, r[k]);
 #pragma unroll
             for (int k = 0; k < CH; ++k) tmem_wait_ld32(r[k]);
+            // (4 bits) a chunk's scores are in units of its keys' reference and the head's queries: powers of two, never 0
+            float unit[CH];
+            int32_t v_ref[CH], new_ref = o_ref;
+            if constexpr (FP4) {
+              const float qu = q_unit[seg & 3][x];
+              const int4 all = *(const int4*)refs[n % kAhead][1];
+              new_ref = max(max(max(all.x, all.y), max(all.z, all.w)), o_ref);
+              float best = kNegInf;
 #pragma unroll
-            for (int k = 0; k < CH; ++k) look(k, r[k]);
+              for (int k = 0; k < CH; ++k) {
+                unit[k] = fmaxf(fminf(fp4::pow2_of(refs[n % kAhead][0][c0 + k] - 12) * qu, 0x1p127f), 0x1p-126f);
+                v_ref[k] = refs[n % kAhead][1][c0 + k];
+                top = kNegInf, top2 = kNegInf;
+                look(k, r[k]);
+                best = fmaxf(best, fmaxf(top, top2) * unit[k]);
+              }
+              top = best, top2 = kNegInf;
+            } else {
+#pragma unroll
+              for (int k = 0; k < CH; ++k) look(k, r[k]);
+            }
             // of the whole row: the other warpgroup's thread has seen the other positions
             top = fmaxf(top, top2);
             row_max[b][g][x] = top;
             bar_sync(pair, 64);
             top = fmaxf(top, row_max[b][g ^ 1][x]);
             // does its weights' reference have to follow?
-            if (__any_sync(~0u, exponent(top, ref, p.scale_log2) > kRaise<BF16>)) {   // (false where both are -infinity)
-              const float raised = fmaxf(ref, top), f = raised == ref ? 1.f : ex2(exponent(ref, raised, p.scale_log2));
+            if (__any_sync(~0u, exponent(top, ref, p.scale_log2) > kRaise<MB> || new_ref != o_ref)) {   // (false where both are -infinity)
+              const float raised = fmaxf(ref, top);
+              float f = raised == ref ? 1.f : ex2(exponent(ref, raised, p.scale_log2));
               ref = raised;
 #pragma unroll
               for (int i = 0; i < 4; ++i) sum[i] *= f;
+              if constexpr (FP4) f *= fp4::pow2_of(127 + o_ref - new_ref), o_ref = new_ref;
               if (had_a || had_b) {
                 ok &= wait(done_pv(b ^ 1), (n - 1) >> 1 & 1, abort, &err);   // the last visit that added to them
                 tc_fence_after();
@@ -544,13 +573,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const float base = -reference(ref);
             auto weigh = [&](int k, const uint32_t (&r)[32]) {
               uint32_t w[16];
+              if constexpr (FP4) {
+                // the weights count in the chunk's values' reference, their sum does not (values 2^-40 below the largest are
+                // taken for 2^-40 of it)
+                const int32_t down = max(v_ref[k] - o_ref, -40);
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                const float shift = kShift<MB> + (float)down;
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float d0 = __uint_as_float(r[i]), d1 = __uint_as_float(r[i + 1]);
-                exponent2(d0, d1, base, p.scale_log2, kShift<BF16>);
-                const float e0 = ex2(d0), e1 = ex2(d1);
-                add2(sum[i & 2], sum[(i & 2) + 1], e0, e1);
-                w[i / 2] = pack2<BF16>(e0, e1);
+                for (int i = 0; i < 32; i += 2) {
+                  float d0 = __uint_as_float(r[i]), d1 = __uint_as_float(r[i + 1]);
+                  fp4::fma2(d0, d1, unit[k], base);
+                  fp4::fma2(d0, d1, p.scale_log2, shift);
+                  const float e0 = ex2(d0), e1 = ex2(d1);
+                  add2(part[i & 2], part[(i & 2) + 1], e0, e1);
+                  w[i / 2] = pack2<MB>(e0, e1);
+                }
+                const float back = fp4::pow2_of(127 - down);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = fmaf(part[i], back, sum[i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float d0 = __uint_as_float(r[i]), d1 = __uint_as_float(r[i + 1]);
+                  exponent2(d0, d1, base, p.scale_log2, kShift<BF16>);
+                  const float e0 = ex2(d0), e1 = ex2(d1);
+                  add2(sum[i & 2], sum[(i & 2) + 1], e0, e1);
+                  w[i / 2] = pack2<BF16>(e0, e1);
+                }
               }
               tmem_st16(w_at + k * 16, w);
             };
@@ -600,7 +649,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (n > 0) ok &= wait(done_pv((n - 1) & 1), (n - 1) >> 1 & 1, abort, &err);
         if (n > 1) ok &= wait(done_pv(n & 1), (n - 2) >> 1 & 1, abort, &err);
         tc_fence_after();
+        ++seg;
         float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if constexpr (FP4) l *= kShiftUp<BF16> / kShiftUp<MB>;   // to the shift that the join expects
         // of the whole row
         row_sum[g][x] = (had_a || had_b) && (!SLOTS || seen) ? l : -1.f;
         bar_sync(pair, 64);
@@ -639,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
         }
         if (whole) f *= inv;
+        if constexpr (FP4) f *= fp4::pow2_of(o_ref - 12) * (kShiftUp<BF16> / kShiftUp<MB>);
         T* out = (T*)p.out + row * p.out_row + (int64_t)qh * p.out_head;
         float* po = p.part_o + part * kHead;
         auto emit = [&](int c, const float (&z)[8]) {   // 8 columns of the thread's row
@@ -707,7 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const int64_t s_page = values ? p.v_page : p.k_page, s_slot = values ? p.v_slot : p.k_slot,
                     s_head = values ? p.v_head : p.k_head;
       // Offsets are in units of 16 bytes (the caches span less than 64 GB).
-      const uint32_t page16 = (uint32_t)(s_page / 8), slot16 = (uint32_t)(s_slot / 8);
+      constexpr int64_t kPiece = FP4 ? 16 : 8;   // elements, or bytes of codes
+      const uint32_t page16 = (uint32_t)(s_page / kPiece), slot16 = (uint32_t)(s_slot / kPiece);
       const int x = lane & 15, r0 = lane / 16;   // this lane's piece of a head, and its rows r0 + 2 i of the warp's 32
       uint32_t n = 0, seg = 0;                   // tiles, segments
       bool ok = true;
@@ -726,6 +779,143 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       };
       if constexpr (SLOTS) ask(p.slots + (int64_t)at.row0 * p.n_slots, at.s);
       bool more = true;
+      if constexpr (FP4) {
+        // Codes are unpacked on their way: 32 positions a warp, a lane 32 elements (a block) of one of 8 positions at a
+        // time.  Loaded a visit ahead into registers, times their scales over the largest of the warp's 32 positions
+        // (attn_fp4.cuh) into the tile; K's warps also publish both references.
+        const uint8_t* codes = (const uint8_t*)cache;
+        const int block = lane >> 3, in8 = lane & 7;
+        uint4 next[4], cur[4];
+        uint32_t next_k = 0, next_v = 0;   // scales of this lane's position: keys' (K's warps) and values'
+        const uint32_t ksp = (uint32_t)p.ks_page, kss = (uint32_t)p.ks_slot, vsp = (uint32_t)p.vs_page, vss = (uint32_t)p.vs_slot;
+        // asks for the codes and scales of the visit whose entry is there
+        auto issue = [&](int32_t kv, int32_t tile, uint32_t rows) {
+          bool on;
+          int32_t page, off;
+          if constexpr (SLOTS) {
+            on = entry >= 0 && entry < p.num_pages * kPage;
+            if (!on && entry != -1) bad = max(bad, (uint32_t)kErrInvalidPage);
+            page = on ? entry / kPage : 0, off = on ? entry % kPage : 0;
+          } else {
+            int32_t lo = 0, hi = INT32_MAX;   // seen by every row of the visit
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+              if (rows >> j & 1) lo = max(lo, at.a[j]), hi = min(hi, at.b[j]);
+            const int32_t first = tile * kPos + quarter * 32;
+            const bool any = first < hi && first + 32 > lo, there = entry >= 0 && entry < p.num_pages;
+            if (any && !there) bad = max(bad, (uint32_t)kErrInvalidPage);
+            on = there && first + lane >= lo && first + lane < hi;
+            page = there ? entry : 0, off = (quarter & 1) * 32 + lane;
+          }
+          const uint32_t from = (uint32_t)page * page16 + (uint32_t)off * slot16;
+          next_k = next_v = 0;
+          if (on) {
+            if (!values) next_k = *(const uint32_t*)(p.k_scale + kv * p.ks_head + (uint32_t)((uint32_t)page * ksp + (uint32_t)off * kss));
+            next_v = *(const uint32_t*)(p.v_scale + kv * p.vs_head + (uint32_t)((uint32_t)page * vsp + (uint32_t)off * vss));
+          }
+          const uint32_t mask = __ballot_sync(~0u, on);
+          const uint8_t* base = codes + kv * s_head + block * 16;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t o = __shfl_sync(~0u, from, i * 8 + in8);
+            next[i] = mask >> (i * 8 + in8) & 1 ? __ldg((const uint4*)(base + (uint64_t)o * 16)) : make_uint4(0, 0, 0, 0);
+          }
+        };
+        bool issued = false;
+        while (more) {
+          const int32_t v0 = at.s, v1 = segment_end();
+          int32_t tile;
+          uint32_t rows = 1;
+          const int32_t* list;
+          at.visit(v0, tile, rows);
+          if constexpr (SLOTS) {
+            list = p.slots + (int64_t)at.row0 * p.n_slots;
+            if (warp == 12 && at.row0 + 1 < p.rows)
+              for (int32_t i = lane * 32; i < p.n_slots; i += 32 * 32)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(list + p.n_slots + i));
+          } else {
+            list = p.page_table + (int64_t)at.req * p.max_pages;
+            ask(list, tile);
+          }
+          // what comes after visit v: its entry is asked for once v's codes are
+          auto ask_after = [&](int32_t v) {
+            if (v + 1 < v1) {
+              int32_t t;
+              uint32_t r;
+              at.visit(v + 1, t, r);
+              ask(list, t);
+            } else if (SLOTS && goes_on()) {
+              ask(list + (next_is_row() ? p.n_slots : 0), 0);   // the next unit's first: of this row, or of the next
+            }
+          };
+          if (!issued) issue(at.kv, tile, rows);
+          ask_after(v0);
+          issued = false;
+          if (!values) {
+            // the queries, with the segment's first tile of keys (one row's stand in both halves): 16 lanes a row
+            ok = __all_sync(~0u, wait(empty_q, (seg & 1) ^ 1, abort, &err));
+            if (!ok) break;
+            const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
+            const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
+#pragma unroll 2
+            for (int i = t; i < 128 * 16; i += kLoaders) {
+              const int r = i / 16, y = i % 16, j = SPLIT ? 0 : r / kCols, h = r % kCols;
+              const bool in = at.b[j] > at.a[j] && h < heads;
+              uint4 u = make_uint4(0, 0, 0, 0);
+              if (in) u = *(const uint4*)((const T*)p.q + (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head + y * 8);
+              float by_unit = 1.f;
+              if constexpr (BF16) fp4::to_f16(u, by_unit);
+              if (y == 0) q_unit[seg & 3][r] = by_unit;
+              *(uint4*)(raw + (smem - smem_addr(raw)) + kQueries + (y / 8) * kHalfTile + r * 128 + (((y & 7) ^ (r & 7)) << 4)) = u;
+            }
+            ++seg;
+          }
+          for (int32_t v = v0; v < v1; ++v) {
+            const uint32_t scale_k = next_k, scale_v = next_v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cur[i] = next[i];
+            if (v + 1 < v1) {
+              int32_t t;
+              uint32_t r;
+              at.visit(v + 1, t, r);
+              issue(at.kv, t, r);
+              ask_after(v + 1);
+            } else if (SLOTS && goes_on()) {
+              issue(next_is_row() ? 0 : at.chunk + 1 < p.chunks ? at.kv : at.kv + 1, 0, 1);
+              issued = true;
+            }
+            const uint32_t largest = fp4::largest_of(scale_v), mine = values ? largest : fp4::largest_of(scale_k);
+            const uint32_t ref = max(__reduce_max_sync(~0u, mine), fp4::kLowest);
+            const uint32_t other = values ? 0 : max(__reduce_max_sync(~0u, largest), fp4::kLowest);
+            if (max(ref, other) > kMaxScaleByte) bad = max(bad, (uint32_t)kErrInvalidValue);
+            const uint32_t slot = n % depth;
+            ok = __all_sync(~0u, wait(values ? empty_v(slot) : empty_k(slot), (n / depth & 1) ^ 1, abort, &err));
+            if (!ok) break;
+            if (!values && lane == 0) refs[n % kAhead][0][quarter] = (int32_t)ref, refs[n % kAhead][1][quarter] = (int32_t)other;
+            const uint32_t dst = ring + slot * kTileBytes + (uint32_t)(block >> 1) * kHalfTile;
+            const uint32_t scale = values ? scale_v : scale_k;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int pos = quarter * 32 + i * 8 + in8;
+              const uint32_t e = __shfl_sync(~0u, scale, i * 8 + in8) >> (8 * block) & 255u;
+              const uint32_t fac = fp4::factor2(e, ref);
+              const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                uint32_t h[4];
+                from_codes(w[y], h);
+                fp4::sts128(dst + (uint32_t)pos * 128 + ((uint32_t)(((block & 1) * 4 + y) ^ in8) << 4),
+                            make_uint4(fp4::hmul2(h[0], fac), fp4::hmul2(h[1], fac), fp4::hmul2(h[2], fac), fp4::hmul2(h[3], fac)));
+              }
+            }
+            fence_proxy_async_smem();   // this thread's writes before the products' reads
+            mbar_arrive(values ? full_v(slot) : full_k(slot));
+            ++n;
+          }
+          if (!ok) break;
+          more = next_segment();
+        }
+      } else
       while (more) {
         const int32_t v0 = at.s, v1 = segment_end();
         int32_t tile;
@@ -820,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       if (warp == 16) {
       // ----------------------------------------------------- scores' products ----
-      constexpr uint32_t kQK = idesc_f16<BF16>(128, kPos, false);
+      constexpr uint32_t kQK = idesc_f16<MB>(128, kPos, false);
       const uint64_t q = desc128(smem + kQueries, 16, 1024);
       uint32_t n = 0;
       bool ok = true, more = true;
@@ -841,6 +1031,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                      kQK, i > 0);
             tc_commit(full_s(b));
             tc_commit(empty_k(slot));
+            // (4 bits) what the copying warps left beside the tile reaches the softmax by this arrival
+            if constexpr (FP4) mbar_arrive(full_s(b));
           }
           __syncwarp();
         }
@@ -851,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       } else if (warp == 17) {
       // ---------------------------------------------------- outputs' products ----
-      constexpr uint32_t kPV = idesc_f16<BF16>(128, kHead, true);
+      constexpr uint32_t kPV = idesc_f16<MB>(128, kHead, true);
       uint32_t n = 0;
       bool ok = true, more = true;
       while (more) {
@@ -917,9 +1109,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   if (warp == 16) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <bool BF16, int NB, bool SLOTS>
+template <bool BF16, int NB, bool SLOTS, bool FP4>
 cudaError_t launch(const AttnParams& p, int sm_count, cudaStream_t stream) {
-  auto* kernel = attn_tc_kernel<BF16, NB, SLOTS>;
+  auto* kernel = attn_tc_kernel<BF16, NB, SLOTS, FP4>;
   static std::atomic<bool> done[64];
   cudaError_t e = set_smem_once(kernel, kSmemBytes, done);
   if (e != cudaSuccess) return e;
