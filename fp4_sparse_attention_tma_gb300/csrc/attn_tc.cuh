@@ -217,8 +217,14 @@ struct Walk {
       load(p, rows, row0 + nrows);
     } while (nsub == 0);
   }
-  // Visit v of the unit: its tile and its rows (bit j).
+  // Visit v of the unit: its tile and its rows (bit j); with it `run` - 1 more visits have the tiles that follow, and the
+  // same rows.
   __device__ void visit(int32_t v, int32_t& tile, uint32_t& rows) const {
+    int32_t run;
+    visit(v, tile, rows, run);
+  }
+  __device__ void visit(int32_t v, int32_t& tile, uint32_t& rows, int32_t& run) const {
+    run = INT32_MAX;
     if constexpr (NB == 1) {
       tile = lo(a[0]) + v;
       rows = 1;
@@ -232,6 +238,7 @@ struct Walk {
         if (v < front + back) {
           tile = v < front ? lo(a[j]) + v : c1 + v - front;
           rows = 1u << j;
+          run = v < front ? front - v : front + back - v;
           return;
         }
         v -= front + back;
@@ -239,6 +246,7 @@ struct Walk {
           if (v < c1 - c0) {
             tile = c0 + v;
             rows = 3;
+            run = c1 - c0 - v;
             return;
           }
           v -= c1 - c0;
@@ -246,6 +254,20 @@ struct Walk {
       }
       tile = 0;   // (not reached)
     }
+  }
+};
+
+// A unit's visits one after another.
+template <int NB, bool SLOTS>
+struct Steps {
+  int32_t tile, run;
+  uint32_t rows;
+  __device__ void start(const Walk<NB, SLOTS>& at, int32_t v) { at.visit(v, tile, rows, run); }
+  __device__ void next(const Walk<NB, SLOTS>& at, int32_t v) {   // from visit v - 1 to v
+    if (NB == 1 || --run > 0)
+      ++tile;
+    else
+      at.visit(v, tile, rows, run);
   }
 };
 
@@ -782,52 +804,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       if constexpr (FP4) {
         // Codes are unpacked on their way: 32 positions a warp, a lane 32 elements (a block) of one of 8 positions at a
         // time.  Loaded a visit ahead into registers, times their scales over the largest of the warp's 32 positions
-        // (attn_fp4.cuh) into the tile; K's warps also publish both references.
+        // (attn_fp4.cuh) into the tile; K's warps also publish both references.  Positions that the rows do not see have
+        // the scale 0 and the codes of some other position: their scores are not used and their weights are 0.
         const uint8_t* codes = (const uint8_t*)cache;
         const int block = lane >> 3, in8 = lane & 7;
-        uint4 next[4], cur[4];
-        uint32_t next_k = 0, next_v = 0;   // scales of this lane's position: keys' (K's warps) and values'
+        uint4 held[4];                     // codes of the next visit to unpack
+        uint32_t scale_k = 0, scale_v = 0;   // scales of this lane's position in it: keys' (K's warps) and values'
         const uint32_t ksp = (uint32_t)p.ks_page, kss = (uint32_t)p.ks_slot, vsp = (uint32_t)p.vs_page, vss = (uint32_t)p.vs_slot;
-        // asks for the codes and scales of the visit whose entry is there
-        auto issue = [&](int32_t kv, int32_t tile, uint32_t rows) {
+        uint32_t to[4];                    // places of a block's four 16-byte pieces, in a tile
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          to[y] = (uint32_t)(block >> 1) * kHalfTile + (uint32_t)(quarter * 32 + in8) * 128 +
+                  ((uint32_t)(((block & 1) * 4 + y) ^ in8) << 4);
+        // the visit whose entry is there: where this lane's position lies, and its scales (asked for)
+        const uint8_t *base, *ks_head = nullptr, *vs_head;   // of the head
+        auto begin_head = [&](int32_t kv) {
+          base = codes + kv * s_head + block * 16;
+          if (!values) ks_head = p.k_scale + kv * p.ks_head;
+          vs_head = p.v_scale + kv * p.vs_head;
+        };
+        auto locate = [&](int32_t tile, uint32_t rows, uint32_t& next_k, uint32_t& next_v) {
           bool on;
-          int32_t page, off;
+          uint32_t page, off;
           if constexpr (SLOTS) {
             on = entry >= 0 && entry < p.num_pages * kPage;
             if (!on && entry != -1) bad = max(bad, (uint32_t)kErrInvalidPage);
-            page = on ? entry / kPage : 0, off = on ? entry % kPage : 0;
+            page = (uint32_t)entry / kPage, off = (uint32_t)entry % kPage;
           } else {
             int32_t lo = 0, hi = INT32_MAX;   // seen by every row of the visit
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-              if (rows >> j & 1) lo = max(lo, at.a[j]), hi = min(hi, at.b[j]);
             const int32_t first = tile * kPos + quarter * 32;
+            if (NB == 1 || rows != 3) {
+#pragma unroll
+              for (int j = 0; j < NB; ++j)
+                if (rows >> j & 1) lo = max(lo, at.a[j]), hi = min(hi, at.b[j]);
+            }
             const bool any = first < hi && first + 32 > lo, there = entry >= 0 && entry < p.num_pages;
             if (any && !there) bad = max(bad, (uint32_t)kErrInvalidPage);
             on = there && first + lane >= lo && first + lane < hi;
-            page = there ? entry : 0, off = (quarter & 1) * 32 + lane;
+            page = (uint32_t)entry, off = (uint32_t)((quarter & 1) * 32 + lane);
           }
-          const uint32_t from = (uint32_t)page * page16 + (uint32_t)off * slot16;
           next_k = next_v = 0;
           if (on) {
-            if (!values) next_k = *(const uint32_t*)(p.k_scale + kv * p.ks_head + (uint32_t)((uint32_t)page * ksp + (uint32_t)off * kss));
-            next_v = *(const uint32_t*)(p.v_scale + kv * p.vs_head + (uint32_t)((uint32_t)page * vsp + (uint32_t)off * vss));
+            if (!values) next_k = *(const uint32_t*)(ks_head + (uint32_t)(page * ksp + off * kss));
+            next_v = *(const uint32_t*)(vs_head + (uint32_t)(page * vsp + off * vss));
           }
-          const uint32_t mask = __ballot_sync(~0u, on);
-          const uint8_t* base = codes + kv * s_head + block * 16;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t o = __shfl_sync(~0u, from, i * 8 + in8);
-            next[i] = mask >> (i * 8 + in8) & 1 ? __ldg((const uint4*)(base + (uint64_t)o * 16)) : make_uint4(0, 0, 0, 0);
-          }
+          return on ? page * page16 + off * slot16 : 0u;
+        };
+        auto load = [&](uint32_t from, int i) {
+          return *(const uint4*)(base + (uint64_t)__shfl_sync(~0u, from, i * 8 + in8) * 16);
         };
         bool issued = false;
         while (more) {
           const int32_t v0 = at.s, v1 = segment_end();
-          int32_t tile;
-          uint32_t rows = 1;
           const int32_t* list;
-          at.visit(v0, tile, rows);
+          Steps<NB, SLOTS> ahead;            // of the visit whose entry is asked for
+          ahead.start(at, v0);
           if constexpr (SLOTS) {
             list = p.slots + (int64_t)at.row0 * p.n_slots;
             if (warp == 12 && at.row0 + 1 < p.rows)
@@ -835,80 +866,99 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(list + p.n_slots + i));
           } else {
             list = p.page_table + (int64_t)at.req * p.max_pages;
-            ask(list, tile);
+            ask(list, ahead.tile);
           }
-          // what comes after visit v: its entry is asked for once v's codes are
-          auto ask_after = [&](int32_t v) {
-            if (v + 1 < v1) {
-              int32_t t;
-              uint32_t r;
-              at.visit(v + 1, t, r);
-              ask(list, t);
+          // on to visit v's entry (past the segment's end: the next unit's first, of this row or of the next)
+          auto ask_for = [&](int32_t v) {
+            if (v < v1) {
+              ahead.next(at, v);
+              ask(list, ahead.tile);
             } else if (SLOTS && goes_on()) {
-              ask(list + (next_is_row() ? p.n_slots : 0), 0);   // the next unit's first: of this row, or of the next
+              ask(list + (next_is_row() ? p.n_slots : 0), 0);
             }
           };
-          if (!issued) issue(at.kv, tile, rows);
-          ask_after(v0);
+          if (!issued) {
+            begin_head(at.kv);
+            const uint32_t from = locate(ahead.tile, ahead.rows, scale_k, scale_v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) held[i] = load(from, i);
+          }
           issued = false;
+          ask_for(v0 + 1);
+          // the queries, with the segment's first tile of keys: 16 lanes a row, copied while that is unpacked, then brought
+          // to fp16 where they lie
+          constexpr int kQRows = SPLIT ? kCols : 128;
+          auto q_at = [&](int i) {
+            const int r = i / 16, y = i % 16;
+            return smem + kQueries + (y / 8) * kHalfTile + r * 128 + (((y & 7) ^ (r & 7)) << 4);
+          };
           if (!values) {
-            // the queries, with the segment's first tile of keys (one row's stand in both halves): 16 lanes a row
             ok = __all_sync(~0u, wait(empty_q, (seg & 1) ^ 1, abort, &err));
             if (!ok) break;
             const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
             const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
-#pragma unroll 2
-            for (int i = t; i < 128 * 16; i += kLoaders) {
-              const int r = i / 16, y = i % 16, j = SPLIT ? 0 : r / kCols, h = r % kCols;
+#pragma unroll 4
+            for (int i = t; i < kQRows * 16; i += kLoaders) {
+              const int r = i / 16, j = SPLIT ? 0 : r / kCols, h = r % kCols;
               const bool in = at.b[j] > at.a[j] && h < heads;
-              uint4 u = make_uint4(0, 0, 0, 0);
-              if (in) u = *(const uint4*)((const T*)p.q + (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head + y * 8);
+              const T* q = (const T*)p.q + (in ? (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head : 0);
+              copy16(q_at(i), q + i % 16 * 8, in ? 16u : 0u);
+            }
+          }
+          auto finish_queries = [&]() {
+            copy_wait_all();
+#pragma unroll 4
+            for (int i = t; i < kQRows * 16; i += kLoaders) {
+              uint4 u = fp4::lds128(q_at(i));
               float by_unit = 1.f;
-              if constexpr (BF16) fp4::to_f16(u, by_unit);
-              if (y == 0) q_unit[seg & 3][r] = by_unit;
-              *(uint4*)(raw + (smem - smem_addr(raw)) + kQueries + (y / 8) * kHalfTile + r * 128 + (((y & 7) ^ (r & 7)) << 4)) = u;
+              if constexpr (BF16) {
+                fp4::to_f16(u, by_unit);
+                fp4::sts128(q_at(i), u);
+              }
+              if (SPLIT) fp4::sts128(q_at(i + kCols * 16), u);   // one row's stand in both halves
+              if (i % 16 == 0) {
+                q_unit[seg & 3][i / 16] = by_unit;
+                if (SPLIT) q_unit[seg & 3][kCols + i / 16] = by_unit;
+              }
             }
             ++seg;
-          }
+          };
           for (int32_t v = v0; v < v1; ++v) {
-            const uint32_t scale_k = next_k, scale_v = next_v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) cur[i] = next[i];
-            if (v + 1 < v1) {
-              int32_t t;
-              uint32_t r;
-              at.visit(v + 1, t, r);
-              issue(at.kv, t, r);
-              ask_after(v + 1);
+            const uint32_t mine_of = values ? scale_v : scale_k, largest_v = fp4::largest_of(scale_v);
+            // the visit after this one: where it lies, and its scales; its codes as this one's registers fall free
+            uint32_t from = 0;
+            bool follow = v + 1 < v1;
+            if (follow) {
+              from = locate(ahead.tile, ahead.rows, scale_k, scale_v);
+              ask_for(v + 2);
             } else if (SLOTS && goes_on()) {
-              issue(next_is_row() ? 0 : at.chunk + 1 < p.chunks ? at.kv : at.kv + 1, 0, 1);
-              issued = true;
+              begin_head(next_is_row() ? 0 : at.chunk + 1 < p.chunks ? at.kv : at.kv + 1);
+              from = locate(0, 1, scale_k, scale_v);
+              follow = issued = true;
             }
-            const uint32_t largest = fp4::largest_of(scale_v), mine = values ? largest : fp4::largest_of(scale_k);
-            const uint32_t ref = max(__reduce_max_sync(~0u, mine), fp4::kLowest);
-            const uint32_t other = values ? 0 : max(__reduce_max_sync(~0u, largest), fp4::kLowest);
+            const uint32_t ref = max(__reduce_max_sync(~0u, values ? largest_v : fp4::largest_of(mine_of)), fp4::kLowest);
+            const uint32_t other = values ? 0 : max(__reduce_max_sync(~0u, largest_v), fp4::kLowest);
             if (max(ref, other) > kMaxScaleByte) bad = max(bad, (uint32_t)kErrInvalidValue);
             const uint32_t slot = n % depth;
             ok = __all_sync(~0u, wait(values ? empty_v(slot) : empty_k(slot), (n / depth & 1) ^ 1, abort, &err));
             if (!ok) break;
             if (!values && lane == 0) refs[n % kAhead][0][quarter] = (int32_t)ref, refs[n % kAhead][1][quarter] = (int32_t)other;
-            const uint32_t dst = ring + slot * kTileBytes + (uint32_t)(block >> 1) * kHalfTile;
-            const uint32_t scale = values ? scale_v : scale_k;
+            const uint32_t dst = ring + slot * kTileBytes;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int pos = quarter * 32 + i * 8 + in8;
-              const uint32_t e = __shfl_sync(~0u, scale, i * 8 + in8) >> (8 * block) & 255u;
-              const uint32_t fac = fp4::factor2(e, ref);
-              const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
+              const uint32_t fac = fp4::factor2(__shfl_sync(~0u, mine_of, i * 8 + in8) >> (8 * block) & 255u, ref);
+              const uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 uint32_t h[4];
                 from_codes(w[y], h);
-                fp4::sts128(dst + (uint32_t)pos * 128 + ((uint32_t)(((block & 1) * 4 + y) ^ in8) << 4),
+                fp4::sts128(dst + to[y] + i * 1024,
                             make_uint4(fp4::hmul2(h[0], fac), fp4::hmul2(h[1], fac), fp4::hmul2(h[2], fac), fp4::hmul2(h[3], fac)));
               }
+              if (follow) held[i] = load(from, i);
             }
-            fence_proxy_async_smem();   // this thread's writes before the products' reads
+            if (!values && v == v0) finish_queries();
+            // (the issuing warp orders these writes before the products' reads, as it does the copies')
             mbar_arrive(values ? full_v(slot) : full_k(slot));
             ++n;
           }
