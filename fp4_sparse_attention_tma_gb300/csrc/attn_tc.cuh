@@ -59,11 +59,18 @@ template <bool BF16>
 constexpr float kRaise = BF16 ? 8.f : 5.f;   // weights are at most 2^(kRaise + kShift)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOut = 256;            // first column of the accumulators, after two tiles of scores
-constexpr int kRingK = 3, kRingV = 2;     // tiles of keys and of values in shared memory
-constexpr uint32_t kKeys = 0, kValues = kKeys + kRingK * kTileBytes, kQueries = kValues + kRingV * kTileBytes,
-                   kStage = kQueries + kTileBytes;   // offsets; then room to pass sums between the halves
-constexpr int kStageRow = 17;             // floats
-constexpr int kSmemBytes = (int)kStage + 4 * kCols * kStageRow * 4 + 1024;   // the base is aligned to 1024 by hand
+// The shared memory: tiles of keys and of values, the queries, room to pass sums between the halves, and (4 bits) each
+// copying warp's codes and scales on their way.
+template <bool FP4>
+struct Memory {
+  static constexpr int kRingK = FP4 ? 2 : 3, kRingV = 2;
+  static constexpr uint32_t kKeys = 0, kValues = kKeys + kRingK * kTileBytes, kQueries = kValues + kRingV * kTileBytes,
+                            kStage = kQueries + kTileBytes;
+  static constexpr int kStageCols = FP4 ? 8 : 16, kStageRow = kStageCols + 1;   // floats
+  static constexpr uint32_t kRaw = kStage + 4 * kCols * kStageRow * 4;
+  static constexpr uint32_t kRawDepth = 2, kRawStage = 2048 + 256;   // codes of 32 positions, keys' and values' scales
+  static constexpr int kBytes = (int)(kRaw + (FP4 ? 8 * kRawDepth * kRawStage : 0)) + 1024;   // the base is aligned to 1024 by hand
+};
 
 // D += A B^T with both operands in shared memory, or A in tensor memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -345,13 +352,16 @@ template <bool BF16, int NB, bool SLOTS, bool FP4>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr bool MB = BF16 && !FP4;         // the matrices' type: bf16, or fp16
+  using M = Memory<FP4>;
+  constexpr int kRingK = M::kRingK, kRingV = M::kRingV;
+  constexpr uint32_t kKeys = M::kKeys, kValues = M::kValues, kQueries = M::kQueries;
   constexpr bool SPLIT = NB == 1;           // one row: either half of the matrix takes half of a tile's positions
   constexpr int kSoft = 256;                // softmax threads
 
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ uint32_t err, tmem_base;
   __shared__ int abort_flag;
-  __shared__ __align__(8) uint64_t bars[2 * kRingK + 2 * kRingV + 1 + 3 * 2 + 1];
+  __shared__ __align__(8) uint64_t bars[2 * kRingK + 2 * kRingV + 1 + 3 * 2 + 2];
   __shared__ float2 half_ml[2][kCols];      // (one row) reference and sum of either half, -1 where nothing was seen
   __shared__ float row_max[2][2][128];      // by visit and warpgroup
   __shared__ float row_sum[2][128];         // by warpgroup, -1 where nothing was seen
@@ -368,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   auto full_v = [&](uint32_t i) { return bar0 + 8 * (2 * kRingK + i); };
   auto empty_v = [&](uint32_t i) { return bar0 + 8 * (2 * kRingK + kRingV + i); };
   constexpr uint32_t kRest = 2 * kRingK + 2 * kRingV;
-  const uint32_t empty_q = bar0 + 8 * kRest, drain = bar0 + 8 * (kRest + 7);
+  const uint32_t empty_q = bar0 + 8 * kRest, drain = bar0 + 8 * (kRest + 7), full_q = bar0 + 8 * (kRest + 8);
   // by tile of scores (visits take them in turn):
   auto full_s = [&](uint32_t b) { return bar0 + 8 * (kRest + 1 + b); };    // scores are there
   auto full_p = [&](uint32_t b) { return bar0 + 8 * (kRest + 3 + b); };    // weights are there
@@ -381,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     for (int i = 0; i < kRingK; ++i) mbar_init(full_k(i), kLoaders), mbar_init(empty_k(i), 1);
     for (int i = 0; i < kRingV; ++i) mbar_init(full_v(i), kLoaders), mbar_init(empty_v(i), 1);
     mbar_init(empty_q, 1);
+    mbar_init(full_q, 64);
     for (int b = 0; b < 2; ++b) mbar_init(full_s(b), FP4 ? 2 : 1), mbar_init(full_p(b), kSoft), mbar_init(done_pv(b), 1);
     mbar_init(drain, 2);
     fence_mbar_init();
@@ -403,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     int64_t end;   // of the CTA's range, counted from the unit's first visit
   };
   __shared__ Place places[kWarps];
+  __shared__ Place asking[FP4 ? 8 : 1];   // (4 bits) of the copying warps: what they copy, ahead
   __shared__ Split split;
   __shared__ Rows meta;
   Walk<NB, SLOTS>& at = places[warp].at;
@@ -728,14 +740,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         };
         if constexpr (SPLIT) {
           // each half finishes 64 columns, 32 a thread; the other half's share of them comes through shared
-          // memory, 16 at a time
-          float* stage = (float*)(raw + (smem - smem_addr(raw)) + kStage);
-          float* give = stage + ((part_of * 2 + g) * kCols + col) * kStageRow;
-          const float* take = stage + (((part_of ^ 1) * 2 + g) * kCols + col) * kStageRow;
+          // memory, some at a time
+          constexpr int kSome = M::kStageCols;
+          float* stage = (float*)(raw + (smem - smem_addr(raw)) + M::kStage);
+          float* give = stage + ((part_of * 2 + g) * kCols + col) * M::kStageRow;
+          const float* take = stage + (((part_of ^ 1) * 2 + g) * kCols + col) * M::kStageRow;
 #pragma unroll 1
-          for (int at_col = 0; at_col < 32; at_col += 16) {
+          for (int at_col = 0; at_col < 32; at_col += kSome) {
 #pragma unroll 1
-            for (int c = 0; c < 16; c += 8) {
+            for (int c = 0; c < kSome; c += 8) {
               float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
               if (has) tmem_load8(out_a + (part_of ^ 1) * 64 + g * 32 + at_col + c, r);
 #pragma unroll
@@ -743,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
             bar_sync(kAll, kSoft);
 #pragma unroll 1
-            for (int c = 0; c < 16; c += 8) {
+            for (int c = 0; c < kSome; c += 8) {
               float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
               if (has) tmem_load8(out_a + part_of * 64 + g * 32 + at_col + c, r);
 #pragma unroll
@@ -799,145 +812,112 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           entry = i < p.max_pages ? list[i] : -1;
         }
       };
-      if constexpr (SLOTS) ask(p.slots + (int64_t)at.row0 * p.n_slots, at.s);
+      if constexpr (SLOTS && !FP4) ask(p.slots + (int64_t)at.row0 * p.n_slots, at.s);
       bool more = true;
       if constexpr (FP4) {
         // Codes are unpacked on their way: 32 positions a warp, a lane 32 elements (a block) of one of 8 positions at a
-        // time.  Loaded a visit ahead into registers, times their scales over the largest of the warp's 32 positions
-        // (attn_fp4.cuh) into the tile; K's warps also publish both references.  Positions that the rows do not see have
-        // the scale 0 and the codes of some other position: their scores are not used and their weights are 0.
+        // time.  Each warp copies its positions' codes and scales into a small ring of its own, two visits ahead, over the
+        // ends of segments, and unpacks them, times their scales over the largest of the 32 positions (attn_fp4.cuh), into
+        // the tile; K's warps also publish both references.  Positions that the rows do not see have the scale 0 and the
+        // codes of some other position: their scores are not used and their weights are 0.
         const uint8_t* codes = (const uint8_t*)cache;
         const int block = lane >> 3, in8 = lane & 7;
-        uint4 held[4];                     // codes of the next visit to unpack
-        uint32_t scale_k = 0, scale_v = 0;   // scales of this lane's position in it: keys' (K's warps) and values'
         const uint32_t ksp = (uint32_t)p.ks_page, kss = (uint32_t)p.ks_slot, vsp = (uint32_t)p.vs_page, vss = (uint32_t)p.vs_slot;
+        constexpr uint32_t kRaw = M::kRaw, kRawDepth = M::kRawDepth, kRawStage = M::kRawStage;
+        const uint32_t mine = smem + kRaw + (uint32_t)(warp - 8) * (kRawDepth * kRawStage);
         uint32_t to[4];                    // places of a block's four 16-byte pieces, in a tile
 #pragma unroll
         for (int y = 0; y < 4; ++y)
           to[y] = (uint32_t)(block >> 1) * kHalfTile + (uint32_t)(quarter * 32 + in8) * 128 +
                   ((uint32_t)(((block & 1) * 4 + y) ^ in8) << 4);
-        // the visit whose entry is there: where this lane's position lies, and its scales (asked for)
+        // position i * 8 + r of the ring: 64 bytes, pieces swizzled so that 8 positions' same piece meets no bank twice
+        const uint32_t copy_to = (uint32_t)(lane >> 2) * 64 + (((uint32_t)lane ^ (uint32_t)(lane >> 3)) & 3u) * 16;
+        const uint32_t take_from = (uint32_t)in8 * 64 + (uint32_t)(block ^ (in8 >> 1)) * 16;
+        // ---- copies: a walk of their own, ahead of the unpacking ----
+        Place& ask_at = asking[warp - 8];
+        if (lane == 0) ask_at = places[warp];
+        __syncwarp();
+        Steps<NB, SLOTS> ahead;            // the visit whose entry is asked for
+        int32_t ask_v, ask_left;           // its number in its segment, and the visits from it to the end; 0: all done
+        const int32_t* list;
         const uint8_t *base, *ks_head = nullptr, *vs_head;   // of the head
-        auto begin_head = [&](int32_t kv) {
-          base = codes + kv * s_head + block * 16;
-          if (!values) ks_head = p.k_scale + kv * p.ks_head;
-          vs_head = p.v_scale + kv * p.vs_head;
-        };
-        auto locate = [&](int32_t tile, uint32_t rows, uint32_t& next_k, uint32_t& next_v) {
-          bool on;
-          uint32_t page, off;
+        auto begin_asking = [&]() {
+          const Walk<NB, SLOTS>& f = ask_at.at;
+          ask_v = f.s;
+          ask_left = (int32_t)min((int64_t)f.nsub, ask_at.end) - f.s;
+          base = codes + f.kv * s_head + (lane & 3) * 16;
+          if (!values) ks_head = p.k_scale + f.kv * p.ks_head;
+          vs_head = p.v_scale + f.kv * p.vs_head;
           if constexpr (SLOTS) {
-            on = entry >= 0 && entry < p.num_pages * kPage;
-            if (!on && entry != -1) bad = max(bad, (uint32_t)kErrInvalidPage);
-            page = (uint32_t)entry / kPage, off = (uint32_t)entry % kPage;
-          } else {
-            int32_t lo = 0, hi = INT32_MAX;   // seen by every row of the visit
-            const int32_t first = tile * kPos + quarter * 32;
-            if (NB == 1 || rows != 3) {
-#pragma unroll
-              for (int j = 0; j < NB; ++j)
-                if (rows >> j & 1) lo = max(lo, at.a[j]), hi = min(hi, at.b[j]);
-            }
-            const bool any = first < hi && first + 32 > lo, there = entry >= 0 && entry < p.num_pages;
-            if (any && !there) bad = max(bad, (uint32_t)kErrInvalidPage);
-            on = there && first + lane >= lo && first + lane < hi;
-            page = (uint32_t)entry, off = (uint32_t)((quarter & 1) * 32 + lane);
-          }
-          next_k = next_v = 0;
-          if (on) {
-            if (!values) next_k = *(const uint32_t*)(ks_head + (uint32_t)(page * ksp + off * kss));
-            next_v = *(const uint32_t*)(vs_head + (uint32_t)(page * vsp + off * vss));
-          }
-          return on ? page * page16 + off * slot16 : 0u;
-        };
-        auto load = [&](uint32_t from, int i) {
-          return *(const uint4*)(base + (uint64_t)__shfl_sync(~0u, from, i * 8 + in8) * 16);
-        };
-        bool issued = false;
-        while (more) {
-          const int32_t v0 = at.s, v1 = segment_end();
-          const int32_t* list;
-          Steps<NB, SLOTS> ahead;            // of the visit whose entry is asked for
-          ahead.start(at, v0);
-          if constexpr (SLOTS) {
-            list = p.slots + (int64_t)at.row0 * p.n_slots;
-            if (warp == 12 && at.row0 + 1 < p.rows)
+            list = p.slots + (int64_t)f.row0 * p.n_slots;
+            if (warp == 12 && f.row0 + 1 < p.rows)
               for (int32_t i = lane * 32; i < p.n_slots; i += 32 * 32)
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(list + p.n_slots + i));
           } else {
-            list = p.page_table + (int64_t)at.req * p.max_pages;
-            ask(list, ahead.tile);
+            list = p.page_table + (int64_t)f.req * p.max_pages;
           }
-          // on to visit v's entry (past the segment's end: the next unit's first, of this row or of the next)
-          auto ask_for = [&](int32_t v) {
-            if (v < v1) {
-              ahead.next(at, v);
-              ask(list, ahead.tile);
-            } else if (SLOTS && goes_on()) {
-              ask(list + (next_is_row() ? p.n_slots : 0), 0);
-            }
-          };
-          if (!issued) {
-            begin_head(at.kv);
-            const uint32_t from = locate(ahead.tile, ahead.rows, scale_k, scale_v);
+          ahead.start(f, ask_v);
+          ask(list, ahead.tile);
+        };
+        begin_asking();
+        // the visit whose entry is there, into stage x of the ring; on to the next entry
+        auto fetch = [&](uint32_t x) {
+          if (ask_left > 0) {
+            bool on;
+            uint32_t page, off;
+            if constexpr (SLOTS) {
+              on = entry >= 0 && entry < p.num_pages * kPage;
+              if (!on && entry != -1) bad = max(bad, (uint32_t)kErrInvalidPage);
+              page = (uint32_t)entry / kPage, off = (uint32_t)entry % kPage;
+            } else {
+              int32_t lo = 0, hi = INT32_MAX;   // seen by every row of the visit
+              const int32_t first = ahead.tile * kPos + quarter * 32;
+              if (NB == 1 || ahead.rows != 3) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) held[i] = load(from, i);
-          }
-          issued = false;
-          ask_for(v0 + 1);
-          // the queries, with the segment's first tile of keys: 16 lanes a row, copied while that is unpacked, then brought
-          // to fp16 where they lie
-          constexpr int kQRows = SPLIT ? kCols : 128;
-          auto q_at = [&](int i) {
-            const int r = i / 16, y = i % 16;
-            return smem + kQueries + (y / 8) * kHalfTile + r * 128 + (((y & 7) ^ (r & 7)) << 4);
-          };
-          if (!values) {
-            ok = __all_sync(~0u, wait(empty_q, (seg & 1) ^ 1, abort, &err));
-            if (!ok) break;
-            const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
-            const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
-#pragma unroll 4
-            for (int i = t; i < kQRows * 16; i += kLoaders) {
-              const int r = i / 16, j = SPLIT ? 0 : r / kCols, h = r % kCols;
-              const bool in = at.b[j] > at.a[j] && h < heads;
-              const T* q = (const T*)p.q + (in ? (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head : 0);
-              copy16(q_at(i), q + i % 16 * 8, in ? 16u : 0u);
-            }
-          }
-          auto finish_queries = [&]() {
-            copy_wait_all();
-#pragma unroll 4
-            for (int i = t; i < kQRows * 16; i += kLoaders) {
-              uint4 u = fp4::lds128(q_at(i));
-              float by_unit = 1.f;
-              if constexpr (BF16) {
-                fp4::to_f16(u, by_unit);
-                fp4::sts128(q_at(i), u);
+                for (int j = 0; j < NB; ++j)
+                  if (ahead.rows >> j & 1) lo = max(lo, ask_at.at.a[j]), hi = min(hi, ask_at.at.b[j]);
               }
-              if (SPLIT) fp4::sts128(q_at(i + kCols * 16), u);   // one row's stand in both halves
-              if (i % 16 == 0) {
-                q_unit[seg & 3][i / 16] = by_unit;
-                if (SPLIT) q_unit[seg & 3][kCols + i / 16] = by_unit;
+              const bool any = first < hi && first + 32 > lo, there = entry >= 0 && entry < p.num_pages;
+              if (any && !there) bad = max(bad, (uint32_t)kErrInvalidPage);
+              on = there && first + lane >= lo && first + lane < hi;
+              page = (uint32_t)entry, off = (uint32_t)((quarter & 1) * 32 + lane);
+            }
+            const uint32_t dst = mine + x * kRawStage, from = on ? page * page16 + off * slot16 : 0u;
+            if (!values) copy4(dst + 2048 + lane * 4, ks_head + (on ? page * ksp + off * kss : 0u), on ? 4u : 0u);
+            copy4(dst + 2176 + lane * 4, vs_head + (on ? page * vsp + off * vss : 0u), on ? 4u : 0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              copy16(dst + copy_to + i * 512, base + (uint64_t)__shfl_sync(~0u, from, i * 8 + (lane >> 2)) * 16, 16u);
+            if (--ask_left > 0) {
+              ahead.next(ask_at.at, ++ask_v);
+              ask(list, ahead.tile);
+            } else {
+              __syncwarp();
+              const int64_t rest = ask_at.end - ask_at.at.nsub - kUnitCost;
+              __syncwarp();
+              if (lane == 0) {
+                ask_at.end = rest;
+                if (rest > 0) ask_at.at.next_unit(p, meta);
               }
+              __syncwarp();
+              if (rest > 0) begin_asking();
             }
-            ++seg;
-          };
-          for (int32_t v = v0; v < v1; ++v) {
-            const uint32_t mine_of = values ? scale_v : scale_k, largest_v = fp4::largest_of(scale_v);
-            // the visit after this one: where it lies, and its scales; its codes as this one's registers fall free
-            uint32_t from = 0;
-            bool follow = v + 1 < v1;
-            if (follow) {
-              from = locate(ahead.tile, ahead.rows, scale_k, scale_v);
-              ask_for(v + 2);
-            } else if (SLOTS && goes_on()) {
-              begin_head(next_is_row() ? 0 : at.chunk + 1 < p.chunks ? at.kv : at.kv + 1);
-              from = locate(0, 1, scale_k, scale_v);
-              follow = issued = true;
-            }
-            const uint32_t ref = max(__reduce_max_sync(~0u, values ? largest_v : fp4::largest_of(mine_of)), fp4::kLowest);
-            const uint32_t other = values ? 0 : max(__reduce_max_sync(~0u, largest_v), fp4::kLowest);
+          }
+          copy_commit();
+        };
+#pragma unroll
+        for (uint32_t x = 0; x < kRawDepth; ++x) fetch(x);
+        // ---- unpacking ----
+        while (more) {
+          const int32_t v1 = segment_end();
+          for (int32_t v = at.s; v < v1; ++v) {
+            copy_wait<kRawDepth - 1>();
+            __syncwarp();
+            const uint32_t x = n % kRawDepth, src = mine + x * kRawStage;
+            const uint32_t scale_v = fp4::lds32(src + 2176 + lane * 4);
+            const uint32_t scales = values ? scale_v : fp4::lds32(src + 2048 + lane * 4);
+            const uint32_t ref = max(__reduce_max_sync(~0u, fp4::largest_of(scales)), fp4::kLowest);
+            const uint32_t other = values ? 0 : max(__reduce_max_sync(~0u, fp4::largest_of(scale_v)), fp4::kLowest);
             if (max(ref, other) > kMaxScaleByte) bad = max(bad, (uint32_t)kErrInvalidValue);
             const uint32_t slot = n % depth;
             ok = __all_sync(~0u, wait(values ? empty_v(slot) : empty_k(slot), (n / depth & 1) ^ 1, abort, &err));
@@ -946,8 +926,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const uint32_t dst = ring + slot * kTileBytes;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t fac = fp4::factor2(__shfl_sync(~0u, mine_of, i * 8 + in8) >> (8 * block) & 255u, ref);
-              const uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
+              const uint4 u = fp4::lds128(src + take_from + i * 512);
+              const uint32_t fac = fp4::factor2(__shfl_sync(~0u, scales, i * 8 + in8) >> (8 * block) & 255u, ref);
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 uint32_t h[4];
@@ -955,11 +936,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 fp4::sts128(dst + to[y] + i * 1024,
                             make_uint4(fp4::hmul2(h[0], fac), fp4::hmul2(h[1], fac), fp4::hmul2(h[2], fac), fp4::hmul2(h[3], fac)));
               }
-              if (follow) held[i] = load(from, i);
             }
-            if (!values && v == v0) finish_queries();
             // (the issuing warp orders these writes before the products' reads, as it does the copies')
             mbar_arrive(values ? full_v(slot) : full_k(slot));
+            __syncwarp();   // every lane has read the stage
+            fetch(x);
             ++n;
           }
           if (!ok) break;
@@ -1062,10 +1043,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       // ----------------------------------------------------- scores' products ----
       constexpr uint32_t kQK = idesc_f16<MB>(128, kPos, false);
       const uint64_t q = desc128(smem + kQueries, 16, 1024);
-      uint32_t n = 0;
+      uint32_t n = 0, seg = 0;
       bool ok = true, more = true;
       while (more) {
         const int32_t v1 = segment_end();
+        if constexpr (FP4) {
+          ok = __all_sync(~0u, wait(full_q, seg++ & 1, abort, &err));
+          if (!ok) break;
+        }
         for (int32_t v = at.s; v < v1; ++v, ++n) {
           const uint32_t slot = n % kRingK, b = n & 1;
           ok = __all_sync(~0u, wait(full_k(slot), n / kRingK & 1, abort, &err));
@@ -1128,6 +1113,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (!ok) break;
         more = next_segment();
       }
+      } else if constexpr (FP4) {
+      // ------------------------------------- queries, a segment ahead of the products ----
+      // 16 lanes a row, brought to fp16's range; one row's stand in both halves
+      constexpr int kQRows = SPLIT ? kCols : 128, U = 8;
+      const int t = threadIdx.x & 63;
+      uint32_t seg = 0;
+      bool ok = true, more = true;
+      while (more) {
+        const int32_t h0 = at.kv * p.group + at.chunk * p.chunk_heads;
+        const int32_t heads = min(p.chunk_heads, p.group - at.chunk * p.chunk_heads);
+        for (int i0 = t; i0 < kQRows * 16; i0 += U * 64) {
+          uint4 u[U];
+#pragma unroll
+          for (int x = 0; x < U; ++x) {
+            const int i = i0 + x * 64, r = i / 16, j = SPLIT ? 0 : r / kCols, h = r % kCols;
+            u[x] = make_uint4(0, 0, 0, 0);
+            if (at.b[j] > at.a[j] && h < heads)
+              u[x] = *(const uint4*)((const T*)p.q + (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head + i % 16 * 8);
+          }
+          if (i0 == t) ok = __all_sync(~0u, wait(empty_q, (seg & 1) ^ 1, abort, &err));
+          if (!ok) break;
+#pragma unroll
+          for (int x = 0; x < U; ++x) {
+            const int i = i0 + x * 64, r = i / 16, y = i % 16;
+            float by_unit = 1.f;
+            if constexpr (BF16) fp4::to_f16(u[x], by_unit);
+            const uint32_t dst = smem + kQueries + (y / 8) * kHalfTile + r * 128 + (((y & 7) ^ (r & 7)) << 4);
+            fp4::sts128(dst, u[x]);
+            if (SPLIT) fp4::sts128(dst + kCols * 128, u[x]);
+            if (y == 0) {
+              q_unit[seg & 3][r] = by_unit;
+              if (SPLIT) q_unit[seg & 3][kCols + r] = by_unit;
+            }
+          }
+        }
+        if (!ok) break;
+        mbar_arrive(full_q);
+        ++seg;
+        more = next_segment();
+      }
       }
     }
   }
@@ -1163,9 +1188,9 @@ template <bool BF16, int NB, bool SLOTS, bool FP4>
 cudaError_t launch(const AttnParams& p, int sm_count, cudaStream_t stream) {
   auto* kernel = attn_tc_kernel<BF16, NB, SLOTS, FP4>;
   static std::atomic<bool> done[64];
-  cudaError_t e = set_smem_once(kernel, kSmemBytes, done);
+  cudaError_t e = set_smem_once(kernel, Memory<FP4>::kBytes, done);
   if (e != cudaSuccess) return e;
-  kernel<<<sm_count, kThreads, kSmemBytes, stream>>>(p);
+  kernel<<<sm_count, kThreads, Memory<FP4>::kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
