@@ -18,7 +18,6 @@
 namespace idxk {
 namespace {
 
-constexpr int kMaxThreads = 1024;
 constexpr int kBitmapBytes = 128 * 1024;
 constexpr int kGatherThreads = 256;
 
@@ -50,6 +49,16 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16-byte asynchronous copy; bytes = 0 writes zeros and reads nothing.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void commit_async() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_async() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // A sum held as a rounded part and what the roundings left (TwoSum, Knuth): the sum of a head's squares
@@ -117,52 +126,139 @@ __device__ uint32_t check_rows(const AppendParams& p, uint32_t* table) {
   return err;
 }
 
+// The lane's dimensions of a head: two groups of 4, at pa and pb.  A head that stays in 16 bits and is rotated half by half:
+// a group of either half, so that the pairs lie within the lane; else 8 in a row (the 4-bit form's blocks are 4 lanes).
+struct Dims {
+  int pa, pb, j;        // j: the first of the lane's 4 angles, -1: none
+  __device__ Dims(int in, int rot, int first, bool halves) {
+    const int d0 = in * 8;
+    pa = d0, pb = d0 + 4, j = -1;
+    if (rot == 0) return;
+    if (!halves) {
+      if (d0 >= first && d0 < first + rot) j = (d0 - first) / 2;
+    } else if (in < rot / 8) {
+      pa = first + in * 4, pb = pa + rot / 2, j = in * 4;
+    } else {
+      pa = d0 - rot, pa += pa < first ? 0 : rot, pb = pa + 4;
+    }
+  }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void unpack4(const uint2& u, float* x) {
+  const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (BF16) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*(const __half2*)&w[i]);
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+}
+
 // A warp takes U x 32 / (D / 8) heads of a row at a time: 16 bytes of a head a lane, D / 8 lanes a head.
 // Bound by HBM where rows are many, by the chain position, page entry, store and one launch where they are
 // few.
+template <bool FP4, int U>
+constexpr int kMaxThreads = FP4 || U == 1 ? 512 : 768;   // of a CTA
+template <int U>
+constexpr int kStages = U == 1 ? 1 : 2;                  // chunks that a warp has on their way
+template <bool FP4, int U>
+constexpr int kRingBytes = kMaxThreads<FP4, U> / 32 * kStages<U> * U * 512;
+
+// Pairs of fp32 numbers, and operations on both at once.
+using Two = uint64_t;
+__device__ __forceinline__ Two two(float x, float y) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 both(Two a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 template <bool BF16, int D, bool FP4, int U>
-__global__ void __launch_bounds__(kMaxThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kMaxThreads<FP4, U>, 1) append_kernel(const __grid_constant__ AppendParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr int L = D / 8;            // lanes of a head
   constexpr int H = 32 / L;           // heads that the warp has in its lanes
   constexpr int HEADS = U * H;        // of a chunk
-  extern __shared__ uint32_t table[];
+  constexpr int STAGES = kStages<U>;
+  extern __shared__ __align__(128) unsigned char shared[];
   const int lane = threadIdx.x & 31, in = lane % L, sub = lane / L;
   const int warps = blockDim.x >> 5;
   const int32_t qc = p.q.data ? (p.q_heads + HEADS - 1) / HEADS : 0, kc = (p.kv_heads + HEADS - 1) / HEADS;
   const int32_t per_row = qc + kc + (p.v.data ? kc : 0);
-  const uint32_t chunks = (uint32_t)p.rows * per_row, stride = gridDim.x * warps;   // (below 2^31 and 2^13)
-  const int d0 = in * 8;
+  const uint32_t chunks = (uint32_t)p.rows * per_row, workers = gridDim.x * warps;   // (below 2^31 and 2^13)
+  const bool halves = p.rope && !p.pairs;
+  const Dims wide(in, p.rot, p.first, halves), flat(in, p.rot, p.first, false);
 
-  uint32_t c = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-  int32_t row = 0, h0 = 0, heads = 0, pos = -1;
-  int kind = 0;                       // 0 query, 1 key, 2 value
-  uint4 raw[U];
-  auto fetch = [&]() {
-    if (c >= chunks) return;
-    row = (int32_t)(c / (uint32_t)per_row);
-    int32_t i = (int32_t)c - row * per_row;
-    kind = i < qc ? 0 : i < qc + kc ? 1 : 2;
-    i -= kind == 0 ? 0 : kind == 1 ? qc : qc + kc;
-    h0 = i * HEADS;
-    heads = kind == 0 ? p.q_heads : p.kv_heads;
-    const HeadsIn& x = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-    pos = p.row_pos[row];
-    const T* from = (const T*)x.data + row * x.row + d0;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t h = h0 + u * H + sub;
-      raw[u] = h < heads ? __ldcs((const uint4*)(from + h * x.head)) : make_uint4(0, 0, 0, 0);
-    }
+  // A warp's chunks follow one another: chunk `i` of a row, its heads h0 .. of kind 0 query, 1 key, 2 value.
+  struct Chunk {
+    int32_t row, i;
   };
-  fetch();
-  const uint32_t err = check_rows(p, table);
+  auto kind_of = [&](const Chunk& x) { return x.i < qc ? 0 : x.i < qc + kc ? 1 : 2; };
+  auto first_head = [&](const Chunk& x, int kind) { return (x.i - (kind == 0 ? 0 : kind == 1 ? qc : qc + kc)) * HEADS; };
+  auto advance = [&](Chunk& x) {
+    if (++x.i == per_row) x.i = 0, ++x.row;
+  };
+  // The warp's ring: a chunk's heads one after another as they are.
+  unsigned char* ring = shared + (size_t)p.table_bytes + (threadIdx.x >> 5) * (STAGES * U * 512);
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  uint32_t to_fetch = 0, left = 0;   // chunks
+  Chunk ahead{}, at_chunk{};
+  auto fetch = [&](int stage) {
+    if (to_fetch > 0) {
+      --to_fetch;
+      const int kind = kind_of(ahead);
+      const int32_t h = first_head(ahead, kind) + sub, heads = kind == 0 ? p.q_heads : p.kv_heads;
+      const HeadsIn& x = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+      const T* from = (const T*)x.data + ahead.row * x.row + h * x.head + in * 8;
+      const int64_t step = H * x.head;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool on = h + u * H < heads;
+        copy_async(ring_at + (uint32_t)((stage * U + u) * 512 + lane * 16), on ? from + u * step : (const T*)x.data, on ? 16u : 0u);
+      }
+      advance(ahead);
+    }
+    commit_async();
+  };
+  {
+    // consecutive warps on different SMs
+    const uint32_t w = (threadIdx.x >> 5) * gridDim.x + blockIdx.x, per = chunks / workers, more = chunks - per * workers;
+    const uint32_t c = w * per + min(w, more);
+    left = to_fetch = per + (w < more ? 1 : 0);
+    ahead.row = (int32_t)(c / (uint32_t)per_row);
+    ahead.i = (int32_t)c - ahead.row * per_row;
+    at_chunk = ahead;
+  }
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) fetch(i);
+  int32_t pos = -1, next_pos = left > 0 ? p.row_pos[at_chunk.row] : -1;
+  const uint32_t err = check_rows(p, (uint32_t*)shared);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status_out = err;
   if (err != kOk) {
     // nothing was written; queries that have a place of their own become NaN
+    wait_async<0>();
     if (!p.out_q || p.q_in_place) return;
     const int64_t n = (int64_t)p.rows * p.q_heads;
-    for (int64_t i = (int64_t)blockIdx.x * warps + (threadIdx.x >> 5); i < n; i += stride) {
+    for (int64_t i = (int64_t)blockIdx.x * warps + (threadIdx.x >> 5); i < n; i += workers) {
       const int64_t r = i / p.q_heads, h = i - r * p.q_heads;
       if (p.out_q_scale) {
         for (int j = lane; j < D / 2; j += 32) ((uint8_t*)p.out_q)[r * p.oq_row + h * p.oq_head + j] = 0;
@@ -174,128 +270,251 @@ __global__ void __launch_bounds__(kMaxThreads) append_kernel(const __grid_consta
     return;
   }
 
-  for (; c < chunks; c += stride, fetch()) {
+  int stage = 0;
+  int64_t k_at = 0, v_at = 0, ks_at = 0, vs_at = 0;   // the row's slot
+  for (bool fresh = true; left > 0; --left, fetch(stage), stage = stage == STAGES - 1 ? 0 : stage + 1) {
+    const Chunk chunk = at_chunk;
+    advance(at_chunk);
+    const int32_t row = chunk.row;
+    if (fresh) {
+      pos = next_pos;
+      next_pos = row + 1 < p.rows ? p.row_pos[row + 1] : -1;
+      if (pos >= 0) {
+        const int64_t page = p.page_table[(int64_t)p.row_req[row] * p.max_pages + pos / kPage];
+        const int32_t off = pos % kPage;
+        k_at = page * p.k_dst.page + off * p.k_dst.slot, v_at = page * p.v_dst.page + off * p.v_dst.slot;
+        if (FP4) ks_at = page * p.k_dst.s_page + off * p.k_dst.s_slot, vs_at = page * p.v_dst.s_page + off * p.v_dst.s_slot;
+      }
+    }
+    fresh = at_chunk.i == 0;
+    const int kind = kind_of(chunk);
+    const int32_t h0 = first_head(chunk, kind), heads = kind == 0 ? p.q_heads : p.kv_heads;
+    const bool four = FP4 && (kind > 0 || p.out_q_scale);   // becomes codes
+    wait_async<STAGES - 1>();
+    __syncwarp();
     if (pos < 0) continue;            // a row that is not there
     const void* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-    float w[8];
-    if (weight) {
-      if (p.weight_f32) {
-        *(float4*)&w[0] = *(const float4*)((const float*)weight + d0);
-        *(float4*)&w[4] = *(const float4*)((const float*)weight + d0 + 4);
-      } else {
-        unpack8<BF16>(*(const uint4*)((const T*)weight + d0), w);
-      }
-    }
-    // the angles of this lane's dimensions: 4 pairs of neighbours, or 8 of a half
-    const bool turn = p.rope && kind < 2, mine = turn && d0 >= p.first && d0 < p.first + p.rot;
-    const int half = p.rot / 2;
-    bool upper = false;
-    int partner = lane;
-    float co[8], si[8];
-    if (mine) {
-      const float* t = p.rope + (int64_t)pos * p.rot;
-      int j = d0 - p.first;
-      if (p.pairs) {
-        j /= 2;
-        *(float4*)&co[0] = *(const float4*)(t + j);
-        *(float4*)&si[0] = *(const float4*)(t + half + j);
-      } else {
-        upper = j >= half;
-        partner = upper ? lane - half / 8 : lane + half / 8;
-        if (upper) j -= half;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          *(float4*)&co[i] = *(const float4*)(t + j + i);
-          *(float4*)&si[i] = *(const float4*)(t + half + j + i);
-        }
-      }
-    }
+    const bool apart = halves && kind < 2 && !four;
+    const int pa = apart ? wide.pa : flat.pa, pb = apart ? wide.pb : flat.pb, j = apart ? wide.j : flat.j;
+    // this lane's elements of the chunk's heads
+    const unsigned char* mine = ring + stage * (U * 512) + sub * (L * 16);
     const PagedOut& dst = kind == 1 ? p.k_dst : p.v_dst;
-    int64_t at = 0, s_at = 0;
-    if (kind == 0) {
-      at = row * p.oq_row, s_at = row * p.oqs_row;
-    } else {
-      const int64_t page = p.page_table[(int64_t)p.row_req[row] * p.max_pages + pos / kPage];
-      at = page * dst.page + pos % kPage * dst.slot;
-      s_at = page * dst.s_page + pos % kPage * dst.s_slot;
-    }
+    const int64_t at = kind == 0 ? row * p.oq_row : kind == 1 ? k_at : v_at;
+    const int64_t s_at = kind == 0 ? row * p.oqs_row : kind == 1 ? ks_at : vs_at;
+    const int64_t head = kind == 0 ? p.oq_head : dst.head;
+    if (!four) {
+      // ---- 16 bits: sums in fp32, one rounding at the end ----
+      T* to = (T*)(kind == 0 ? p.out_q : dst.data) + at + (int64_t)(h0 + sub) * head;
+      T *ta = to + pa, *tb = to + pb;
+      const int64_t step = H * head;
+      if (kind == 2) {                // a copy
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int32_t h = h0 + u * H + sub;
-      const bool on = h < heads;
-      if (h0 + u * H >= heads) break;   // (the same for the whole warp)
-      if (!FP4 && kind == 2) {          // a copy
-        if (on) *(uint4*)((T*)dst.data + at + h * dst.head + d0) = raw[u];
+        for (int u = 0; u < U; ++u)
+          if (h0 + u * H + sub < heads) *(uint4*)(ta + u * step) = *(const uint4*)(mine + u * 512 + pa * 2);
         continue;
       }
-      float x[8];
-      unpack8<BF16>(raw[u], x);
-      if (weight) {
-        float s = 0.f, rest = 0.f;      // squares of 16-bit numbers are exact in fp32
-#pragma unroll
-        for (int i = 0; i < 8; ++i) add_exactly(s, rest, __fmul_rn(x[i], x[i]));
-#pragma unroll
-        for (int o = 1; o < L; o <<= 1) {
-          const float s1 = __shfl_xor_sync(~0u, s, o), r1 = __shfl_xor_sync(~0u, rest, o);
-          rest = __fadd_rn(rest, r1);
-          float r2 = 0.f;
-          add_exactly(s, r2, s1);
-          rest = __fadd_rn(rest, r2);
-        }
-        const float sum = fabsf(s) < INFINITY ? __fadd_rn(s, rest) : s;
-        const float r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(sum / D, p.eps)));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
-      }
-      if (turn) {
-        if (p.pairs) {
-          if (mine) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = x[2 * i], b = x[2 * i + 1];
-              x[2 * i] = __fsub_rn(__fmul_rn(a, co[i]), __fmul_rn(b, si[i]));
-              x[2 * i + 1] = __fadd_rn(__fmul_rn(b, co[i]), __fmul_rn(a, si[i]));
-            }
-          }
+      // Pairs: of dimensions that are turned alike, (0, 1), (2, 3) and their partners (4, 5), (6, 7) where those lie in the
+      // other group, else (0, 2) and (1, 3), (4, 6) and (5, 7).
+      auto pairs = [&](const float (&x)[8], Two (&t)[4]) {
+        if (apart) {
+          t[0] = two(x[0], x[1]), t[1] = two(x[2], x[3]), t[2] = two(x[4], x[5]), t[3] = two(x[6], x[7]);
         } else {
+          t[0] = two(x[0], x[2]), t[1] = two(x[4], x[6]), t[2] = two(x[1], x[3]), t[3] = two(x[5], x[7]);
+        }
+      };
+      Two w[4], co[2], si[2], minus[2];
+      if (weight) {
+        float y[8];
+        if (p.weight_f32) {
+          *(float4*)&y[0] = *(const float4*)((const float*)weight + pa);
+          *(float4*)&y[4] = *(const float4*)((const float*)weight + pb);
+        } else {
+          unpack4<BF16>(*(const uint2*)((const T*)weight + pa), &y[0]);
+          unpack4<BF16>(*(const uint2*)((const T*)weight + pb), &y[4]);
+        }
+        pairs(y, w);
+      }
+      if (j >= 0) {
+        const float* t = p.rope + (int64_t)pos * p.rot + j;
+        const float4 x = *(const float4*)t, y = *(const float4*)(t + p.rot / 2);
+        co[0] = two(x.x, x.y), co[1] = two(x.z, x.w), si[0] = two(y.x, y.y), si[1] = two(y.z, y.w);
+        minus[0] = two(-y.x, -y.y), minus[1] = two(-y.z, -y.w);
+      }
+      // (the branches outside the loop over the heads)
+      auto heads_of = [&](auto normed, auto lies_apart, auto full) {
+        constexpr bool NORM = decltype(normed)::value, APART = decltype(lies_apart)::value, FULL = decltype(full)::value;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(~0u, x[i], partner);
-            if (mine) {
-              const float cross = __fmul_rn(o, si[i]), own = __fmul_rn(x[i], co[i]);
-              x[i] = upper ? __fadd_rn(own, cross) : __fsub_rn(own, cross);
+        for (int u = 0; u < U; ++u) {
+          if (!FULL && h0 + u * H >= heads) break;   // (the same for the whole warp)
+          Two t[4];
+          {
+            float x[8];
+            if (APART) {
+              unpack4<BF16>(*(const uint2*)(mine + u * 512 + pa * 2), &x[0]);
+              unpack4<BF16>(*(const uint2*)(mine + u * 512 + pb * 2), &x[4]);
+              t[0] = two(x[0], x[1]), t[1] = two(x[2], x[3]), t[2] = two(x[4], x[5]), t[3] = two(x[6], x[7]);
+            } else {
+              unpack8<BF16>(*(const uint4*)(mine + u * 512 + pa * 2), x);
+              t[0] = two(x[0], x[2]), t[1] = two(x[4], x[6]), t[2] = two(x[1], x[3]), t[3] = two(x[5], x[7]);
+            }
+          }
+          if constexpr (NORM) {
+            const float2 q = both(fma2(t[3], t[3], fma2(t[2], t[2], fma2(t[1], t[1], mul2(t[0], t[0])))));
+            float s = q.x + q.y;
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
+            const float r = rsqrtf(fmaf(s, 1.f / D, p.eps));
+            const Two rr = two(r, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = mul2(mul2(t[i], rr), w[i]);
+          }
+          if (j >= 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const Two a = t[i], b = t[i + 2];
+              t[i] = fma2(a, co[i], mul2(b, minus[i]));
+              t[i + 2] = fma2(b, co[i], mul2(a, si[i]));
+            }
+          }
+          if (FULL || h0 + u * H + sub < heads) {
+            const float2 a = both(t[0]), b = both(t[1]), c = both(t[2]), d = both(t[3]);
+            if (APART) {
+              const float x[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+              const uint4 o = pack8<BF16>(x);
+              *(uint2*)(ta + u * step) = make_uint2(o.x, o.y);
+              *(uint2*)(tb + u * step) = make_uint2(o.z, o.w);
+            } else {
+              const float x[8] = {a.x, c.x, a.y, c.y, b.x, d.x, b.y, d.y};
+              *(uint4*)(ta + u * step) = pack8<BF16>(x);
             }
           }
         }
+      };
+      auto by_fill = [&](auto normed, auto lies_apart) {
+        if (h0 + HEADS <= heads)
+          heads_of(normed, lies_apart, std::true_type{});
+        else
+          heads_of(normed, lies_apart, std::false_type{});
+      };
+      if (weight && apart)
+        by_fill(std::true_type{}, std::true_type{});
+      else if (weight)
+        by_fill(std::true_type{}, std::false_type{});
+      else if (apart)
+        by_fill(std::false_type{}, std::true_type{});
+      else
+        by_fill(std::false_type{}, std::false_type{});
+      continue;
+    }
+    // ---- 4 bits: every rounding in the documented order ----
+    if constexpr (FP4) {
+      const bool turn = p.rope && kind < 2, turned = turn && flat.j >= 0;
+      float w[8];
+      if (weight) {
+        if (p.weight_f32) {
+          *(float4*)&w[0] = *(const float4*)((const float*)weight + pa);
+          *(float4*)&w[4] = *(const float4*)((const float*)weight + pb);
+        } else {
+          unpack4<BF16>(*(const uint2*)((const T*)weight + pa), &w[0]);
+          unpack4<BF16>(*(const uint2*)((const T*)weight + pb), &w[4]);
+        }
       }
-      if (kind == 0 ? p.out_q_scale != nullptr : FP4) {
-        uint32_t top = 0;               // as integers: a NaN counts as the largest
+      // the angles of this lane's dimensions: 4 pairs of neighbours, or 8 of a half whose partners another lane has
+      bool upper = false;
+      int partner = lane;
+      float co[8], si[8];
+      if (turned) {
+        const float* t = p.rope + (int64_t)pos * p.rot;
+        if (p.pairs) {
+          *(float4*)&co[0] = *(const float4*)(t + flat.j);
+          *(float4*)&si[0] = *(const float4*)(t + p.rot / 2 + flat.j);
+        } else {
+          int j = 2 * flat.j;
+          upper = j >= p.rot / 2;
+          partner = upper ? lane - p.rot / 16 : lane + p.rot / 16;
+          if (upper) j -= p.rot / 2;
+#pragma unroll
+          for (int i = 0; i < 8; i += 4) {
+            *(float4*)&co[i] = *(const float4*)(t + j + i);
+            *(float4*)&si[i] = *(const float4*)(t + p.rot / 2 + j + i);
+          }
+        }
+      }
+      uint8_t* to = (uint8_t*)(kind == 0 ? p.out_q : dst.data) + at + (int64_t)(h0 + sub) * head + in * 4;
+      const int64_t s_head = kind == 0 ? p.oqs_head : dst.s_head;
+      uint8_t* st = (kind == 0 ? p.out_q_scale : dst.scale) + s_at + (int64_t)(h0 + sub) * s_head + in / 4;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (h0 + u * H >= heads) break;   // (the same for the whole warp)
+        float x[8];
+        unpack8<BF16>(*(const uint4*)(mine + u * 512 + pa * 2), x);
+        if (weight) {
+          float s = 0.f, rest = 0.f;      // squares of 16-bit numbers are exact in fp32
+#pragma unroll
+          for (int i = 0; i < 8; ++i) add_exactly(s, rest, __fmul_rn(x[i], x[i]));
+#pragma unroll
+          for (int o = 1; o < L; o <<= 1) {
+            const float s1 = __shfl_xor_sync(~0u, s, o), r1 = __shfl_xor_sync(~0u, rest, o);
+            rest = __fadd_rn(rest, r1);
+            float r2 = 0.f;
+            add_exactly(s, r2, s1);
+            rest = __fadd_rn(rest, r2);
+          }
+          const float sum = fabsf(s) < INFINITY ? __fadd_rn(s, rest) : s;
+          const float r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(sum / D, p.eps)));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
+        }
+        if (turn) {
+          if (p.pairs) {
+            if (turned) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i], b = x[2 * i + 1];
+                x[2 * i] = __fsub_rn(__fmul_rn(a, co[i]), __fmul_rn(b, si[i]));
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(b, co[i]), __fmul_rn(a, si[i]));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float o = __shfl_sync(~0u, x[i], partner);
+              if (turned) {
+                const float cross = __fmul_rn(o, si[i]), own = __fmul_rn(x[i], co[i]);
+                x[i] = upper ? __fadd_rn(own, cross) : __fsub_rn(own, cross);
+              }
+            }
+          }
+        }
+        uint32_t top = 0;                 // as integers: a NaN counts as the largest
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
         top = max(top, __shfl_xor_sync(~0u, top, 1));
         top = max(top, __shfl_xor_sync(~0u, top, 2));
         const uint32_t e = scale_byte(top), codes = to_codes(x, e);
-        if (on) {
-          uint8_t* to = (kind == 0 ? (uint8_t*)p.out_q + h * p.oq_head : (uint8_t*)dst.data + h * dst.head) + at;
-          uint8_t* st = (kind == 0 ? p.out_q_scale + h * p.oqs_head : dst.scale + h * dst.s_head) + s_at;
-          *(uint32_t*)(to + in * 4) = codes;
-          if (in % 4 == 0) st[in / 4] = (uint8_t)e;
+        if (h0 + u * H + sub < heads) {
+          *(uint32_t*)(to + u * (H * head)) = codes;
+          if (in % 4 == 0) st[u * (H * s_head)] = (uint8_t)e;
         }
-      } else if (on) {
-        T* to = (kind == 0 ? (T*)p.out_q + h * p.oq_head : (T*)dst.data + h * dst.head) + at;
-        *(uint4*)(to + d0) = pack8<BF16>(x);
       }
     }
   }
 }
 
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void store32(void* a, const uint4& x, const uint4& y) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w),
+               "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+               : "memory");
+}
+
 // Listed slots of a 4-bit cache as 16-bit rows, rounded once (exact unless beyond the type's range or below its
-// last place): 4 bytes of codes, 8 elements, a thread.  Bound by HBM: 0.53 bytes read and 2 written an element.
+// last place): 8 bytes of codes, 16 elements, a thread.  Bound by HBM: 0.53 bytes read and 2 written an element.
 // The last CTA only looks for slots that are none.
 template <bool BF16, int D, int U>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  constexpr int L = D / 8;              // threads of a head
+  constexpr int L = D / 16;             // threads of a head
   const int32_t most = p.num_pages * kPage;
   if (blockIdx.x == gridDim.x - 1) {
     bool bad = false;
@@ -305,60 +524,75 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
     if (threadIdx.x == 0) *p.status_out = bad ? kErrInvalidPage : kOk;
     return;
   }
-  const int j = threadIdx.x % L;
+  const uint32_t j = threadIdx.x % L;
   const int32_t step = (int32_t)(gridDim.x - 1) * (kGatherThreads / L);   // heads from one of a thread's to its next
   const int32_t dr = step / p.kv_heads, dh = step - dr * p.kv_heads;
   const int32_t v0 = (int32_t)blockIdx.x * (kGatherThreads / L) + (int32_t)threadIdx.x / L;
   int32_t r = v0 / p.kv_heads, h = v0 - r * p.kv_heads;
   while (r < p.n) {
-    int32_t rs[U], hs[U];
-    uint32_t codes[2][U], e[2][U];
+    int32_t rs[U], hs[U], slots[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       rs[u] = r, hs[u] = h;
-      const int32_t slot = r < p.n ? p.slots[r] : -1;
-      const bool on = slot >= 0 && slot < most;
-      const int64_t page = slot / kPage, off = slot % kPage;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const GatherParams::From& f = p.t[t];
-        codes[t][u] = 0, e[t][u] = slot == -1 ? 127u : 255u;   // what is no slot becomes NaN
-        if (!on || !f.codes) continue;
-        codes[t][u] = *(const uint32_t*)(f.codes + page * f.page + off * f.slot + h * f.head + j * 4);
-        e[t][u] = f.scale[page * f.s_page + off * f.s_slot + h * f.s_head + j / 4];
-      }
+      slots[u] = r < p.n ? p.slots[r] : -1;
       r += dr, h += dh;
       if (h >= p.kv_heads) h -= p.kv_heads, ++r;
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (rs[u] >= p.n) break;
+    for (int t = 0; t < 2; ++t) {
+      const GatherParams::From& f = p.t[t];
+      if (!f.codes) continue;
+      uint2 codes[U];
+      uint32_t e[U];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const GatherParams::From& f = p.t[t];
-        if (!f.codes) continue;
-        uint32_t w[4];
-        from_codes(codes[t][u], w);
-        const float s = scale_of(e[t][u]);
-        float x[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 y = __half22float2(*(const __half2*)&w[k]);
-          x[2 * k] = y.x * s, x[2 * k + 1] = y.y * s;
+      for (int u = 0; u < U; ++u) {
+        codes[u] = make_uint2(0, 0), e[u] = slots[u] == -1 ? 127u : 255u;   // what is no slot becomes NaN
+        if (slots[u] < 0 || slots[u] >= most) continue;
+        const uint32_t page = (uint32_t)slots[u] / kPage, off = (uint32_t)slots[u] % kPage, head = (uint32_t)hs[u];
+        if (p.far) {
+          codes[u] = *(const uint2*)(f.codes + (page * f.page + off * f.slot + head * f.head) + j * 8);
+          e[u] = f.scale[page * f.s_page + off * f.s_slot + head * f.s_head + j / 2];
+        } else {
+          const uint32_t at16 = page * (uint32_t)(f.page / 16) + off * (uint32_t)(f.slot / 16) + head * (uint32_t)(f.head / 16);
+          codes[u] = *(const uint2*)(f.codes + (uint64_t)at16 * 16 + j * 8);
+          e[u] = f.scale[page * (uint32_t)f.s_page + off * (uint32_t)f.s_slot + head * (uint32_t)f.s_head + j / 2];
         }
-        __stcs((uint4*)((T*)f.out + rs[u] * f.row + hs[u] * f.out_head + j * 8), pack8<BF16>(x));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (rs[u] >= p.n) break;
+        const float s = scale_of(e[u]);
+        uint4 out[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t w[4];
+          from_codes(x ? codes[u].y : codes[u].x, w);
+          float y[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 z = __half22float2(*(const __half2*)&w[k]);
+            y[2 * k] = z.x * s, y[2 * k + 1] = z.y * s;
+          }
+          out[x] = pack8<BF16>(y);
+        }
+        T* to = (T*)f.out + rs[u] * f.row + hs[u] * f.out_head + j * 16;
+        if (p.wide) {
+          store32(to, out[0], out[1]);
+        } else {
+          *(uint4*)to = out[0], *(uint4*)(to + 8) = out[1];
+        }
       }
     }
   }
 }
 
 template <bool BF16, int D, bool FP4, int U>
-cudaError_t launch_append_u(const AppendParams& p, int threads, int grid, size_t smem, cudaStream_t stream) {
+cudaError_t launch_append_u(const AppendParams& p, int threads, int grid, cudaStream_t stream) {
   auto* kernel = append_kernel<BF16, D, FP4, U>;
   static std::atomic<bool> done[64];
-  cudaError_t e = set_smem_once(kernel, kBitmapBytes, done);
+  cudaError_t e = set_smem_once(kernel, kBitmapBytes + kRingBytes<FP4, U>, done);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, threads, smem, stream>>>(p);
+  kernel<<<grid, threads, p.table_bytes + threads / 32 * kStages<U> * U * 512, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -374,15 +608,15 @@ cudaError_t launch_append_as(AppendParams p, int sm, cudaStream_t stream) {
   p.table_bits = 0;
   for (int b = 6; b <= 15 && !p.table_bits; ++b)
     if ((int64_t)1 << b >= 2 * (int64_t)p.rows) p.table_bits = b;
-  const size_t smem = p.table_bits ? (size_t)4 << p.table_bits : kBitmapBytes;
+  p.table_bytes = p.table_bits ? 4 << p.table_bits : kBitmapBytes;
   if (chunks(H) <= (int64_t)sm * 16) {
     const int64_t n = chunks(H);
     const int64_t want = (n + sm - 1) / sm;      // warps an SM
     const int warps = want <= 4 ? 4 : want <= 8 ? 8 : 16;
     const int64_t grid = (n + warps - 1) / warps;
-    return launch_append_u<BF16, D, FP4, 1>(p, warps * 32, (int)(grid < 1 ? 1 : grid), smem, stream);
+    return launch_append_u<BF16, D, FP4, 1>(p, warps * 32, (int)(grid < 1 ? 1 : grid), stream);
   }
-  return launch_append_u<BF16, D, FP4, 4>(p, kMaxThreads, sm, smem, stream);
+  return launch_append_u<BF16, D, FP4, 4>(p, kMaxThreads<FP4, 4>, sm, stream);
 }
 
 template <bool BF16>
@@ -399,7 +633,7 @@ cudaError_t launch_append_dim(const AppendParams& p, int dim, bool fp4, int sm, 
 
 template <bool BF16, int D>
 cudaError_t launch_gather_as(const GatherParams& p, int sm, cudaStream_t stream) {
-  const int64_t ctas = ((int64_t)p.n * p.kv_heads * (D / 8) + kGatherThreads - 1) / kGatherThreads;
+  const int64_t ctas = ((int64_t)p.n * p.kv_heads * (D / 16) + kGatherThreads - 1) / kGatherThreads;
   if (ctas <= 2 * sm)
     gather_kernel<BF16, D, 1><<<(int)ctas + 1, kGatherThreads, 0, stream>>>(p);
   else

@@ -35,6 +35,7 @@ struct AppendParams {
   int64_t oq_row, oq_head, oqs_row, oqs_head;
   int32_t q_in_place;
   PagedOut k_dst, v_dst;
+  int32_t table_bytes;              // of shared memory, before the rings of the warps
   int32_t table_bits;               // log2 of the entries of the table that finds slots named twice, or 0: a bitmap
   uint32_t* status_out;
 };
@@ -50,6 +51,8 @@ struct GatherParams {
   } t[2];
   const int32_t* slots;
   int32_t n, num_pages, kv_heads;
+  int32_t far;                      // codes that span 64 GB or scales that span 4
+  int32_t wide;                     // outputs' heads begin at 32-byte boundaries
   uint32_t* status_out;
 };
 

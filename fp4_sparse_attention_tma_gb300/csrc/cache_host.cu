@@ -219,6 +219,7 @@ int run_gather(const GatherCall& c, const Space& space, cudaStream_t stream) {
   if (!guard.ok()) return IDX_ERR_CUDA;
   if ((st = check_arch(&m))) return st;
   GatherParams p{};
+  bool narrow = false;
   for (int i = 0; i < 2; ++i) {
     const idx_tensor_t *t = i ? c.v : c.k, *s = i ? c.v_scale : c.k_scale, *o = i ? c.out_v : c.out_k;
     if (!t) continue;
@@ -226,7 +227,10 @@ int run_gather(const GatherCall& c, const Space& space, cudaStream_t stream) {
     f.codes = (const uint8_t*)t->data, f.page = step(t, 0), f.slot = step(t, 1), f.head = step(t, 2);
     f.scale = (const uint8_t*)s->data, f.s_page = step(s, 0), f.s_slot = step(s, 1), f.s_head = step(s, 2);
     f.out = o->data, f.row = step(o, 0), f.out_head = step(o, 1);
+    p.far |= span_of(t) >= kFar || span_of(s) > UINT32_MAX;
+    narrow |= ((uintptr_t)o->data | (uintptr_t)(f.row * 2) | (uintptr_t)(f.out_head * 2)) % 32 != 0;
   }
+  p.wide = !narrow;
   p.slots = (const int32_t*)c.slots->data;
   p.n = (int32_t)N, p.num_pages = (int32_t)NP, p.kv_heads = (int32_t)Hk;
   return with_space(space, 0, m, stream, [&](char*, uint32_t* status) -> cudaError_t {

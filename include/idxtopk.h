@@ -636,10 +636,8 @@ int idx_cache_evict_scratch_bytes(int32_t num_req, int32_t max_pages, int32_t ds
  *       + i + rot / 2); NULL: nothing is rotated;
  *   out_q[r] = q's result; k's result and v[r] become slot pos % 64 of page
  *       page_table[row_req[r], pos / 64].
- * A row with position -1 is not there (padding): nothing of it is read or written.  Rows may
- * come in any order.  All in fp32, in the order written, each product and sum rounded by
- * itself and the sum of squares as if it were rounded once, so that the results do not depend
- * on how the work is divided; results are rounded once to the output's type.
+ * A row with position -1 is not there (padding): nothing of it is written.  Rows may
+ * come in any order.  All in fp32; results are rounded once to the output's type.
  *   q [R, Hq, D] or NULL (then out_q is too), k [R, Hk, D], v [R, Hk, D] or NULL (then v_cache
  *              is too); strides as above
  *   q_weight, k_weight [D] or NULL, in q's type or IDX_F32 (both alike); eps >= 0, finite
@@ -680,7 +678,10 @@ int idx_cache_append_async(const idx_tensor_t* q, const idx_tensor_t* k, const i
  * idx_cache_append_fp4 is idx_cache_append into such a cache: of the normed and rotated key in
  * fp32, and of the value, e is the smallest of 0 .. 254 such that no element of the block
  * exceeds 6 * 2^(e - 127), and an element becomes the nearest code, ties to the even one.  A
- * block with a NaN or an infinity gets e = 255, and codes 0.
+ * block with a NaN or an infinity gets e = 255, and codes 0.  What becomes codes is computed in
+ * the order written, x * (1 / sqrt(mean + eps)) * weight, each operation rounded by itself and
+ * the sum of squares as if it were rounded once: the codes do not depend on how the work is
+ * divided.
  *   out_q, out_q_scale  out_q [R, Hq, D] in q's type with out_q_scale NULL, or in 4 bits: codes
  *                       u8 [R, Hq, D / 2] with scales u8 [R, Hq, D / 32] (after a device error
  *                       codes 0 and scales 255)

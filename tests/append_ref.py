@@ -1,10 +1,13 @@
 """Plain forms of writing a paged cache for the tests, written from the formulas: the norm and the rotation in 64
 bits with the bound that the kernel's arithmetic gives, the same in 32 bits rounding by rounding, and the 4-bit form.
 
-Bound.  The kernel rounds, each to 2^-24 relative: the sum of squares, the addition of eps (both under a root: half),
-the root, the reciprocal, the product with x and that with the weight: 5 * 2^-24 of a normed element.  A rotation adds
-a rounded product each (6 * 2^-24 of |a cos| and of |b sin|) and the rounding of their sum: 7 * 2^-24 (|a cos| + |b sin|)
-at most.  The cosines and sines are inputs.  A 16-bit output adds u |y| (fp16 below its normal range: 2^-25).
+Bounds, in units of 2^-24 relative.  What becomes 4 bits is rounded where the documented order says: the sum of squares,
+the addition of eps (both under a root: half), the root, the reciprocal, the product with x and that with the weight: 5 of
+a normed element.  A rotation adds a rounded product each (6 of |a cos| and of |b sin|) and the rounding of their sum: 7
+(|a cos| + |b sin|) at most.  What stays in 16 bits sums the squares (all positive) in fp32, 8 a lane and then up to 32
+lanes: at most 13 roundings; one with eps, half of these 14 in the root; a reciprocal root of 2 units in the last place (4);
+two products: 13 of a normed element, 15 (|a cos| + |b sin|) of a rotated one.  The cosines and sines are inputs.  A 16-bit
+output adds u |y| (fp16 below its normal range: 2^-25).
 """
 import numpy as np
 
@@ -17,20 +20,20 @@ def _pairs(rot, first, pairs):
     return (first + 2 * i, first + 2 * i + 1) if pairs else (first + i, first + rot // 2 + i)
 
 
-def turned64(x, weight, eps, cos, sin, first, pairs):
+def turned64(x, weight, eps, cos, sin, first, pairs, four=True):
     """x [R, H, D] (float64 of the inputs), weight [D] or None, cos and sin [R, rot / 2] or None ->
-    y and the bound of the kernel's error before the last rounding."""
+    y and the bound of the kernel's error before the last rounding (`four`: to 4 bits)."""
     x = np.asarray(x, dtype=np.float64)
     y, units = x.copy(), np.zeros_like(x)
     if weight is not None:
         y = x / np.sqrt((x * x).mean(-1, keepdims=True) + float(np.float32(eps))) * weight
-        units = 5 * np.abs(y)
+        units = (5 if four else 13) * np.abs(y)
     if cos is not None:
         a, b = _pairs(2 * cos.shape[1], first, pairs)
         c, s = cos[:, None].astype(np.float64), sin[:, None].astype(np.float64)
         ya, yb = y[..., a], y[..., b]
-        units[..., a] = 7 * (np.abs(ya * c) + np.abs(yb * s))
-        units[..., b] = 7 * (np.abs(yb * c) + np.abs(ya * s))
+        units[..., a] = (7 if four else 15) * (np.abs(ya * c) + np.abs(yb * s))
+        units[..., b] = (7 if four else 15) * (np.abs(yb * c) + np.abs(ya * s))
         y[..., a], y[..., b] = ya * c - yb * s, yb * c + ya * s
     return y, units * 2.0 ** -24 * (1 + 1e-6) + 1e-44
 
