@@ -110,6 +110,34 @@ def _descs(ts):
     return buf, [None if t is None else at + 80 * i for i, t in enumerate(ts)]
 
 
+# What a descriptor holds behind the pointer, by (dtype, shape, strides): a serving loop's calls
+# have few different ones.
+_layouts = {}
+_pointer = struct.Struct("=Q").pack
+
+
+def _packed(ts):
+    """Descriptors of the tensors `ts` as bytes objects (None for an absent one), which ctypes
+    passes by address."""
+    out = []
+    for t in ts:
+        if t is None:
+            out.append(None)
+            continue
+        key = (t.dtype, t.shape, t.stride())
+        layout = _layouts.get(key)
+        if layout is None:
+            dt, sh, st = key
+            nd = len(st)
+            fill = _FILL[nd] if nd <= 4 else ()
+            if len(_layouts) >= 4096:
+                _layouts.clear()
+            layout = _pack(0, _dtype_code(dt), nd, *sh[:4], *fill, *st[:4], *fill)[8:]
+            _layouts[key] = layout
+        out.append(_pointer(t.data_ptr()) + layout)
+    return out
+
+
 def _raw_stream():
     """Function that gives the handle of the current device's current stream."""
     import torch
@@ -461,10 +489,9 @@ def idx_cache_evict_scratch_bytes(num_req: int, max_pages: int, dst_pages: int, 
 def _append(fn, fp4, k, v, page_table, row_req, row_pos, places, tail, q, out_q, out_q_scale,
             q_weight, k_weight, eps, rope, rope_first, rope_pairs, raise_on_error):
     outs = (out_q, out_q_scale) if fp4 else (out_q,)
-    keep, ds = _descs((q, k, v, page_table, row_req, row_pos, q_weight, k_weight, rope, *outs,
-                       *places))
-    code = getattr(_lib.load(), fn)(*ds[:8], float(eps), ds[8], int(rope_first),
-                                    1 if rope_pairs else 0, *ds[9:], *tail)
+    ds = _packed((q, k, v, page_table, row_req, row_pos, q_weight, k_weight, rope, *outs, *places))
+    code = getattr(_lib.load(), fn)(*ds[:8], float(eps), ds[8], int(rope_first), 1 if rope_pairs else 0,
+                                    *ds[9:], *tail)
     return _check(code, fn, raise_on_error)
 
 
@@ -519,7 +546,7 @@ def idx_cache_gather_fp4(k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v
                          raise_on_error=True) -> int:
     """Listed physical slots [N] (-1: zeros) of a 4-bit cache as 16-bit rows [N, Hk, D];
     v_codes, v_scale and out_v may be None."""
-    keep, ds = _descs((k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v))
+    ds = _packed((k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v))
     code = _lib.load().idx_cache_gather_fp4(*ds, _stream(stream))
     return _check(code, "idx_cache_gather_fp4", raise_on_error)
 
@@ -527,7 +554,7 @@ def idx_cache_gather_fp4(k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v
 def idx_cache_gather_fp4_async(k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v, status,
                                stream=None, raise_on_error=True) -> int:
     """idx_cache_gather_fp4 without host synchronisation or allocation (graph-capturable)."""
-    keep, ds = _descs((k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v))
+    ds = _packed((k_codes, k_scale, v_codes, v_scale, slots, out_k, out_v))
     code = _lib.load().idx_cache_gather_fp4_async(*ds, status.data_ptr(), _stream(stream))
     return _check(code, "idx_cache_gather_fp4_async", raise_on_error)
 
@@ -536,8 +563,8 @@ def idx_attn_paged_fp4(q, k_codes, k_scale, v_codes, v_scale, page_table, row_re
                        row_end, scale, out, out_lse=None, stream=None, raise_on_error=True) -> int:
     """idx_attn_paged over a cache in 4 bits: codes u8 [NP, 64, Hk, D / 2] with scales u8
     [NP, 64, Hk, D / 32], as idx_cache_append_fp4 writes them."""
-    keep, ds = _descs((q, k_codes, k_scale, v_codes, v_scale, page_table, row_req, row_start,
-                       row_end, out, out_lse))
+    ds = _packed((q, k_codes, k_scale, v_codes, v_scale, page_table, row_req, row_start,
+                  row_end, out, out_lse))
     code = _lib.load().idx_attn_paged_fp4(*ds[:9], float(scale), *ds[9:], _stream(stream))
     return _check(code, "idx_attn_paged_fp4", raise_on_error)
 
@@ -547,8 +574,8 @@ def idx_attn_paged_fp4_async(q, k_codes, k_scale, v_codes, v_scale, page_table, 
                              stream=None, raise_on_error=True) -> int:
     """idx_attn_paged_fp4 without host synchronisation or allocation (graph-capturable);
     `workspace` of idx_attn_paged_fp4_scratch_bytes bytes."""
-    keep, ds = _descs((q, k_codes, k_scale, v_codes, v_scale, page_table, row_req, row_start,
-                       row_end, out, out_lse))
+    ds = _packed((q, k_codes, k_scale, v_codes, v_scale, page_table, row_req, row_start,
+                  row_end, out, out_lse))
     code = _lib.load().idx_attn_paged_fp4_async(*ds[:9], float(scale), *ds[9:],
                                                 *_space(workspace, status), _stream(stream))
     return _check(code, "idx_attn_paged_fp4_async", raise_on_error)
@@ -567,7 +594,7 @@ def idx_attn_paged_fp4_scratch_bytes(rows: int, q_heads: int, kv_heads: int, hea
 def idx_attn_selected_fp4(q, k_codes, k_scale, v_codes, v_scale, slots, scale, out, out_lse=None,
                           stream=None, raise_on_error=True) -> int:
     """idx_attn_selected over a cache in 4 bits."""
-    keep, ds = _descs((q, k_codes, k_scale, v_codes, v_scale, slots, out, out_lse))
+    ds = _packed((q, k_codes, k_scale, v_codes, v_scale, slots, out, out_lse))
     code = _lib.load().idx_attn_selected_fp4(*ds[:6], float(scale), ds[6], ds[7],
                                              _stream(stream))
     return _check(code, "idx_attn_selected_fp4", raise_on_error)
@@ -578,7 +605,7 @@ def idx_attn_selected_fp4_async(q, k_codes, k_scale, v_codes, v_scale, slots, sc
                                 raise_on_error=True) -> int:
     """idx_attn_selected_fp4 without host synchronisation or allocation (graph-capturable);
     `workspace` of idx_attn_selected_fp4_scratch_bytes bytes."""
-    keep, ds = _descs((q, k_codes, k_scale, v_codes, v_scale, slots, out, out_lse))
+    ds = _packed((q, k_codes, k_scale, v_codes, v_scale, slots, out, out_lse))
     code = _lib.load().idx_attn_selected_fp4_async(*ds[:6], float(scale), ds[6], ds[7],
                                                    *_space(workspace, status), _stream(stream))
     return _check(code, "idx_attn_selected_fp4_async", raise_on_error)

@@ -14,6 +14,7 @@
 #include "append.h"
 #include "fp4.cuh"
 #include "idx_launch.h"
+#include "pairs.cuh"
 
 namespace idxk {
 namespace {
@@ -168,29 +169,6 @@ template <int U>
 constexpr int kStages = U == 1 ? 1 : 2;                  // chunks that a warp has on their way
 template <bool FP4, int U>
 constexpr int kRingBytes = kMaxThreads<FP4, U> / 32 * kStages<U> * U * 512;
-
-// Pairs of fp32 numbers, and operations on both at once.
-using Two = uint64_t;
-__device__ __forceinline__ Two two(float x, float y) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 both(Two a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 template <bool BF16, int D, bool FP4, int U>
 __global__ void __launch_bounds__(kMaxThreads<FP4, U>, 1) append_kernel(const __grid_constant__ AppendParams p) {

@@ -19,6 +19,7 @@
 
 #include "attn_common.cuh"
 #include "fp4.cuh"
+#include "pairs.cuh"
 
 namespace idxk {
 namespace attn {
@@ -138,28 +139,6 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
   asm volatile("{\n\t.reg .u16 t;\n\tcvt.u16.u32 t, %1;\n\tst.shared.u16 [%0], t;\n\t}" ::"r"(a), "r"(v) : "memory");
 }
 
-// Two fp32 operations in one instruction: x * a + b and x + y of pairs.
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 v, m, s;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\tmov.b64 s, {%3, %3};\n\t"
-      "fma.rn.f32x2 v, v, m, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
-__device__ __forceinline__ void mul2(float& x, float& y, float a) {
-  asm("{\n\t.reg .b64 v, m;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %2};\n\t"
-      "mul.rn.f32x2 v, v, m;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a));
-}
-__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 v, s;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\t"
-      "add.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
-}
 __device__ __forceinline__ void mma_from_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -385,11 +364,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
     // ---- computing side ----
     int stage = 0;
     const float c = p.scale_log2;
+    const Two cc = two(c, c), shift = two((float)kF16Shift, (float)kF16Shift);
     for (bool more = true; more;) {
       int32_t left, sub;                  // subtiles of the segment to go, and the next one
       uint32_t qf[MT][KS][4];
       float o[MT][NT][4];
-      float mx[MT][2], sum[MT][2][2], unit[MT][2];   // unit: what the queries were divided by
+      float mx[MT][2], unit[MT][2];       // unit: what the queries were divided by
+      Two sum[MT][2];
       uint32_t live = 0;                  // bit 2t + e: the thread's tile row is a row that sees something
       bool seen = false;                  // (slots) some slot of the segment was one
       uint32_t o_ref = kLowest;           // the weighted values' reference
@@ -418,7 +399,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
             }
             if (on) live |= 1u << (2 * t + e);
             full_lo = max(full_lo, a), full_hi = min(full_hi, b);
-            mx[t][e] = kNegInf, sum[t][e][0] = sum[t][e][1] = 0.f, unit[t][e] = 1.f;
+            mx[t][e] = kNegInf, sum[t][e] = two(0.f, 0.f), unit[t][e] = 1.f;
             // this lane's quarter of the head
             const uint2* src = (const uint2*)((const T*)p.q + (int64_t)(at.row0 + j) * p.q_row + (int64_t)(h0 + h) * p.q_head +
                                               quad * (D / 4));
@@ -577,10 +558,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
           for (int t = 0; t < MT; ++t) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              sum[t][e][0] *= alpha[t][e], sum[t][e][1] *= alpha[t][e];
+              sum[t][e] = mul2(sum[t][e], two(alpha[t][e], alpha[t][e]));
               const float a = alpha[t][e] * down;
+              const Two aa = two(a, a);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mul2(o[t][n][2 * e], o[t][n][2 * e + 1], a);
+              for (int n = 0; n < NT; ++n) {
+                const float2 z = both(mul2(two(o[t][n][2 * e], o[t][n][2 * e + 1]), aa));
+                o[t][n][2 * e] = z.x, o[t][n][2 * e + 1] = z.y;
+              }
             }
           }
         }
@@ -588,17 +573,17 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int e = 0; e < 2; ++e) {
+            const Two uu = two(u[t][e], u[t][e]), minus = two(-base[t][e], -base[t][e]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int n = 0; n < 4; ++n) {
               // (the product with a power of two is exact: one rounding, that of the difference)
-              float &a = s[t][n][2 * e], &b = s[t][n][2 * e + 1];
-              fma2(a, b, u[t][e], -base[t][e]);
-              fma2(a, b, c, (float)kF16Shift);
-              a = ex2(a), b = ex2(b);
-              add2(sum[t][e][0], sum[t][e][1], a, b);
+              const float2 d = both(fma2(fma2(two(s[t][n][2 * e], s[t][n][2 * e + 1]), uu, minus), cc, shift));
+              const float a = ex2(d.x), b = ex2(d.y);
+              sum[t][e] = add2(sum[t][e], two(a, b));
               pf[t][n / 2][(n & 1) * 2 + e] = pack2<false>(a, b);
             }
+          }
 
         // the second product: 16 positions a step; this lane's D / 8 elements of four positions, all of one block
         const uint4 vf = lds128(st + S::kVf + (uint32_t)((col * (D / 8) / 32) * 4 + quad) * 16);
@@ -654,7 +639,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float l = sum[t][e][0] + sum[t][e][1];
+            const float2 halves = both(sum[t][e]);
+            float l = halves.x + halves.y;
             l += __shfl_xor_sync(~0u, l, 1);
             l += __shfl_xor_sync(~0u, l, 2);
             l *= kBack;

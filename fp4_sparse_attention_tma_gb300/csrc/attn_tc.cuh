@@ -611,20 +611,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 // the weights count in the chunk's values' reference, their sum does not (values 2^-40 below the largest are
                 // taken for 2^-40 of it)
                 const int32_t down = max(v_ref[k] - o_ref, -40);
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
-                const float shift = kShift<MB> + (float)down;
+                Two part[2] = {two(0.f, 0.f), two(0.f, 0.f)};
+                const float up = kShift<MB> + (float)down;
+                const Two shift = two(up, up), uu = two(unit[k], unit[k]), minus = two(base, base), cc = two(p.scale_log2, p.scale_log2);
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                  float d0 = __uint_as_float(r[i]), d1 = __uint_as_float(r[i + 1]);
-                  fp4::fma2(d0, d1, unit[k], base);
-                  fp4::fma2(d0, d1, p.scale_log2, shift);
-                  const float e0 = ex2(d0), e1 = ex2(d1);
-                  add2(part[i & 2], part[(i & 2) + 1], e0, e1);
+                  const float2 d = both(fma2(fma2(two(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), uu, minus), cc, shift));
+                  const float e0 = ex2(d.x), e1 = ex2(d.y);
+                  part[i / 2 & 1] = idxk::add2(part[i / 2 & 1], two(e0, e1));
                   w[i / 2] = pack2<MB>(e0, e1);
                 }
+                const float2 all = both(idxk::add2(part[0], part[1]));
                 const float back = fp4::pow2_of(127 - down);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sum[i] = fmaf(part[i], back, sum[i]);
+                sum[0] = fmaf(all.x, back, sum[0]), sum[1] = fmaf(all.y, back, sum[1]);
               } else {
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {

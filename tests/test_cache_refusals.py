@@ -162,6 +162,17 @@ def test_interleaved_places():
     assert call(a, True) == INVALID
 
 
+def test_packed_descriptors():
+    """The descriptors that these calls pass, remembered by layout, are those of the struct; again, and at another
+    address."""
+    ts = [torch.zeros(7, 64, 64, dtype=torch.uint8), torch.zeros(5, dtype=torch.int32), torch.zeros(0, dtype=torch.int32),
+          torch.zeros(3, 4)[:, ::2], torch.zeros(2, 3, 4, 5, 6), torch.zeros((), dtype=torch.float16), None,
+          torch.zeros(6, 2, dtype=torch.float64), torch.zeros(9, 64, 64, dtype=torch.uint8)[2:], torch.zeros(3, 4).t()]
+    for _ in range(2):
+        for t, got in zip(ts, m._packed(ts)):
+            assert got == (None if t is None else bytes(m._desc(t)))
+
+
 def gather(a):
     s = Stream()
     code = m.idx_cache_gather_fp4_async(*a, torch.zeros(1, dtype=torch.int32), stream=s, raise_on_error=False)
