@@ -52,7 +52,7 @@ struct AttnParams {
   int32_t group_rows;               // rows per group, at most (1 where there are several chunks)
   int32_t row_cols;                 // tile rows between the rows of a group (chunk_heads of them in use)
   int32_t tensor_core;              // 1: the kernel of attn_tc.cuh
-  int32_t far;                      // 1: a cache spans 64 GB or more
+  int32_t far;                      // 1: a cache spans 64 GB or more (attn_fp4.cuh: 4 GB)
   int32_t workers;                  // warps of the grid
   int32_t team;                     // (attn_fp4.cuh) warps that walk over the same range, a key-value head each; else 1
   int32_t ranges;                   // workers / team

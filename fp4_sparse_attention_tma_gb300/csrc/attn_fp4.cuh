@@ -28,6 +28,7 @@ namespace fp4 {
 constexpr int kSub4 = 32;                 // cached positions per subtile
 constexpr uint32_t kLowest = 26;          // no reference is below this byte: no scale is below 2^-26 of it then
 constexpr uint32_t kF16Shift = 10;        // weights are 2^kF16Shift times what they stand for
+constexpr float kRaise = 5.f;             // and at most 2^(kRaise + kF16Shift)
 
 // 2^(12 + e - E) as an fp16 number in both halves of a word (0 where e < E - 26).
 __device__ __forceinline__ uint32_t factor2(uint32_t e, uint32_t E) {
@@ -205,13 +206,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
     constexpr int ROWS = 32 / CH;                     // positions that one copy of the warp covers
     constexpr int COPIES = kSub4 / ROWS;
     const int piece = lane % CH, row_in = lane / CH;
-    const uint32_t kp16 = (uint32_t)(p.k_page / 16), ks16 = (uint32_t)(p.k_slot / 16), vp16 = (uint32_t)(p.v_page / 16),
-                   vs16 = (uint32_t)(p.v_slot / 16);
+    // (offsets in 32 bits; where a tensor spans 4 GB or more, `far`, in 64)
+    const uint32_t kp = (uint32_t)p.k_page, ks = (uint32_t)p.k_slot, vp = (uint32_t)p.v_page, vs = (uint32_t)p.v_slot;
+    const uint32_t ksp = (uint32_t)p.ks_page, kss = (uint32_t)p.ks_slot, vsp = (uint32_t)p.vs_page, vss = (uint32_t)p.vs_slot;
     int32_t f_left;                                   // subtiles of the segment that are still to be fetched; 0: all done
     int32_t f_sub;                                    // the next subtile, counted from position 0
     int32_t f_lo, f_hi;                               // what the group's rows see of it
-    uint32_t f_k16, f_v16;                            // the head and this lane's piece of it, in units of 16 bytes
-    uint32_t f_ks, f_vs;                              // the head's scales, in bytes
+    uint32_t f_k, f_v, f_ks, f_vs;                    // the head: this lane's first copy and scales in a page (slots: the head)
     const int32_t* f_list;                            // the request's pages, or the row's slots
     bool f_first;                                     // the next subtile fetched is a segment's first
     int32_t entry;                                    // page of the next subtile, or slot of its position `lane`
@@ -235,9 +236,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
       f_lo = f.lo, f_hi = f.hi;
       f_first = true;
       const int32_t kv = f.kv * p.team + member;
-      f_k16 = (uint32_t)(kv * (p.k_head / 16)) + piece;
-      f_v16 = (uint32_t)(kv * (p.v_head / 16)) + piece;
+      f_k = (uint32_t)(kv * p.k_head) + piece * 16, f_v = (uint32_t)(kv * p.v_head) + piece * 16;
       f_ks = (uint32_t)(kv * p.ks_head), f_vs = (uint32_t)(kv * p.vs_head);
+      if constexpr (!SLOTS) f_k += row_in * ks, f_v += row_in * vs, f_ks += lane * kss, f_vs += lane * vss;
       f_list = SLOTS ? p.slots + (int64_t)f.row0 * p.n_slots : p.page_table + (int64_t)f.req * p.max_pages;
       look_up();
     };
@@ -266,23 +267,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
     auto key_to = [&](uint32_t dst, int i) {
       return dst + (D == 256 ? (i & 1 ? key1 : key0) + (uint32_t)(i >> 1) * 8 * S::kRow : key0 + (uint32_t)(i * ROWS) * S::kRow);
     };
-    const uint32_t ksp = (uint32_t)p.ks_page, kss = (uint32_t)p.ks_slot, vsp = (uint32_t)p.vs_page, vss = (uint32_t)p.vs_slot;
-    auto load_scales = [&](int32_t page, int32_t off) {
-      if (!p.far) {
-        sk.load(p.k_scale + (f_ks + (uint32_t)page * ksp + (uint32_t)off * kss));
-        sv.load(p.v_scale + (f_vs + (uint32_t)page * vsp + (uint32_t)off * vss));
-      } else {
-        const int64_t kv = w.fetch.kv * p.team + member;
-        sk.load(p.k_scale + kv * p.ks_head + page * p.ks_page + off * p.ks_slot);
-        sv.load(p.v_scale + kv * p.vs_head + page * p.vs_page + off * p.vs_slot);
-      }
-    };
     auto fetch = [&](int stage, int stage_before) {
       put_scales(stage_before);
       pend = f_left > 0;
       if (f_left > 0) {
         const uint32_t dst = my_ring + (uint32_t)stage * S::kStage, dv = dst + value0;
-        sk.clear(), sv.clear();
+        auto to_v = [&](int i) { return dv + (uint32_t)(i * ROWS) * S::kRow; };
+        // where a tensor is far, from its first byte: the head's
+        auto far_head = [&](int64_t head) { return (w.fetch.kv * p.team + member) * head; };
         if constexpr (SLOTS) {
           const bool on = entry >= 0 && entry < p.num_pages * kPage;
           if (!on && entry != -1) warp_err = kErrInvalidPage;
@@ -290,52 +282,64 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < STAGES; ++i)
             if (i == stage) shown[i] = mask;
-          const int32_t page = on ? entry / kPage : 0, off = on ? entry % kPage : 0;
-          if (on) load_scales(page, off);
+          const uint32_t page = on ? (uint32_t)entry / kPage : 0, off = on ? (uint32_t)entry % kPage : 0;
+          sk.clear(), sv.clear();
           if (!p.far) {
-            const uint32_t ok = (uint32_t)page * kp16 + (uint32_t)off * ks16, ov = (uint32_t)page * vp16 + (uint32_t)off * vs16;
+            if (on) sk.load(p.k_scale + (f_ks + page * ksp + off * kss)), sv.load(p.v_scale + (f_vs + page * vsp + off * vss));
+            const uint32_t ok = page * kp + off * ks, ov = page * vp + off * vs;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i) {
               const int r = i * ROWS + row_in;
               const uint32_t bytes = mask >> r & 1u ? 16u : 0u;
-              copy16(key_to(dst, i), (const uint8_t*)p.k + (uint64_t)(__shfl_sync(~0u, ok, r) + f_k16) * 16, bytes);
-              copy16(dv + (uint32_t)(i * ROWS) * S::kRow, (const uint8_t*)p.v + (uint64_t)(__shfl_sync(~0u, ov, r) + f_v16) * 16, bytes);
+              copy16(key_to(dst, i), (const uint8_t*)p.k + (__shfl_sync(~0u, ok, r) + f_k), bytes);
+              copy16(to_v(i), (const uint8_t*)p.v + (__shfl_sync(~0u, ov, r) + f_v), bytes);
             }
           } else {
+            if (on) {
+              sk.load(p.k_scale + far_head(p.ks_head) + page * p.ks_page + off * p.ks_slot);
+              sv.load(p.v_scale + far_head(p.vs_head) + page * p.vs_page + off * p.vs_slot);
+            }
             const unsigned long long ok = page * p.k_page + off * p.k_slot, ov = page * p.v_page + off * p.v_slot;
-            const int64_t kv = w.fetch.kv * p.team + member;
-            const uint8_t *k = (const uint8_t*)p.k + kv * p.k_head + piece * 16, *v = (const uint8_t*)p.v + kv * p.v_head + piece * 16;
+            const uint8_t *k = (const uint8_t*)p.k + far_head(p.k_head) + piece * 16, *v = (const uint8_t*)p.v + far_head(p.v_head) + piece * 16;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i) {
               const int r = i * ROWS + row_in;
               const uint32_t bytes = mask >> r & 1u ? 16u : 0u;
               copy16(key_to(dst, i), k + __shfl_sync(~0u, ok, r), bytes);
-              copy16(dv + (uint32_t)(i * ROWS) * S::kRow, v + __shfl_sync(~0u, ov, r), bytes);
+              copy16(to_v(i), v + __shfl_sync(~0u, ov, r), bytes);
             }
           }
         } else {
           const bool there = entry >= 0 && entry < p.num_pages;
-          if (!there) warp_err = kErrInvalidPage;
-          const int32_t pos0 = f_sub * kSub4, off = pos0 % kPage, page = there ? entry : 0;
-          if (there && pos0 + lane >= f_lo && pos0 + lane < f_hi) load_scales(page, off + lane);
+          const int32_t pos0 = f_sub * kSub4;
+          const uint32_t page = (uint32_t)entry;
           if (!p.far && there && pos0 >= f_lo && pos0 + kSub4 <= f_hi) {
-            uint32_t k = f_k16 + (uint32_t)page * kp16 + (uint32_t)(off + row_in) * ks16;
-            uint32_t v = f_v16 + (uint32_t)page * vp16 + (uint32_t)(off + row_in) * vs16;
+            const bool second = f_sub & 1;            // of the page's halves
+            sk.load(p.k_scale + (f_ks + page * ksp + (second ? kSub4 * kss : 0u)));
+            sv.load(p.v_scale + (f_vs + page * vsp + (second ? kSub4 * vss : 0u)));
+            uint32_t k = f_k + page * kp + (second ? kSub4 * ks : 0u), v = f_v + page * vp + (second ? kSub4 * vs : 0u);
 #pragma unroll
-            for (int i = 0; i < COPIES; ++i, k += ROWS * ks16, v += ROWS * vs16) {
-              copy16(key_to(dst, i), (const uint8_t*)p.k + (uint64_t)k * 16, 16u);
-              copy16(dv + (uint32_t)(i * ROWS) * S::kRow, (const uint8_t*)p.v + (uint64_t)v * 16, 16u);
+            for (int i = 0; i < COPIES; ++i, k += ROWS * ks, v += ROWS * vs) {
+              copy16(key_to(dst, i), (const uint8_t*)p.k + k, 16u);
+              copy16(to_v(i), (const uint8_t*)p.v + v, 16u);
             }
           } else {
-            const int64_t kv = w.fetch.kv * p.team + member;
-            const uint8_t* k = (const uint8_t*)p.k + kv * p.k_head + piece * 16 + page * p.k_page + (off + row_in) * p.k_slot;
-            const uint8_t* v = (const uint8_t*)p.v + kv * p.v_head + piece * 16 + page * p.v_page + (off + row_in) * p.v_slot;
+            if (!there) warp_err = kErrInvalidPage;
+            const int64_t at = there ? entry : 0;
+            const int32_t off = pos0 % kPage;
+            sk.clear(), sv.clear();
+            if (there && pos0 + lane >= f_lo && pos0 + lane < f_hi) {
+              sk.load(p.k_scale + far_head(p.ks_head) + at * p.ks_page + (off + lane) * p.ks_slot);
+              sv.load(p.v_scale + far_head(p.vs_head) + at * p.vs_page + (off + lane) * p.vs_slot);
+            }
+            const uint8_t* k = (const uint8_t*)p.k + far_head(p.k_head) + piece * 16 + at * p.k_page + (off + row_in) * p.k_slot;
+            const uint8_t* v = (const uint8_t*)p.v + far_head(p.v_head) + piece * 16 + at * p.v_page + (off + row_in) * p.v_slot;
 #pragma unroll
             for (int i = 0; i < COPIES; ++i, k += ROWS * p.k_slot, v += ROWS * p.v_slot) {
               const int32_t pos = pos0 + i * ROWS + row_in;
               const bool on = there && pos >= f_lo && pos < f_hi;
               copy16(key_to(dst, i), on ? k : (const uint8_t*)p.k, on ? 16u : 0u);
-              copy16(dv + (uint32_t)(i * ROWS) * S::kRow, on ? v : (const uint8_t*)p.v, on ? 16u : 0u);
+              copy16(to_v(i), on ? v : (const uint8_t*)p.v, on ? 16u : 0u);
             }
           }
         }
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
       int32_t left, sub;                  // subtiles of the segment to go, and the next one
       uint32_t qf[MT][KS][4];
       float o[MT][NT][4];
-      float mx[MT][2], unit[MT][2];       // unit: what the queries were divided by
+      float mx[MT][2], unit[MT][2];       // the weights' reference; what the queries were divided by
       Two sum[MT][2];
       uint32_t live = 0;                  // bit 2t + e: the thread's tile row is a row that sees something
       bool seen = false;                  // (slots) some slot of the segment was one
@@ -529,11 +533,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
             }
         }
 
-        // running maximum; the sums are scaled where it moved, the weighted values also where their reference did
+        // The reference follows a maximum from 2^kRaise on: until then nothing is scaled, and the lanes of a row need not
+        // know one another's maxima.
         const float k_unit = pow2_of((int32_t)refs.x - 12);
-        float base[MT][2], u[MT][2];
-        bool moved = refs.y != o_ref;
-        float alpha[MT][2];
+        float u[MT][2], top[MT][2];
+        bool raise = refs.y != o_ref;
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -541,25 +545,26 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
             float m = fmaxf(s[t][0][2 * e], s[t][0][2 * e + 1]);
 #pragma unroll
             for (int n = 1; n < 4; ++n) m = fmaxf(m, fmaxf(s[t][n][2 * e], s[t][n][2 * e + 1]));
-            m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
             // in true units (the factor a power of two, never 0: -infinity stays)
             u[t][e] = BF16 ? fmaxf(fminf(k_unit * unit[t][e], 0x1p127f), 0x1p-126f) : k_unit;
-            m = fmaxf(m * u[t][e], mx[t][e]);
-            base[t][e] = reference(m);
-            alpha[t][e] = m == mx[t][e] ? 1.f : ex2(exponent(mx[t][e], base[t][e], c));
-            moved |= m != mx[t][e];
-            mx[t][e] = m;
+            top[t][e] = m * u[t][e];
+            raise |= exponent(top[t][e], mx[t][e], c) > kRaise;   // (false where both are -infinity)
           }
-        if (__any_sync(~0u, moved)) {
+        if (__any_sync(~0u, raise)) {
           const float down = pow2_of(127 + (int32_t)o_ref - (int32_t)refs.y);
           o_ref = refs.y;
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              sum[t][e] = mul2(sum[t][e], two(alpha[t][e], alpha[t][e]));
-              const float a = alpha[t][e] * down;
+              float m = top[t][e];
+              m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+              m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+              const float raised = exponent(m, mx[t][e], c) > kRaise ? m : mx[t][e];
+              const float alpha = raised == mx[t][e] ? 1.f : ex2(exponent(mx[t][e], raised, c));
+              mx[t][e] = raised;
+              sum[t][e] = mul2(sum[t][e], two(alpha, alpha));
+              const float a = alpha * down;
               const Two aa = two(a, a);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
@@ -574,7 +579,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_fp4_kernel(const __grid_co
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const Two uu = two(u[t][e], u[t][e]), minus = two(-base[t][e], -base[t][e]);
+            const float base = reference(mx[t][e]);
+            const Two uu = two(u[t][e], u[t][e]), minus = two(-base, -base);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
               // (the product with a power of two is exact: one rounding, that of the difference)

@@ -208,7 +208,8 @@ int run_attn(const AttnCall& c, const Space& space, cudaStream_t stream) {
   p.q_heads = (int32_t)Hq, p.kv_heads = (int32_t)Hk;
   p.group = a.group, p.chunks = a.chunks, p.chunk_heads = a.chunk_heads, p.group_rows = a.group_rows;
   p.row_cols = a.row_cols, p.tensor_core = a.tensor_core;
-  p.far = far;
+  // (attn_fp4.cuh: offsets in 32 bits)
+  p.far = c.fp4 && !a.tensor_core ? far || span_of(c.k) > UINT32_MAX || span_of(c.v) > UINT32_MAX : far;
   p.workers = R > 0 ? a.workers : 0;
   p.team = a.team, p.ranges = p.workers / a.team, p.kv_units = (int32_t)Hk / a.team;
   p.n_cta = R > 0 ? m.sm : 0;
