@@ -68,7 +68,7 @@ struct Memory {
                             kStage = kQueries + kTileBytes;
   static constexpr int kStageCols = FP4 ? 8 : 16, kStageRow = kStageCols + 1;   // floats
   static constexpr uint32_t kRaw = kStage + 4 * kCols * kStageRow * 4;
-  static constexpr uint32_t kRawDepth = 2, kRawStage = 2048 + 256;   // codes of 32 positions, keys' and values' scales
+  static constexpr uint32_t kRawDepth = 2, kRawStage = 2048 + 128;   // codes and scales of 32 positions
   static constexpr int kBytes = (int)(kRaw + (FP4 ? 8 * kRawDepth * kRawStage : 0)) + 1024;   // the base is aligned to 1024 by hand
 };
 
@@ -556,6 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             float unit[CH];
             int32_t v_ref[CH], new_ref = o_ref;
             if constexpr (FP4) {
+              // the values' references are there with the values (whose next tile waits for this visit's weights)
+              ok &= wait(full_v(n % kRingV), n / kRingV & 1, abort, &err);
               const float qu = q_unit[seg & 3][x];
               const int4 all = *(const int4*)refs[n % kAhead][1];
               new_ref = max(max(max(all.x, all.y), max(all.z, all.w)), o_ref);
@@ -817,11 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // Codes are unpacked on their way: 32 positions a warp, a lane 32 elements (a block) of one of 8 positions at a
         // time.  Each warp copies its positions' codes and scales into a small ring of its own, two visits ahead, over the
         // ends of segments, and unpacks them, times their scales over the largest of the 32 positions (attn_fp4.cuh), into
-        // the tile; K's warps also publish both references.  Positions that the rows do not see have the scale 0 and the
+        // the tile, and publish the reference beside it.  Positions that the rows do not see have the scale 0 and the
         // codes of some other position: their scores are not used and their weights are 0.
         const uint8_t* codes = (const uint8_t*)cache;
         const int block = lane >> 3, in8 = lane & 7;
-        const uint32_t ksp = (uint32_t)p.ks_page, kss = (uint32_t)p.ks_slot, vsp = (uint32_t)p.vs_page, vss = (uint32_t)p.vs_slot;
+        const uint32_t scale_page = (uint32_t)(values ? p.vs_page : p.ks_page), scale_slot = (uint32_t)(values ? p.vs_slot : p.ks_slot);
         constexpr uint32_t kRaw = M::kRaw, kRawDepth = M::kRawDepth, kRawStage = M::kRawStage;
         const uint32_t mine = smem + kRaw + (uint32_t)(warp - 8) * (kRawDepth * kRawStage);
         uint32_t to[4];                    // places of a block's four 16-byte pieces, in a tile
@@ -839,14 +841,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         Steps<NB, SLOTS> ahead;            // the visit whose entry is asked for
         int32_t ask_v, ask_left;           // its number in its segment, and the visits from it to the end; 0: all done
         const int32_t* list;
-        const uint8_t *base, *ks_head = nullptr, *vs_head;   // of the head
+        const uint8_t *base, *scale_head;  // of the head
         auto begin_asking = [&]() {
           const Walk<NB, SLOTS>& f = ask_at.at;
           ask_v = f.s;
           ask_left = (int32_t)min((int64_t)f.nsub, ask_at.end) - f.s;
           base = codes + f.kv * s_head + (lane & 3) * 16;
-          if (!values) ks_head = p.k_scale + f.kv * p.ks_head;
-          vs_head = p.v_scale + f.kv * p.vs_head;
+          scale_head = values ? p.v_scale + f.kv * p.vs_head : p.k_scale + f.kv * p.ks_head;
           if constexpr (SLOTS) {
             list = p.slots + (int64_t)f.row0 * p.n_slots;
             if (warp == 12 && f.row0 + 1 < p.rows)
@@ -882,8 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               page = (uint32_t)entry, off = (uint32_t)((quarter & 1) * 32 + lane);
             }
             const uint32_t dst = mine + x * kRawStage, from = on ? page * page16 + off * slot16 : 0u;
-            if (!values) copy4(dst + 2048 + lane * 4, ks_head + (on ? page * ksp + off * kss : 0u), on ? 4u : 0u);
-            copy4(dst + 2176 + lane * 4, vs_head + (on ? page * vsp + off * vss : 0u), on ? 4u : 0u);
+            copy4(dst + 2048 + lane * 4, scale_head + (on ? page * scale_page + off * scale_slot : 0u), on ? 4u : 0u);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               copy16(dst + copy_to + i * 512, base + (uint64_t)__shfl_sync(~0u, from, i * 8 + (lane >> 2)) * 16, 16u);
@@ -913,15 +913,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             copy_wait<kRawDepth - 1>();
             __syncwarp();
             const uint32_t x = n % kRawDepth, src = mine + x * kRawStage;
-            const uint32_t scale_v = fp4::lds32(src + 2176 + lane * 4);
-            const uint32_t scales = values ? scale_v : fp4::lds32(src + 2048 + lane * 4);
+            const uint32_t scales = fp4::lds32(src + 2048 + lane * 4);
             const uint32_t ref = max(__reduce_max_sync(~0u, fp4::largest_of(scales)), fp4::kLowest);
-            const uint32_t other = values ? 0 : max(__reduce_max_sync(~0u, fp4::largest_of(scale_v)), fp4::kLowest);
-            if (max(ref, other) > kMaxScaleByte) bad = max(bad, (uint32_t)kErrInvalidValue);
+            if (ref > kMaxScaleByte) bad = max(bad, (uint32_t)kErrInvalidValue);
             const uint32_t slot = n % depth;
             ok = __all_sync(~0u, wait(values ? empty_v(slot) : empty_k(slot), (n / depth & 1) ^ 1, abort, &err));
             if (!ok) break;
-            if (!values && lane == 0) refs[n % kAhead][0][quarter] = (int32_t)ref, refs[n % kAhead][1][quarter] = (int32_t)other;
+            if (lane == 0) refs[n % kAhead][values][quarter] = (int32_t)ref;
             const uint32_t dst = ring + slot * kTileBytes;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
