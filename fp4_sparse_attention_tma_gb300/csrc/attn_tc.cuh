@@ -66,7 +66,7 @@ struct Memory {
   static constexpr int kRingK = FP4 ? 2 : 3, kRingV = 2;
   static constexpr uint32_t kKeys = 0, kValues = kKeys + kRingK * kTileBytes, kQueries = kValues + kRingV * kTileBytes,
                             kStage = kQueries + kTileBytes;
-  static constexpr int kStageCols = FP4 ? 8 : 16, kStageRow = kStageCols + 1;   // floats
+  static constexpr int kStageCols = 16, kStageRow = kStageCols + 1;   // floats
   static constexpr uint32_t kRaw = kStage + 4 * kCols * kStageRow * 4;
   static constexpr uint32_t kRawDepth = 2, kRawStage = 2048 + 128;   // codes and scales of 32 positions
   static constexpr int kBytes = (int)(kRaw + (FP4 ? 8 * kRawDepth * kRawStage : 0)) + 1024;   // the base is aligned to 1024 by hand
@@ -116,6 +116,31 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// 16 columns; one or two such loads waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16], uint32_t (&s)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(s[0]),
+                 "+r"(s[1]), "+r"(s[2]), "+r"(s[3]), "+r"(s[4]), "+r"(s[5]), "+r"(s[6]), "+r"(s[7]), "+r"(s[8]),
+                 "+r"(s[9]), "+r"(s[10]), "+r"(s[11]), "+r"(s[12]), "+r"(s[13]), "+r"(s[14]), "+r"(s[15])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
@@ -592,6 +617,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 ok &= wait(done_pv(b ^ 1), (n - 1) >> 1 & 1, abort, &err);   // the last visit that added to them
                 tc_fence_after();
                 // a half of the columns each
+                if constexpr (FP4 && SPLIT) {
+                  // 16 at a time: a unit of 1024 slots has 8 visits, and the reference follows in most of them.
+                  // 8192 rows of 1024 slots: 633 us, with 8 at a time 736, with 32 (which spills) 719.
+                  const Two ff = two(f, f);
+#pragma unroll 1
+                  for (int y = 0; y < 64; y += 16) {
+                    uint32_t a[16];
+                    tmem_ld16(out_a + g * 64 + y, a);
+                    tmem_wait_ld16(a);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                      const float2 c = both(mul2(two(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), ff));
+                      a[i] = __float_as_uint(c.x), a[i + 1] = __float_as_uint(c.y);
+                    }
+                    tmem_st16(out_a + g * 64 + y, a);
+                  }
+                } else
 #pragma unroll 1
                 for (int y = 0; y < kHead; y += 8) {
                   if (y < 64 ? !had_a : !had_b) continue;
@@ -746,6 +788,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           float* stage = (float*)(raw + (smem - smem_addr(raw)) + M::kStage);
           float* give = stage + ((part_of * 2 + g) * kCols + col) * M::kStageRow;
           const float* take = stage + (((part_of ^ 1) * 2 + g) * kCols + col) * M::kStageRow;
+          if constexpr (FP4) {
+#pragma unroll 1
+            for (int at_col = 0; at_col < 32; at_col += kSome) {
+              uint32_t theirs[16], ours[16];
+              static_assert(kSome == 16, "columns of a round");
+              tmem_ld16(out_a + (part_of ^ 1) * 64 + g * 32 + at_col, theirs);
+              tmem_ld16(out_a + part_of * 64 + g * 32 + at_col, ours);
+              tmem_wait_ld16(theirs, ours);
+#pragma unroll
+              for (int c = 0; c < kSome; ++c) give[c] = has ? __uint_as_float(theirs[c]) * f : 0.f;
+              bar_sync(kAll, kSoft);
+#pragma unroll
+              for (int c = 0; c < kSome; c += 8) {
+                float r[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[i] = (has ? __uint_as_float(ours[c + i]) * f : 0.f) + take[c + i];
+                emit((int)part_of * 64 + g * 32 + at_col + c, r);
+              }
+              bar_sync(kAll, kSoft);
+            }
+          } else
 #pragma unroll 1
           for (int at_col = 0; at_col < 32; at_col += kSome) {
 #pragma unroll 1
