@@ -71,6 +71,8 @@ __device__ __forceinline__ void add_exactly(float& s, float& rest, float x) {
   s = t;
 }
 
+constexpr int kChecked = 8;
+
 // Checks every row of the call, so that all CTAs agree on whether anything is written: rows in range,
 // pages in range, no slot named twice.  Returns the error (kOk: none) to every thread.
 __device__ uint32_t check_rows(const AppendParams& p, uint32_t* table) {
@@ -83,26 +85,46 @@ __device__ uint32_t check_rows(const AppendParams& p, uint32_t* table) {
   // the bitmap holds a part of the slots at a time
   const int64_t span = bitmap ? (int64_t)entries * 32 : slots;
   for (int64_t s0 = 0; s0 < slots; s0 += span) {
-    for (uint32_t i = tid; i < entries; i += n) table[i] = bitmap ? 0u : ~0u;
+    const uint32_t none = bitmap ? 0u : ~0u;
+    for (uint32_t i = tid; i < entries / 4; i += n) ((uint4*)table)[i] = make_uint4(none, none, none, none);
     __syncthreads();
-    for (int32_t r = tid; r < p.rows; r += n) {
-      const int32_t pos = p.row_pos[r];
-      if (pos == -1) continue;
-      const int32_t req = p.row_req[r];
-      uint32_t e = kOk;
-      int32_t page = 0;
-      if (pos < 0 || req < 0 || req >= p.num_req || pos / kPage >= p.max_pages || (p.rope && pos >= p.rope_rows)) {
-        e = kErrInvalidMetadata;
-      } else {
-        page = p.page_table[(int64_t)req * p.max_pages + pos / kPage];
-        if (page < 0 || page >= p.num_pages) e = kErrInvalidPage;
+    // Some rows a thread at once, so that their loads wait for one another only by kind (8208 rows to
+    // 4 bits: 8 at once 40 us a call, 4 at once 42, one 48, not looking 33).
+    for (int32_t r0 = tid; r0 < p.rows; r0 += n * kChecked) {
+      int32_t pos[kChecked], req[kChecked], page[kChecked];
+#pragma unroll
+      for (int k = 0; k < kChecked; ++k) {
+        const int64_t r = r0 + (int64_t)k * n;
+        pos[k] = -1;
+        if (k * n >= p.rows) continue;      // (the same for all)
+        pos[k] = r < p.rows ? p.row_pos[r] : -1;
+        req[k] = r < p.rows ? p.row_req[r] : 0;
       }
-      if (e == kOk) {
-        const int64_t slot = (int64_t)page * kPage + pos % kPage;
+      uint32_t e = kOk;
+#pragma unroll
+      for (int k = 0; k < kChecked; ++k) {
+        page[k] = -1;
+        if (k * n >= p.rows || pos[k] == -1) continue;
+        if (pos[k] < 0 || req[k] < 0 || req[k] >= p.num_req || pos[k] / kPage >= p.max_pages ||
+            (p.rope && pos[k] >= p.rope_rows)) {
+          e = max(e, (uint32_t)kErrInvalidMetadata);
+          pos[k] = -1;
+        } else {
+          page[k] = p.page_table[(int64_t)req[k] * p.max_pages + pos[k] / kPage];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kChecked; ++k) {
+        if (k * n >= p.rows || pos[k] == -1) continue;
+        if (page[k] < 0 || page[k] >= p.num_pages) {
+          e = max(e, (uint32_t)kErrInvalidPage);
+          continue;
+        }
+        const int64_t slot = (int64_t)page[k] * kPage + pos[k] % kPage;
         if (bitmap) {
           if (slot >= s0 && slot < s0 + span) {
             const uint32_t bit = 1u << (slot & 31);
-            if (atomicOr(&table[(slot - s0) >> 5], bit) & bit) e = kErrInvalidPage;
+            if (atomicOr(&table[(slot - s0) >> 5], bit) & bit) e = max(e, (uint32_t)kErrInvalidPage);
           }
         } else {
           // open addressing: at most half of the entries are taken
@@ -112,7 +134,7 @@ __device__ uint32_t check_rows(const AppendParams& p, uint32_t* table) {
             const uint32_t old = atomicCAS(&table[at], ~0u, key);
             if (old == ~0u) break;
             if (old == key) {
-              e = kErrInvalidPage;
+              e = max(e, (uint32_t)kErrInvalidPage);
               break;
             }
             at = (at + 1) & (entries - 1);
@@ -554,7 +576,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
           out[x] = pack8<BF16>(y);
         }
         T* to = (T*)f.out + rs[u] * f.row + hs[u] * f.out_head + j * 16;
-        if (p.wide) {
+        if (p.wide) {   // (65535 slots x 8 heads 72 us, in halves 85)
           store32(to, out[0], out[1]);
         } else {
           *(uint4*)to = out[0], *(uint4*)(to + 8) = out[1];
@@ -582,7 +604,11 @@ cudaError_t launch_append_as(AppendParams p, int sm, cudaStream_t stream) {
     return p.rows * (q + k * (p.v.data ? 2 : 1));
   };
   // Few chunks: one head's worth a lane, small CTAs on as many SMs as there are.  Many: four in flight a lane, one CTA an SM
-  // (every CTA looks over all rows).
+  // (every CTA looks over all rows).  Measured (us between events; one head, four), 128 elements, 64 heads on 8:
+  // to 4 bits, 4 chunks an SM 13, 17, 8 chunks 15, 15, 16 chunks 15, 17, 26 chunks 19, 17, 45 chunks 23, 19; in
+  // 16 bits, up to 16 chunks 9, 9, 26 chunks 11, 11, 45 chunks 15, 11.
+  // The slots named twice are found in a table with room for twice the rows; past 2^14 rows it would not fit, and
+  // the bitmap, which takes a walk over the rows for every 2^20 slots, does it (8208 rows 48, 49; 1200 rows 19, 21).
   p.table_bits = 0;
   for (int b = 6; b <= 15 && !p.table_bits; ++b)
     if ((int64_t)1 << b >= 2 * (int64_t)p.rows) p.table_bits = b;
@@ -611,8 +637,10 @@ cudaError_t launch_append_dim(const AppendParams& p, int dim, bool fp4, int sm, 
 
 template <bool BF16, int D>
 cudaError_t launch_gather_as(const GatherParams& p, int sm, cudaStream_t stream) {
+  // One head a thread where that is a few waves of CTAs, else four at a time.  Measured (us between events; one, four),
+  // 128 elements: 512 slots x 1 head 7, 9; x 8 heads: 1000 slots 9, 9, 4000 13, 13, 8000 17, 19, 16000 25, 27, 65535 79, 72.
   const int64_t ctas = ((int64_t)p.n * p.kv_heads * (D / 16) + kGatherThreads - 1) / kGatherThreads;
-  if (ctas <= 2 * sm)
+  if (ctas <= 32 * (int64_t)sm)
     gather_kernel<BF16, D, 1><<<(int)ctas + 1, kGatherThreads, 0, stream>>>(p);
   else
     gather_kernel<BF16, D, 4><<<sm * 4 + 1, kGatherThreads, 0, stream>>>(p);

@@ -51,6 +51,21 @@ bool tensor_core_for(int64_t group, int64_t rows, int64_t per_req, int64_t kv_he
   return per_req <= 2 && positions >= 2048 && (rows + per_req - 1) / per_req * kv_heads <= 2 * sm;
 }
 
+// The same for a 4-bit cache (attn_fp4.cuh; its form on tensor memory is attn_tc.cuh's).  There decoding the
+// codes costs more than the products: attn_tc.cuh does it once for 64 pairs of query head and row, attn_fp4.cuh
+// for 16 or 32, by more warps.  Measured (us between events; attn_tc.cuh, attn_fp4.cuh), fp16, heads on one:
+//   32 requests of 4096..65536: 1 row, 8 heads 74, 75, 16 75, 82, 17 76, 118, 32 76, 127, 64 81, 212, 128 133, 357;
+//     2 rows, 8 heads 105, 82, 12 106, 126, 16 109, 127, 17 108, 200, 32 112, 211, 64 120, 358, 128 239, 661
+//   2 rows of 700..1000 positions: 8 heads 29, 25, 12 29, 33, 16 30, 37, 24 29, 46, 64 33, 40
+//   2 rows of 100..200: 12 heads 25, 23, 24 25, 24, 64 27, 28; windows of 100, 256 requests: 16 51, 40, 24 52, 43,
+//     64 58, 56, 128 70, 73 (how long a window is, the host does not know)
+//   chosen slots, 512 rows of 1024: 16 heads 61, 48, 20 60, 85, 64 67, 146; 8192 of 128: 16 277, 85, 24 235, 196,
+//     32 241, 211, 64 267, 378; 64 of 16384: 16 72, 70, 20 73, 133
+bool tensor_core_for_fp4(int64_t group, int64_t per_req, int64_t dim, bool slots, bool far) {
+  if (dim != 128 || far) return false;
+  return group > 16 || (!slots && group > 10 && group * per_req > 16);
+}
+
 // How the query heads of a key-value head are laid on the kernel's tiles.  The page table's rows stand for
 // the number of requests, which the host does not know: under a table of more rows than the call has, rows
 // are taken for single ones (one call between events: 32 requests x 2 rows x 64 heads on one 178 us, 120
@@ -65,7 +80,7 @@ AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_head
   AttnPlan a{};
   a.group = (int32_t)(q_heads / kv_heads);
   const int64_t per_req = rows > num_req && num_req > 0 ? (rows + num_req - 1) / num_req : 1;
-  a.tensor_core = fp4 ? dim == 128 && !far && a.group > 16
+  a.tensor_core = fp4 ? tensor_core_for_fp4(a.group, per_req, dim, slots, far)
                        : tensor_core_for(a.group, rows, per_req, kv_heads, dim, positions, slots, far, sm);
   const int32_t most = a.tensor_core ? 64 : dim <= 128 && (int64_t)a.group * per_req > 16 ? 32 : 16;
   a.chunks = (a.group + most - 1) / most;
