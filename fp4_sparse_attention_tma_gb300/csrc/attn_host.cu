@@ -56,6 +56,7 @@ bool tensor_core_for(int64_t group, int64_t rows, int64_t per_req, int64_t kv_he
 // for 16 or 32, by more warps.  Measured (us between events; attn_tc.cuh, attn_fp4.cuh), fp16, heads on one:
 //   32 requests of 4096..65536: 1 row, 8 heads 74, 75, 16 75, 82, 17 76, 118, 32 76, 127, 64 81, 212, 128 133, 357;
 //     2 rows, 8 heads 105, 82, 12 106, 126, 16 109, 127, 17 108, 200, 32 112, 211, 64 120, 358, 128 239, 661
+//     (2 rows, 64 heads on 4 351, 347); 4 rows, 12 heads 185, 206, 16 188, 211
 //   2 rows of 700..1000 positions: 8 heads 29, 25, 12 29, 33, 16 30, 37, 24 29, 46, 64 33, 40
 //   2 rows of 100..200: 12 heads 25, 23, 24 25, 24, 64 27, 28; windows of 100, 256 requests: 16 51, 40, 24 52, 43,
 //     64 58, 56, 128 70, 73 (how long a window is, the host does not know)
