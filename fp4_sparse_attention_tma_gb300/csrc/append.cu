@@ -71,6 +71,20 @@ __device__ __forceinline__ void add_exactly(float& s, float& rest, float x) {
   s = t;
 }
 
+// The same for two sums at once (a - b as b * -1 + a, which rounds alike).
+__device__ __forceinline__ void add_exactly(Two& s, Two& rest, Two x) {
+  const Two minus = two(-1.f, -1.f);
+  const Two t = add2(s, x), b = fma2(s, minus, t);
+  rest = add2(rest, add2(fma2(fma2(b, minus, t), minus, s), fma2(b, minus, x)));
+  s = t;
+}
+// The larger magnitude; NaN if one is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
 constexpr int kChecked = 8;
 
 // Checks every row of the call, so that all CTAs agree on whether anything is written: rows in range,
@@ -183,8 +197,10 @@ __device__ __forceinline__ void unpack4(const uint2& u, float* x) {
 }
 
 // A warp takes U x 32 / (D / 8) heads of a row at a time: 16 bytes of a head a lane, D / 8 lanes a head.
-// Bound by HBM where rows are many, by the chain position, page entry, store and one launch where they are
-// few.
+// Bound by HBM in 16 bits where rows are many (8192 rows, 64 heads of 128 on 8: 336 MB each way in 66 us, 5.1 TB/s
+// each pass with the check of the rows, 4 us, before it); to 4 bits by the instructions between (8208 rows, 8
+// heads of 64: 76 MB in 25 us; 24000 rows, 8 heads of 128, without norm and rotation: 75 us, 1900 instructions a
+// row); by the chain position, page entry, store and one launch where rows are few (one row 3 us of device time).
 template <bool FP4, int U>
 constexpr int kMaxThreads = FP4 || U == 1 ? 512 : 768;   // of a CTA
 template <int U>
@@ -422,7 +438,7 @@ __global__ void __launch_bounds__(kMaxThreads<FP4, U>, 1) append_kernel(const __
       // the angles of this lane's dimensions: 4 pairs of neighbours, or 8 of a half whose partners another lane has
       bool upper = false;
       int partner = lane;
-      float co[8], si[8];
+      float co[8], si[8];                // (halves: the sines with the sign that the lane's half has)
       if (turned) {
         const float* t = p.rope + (int64_t)pos * p.rot;
         if (p.pairs) {
@@ -438,6 +454,8 @@ __global__ void __launch_bounds__(kMaxThreads<FP4, U>, 1) append_kernel(const __
             *(float4*)&co[i] = *(const float4*)(t + j + i);
             *(float4*)&si[i] = *(const float4*)(t + p.rot / 2 + j + i);
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) si[i] = upper ? si[i] : -si[i];
         }
       }
       uint8_t* to = (uint8_t*)(kind == 0 ? p.out_q : dst.data) + at + (int64_t)(h0 + sub) * head + in * 4;
@@ -449,9 +467,18 @@ __global__ void __launch_bounds__(kMaxThreads<FP4, U>, 1) append_kernel(const __
         float x[8];
         unpack8<BF16>(*(const uint4*)(mine + u * 512 + pa * 2), x);
         if (weight) {
-          float s = 0.f, rest = 0.f;      // squares of 16-bit numbers are exact in fp32
+          // squares of 16-bit numbers are exact in fp32
+          Two s2 = two(x[0], x[1]), rest2 = two(0.f, 0.f);
+          s2 = mul2(s2, s2);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) add_exactly(s, rest, __fmul_rn(x[i], x[i]));
+          for (int i = 2; i < 8; i += 2) {
+            const Two t = two(x[i], x[i + 1]);
+            add_exactly(s2, rest2, mul2(t, t));
+          }
+          const float2 ss = both(s2), rr = both(rest2);
+          float s = ss.x, rest = __fadd_rn(rr.x, rr.y), less = 0.f;
+          add_exactly(s, less, ss.y);
+          rest = __fadd_rn(rest, less);
 #pragma unroll
           for (int o = 1; o < L; o <<= 1) {
             const float s1 = __shfl_xor_sync(~0u, s, o), r1 = __shfl_xor_sync(~0u, rest, o);
@@ -463,7 +490,10 @@ __global__ void __launch_bounds__(kMaxThreads<FP4, U>, 1) append_kernel(const __
           const float sum = fabsf(s) < INFINITY ? __fadd_rn(s, rest) : s;
           const float r = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(sum / D, p.eps)));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
+          for (int i = 0; i < 8; i += 2) {
+            const float2 y = both(mul2(mul2(two(x[i], x[i + 1]), two(r, r)), two(w[i], w[i + 1])));
+            x[i] = y.x, x[i + 1] = y.y;
+          }
         }
         if (turn) {
           if (p.pairs) {
@@ -477,18 +507,19 @@ __global__ void __launch_bounds__(kMaxThreads<FP4, U>, 1) append_kernel(const __
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float o = __shfl_sync(~0u, x[i], partner);
+            for (int i = 0; i < 8; i += 2) {
+              const float o0 = __shfl_sync(~0u, x[i], partner), o1 = __shfl_sync(~0u, x[i + 1], partner);
               if (turned) {
-                const float cross = __fmul_rn(o, si[i]), own = __fmul_rn(x[i], co[i]);
-                x[i] = upper ? __fadd_rn(own, cross) : __fsub_rn(own, cross);
+                const float2 y = both(add2(mul2(two(x[i], x[i + 1]), two(co[i], co[i + 1])),
+                                           mul2(two(o0, o1), two(si[i], si[i + 1]))));
+                x[i] = y.x, x[i + 1] = y.y;
               }
             }
           }
         }
-        uint32_t top = 0;                 // as integers: a NaN counts as the largest
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        // (as integers from here on: a NaN counts as the largest)
+        uint32_t top = __float_as_uint(larger(larger(larger(x[0], x[1]), larger(x[2], x[3])),
+                                              larger(larger(x[4], x[5]), larger(x[6], x[7]))));
         top = max(top, __shfl_xor_sync(~0u, top, 1));
         top = max(top, __shfl_xor_sync(~0u, top, 2));
         const uint32_t e = scale_byte(top), codes = to_codes(x, e);

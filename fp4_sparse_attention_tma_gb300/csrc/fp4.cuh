@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "pairs.cuh"
+
 namespace idxk {
 
 constexpr int kFp4Block = 32;
@@ -27,12 +29,14 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
 // 8 elements over their block's scale as codes, element 0 in the lowest bits: the multiplication by a
 // power of two is exact, the conversion rounds to the nearest code, ties to the even one.
 __device__ __forceinline__ uint32_t to_codes(const float (&x)[8], uint32_t e) {
-  // 2^(127 - e); e = 255 (not finite): codes 0
-  const float inv = e == 255 ? 0.f : __uint_as_float((254u - e) << 23);
+  const float inv = __uint_as_float((254u - e) << 23);   // 2^(127 - e)
   uint32_t r;
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = e == 255 ? 0.f : x[i] * inv;
+  for (int i = 0; i < 8; i += 2) {
+    const float2 z = both(mul2(two(x[i], x[i + 1]), two(inv, inv)));
+    y[i] = z.x, y[i + 1] = z.y;
+  }
   asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 t0, %2, %1;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 t1, %4, %3;\n\t"
@@ -41,7 +45,7 @@ __device__ __forceinline__ uint32_t to_codes(const float (&x)[8], uint32_t e) {
       "mov.b32 %0, {t0, t1, t2, t3};\n\t}"
       : "=r"(r)
       : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
-  return r;
+  return e == 255 ? 0u : r;   // not finite: codes 0
 }
 
 // The 8 codes of a word as pairs of fp16 numbers (exact).

@@ -516,3 +516,30 @@ def test_from_writing_to_attending(hq, hk, dim):
         A.check_rows(q, out, lse, rows, dim ** -0.5)
         m.idx_attn_selected_fp4(q, *cache, slots, dim ** -0.5, out, out_lse=lse)
         A.check_rows(q, out, lse, rows, dim ** -0.5)
+
+
+@pytest.mark.parametrize("heads", [(64, 2), (16, 1)])
+def test_offsets_beyond_32_bits_many_heads(heads):
+    """A cache of more than 2^32 bytes where its tiles are fed to the tensor memory's products."""
+    import torch
+    import fp4_sparse_attention_tma_gb300 as m
+    (hq, hk), pages, dim, each, rows = heads, 4300, 128, 1 << 20, 2
+    codes = torch.empty(pages * each, dtype=torch.uint8, device="cuda")
+    assert codes.numel() > 2 ** 32
+    used = [pages - 1, 0, pages - 2, 4097]
+    k = codes.as_strided((pages, PAGE, hk, dim // 2), (each, hk * dim // 2, dim // 2, 1))
+    v = codes.as_strided((pages, PAGE, hk, dim // 2), (each, hk * dim // 2, dim // 2, 1), 262144)
+    ks, vs = (torch.randint(120, 128, (pages, PAGE, hk, dim // 32), dtype=torch.uint8, device="cuda") for _ in range(2))
+    for t in (k, v):
+        for p in used:
+            t[p] = torch.randint(0, 256, t[p].shape, dtype=torch.uint8, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table, pos = i32([used]), torch.arange(250, device="cuda")
+    q = torch.randn(rows, hq, dim, device="cuda").to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty(rows, hq, device="cuda")
+    m.idx_attn_paged_fp4(q, k, ks, v, vs, table, i32([0, 0]), i32([0, 3]), i32([250, 251]), 0.06, out, out_lse=lse)
+    at = lambda pos: tuple(t[table[0][pos // PAGE].long(), pos % PAGE] for t in (k, ks, v, vs))
+    A.check_rows(q, out, lse, [at(pos), at(pos[2:] + 1)], 0.06)
+    slots = (table[0][pos // PAGE].long() * PAGE + pos % PAGE).to(torch.int32)[None].expand(rows, -1).contiguous()
+    m.idx_attn_selected_fp4(q, k, ks, v, vs, slots, 0.06, out, out_lse=lse)
+    A.check_rows(q, out, lse, [at(pos)] * rows, 0.06)
