@@ -12,8 +12,9 @@ The operation follows "[FlyDSL] Add FP4 LiteTopK prefill operator"
 K cache, score = sum_h w * ReLU(q_h . k), and return the exact TopK positions
 (physical slots and optional raw positions) without materialising the
 [rows, context] score matrix.  The attention over the cache that the selection
-serves (paged, and over the selected slots) and the cache's eviction by
-accumulated weight are here as well.
+serves (paged, and over the selected slots), the cache's eviction by
+accumulated weight and the writing of new tokens into it are here as well, the
+cache in 16 bits or in the indexer's 4-bit format.
 """
 from __future__ import annotations
 

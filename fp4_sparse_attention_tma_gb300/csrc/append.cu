@@ -197,8 +197,8 @@ __device__ __forceinline__ void unpack4(const uint2& u, float* x) {
 }
 
 // A warp takes U x 32 / (D / 8) heads of a row at a time: 16 bytes of a head a lane, D / 8 lanes a head.
-// Bound by HBM in 16 bits where rows are many (8192 rows, 64 heads of 128 on 8: 336 MB each way in 66 us, 5.1 TB/s
-// each pass with the check of the rows, 4 us, before it); to 4 bits by the instructions between (8208 rows, 8
+// Bound by HBM in 16 bits where rows are many (8192 rows, 64 heads of 128 on 8: 336 MB in 64 us, 5.2 TB/s with
+// the check of the rows, 4 us, before it; 131072 rows: 941 us, 5.7 TB/s); to 4 bits by the instructions between (8208 rows, 8
 // heads of 64: 76 MB in 25 us; 24000 rows, 8 heads of 128, without norm and rotation: 75 us, 1900 instructions a
 // row); by the chain position, page entry, store and one launch where rows are few (one row 3 us of device time).
 template <bool FP4, int U>
