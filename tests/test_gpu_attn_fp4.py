@@ -543,3 +543,23 @@ def test_offsets_beyond_32_bits_many_heads(heads):
     slots = (table[0][pos // PAGE].long() * PAGE + pos % PAGE).to(torch.int32)[None].expand(rows, -1).contiguous()
     m.idx_attn_selected_fp4(q, k, ks, v, vs, slots, 0.06, out, out_lse=lse)
     A.check_rows(q, out, lse, [at(pos)] * rows, 0.06)
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (64, 1)])
+def test_no_rows(heads):
+    """No rows, and no pages either: nothing to do, and no error."""
+    import torch
+    import fp4_sparse_attention_tma_gb300 as m
+    hq, hk = heads
+    z = lambda *s, dtype=torch.uint8: torch.zeros(*s, dtype=dtype, device="cuda")
+    i32 = lambda *s: z(*s, dtype=torch.int32)
+    for pages in (0, 2):
+        cache = [z(pages, PAGE, hk, w) for w in (64, 4, 64, 4)]
+        q, out = (z(0, hq, 128, dtype=torch.bfloat16) for _ in range(2))
+        lse = z(0, hq, dtype=torch.float32)
+        m.idx_attn_paged_fp4(q, *cache, i32(1, 2), i32(0), i32(0), i32(0), 0.1, out, out_lse=lse)
+        m.idx_attn_selected_fp4(q, *cache, i32(0, 8), 0.1, out, out_lse=lse)
+        st = i32(1) + 7
+        ws = z(m.idx_attn_selected_fp4_scratch_bytes(0, hq, hk, 128, 8))
+        m.idx_attn_selected_fp4_async(q, *cache, i32(0, 8), 0.1, out, ws, st)
+        assert int(st.item()) == 0
