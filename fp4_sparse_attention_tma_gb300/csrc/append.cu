@@ -19,7 +19,8 @@
 namespace idxk {
 namespace {
 
-constexpr int kBitmapBytes = 128 * 1024;
+constexpr int kMostBits = 15;                        // of the words of the table or bitmap that finds slots named twice
+constexpr int kTableBytes = 4 << kMostBits;
 constexpr int kGatherThreads = 256;
 
 template <bool BF16>
@@ -93,10 +94,10 @@ __device__ uint32_t check_rows(const AppendParams& p, uint32_t* table) {
   __shared__ uint32_t err;
   const int tid = threadIdx.x, n = blockDim.x;
   if (tid == 0) err = kOk;
-  const bool bitmap = p.table_bits == 0;
-  const uint32_t entries = bitmap ? kBitmapBytes / 4 : 1u << p.table_bits;
+  const bool bitmap = p.bitmap;
+  const uint32_t entries = 1u << p.table_bits;
   const int64_t slots = (int64_t)p.num_pages * kPage;
-  // the bitmap holds a part of the slots at a time
+  // the bitmap holds a part of the slots at a time; neighbours in different words, as rows of a prompt follow one another
   const int64_t span = bitmap ? (int64_t)entries * 32 : slots;
   for (int64_t s0 = 0; s0 < slots; s0 += span) {
     const uint32_t none = bitmap ? 0u : ~0u;
@@ -137,8 +138,8 @@ __device__ uint32_t check_rows(const AppendParams& p, uint32_t* table) {
         const int64_t slot = (int64_t)page[k] * kPage + pos[k] % kPage;
         if (bitmap) {
           if (slot >= s0 && slot < s0 + span) {
-            const uint32_t bit = 1u << (slot & 31);
-            if (atomicOr(&table[(slot - s0) >> 5], bit) & bit) e = max(e, (uint32_t)kErrInvalidPage);
+            const uint32_t x = (uint32_t)(slot - s0), bit = 1u << (x >> p.table_bits);
+            if (atomicOr(&table[x & (entries - 1)], bit) & bit) e = max(e, (uint32_t)kErrInvalidPage);
           }
         } else {
           // open addressing: at most half of the entries are taken
@@ -679,7 +680,7 @@ template <bool BF16, int D, bool FP4, int U>
 cudaError_t launch_append_u(const AppendParams& p, int threads, int grid, cudaStream_t stream) {
   auto* kernel = append_kernel<BF16, D, FP4, U>;
   static std::atomic<bool> done[64];
-  cudaError_t e = set_smem_once(kernel, kBitmapBytes + kRingBytes<FP4, U>, done);
+  cudaError_t e = set_smem_once(kernel, kTableBytes + kRingBytes<FP4, U>, done);
   if (e != cudaSuccess) return e;
   kernel<<<grid, threads, p.table_bytes + threads / 32 * kStages<U> * U * 512, stream>>>(p);
   return cudaGetLastError();
@@ -696,12 +697,17 @@ cudaError_t launch_append_as(AppendParams p, int sm, cudaStream_t stream) {
   // (every CTA looks over all rows).  Measured (us between events; one head, four), 128 elements, 64 heads on 8:
   // to 4 bits, 4 chunks an SM 13, 17, 8 chunks 15, 15, 16 chunks 15, 17, 26 chunks 19, 17, 45 chunks 23, 19; in
   // 16 bits, up to 16 chunks 9, 9, 26 chunks 11, 11, 45 chunks 15, 11.
-  // The slots named twice are found in a table with room for twice the rows; past 2^14 rows it would not fit, and
-  // the bitmap, which takes a walk over the rows for every 2^20 slots, does it (8208 rows 48, 49; 1200 rows 19, 21).
-  p.table_bits = 0;
-  for (int b = 6; b <= 15 && !p.table_bits; ++b)
-    if ((int64_t)1 << b >= 2 * (int64_t)p.rows) p.table_bits = b;
-  p.table_bytes = p.table_bits ? 4 << p.table_bits : kBitmapBytes;
+  // The slots named twice are found in a table with room for twice the rows.  Past 2^14 rows it would not fit, and a bitmap
+  // does it, which takes a walk over the rows for every 2^20 slots (one walk: as fast as the table, 8208 rows 37.5 us with
+  // either; bits of neighbouring slots in one word instead: 96000 rows 418 -> 430).
+  const int64_t slots = (int64_t)p.num_pages * kPage;
+  int table = 0, map = 6;
+  for (int b = 6; b <= kMostBits && !table; ++b)
+    if ((int64_t)1 << b >= 2 * (int64_t)p.rows) table = b;
+  while (map < kMostBits && (int64_t)32 << map < slots) ++map;
+  p.bitmap = !table;
+  p.table_bits = p.bitmap ? map : table;
+  p.table_bytes = 4 << p.table_bits;
   if (chunks(H) <= (int64_t)sm * 16) {
     const int64_t n = chunks(H);
     const int64_t want = (n + sm - 1) / sm;      // warps an SM

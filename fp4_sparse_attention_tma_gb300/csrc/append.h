@@ -35,8 +35,9 @@ struct AppendParams {
   int64_t oq_row, oq_head, oqs_row, oqs_head;
   int32_t q_in_place;
   PagedOut k_dst, v_dst;
-  int32_t table_bytes;              // of shared memory, before the rings of the warps
-  int32_t table_bits;               // log2 of the entries of the table that finds slots named twice, or 0: a bitmap
+  int32_t table_bytes;              // of what finds slots named twice, in shared memory before the rings of the warps
+  int32_t table_bits;               // log2 of its words: slots' numbers, or (bitmap) a bit for each slot
+  int32_t bitmap;
   uint32_t* status_out;
 };
 

@@ -481,3 +481,24 @@ def test_offsets_beyond_32_bits():
     assert c.run() == 0
     assert torch.equal(c.caches[0][pages - 1, 6], c.k[0]) and torch.equal(c.caches[1][pages - 1, 6], c.v[0])
     assert int((c.caches[0] != 0).any(-1).sum()) == 8
+
+
+@pytest.mark.parametrize("pages", [3, 40, 200, 17000])
+@pytest.mark.parametrize("n", [2, 33, 190])
+def test_slots_named_twice_in_pools_of_many_sizes(pages, n):
+    """Found whatever finds them; slots that differ by a page, or by many, are not taken for one another."""
+    import torch
+    rng = np.random.default_rng(pages + n)
+    mp = min(pages, 190)
+    n = min(n, mp * PAGE)
+    table = np.sort(rng.permutation(pages)[:mp]).reshape(1, mp).astype(np.int32)
+    for step in (1, PAGE):                       # neighbours; the first slots of the pages, then the second ones
+        at = [(i * step) % (mp * PAGE) + (i * step) // (mp * PAGE) for i in range(n)]
+        c = Case([(0, x) for x in at], 0, 1, 64, "f16", True, norm=None, table=table, pages=pages, nr=1, mp=mp)
+        assert c.run() == 0
+        c.check()
+        c.before = [x.clone() for x in c.caches]
+        c.pos[0] = at[n - 1]
+        c.k.zero_()
+        assert c.run() == INVALID_PAGE
+        assert all(bool((a == b).all()) for a, b in zip(c.caches, c.before))
