@@ -198,10 +198,10 @@ __device__ __forceinline__ void unpack4(const uint2& u, float* x) {
 }
 
 // A warp takes U x 32 / (D / 8) heads of a row at a time: 16 bytes of a head a lane, D / 8 lanes a head.
-// Bound by HBM in 16 bits where rows are many (8192 rows, 64 heads of 128 on 8: 336 MB in 64 us, 5.2 TB/s with
-// the check of the rows, 4 us, before it; 131072 rows: 941 us, 5.7 TB/s); to 4 bits by the instructions between (8208 rows, 8
-// heads of 64: 76 MB in 25 us; 24000 rows, 8 heads of 128, without norm and rotation: 75 us, 1900 instructions a
-// row); by the chain position, page entry, store and one launch where rows are few (one row 3 us of device time).
+// Bound by HBM in 16 bits where rows are many (8192 rows, 64 heads of 128 on 8: 336 MB in 63 us, 5.3 TB/s with
+// the check of the rows, 4 us, before it; 131072 rows: 930 us, 5.8 TB/s); to 4 bits by the instructions between and the
+// check (24000 rows, 8 heads of 128 of each kind, without norm and rotation: 223 MB in 65 us, of them 15 for the check; half
+// of the issue slots used); by the chain position, page entry, store and one launch where rows are few (one row 3 us of device time).
 template <bool FP4, int U>
 constexpr int kMaxThreads = FP4 || U == 1 ? 512 : 768;   // of a CTA
 template <int U>
