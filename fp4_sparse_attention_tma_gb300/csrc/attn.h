@@ -101,8 +101,13 @@ inline AttnLayout attn_layout(int64_t workers, int64_t n_cta, int64_t tile, int6
 // memory of an SM).
 inline int attn_warps(int32_t dim, int32_t tile) { return dim == 256 ? 4 : dim == 128 ? 8 : tile == 32 ? 12 : 16; }
 
-// The same of the kernel of attn_fp4.cuh.
-inline int attn_fp4_warps(int32_t dim, int32_t tile) { return dim == 256 ? 6 : tile == 32 ? 8 : 12; }
+// The same of the kernel of attn_fp4.cuh.  Measured (us between events), head dimension 128, tiles of 16: 12 and 8 warps, 32
+// requests x 2 rows x 64 heads on 8 314, 328; over slots, whose addresses take more registers than 12 warps leave, 64 rows
+// x 1024 x 32 heads on 8 52, 48, 512 rows 239, 220.  64: 12 and 16 warps 195, 205; over slots 512 rows 138, 134; 64 rows
+// 35, 37.  256: 6 and 4 warps 947, 985; over slots 679, 672.
+inline int attn_fp4_warps(int32_t dim, int32_t tile, bool slots) {
+  return dim == 256 ? 6 : tile == 32 || (slots && dim == 128) ? 8 : 12;
+}
 
 // Warps of a team there: key-value heads whose scales (4 bytes a position at head dimension 128) may share a sector of
 // memory are read at the same time, by warps of one CTA.  32 requests x 2 rows x 64 heads on 8, slot by slot: each

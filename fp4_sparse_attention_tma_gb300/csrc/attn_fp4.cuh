@@ -728,7 +728,7 @@ template <bool BF16, bool SLOTS>
 cudaError_t pick(const AttnParams& p, int sm_count, cudaStream_t stream) {
   if (p.dim == 64 && p.tile == 16) return launch_one<BF16, 64, 16, 12, 3, SLOTS>(p, sm_count, stream);
   if (p.dim == 64 && p.tile == 32) return launch_one<BF16, 64, 32, 8, 3, SLOTS>(p, sm_count, stream);
-  if (p.dim == 128 && p.tile == 16) return launch_one<BF16, 128, 16, 12, 3, SLOTS>(p, sm_count, stream);
+  if (p.dim == 128 && p.tile == 16) return launch_one<BF16, 128, 16, SLOTS ? 8 : 12, 3, SLOTS>(p, sm_count, stream);
   if (p.dim == 128 && p.tile == 32) return launch_one<BF16, 128, 32, 8, 3, SLOTS>(p, sm_count, stream);
   if (p.dim == 256 && p.tile == 16) return launch_one<BF16, 256, 16, 6, 3, SLOTS>(p, sm_count, stream);
   return cudaErrorInvalidValue;

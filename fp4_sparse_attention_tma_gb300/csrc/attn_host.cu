@@ -60,8 +60,8 @@ bool tensor_core_for(int64_t group, int64_t rows, int64_t per_req, int64_t kv_he
 //   2 rows of 700..1000 positions: 8 heads 29, 25, 12 29, 33, 16 30, 37, 24 29, 46, 64 33, 40
 //   2 rows of 100..200: 12 heads 25, 23, 24 25, 24, 64 27, 28; windows of 100, 256 requests: 16 51, 40, 24 52, 43,
 //     64 58, 56, 128 70, 73 (how long a window is, the host does not know)
-//   chosen slots, 512 rows of 1024: 16 heads 61, 48, 20 60, 85, 64 67, 146; 8192 of 128: 16 277, 85, 24 235, 196,
-//     32 241, 211, 64 267, 378; 64 of 16384: 16 72, 70, 20 73, 133
+//   chosen slots, 512 rows of 1024: 16 heads 61, 46, 20 58, 85, 64 67, 146; 8192 of 128: 16 277, 87, 24 235, 196,
+//     32 230, 211, 64 267, 378; 64 of 16384: 16 72, 70, 20 72, 133
 bool tensor_core_for_fp4(int64_t group, int64_t per_req, int64_t dim, bool slots, bool far) {
   if (dim != 128 || far) return false;
   return group > 16 || (!slots && group > 10 && group * per_req > 16);
@@ -95,7 +95,7 @@ AttnPlan plan_of(int64_t rows, int64_t num_req, int64_t q_heads, int64_t kv_head
     a.group_rows = a.chunks > 1 ? 1 : most / a.group;
     a.row_cols = a.chunk_heads;
     a.tile = most;
-    a.workers = sm * (fp4 ? attn_fp4_warps((int32_t)dim, most) : attn_warps((int32_t)dim, most));
+    a.workers = sm * (fp4 ? attn_fp4_warps((int32_t)dim, most, slots) : attn_warps((int32_t)dim, most));
   }
   a.team = fp4 && !a.tensor_core ? attn_fp4_team(kv_heads, a.workers / sm) : 1;
   return a;
