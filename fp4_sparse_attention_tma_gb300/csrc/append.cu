@@ -266,6 +266,8 @@ __global__ void __launch_bounds__(kMaxThreads<FP4, U>, 1) append_kernel(const __
   };
   auto fetch = [&](int stage) {
     if (to_fetch > 0) {
+      // every lane has read the stage: what is rotated half by half is read from pieces that other lanes copy
+      __syncwarp();
       --to_fetch;
       if (!BY_KIND) aim();
       const T* at = from + ahead.row * from_row;
