@@ -72,7 +72,8 @@ __device__ __forceinline__ void add_exactly(float& s, float& rest, float x) {
   s = t;
 }
 
-// The same for two sums at once (a - b as b * -1 + a, which rounds alike).
+// The same for two sums at once (a - b as b * -1 + a, which rounds alike).  x is a square that fp32 holds exactly, so that
+// it makes no difference whether the sums that take it are fused with its product.
 __device__ __forceinline__ void add_exactly(Two& s, Two& rest, Two x) {
   const Two minus = two(-1.f, -1.f);
   const Two t = add2(s, x), b = fma2(s, minus, t);
@@ -571,9 +572,9 @@ __global__ void __launch_bounds__(kMaxThreads<FP4, U>, 1) append_kernel(const __
             for (int i = 0; i < 8; i += 2) {
               const float o0 = __shfl_sync(~0u, x[i], partner), o1 = __shfl_sync(~0u, x[i + 1], partner);
               if (turned) {
-                const float2 y = both(add2(mul2(two(x[i], x[i + 1]), two(co[i], co[i + 1])),
-                                           mul2(two(o0, o1), two(si[i], si[i + 1]))));
-                x[i] = y.x, x[i + 1] = y.y;
+                // (one by one: a packed sum and a packed product that it takes may become one operation, of one rounding)
+                x[i] = __fadd_rn(__fmul_rn(x[i], co[i]), __fmul_rn(o0, si[i]));
+                x[i + 1] = __fadd_rn(__fmul_rn(x[i + 1], co[i + 1]), __fmul_rn(o1, si[i + 1]));
               }
             }
           }

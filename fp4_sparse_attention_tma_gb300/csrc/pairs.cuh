@@ -1,4 +1,6 @@
-// Pairs of fp32 numbers in 64-bit registers, and operations on both at once.
+// Pairs of fp32 numbers in 64-bit registers, and operations on both at once.  The compiler may make one
+// operation, with one rounding, of a sum and a product that it takes (seen for add2 of two mul2): where each
+// rounding counts, products are taken one by one with __fmul_rn.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -71,7 +71,8 @@ def test_queries_in_4_bits(norm, rot):
     run(64, rot if rot[0] != 48 else (32, 8, False), norm, "bf16", True, q4=True, heads=(5, 1), values=False)
 
 
+@pytest.mark.parametrize("fp4", [False, True])
 @pytest.mark.parametrize("norm", [None, "same"])
-def test_without_queries(norm):
+def test_without_queries(fp4, norm):
     """Two full chunks of keys and one of a single head, then those of values."""
-    run(128, ("all", 0, False), norm, "bf16", False, heads=(0, 17))
+    run(128, ("all", 0, False), norm, "bf16", fp4, heads=(0, 17))
