@@ -525,7 +525,9 @@ def idx_cache_append_fp4(k, v, page_table, row_req, row_pos, k_codes, k_scale, v
                          raise_on_error=True) -> int:
     """idx_cache_append into a 4-bit cache: E2M1 codes u8 [NP, 64, Hk, D / 2] with UE8M0
     scales u8 [NP, 64, Hk, D / 32], the format of the indexer's keys.  out_q in q's type, or
-    codes u8 [R, Hq, D / 2] with out_q_scale u8 [R, Hq, D / 32], as the indexer takes them."""
+    codes u8 [R, Hq, D / 2] with out_q_scale u8 [R, Hq, D / 32], as the indexer takes them.
+    What is not finite or above 6 * 2^40 gets a scale byte above 167, which the indexer and
+    attention refuse for the whole call."""
     return _append("idx_cache_append_fp4", True, k, v, page_table, row_req, row_pos,
                    (k_codes, k_scale, v_codes, v_scale), (_stream(stream),), q, out_q,
                    out_q_scale, q_weight, k_weight, eps, rope, rope_first, rope_pairs,

@@ -81,7 +81,8 @@ typedef enum {
                                    IDX_MAX_SCALE_BYTE and IDX_MAX_ABS_WEIGHT): a scale byte
                                    above 167 in the query block of a scored row or in a K page
                                    that a window covers, or a weight of a scored row that is not
-                                   finite or exceeds 2^24 in magnitude */
+                                   finite or exceeds 2^24 in magnitude; attention over a 4-bit
+                                   cache: a scale byte above 167 of a position that a row sees */
 } idx_status_t;
 
 /*
@@ -678,7 +679,10 @@ int idx_cache_append_async(const idx_tensor_t* q, const idx_tensor_t* k, const i
  * idx_cache_append_fp4 is idx_cache_append into such a cache: of the normed and rotated key in
  * fp32, and of the value, e is the smallest of 0 .. 254 such that no element of the block
  * exceeds 6 * 2^(e - 127), and an element becomes the nearest code, ties to the even one.  A
- * block with a NaN or an infinity gets e = 255, and codes 0.  What becomes codes is computed in
+ * block with a NaN or an infinity gets e = 255, and codes 0.  Bytes above IDX_MAX_SCALE_BYTE
+ * (these, and magnitudes above 6 * 2^40) are written like others and are no error here, but the
+ * indexer and attention refuse a call of which a row sees one, with all its rows: a caller whose
+ * requests share calls finds the request by its scales.  What becomes codes is computed in
  * the order written, x * (1 / sqrt(mean + eps)) * weight, each operation rounded by itself and
  * the sum of squares as if it were rounded once: the codes do not depend on how the work is
  * divided.
@@ -736,14 +740,16 @@ int idx_cache_gather_fp4_async(const idx_tensor_t* k_codes, const idx_tensor_t* 
  * idx_cache_append_fp4 (keys and values may share elements here).  Rows, windows, slots, empty
  * rows, outputs and errors as there, and:
  *   a scale byte above IDX_MAX_SCALE_BYTE of a position that a row sees (NaN included) is
- *   IDX_ERR_INVALID_VALUE.
+ *   IDX_ERR_INVALID_VALUE: as after every error all rows are NaN, of other requests too (in 16
+ *   bits a NaN reaches the rows that see it).  idx_cache_append_fp4 writes such bytes.
  * Sums, maxima and weights are held in fp32; softmax weights are rounded to fp16 for their
  * product with the values, for queries of either type: an error of 2^-11 sum p |v| at most, n
  * weights below 2^-24 of a row's largest lose n 2^-35 max |v|.  Of keys, blocks whose scale is
  * below 2^-26 of the largest within 128 positions, and of values, blocks below 2^-26 of the
  * largest that the head has in the request or list, may count as 0 (their elements are below
  * 2^-24 of what the largest block can hold); bf16 queries' elements below 2^-38 of the head's
- * largest lose bits.
+ * largest lose bits, and that largest (2^x or more), times the largest 2^(e - 127) of keys near
+ * (e 26 or more), is taken for 2^153 at most and 2^-100 at least: scores beyond are held there.
  */
 int idx_attn_paged_fp4(const idx_tensor_t* q, const idx_tensor_t* k_codes,
                        const idx_tensor_t* k_scale, const idx_tensor_t* v_codes,
