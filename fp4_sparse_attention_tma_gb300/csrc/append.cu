@@ -702,7 +702,9 @@ cudaError_t launch_append_as(AppendParams p, int sm, cudaStream_t stream) {
   // 16 bits, up to 16 chunks 9, 9, 26 chunks 11, 11, 45 chunks 15, 11.
   // The slots named twice are found in a table with room for twice the rows.  Past 2^14 rows it would not fit, and a bitmap
   // does it, which takes a walk over the rows for every 2^20 slots (one walk: as fast as the table, 8208 rows 37.5 us with
-  // either; bits of neighbouring slots in one word instead: 96000 rows 418 -> 430).
+  // either; bits of neighbouring slots in one word instead: 96000 rows 418 -> 430).  So the cost grows with the pool: 32768
+  // rows of one head of 64, keys only, pools of 2^18 and 2^20 slots 40 us, 2^22 91, 2^24 298, 2^26 1117.  A table that is
+  // nearly half full takes longer than the bitmap's one walk: 16384 such rows 48 to 76 us, 24000 with the bitmap 31.
   const int64_t slots = (int64_t)p.num_pages * kPage;
   int table = 0, map = 6;
   for (int b = 6; b <= kMostBits && !table; ++b)

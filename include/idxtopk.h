@@ -649,7 +649,9 @@ int idx_cache_evict_scratch_bytes(int32_t num_req, int32_t max_pages, int32_t ds
  * Errors: a position below -1, at or above MP * 64 or (with rope) P, or a request out of range
  * IDX_ERR_INVALID_METADATA; a page outside [0, NP), or a slot named by two rows
  * IDX_ERR_INVALID_PAGE.  After an error that the device finds the caches, and queries in place,
- * are as they were, and out_q is NaN.
+ * are as they were, and out_q is NaN.  (Every call looks for such rows before it writes; with more
+ * than 2^14 rows, padding among them, that takes a walk over the rows for every 2^20 slots of
+ * the pool.)
  */
 int idx_cache_append(const idx_tensor_t* q, const idx_tensor_t* k, const idx_tensor_t* v,
                      const idx_tensor_t* page_table, const idx_tensor_t* row_req,
